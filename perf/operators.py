@@ -164,7 +164,7 @@ def prepare(case, seed):
             kept = np.minimum(rng.permutation(_spread(0, case["new"], B)), new)
             if case["finish"]:
                 kept[rng.permutation(B)[:B // case["finish"]]] = -1
-            s["kept_len"] = _i32(kept)
+            s.update(kept_len=_i32(kept), reserved_len=_i32(ctx + new + 1))
         if own:  # the outputs and scratch that a serving loop allocates once
             from speculative_decoding_verification_41_gb300 import paged
             s["buffers"] = (paged.ReleaseBuffers(B, "cuda") if after else
@@ -204,8 +204,9 @@ def prepare(case, seed):
              scale=case["D"] ** -0.5)
     if own:
         from speculative_decoding_verification_41_gb300 import paged
-        s["buffers"] = paged.AttentionBuffers(int(off[-1]), case["Hq"], case["D"],
-                                              DTYPES[case["dtype"]], "cuda", with_lse=True)
+        s["buffers"] = paged.AttentionBuffers(int(off[-1]), case["Hq"], case["Hkv"],
+                                              case["D"], case["new"], DTYPES[case["dtype"]],
+                                              "cuda", with_lse=True)
     return s
 
 
@@ -222,9 +223,9 @@ def _run_own(s):
         return [s["table"], o["context_len"], o["row_off"], o["draft_off"], o["slot_map"],
                 o["positions"], o["free_count"]]
     if s["op"] == "release":
-        o = paged.dspark_pages_release(s["context_len"], s["new_len"], s["kept_len"], s["table"],
-                                       s["stack"], s["stack_count"], page_size=s["page"],
-                                       extra=1, buffers=s["buffers"])
+        o = paged.dspark_pages_release(s["context_len"], s["reserved_len"], s["kept_len"],
+                                       s["table"], s["stack"], s["stack_count"],
+                                       page_size=s["page"], extra=1, buffers=s["buffers"])
         return [s["stack"], o["context_len"], o["free_count"]]
     if s["op"] == "append":
         paged.dspark_kv_append(s["k"], s["v"], s["slot_map"], s["k_cache"], s["v_cache"],
@@ -272,7 +273,7 @@ def _release(s):
     ps, table, stack = s["page"], s["table"], s["stack"]
     ctx, kept = s["context_len"].long(), s["kept_len"].long()
     keep = torch.where(kept < 0, 0, ctx + kept + 1)
-    stay, had = (keep + ps - 1) // ps, (ctx + s["new_len"].long() + 1 + ps - 1) // ps
+    stay, had = (keep + ps - 1) // ps, (s["reserved_len"].long() + ps - 1) // ps
     gone = had - stay
     first = s["stack_count"].long() + torch.cumsum(gone, 0) - gone
     j = torch.arange(table.shape[1], device=table.device)[None, :]
