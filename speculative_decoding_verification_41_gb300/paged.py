@@ -1,0 +1,349 @@
+"""The paged key-value cache around a speculative step (include/dspark_paged.h),
+through ctypes: argument checks and marshalling only, every step runs in the
+CUDA kernels of libdspark.so.
+
+  dspark_pages_reserve(...)    pages, slots, positions and row offsets of new tokens
+  dspark_kv_append(...)        their keys and values into the cache
+  dspark_paged_attention(...)  attention of the new tokens over the cache
+  dspark_pages_release(...)    pages of rejected tokens and finished requests back
+
+Caches are [num_pages, page_size, heads, D] tensors of any strides with
+contiguous D: a cache stored [num_pages, heads, page_size, D] is passed as its
+.transpose(1, 2).
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+import re
+from typing import Optional
+
+import torch
+
+from . import binding
+from .binding import DSPARK_BF16, DsparkError
+
+HEADER = os.path.join(binding.ROOT, "include", "dspark_paged.h")
+EXPORTED = ("dspark_pages_reserve", "dspark_pages_release", "dspark_kv_append",
+            "dspark_paged_attention")
+
+
+def _header_const(name: str) -> int:
+    return int(re.search(rf"#define {name} (\d+)", open(HEADER).read()).group(1))
+
+
+DSPARK_F16 = _header_const("DSPARK_F16")
+DSPARK_ERR_TOO_LARGE = 6
+DSPARK_ERR_NO_PAGES = _header_const("DSPARK_ERR_NO_PAGES")
+PAGED_MAX_ROWS = _header_const("DSPARK_PAGED_MAX_ROWS")
+PAGED_MAX_CTAS = _header_const("DSPARK_PAGED_MAX_CTAS")
+binding.STATUS_NAMES[DSPARK_ERR_NO_PAGES] = "DSPARK_ERR_NO_PAGES"
+_DTYPES = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16}
+
+_fns = None
+
+
+def _load():
+    global _fns
+    if _fns is None:
+        lib = binding.load()
+        vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
+                                 ctypes.c_size_t)
+        lib.dspark_pages_reserve.argtypes = [vp, vp, i32, i32, i32, i32, vp, i64, i32, vp, vp, i32,
+                                             vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.dspark_pages_release.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, i64, i32, vp, vp,
+                                             vp, vp, vp, vp]
+        lib.dspark_kv_append.argtypes = [vp, vp, i64, i64, vp, i32, i32, i32, i32, vp, vp, i64,
+                                         i64, i64, i32, i32, vp, vp]
+        lib.dspark_paged_attention.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, i32, i32, vp,
+                                               i64, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32,
+                                               i32, i32, vp, vp, vp, vp, sz, vp]
+        for name in EXPORTED:
+            getattr(lib, name).restype = ctypes.c_int
+        _fns = lib
+    return _fns
+
+
+def paged_attention_workspace_bytes(Hq: int, Hkv: int, max_new: int, D: int) -> int:
+    """Python statement of DSPARK_PAGED_ATTENTION_WS_BYTES (include/dspark_paged.h)."""
+    rows = min(16 * (-(-(Hq // Hkv) * max_new // 16)), PAGED_MAX_ROWS)
+    return ((PAGED_MAX_CTAS * 64 + 255) & ~255) + 2 * PAGED_MAX_CTAS * rows * (4 * D + 8)
+
+
+def _want(name: str, t: torch.Tensor, dtype, device, shape=None):
+    """A contiguous CUDA tensor of this type, place and shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libdspark has no CPU path)")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _table(block_table: torch.Tensor, B: int, device):
+    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
+        raise ValueError("block_table must be a CUDA tensor (libdspark has no CPU path)")
+    if block_table.dtype != torch.int32 or block_table.device != device:
+        raise ValueError(f"block_table must be torch.int32 on {device}")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages]")
+    width = block_table.shape[1]
+    stride, inner = block_table.stride()
+    if inner != 1 and width > 1 and B > 0:
+        raise ValueError("rows of block_table must be contiguous")
+    return (stride if B > 1 else width), width
+
+
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, device):
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+            raise ValueError(f"{name} must be a CUDA tensor on {device}")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be [pages, page_size, heads, D] with contiguous D")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if k_cache.dtype not in _DTYPES or v_cache.dtype != k_cache.dtype:
+        raise ValueError(f"caches must be bfloat16 or float16 alike, got {k_cache.dtype} and "
+                         f"{v_cache.dtype}")
+
+
+def _on(stream, device):
+    """The stream's handle; a stream of another device than the tensors' is refused."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device != device:
+        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
+    return s
+
+
+def _kept(buffers, stream):
+    """Memory that the call allocated stays the stream's until its work is done."""
+    if stream is not None:
+        for t in vars(buffers).values():
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+
+
+def _call(name: str, device, *args):
+    fn = getattr(_load(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc != 0:
+        raise DsparkError(name, rc)
+
+
+def _checked(name: str, status: torch.Tensor, check: bool, stream):
+    if check:
+        stream.synchronize()
+        st = int(status.item())
+        if st != 0:
+            raise DsparkError(f"{name} (device)", st)
+
+
+class ReserveBuffers:
+    """Outputs of dspark_pages_reserve for B requests and max_tokens rows, so that
+    repeated calls (and CUDA-graph capture) allocate nothing."""
+
+    def __init__(self, B: int, max_tokens: int, device):
+        dev = torch.device(device)
+        self.B, self.max_tokens = B, max_tokens
+        self.context_len = torch.empty(B, dtype=torch.int32, device=dev)
+        self.row_off = torch.empty(B + 1, dtype=torch.int64, device=dev)
+        self.draft_off = torch.empty(B + 1, dtype=torch.int64, device=dev)
+        self.slot_map = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        self.positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        self.free_count = torch.empty(1, dtype=torch.int32, device=dev)
+        self.device_status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+def dspark_pages_reserve(context_len: torch.Tensor, new_len: torch.Tensor,
+                         block_table: torch.Tensor, free_pages: torch.Tensor,
+                         free_count: torch.Tensor, *, page_size: int, max_tokens: int,
+                         extra: int = 0, buffers: Optional[ReserveBuffers] = None, stream=None,
+                         check: bool = False) -> dict:
+    """Pages, slots and row offsets for new_len[r] + extra new tokens of every
+    request (include/dspark_paged.h). block_table is written in place; free_pages
+    is an array of all the pool's ids, the first free_count[0] of them free.
+
+    Returns context_len [B], row_off [B+1] int64 (dspark_verify's target_row_off
+    with extra = 1), draft_off [B+1] int64 (its draft_row_off), slot_map and
+    positions [max_tokens], free_count [1], device_status [1] (device tensors).
+    With check=True the call synchronises and raises on a non-OK device status."""
+    dev = context_len.device
+    _want("context_len", context_len, torch.int32, None)
+    B = context_len.numel()
+    _want("new_len", new_len, torch.int32, dev, context_len.shape)
+    stride, width = _table(block_table, B, dev)
+    _want("free_pages", free_pages, torch.int32, dev)
+    _want("free_count", free_count, torch.int32, dev, (1,))
+    buf = buffers or ReserveBuffers(B, max_tokens, dev)
+    if (buf.B, buf.max_tokens) != (B, max_tokens):
+        raise ValueError("buffers were made for another shape")
+    s = _on(stream, dev)
+    if buffers is None:
+        _kept(buf, stream)
+    _call("dspark_pages_reserve", dev, context_len.data_ptr(), new_len.data_ptr(), extra, B,
+          page_size, free_pages.numel(), block_table.data_ptr(), stride, width,
+          free_pages.data_ptr(), free_count.data_ptr(), max_tokens, buf.context_len.data_ptr(),
+          buf.row_off.data_ptr(), buf.draft_off.data_ptr(), buf.slot_map.data_ptr(),
+          buf.positions.data_ptr(), buf.free_count.data_ptr(), buf.device_status.data_ptr(),
+          s.cuda_stream)
+    _checked("dspark_pages_reserve", buf.device_status, check, s)
+    return {"context_len": buf.context_len, "row_off": buf.row_off, "draft_off": buf.draft_off,
+            "slot_map": buf.slot_map, "positions": buf.positions, "free_count": buf.free_count,
+            "device_status": buf.device_status}
+
+
+class ReleaseBuffers:
+    """Outputs of dspark_pages_release for B requests."""
+
+    def __init__(self, B: int, device):
+        dev = torch.device(device)
+        self.B = B
+        self.context_len = torch.empty(B, dtype=torch.int32, device=dev)
+        self.free_count = torch.empty(1, dtype=torch.int32, device=dev)
+        self.device_status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+def dspark_pages_release(context_len: torch.Tensor, reserved_len: torch.Tensor,
+                         kept_len: torch.Tensor, block_table: torch.Tensor,
+                         free_pages: torch.Tensor, free_count: torch.Tensor, *, page_size: int,
+                         extra: int = 0, buffers: Optional[ReleaseBuffers] = None, stream=None,
+                         check: bool = False) -> dict:
+    """After the verification: request r keeps context_len[r] + kept_len[r] + extra
+    of its reserved_len[r] tokens (kept_len[r] = -1: none, it is finished); the
+    pages past them go back on free_pages, in place (include/dspark_paged.h).
+
+    Returns context_len [B], free_count [1], device_status [1] (device tensors)."""
+    dev = context_len.device
+    _want("context_len", context_len, torch.int32, None)
+    B = context_len.numel()
+    _want("reserved_len", reserved_len, torch.int32, dev, context_len.shape)
+    _want("kept_len", kept_len, torch.int32, dev, context_len.shape)
+    stride, width = _table(block_table, B, dev)
+    _want("free_pages", free_pages, torch.int32, dev)
+    _want("free_count", free_count, torch.int32, dev, (1,))
+    buf = buffers or ReleaseBuffers(B, dev)
+    if buf.B != B:
+        raise ValueError("buffers were made for another shape")
+    s = _on(stream, dev)
+    if buffers is None:
+        _kept(buf, stream)
+    _call("dspark_pages_release", dev, context_len.data_ptr(), reserved_len.data_ptr(),
+          kept_len.data_ptr(), extra, B, page_size, free_pages.numel(), block_table.data_ptr(),
+          stride, width, free_pages.data_ptr(), free_count.data_ptr(),
+          buf.context_len.data_ptr(), buf.free_count.data_ptr(), buf.device_status.data_ptr(),
+          s.cuda_stream)
+    _checked("dspark_pages_release", buf.device_status, check, s)
+    return {"context_len": buf.context_len, "free_count": buf.free_count,
+            "device_status": buf.device_status}
+
+
+def dspark_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
+                     k_cache: torch.Tensor, v_cache: torch.Tensor, *,
+                     device_status: Optional[torch.Tensor] = None, stream=None,
+                     check: bool = False) -> dict:
+    """Row i of k and v ([n, heads, D], any strides alike, contiguous D) into slot
+    slot_map[i] of the caches, in place; negative slots are skipped
+    (include/dspark_paged.h). slot_map may be longer than n (a reservation's whole
+    map): its first n entries count. Returns device_status [1]."""
+    dev = k_cache.device
+    _cache(k_cache, v_cache, dev)
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+        if t.dtype != k_cache.dtype:
+            raise ValueError(f"{name} must be {k_cache.dtype}, got {t.dtype}")
+        if t.dim() != 3 or t.stride(2) != 1 or t.shape[1:] != k_cache.shape[2:]:
+            raise ValueError(f"{name} must be [n, {k_cache.shape[2]}, {k_cache.shape[3]}] with "
+                             "contiguous rows")
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("k and v must have the same shape and strides")
+    n, Hkv, D = k.shape
+    _want("slot_map", slot_map, torch.int32, dev)
+    if slot_map.numel() < n:
+        raise ValueError(f"slot_map has {slot_map.numel()} entries for {n} rows")
+    s = _on(stream, dev)
+    if device_status is None:
+        device_status = torch.empty(1, dtype=torch.int32, device=dev)
+        if stream is not None:
+            device_status.record_stream(stream)
+    else:
+        _want("device_status", device_status, torch.int32, dev, (1,))
+    sp, st, sh, _ = k_cache.stride()
+    _call("dspark_kv_append", dev, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+          slot_map.data_ptr(), n, Hkv, D, _DTYPES[k.dtype], k_cache.data_ptr(),
+          v_cache.data_ptr(), sp, st, sh, k_cache.shape[1], k_cache.shape[0],
+          device_status.data_ptr(), s.cuda_stream)
+    _checked("dspark_kv_append", device_status, check, s)
+    return {"device_status": device_status}
+
+
+class AttentionBuffers:
+    """Outputs and workspace of dspark_paged_attention for n_tokens rows, so that
+    repeated calls (and CUDA-graph capture) allocate nothing."""
+
+    def __init__(self, n_tokens: int, Hq: int, Hkv: int, D: int, max_new: int, dtype, device,
+                 with_lse: bool = False):
+        dev = torch.device(device)
+        self.shape = (n_tokens, Hq, D)
+        self.out = torch.empty(self.shape, dtype=dtype, device=dev)
+        self.lse = torch.empty(n_tokens, Hq, dtype=torch.float32, device=dev) if with_lse else None
+        self.device_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.workspace = torch.empty(paged_attention_workspace_bytes(Hq, Hkv, max_new, D),
+                                     dtype=torch.uint8, device=dev)
+
+
+def dspark_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           block_table: torch.Tensor, context_len: torch.Tensor,
+                           row_off: torch.Tensor, *, scale: float, max_new: int, window: int = 0,
+                           with_lse: bool = False, buffers: Optional[AttentionBuffers] = None,
+                           stream=None, check: bool = False) -> dict:
+    """Attention of each request's newest tokens over its pages
+    (include/dspark_paged.h). q is [n_tokens, Hq, D] (contiguous D); rows
+    row_off[r] .. row_off[r+1]-1, at most max_new, are the last ones of request
+    r's context_len[r] cached tokens, and each sees those up to itself (with a
+    window, the last `window` of them).
+
+    Returns out [n_tokens, Hq, D], lse [n_tokens, Hq] float32 (or None) and
+    device_status [1] (device tensors)."""
+    dev = k_cache.device
+    _cache(k_cache, v_cache, dev)
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.device != dev:
+        raise ValueError(f"q must be a CUDA tensor on {dev}")
+    if q.dtype != k_cache.dtype:
+        raise ValueError(f"q must be {k_cache.dtype}, got {q.dtype}")
+    pages, page_size, Hkv, D = k_cache.shape
+    if q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != D:
+        raise ValueError(f"q must be [n_tokens, heads, {D}] with contiguous rows")
+    n, Hq, _ = q.shape
+    _want("context_len", context_len, torch.int32, dev)
+    B = context_len.numel()
+    _want("row_off", row_off, torch.int64, dev, (B + 1,))
+    stride, width = _table(block_table, B, dev)
+    if Hkv < 1 or Hq < 1 or Hq % Hkv != 0 or max_new < 1:
+        raise ValueError(f"{Hq} query heads on {Hkv} key heads, max_new {max_new}")
+    buf = buffers or AttentionBuffers(n, Hq, Hkv, D, max_new, q.dtype, dev, with_lse)
+    if buf.shape != (n, Hq, D) or buf.out.dtype != q.dtype:
+        raise ValueError("buffers were made for another shape or type")
+    if with_lse and buf.lse is None:
+        raise ValueError("buffers were made without lse (AttentionBuffers(..., with_lse=True))")
+    s = _on(stream, dev)
+    if buffers is None:
+        _kept(buf, stream)
+    sp, st, sh, _ = k_cache.stride()
+    _call("dspark_paged_attention", dev, q.data_ptr(), q.stride(0), q.stride(1),
+          k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, page_size, pages,
+          block_table.data_ptr(), stride, width, context_len.data_ptr(), row_off.data_ptr(), B, n,
+          Hq, Hkv, D, max_new, scale, window, _DTYPES[q.dtype], buf.out.data_ptr(),
+          buf.lse.data_ptr() if with_lse else None, buf.device_status.data_ptr(),
+          buf.workspace.data_ptr(), buf.workspace.numel(), s.cuda_stream)
+    _checked("dspark_paged_attention", buf.device_status, check, s)
+    return {"out": buf.out, "lse": buf.lse if with_lse else None,
+            "device_status": buf.device_status}
