@@ -26,6 +26,10 @@ bool attn_map(CUtensorMap* map, bool f16, const void* base, int rank, const cuui
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Shared memory of a CTA that has its SM to itself; two share it with 1 KB each
+// for the system.
+constexpr int kSmemCta = 231424;
+
 struct Launch {
   CUtensorMap q, k, v;
   AttnArgs a;
@@ -43,7 +47,7 @@ int attn_launch(Launch& c, int sms) {
     std::lock_guard<std::mutex> lock(g_attn_mutex);
     if (!ready[dev]) {
       if (cudaFuncSetAttribute(k_attention<S, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(attn_smem<S>())) != cudaSuccess)
+                               kSmemCta / S::CTAS) != cudaSuccess)
         return DSPARK_ERR_CUDA;
       ready[dev] = true;
     }
@@ -51,8 +55,15 @@ int attn_launch(Launch& c, int sms) {
   AttnArgs& a = c.a;
   a.ctas = std::max(1, std::min(sms * S::CTAS, DSPARK_PAGED_MAX_CTAS) / a.n_chunks);
   const int grid = a.ctas * a.n_chunks;
-  if (launch_pdl(k_attention<S, F16>, grid, S::THREADS, attn_smem<S>(), c.stream, c.q, c.k, c.v,
-                 a) != cudaSuccess)
+  // Shared memory: what the queries and two buffers of weights leave is the ring's.
+  a.p_off = kCtlBytes<S> + static_cast<uint32_t>(S::HALVES * a.n_cols * 128);
+  a.p_bytes = static_cast<uint32_t>(a.n_cols / 16 * 4096);
+  a.ring_off = a.p_off + 2 * a.p_bytes;
+  a.stages = std::min<int>(kMaxStages, (kSmemCta / S::CTAS - a.ring_off) / S::kStage);
+  a.lead = 1;
+  const size_t smem = a.ring_off + static_cast<size_t>(a.stages) * S::kStage;
+  if (launch_pdl(k_attention<S, F16>, grid, S::THREADS, smem, c.stream, c.q, c.k, c.v, a) !=
+      cudaSuccess)
     return DSPARK_ERR_CUDA;
   JoinArgs& j = c.j;
   j.n = grid;
@@ -71,11 +82,10 @@ int attn_launch(Launch& c, int sms) {
 // The smallest row block that holds the rows; keys are copied once for all of them.
 template <int D, bool F16>
 int attn_shape(Launch& c, int sms) {
-  constexpr int kMore = D == 64 ? 2 : 1;  // a 64-element tile is half as large
-  if (c.a.n_cols <= 16) return attn_launch<AttnShape<D, 16, 1, 2, 3 * kMore>, F16>(c, sms);
-  if (c.a.n_cols <= 32) return attn_launch<AttnShape<D, 32, 1, 1, 6 * kMore>, F16>(c, sms);
-  if (c.a.n_cols <= 64) return attn_launch<AttnShape<D, 64, 2, 1, 5 * kMore>, F16>(c, sms);
-  return attn_launch<AttnShape<D, 160, 2, 1, 4 * kMore>, F16>(c, sms);
+  if (c.a.n_cols <= 16) return attn_launch<AttnShape<D, 16, 1, 2>, F16>(c, sms);
+  if (c.a.n_cols <= 32) return attn_launch<AttnShape<D, 32, 2, 1>, F16>(c, sms);
+  if (c.a.n_cols <= 64) return attn_launch<AttnShape<D, 64, 4, 1>, F16>(c, sms);
+  return attn_launch<AttnShape<D, 160, 4, 1>, F16>(c, sms);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -13,24 +13,28 @@
 // rearranged. A thread of the softmax warps owns one token of the tile and
 // walks the rows: its weights P land in shared memory as 16-byte stores.
 //
-// The reference m of a row need not be its running maximum, only near it: a
-// tile in which no score exceeds its row's m by 8 (a factor 2^8, which neither
-// bf16 nor half precision nor the f32 sums mind) is used as it is, and that is
-// one vote per tile instead of a maximum over 128 tokens for every row. Only
-// when the vote fails (in a request's first tile, and rarely after it) are the
-// maxima taken, m raised and O and l scaled.
+// The reference m of a row need not be its running maximum: any m with 2^(c s - m)
+// in range for every score s serves, and one that some score reaches keeps the
+// largest weight at 1 or more. A tile whose scores exceed their rows' references
+// by less than kSlack (log2) is used as it is: that is one vote per tile instead
+// of a maximum over 128 tokens for every row. Bf16 weights have binary32's range,
+// so there a row starts with the score of one token that it sees, whichever, and
+// a slack of 2^60; half precision ends at 2^16 and starts with the first tile's
+// maxima. When a vote fails, the maxima are taken, m raised and O and l scaled.
 //
 // Bound. Every cached key and value is read once: 4 D bytes per token and key
 // head against 4 D R flops, so up to R of about 280 the copy rate of HBM bounds
 // the call. So: (1) a ring of TMA copies that runs ahead of the arithmetic
 // across requests; (2) work split evenly over the CTAs whatever the lengths:
-// all (request, head, tile) units form one line, CTA c of C takes units
-// [cW/C, (c+1)W/C), found from the lengths on the device; a request cut by such
-// a border leaves partial (m, l, O) rows that k_attention_join adds up in
+// all (request, head) items form one line, each as long as its tiles and `lead`
+// more for what it costs to begin and end one; CTA c of C takes [cW/C, (c+1)W/C)
+// of it, found from the lengths on the device; a request cut by such a border leaves partial (m, l, O) rows that k_attention_join adds up in
 // the order of the tiles, so results do not depend on timing.
 //
-// Warps: 0 copies (TMA), 1 issues the products, the others (one or two groups
-// of four, which share the rows) do the softmax and write the results.
+// Warps: 0 copies (TMA), 1 issues the products, the others, in groups of four
+// that share the rows among them, do the softmax and write the results. S and P
+// have two buffers each: while a group is at a tile's exponents the products of
+// the next scores and of the weights before are under way.
 #pragma once
 
 #include <climits>
@@ -42,7 +46,9 @@ namespace dspark {
 
 constexpr int kTileTok = 128;
 constexpr float kNoRef = 1e38f;  // minus the reference of a row that has seen no token yet
-constexpr float kSlack = 8.f;    // how far (log2) a score may exceed its row's reference
+// how far (log2) a score may exceed its row's reference
+template <bool F16>
+constexpr float kSlack = F16 ? 14.f : 60.f;
 
 struct AttnArgs {
   const int32_t* table;
@@ -57,6 +63,9 @@ struct AttnArgs {
   int64_t stride, page_stride, token_stride, head_stride;
   int32_t B, n_tokens, Hq, Hkv, G, Gs, parts, max_new, t_chunk, n_chunks, ctas, n_cols;
   int32_t shift, num_pages, max_pages, window;  // window INT_MAX: none
+  int32_t lead;     // length of an item besides its tiles
+  int32_t stages;   // of the ring
+  uint32_t p_off, p_bytes, ring_off;  // shared memory: weights (two buffers), ring
   float c;  // scale * log2(e)
 };
 
@@ -86,7 +95,7 @@ static_assert(sizeof(AttnItem) == 64, "AttnItem layout");
 
 struct AttnReq {  // a request, as the partition sees it
   int64_t row0;
-  int32_t units;  // per key head
+  int32_t units;  // length of the item of a key head; 0: no rows
   int32_t t_rows, lim0, begin, end;
 };
 
@@ -104,7 +113,8 @@ __device__ __forceinline__ bool attn_request(const AttnArgs& a, int r, int t0, A
   q.lim0 = len - static_cast<int32_t>(T) + t0 + 1;
   q.end = max(0, q.lim0 + q.t_rows - 1);
   q.begin = min(q.end, max(0, q.lim0 > a.window ? q.lim0 - a.window : 0));
-  q.units = q.end > 0 ? (q.end + kTileTok - 1) / kTileTok - q.begin / kTileTok : 1;
+  // an item without tiles still has rows to write: it counts as one
+  q.units = a.lead + (q.end > 0 ? (q.end + kTileTok - 1) / kTileTok - q.begin / kTileTok : 1);
   return true;
 }
 
@@ -127,28 +137,54 @@ __device__ __forceinline__ void tma_load_3d_to(uint32_t dst, const CUtensorMap* 
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
-// 16 consecutive f32 columns of this thread's lane, complete on return
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
+// 8 consecutive f32 columns of this thread's lane; the values are there after
+// tmem_arrived() on them.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7])
       : "r"(taddr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Ties the values of a load to a wait before this statement.
+__device__ __forceinline__ void tmem_arrived(float* v) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
       : "memory");
+}
+// Sum or maximum of 8 columns over the warp's lanes: each step halves the
+// columns a lane holds and doubles the lanes they stand for. Lanes 4k .. 4k+3
+// return column k's.
+template <bool MAX>
+__device__ __forceinline__ float columns_over_warp(float (&v)[8], int lane) {
+#pragma unroll
+  for (int h = 4, o = 16; h >= 1; h >>= 1, o >>= 1) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int k = 0; k < h; ++k) {
+      const float give = upper ? v[k] : v[k + h], have = upper ? v[k + h] : v[k];
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, give, o);
+      v[k] = MAX ? fmaxf(have, got) : have + got;
+    }
+  }
+#pragma unroll
+  for (int o = 2; o >= 1; o >>= 1) {
+    const float got = __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+    v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+  }
+  return v[0];
 }
 __device__ __forceinline__ void bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -220,71 +256,71 @@ __device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t saddr) {
 // ---------------------------------------------------------------------------
 // shapes
 // ---------------------------------------------------------------------------
-template <int D_, int NB_, int GROUPS_, int CTAS_, int STAGES_>
+constexpr int kMaxStages = 12;
+
+template <int D_, int NB_, int GROUPS_, int CTAS_>
 struct AttnShape {
-  static constexpr int D = D_, NB = NB_, GROUPS = GROUPS_, CTAS = CTAS_, STAGES = STAGES_;
+  static constexpr int D = D_, NB = NB_, GROUPS = GROUPS_, CTAS = CTAS_;
   static constexpr int THREADS = 64 + 128 * GROUPS;
-  static constexpr int NC = NB / GROUPS;           // columns (rows of q) of a softmax group
-  static constexpr int HALVES = D / 64;            // 128-byte wide slabs of a K, V or Q tile
+  static constexpr int NC = (NB / 8 + GROUPS - 1) / GROUPS * 8;  // columns of a softmax group
+  static constexpr int HALVES = D / 64;         // 128-byte wide slabs of a K, V or Q tile
   static constexpr uint32_t kSlab = kTileTok * 128;
   static constexpr uint32_t kStage = HALVES * kSlab;
-  static constexpr uint32_t kQ = 0, kQBytes = HALVES * NB * 128;
-  static constexpr uint32_t kP = kQ + kQBytes, kPBytes = NB / 16 * 4096;
-  static constexpr uint32_t kRing = kP + kPBytes;
-  static constexpr uint32_t kCtl = kRing + STAGES * kStage;
   static constexpr uint32_t kColS = 0, kColO = 2 * NB;
   static constexpr uint32_t kTmem = 3 * NB <= 64 ? 64 : 3 * NB <= 128 ? 128 : 3 * NB <= 256 ? 256 : 512;
 };
 
 template <class S>
 struct AttnCtl {
-  uint64_t full[S::STAGES], empty[S::STAGES];
-  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, item_full[2], item_empty[2], drained;
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], item_full[2], item_empty[2];
+  uint64_t odd_full, drained;
   uint32_t tmem;
-  int32_t status, abort, odd_n;
-  AttnItem item[2];
-  alignas(16) float nref[S::NB];       // minus the rows' references
-  alignas(16) int32_t lim[S::NB];      // a row sees the tokens below (and within the window)
-  alignas(16) float fac[S::NB];        // a row's factor: of its sums, or of its result
-  float red[4][S::NB];                 // per warp: maxima, sums
-  int32_t odd[2 * S::NB];              // tokens whose values are not finite and not for all rows
-  int64_t scan[S::THREADS / 32];
+  int32_t status, abort, start_r, start_off;
   int64_t u_total;
-  int32_t start_r, start_off;
+  int64_t scan[S::THREADS / 32];
+  AttnItem item[2];
+  // per column (row of q); a group's own
+  alignas(16) float nref[S::NB + 8];    // minus the rows' references
+  alignas(16) int32_t lim[S::NB + 8];   // a row sees the tokens below (and within the window)
+  alignas(16) int32_t at[S::NB + 8];    // element of a row in out, from the item's first
+  alignas(16) float fac[S::NB + 8];     // a row's factor: of its sums, or of its result
+  float red[4][S::NB + 8];              // per warp: maxima, sums
+  int32_t odd_n[2], odd[2][2 * S::NB];  // tokens whose values are not finite and not for all rows
 };
 
 template <class S>
-constexpr uint32_t attn_smem() {
-  return S::kCtl + static_cast<uint32_t>(sizeof(AttnCtl<S>));
-}
+constexpr uint32_t kCtlBytes = (static_cast<uint32_t>(sizeof(AttnCtl<S>)) + 1023u) & ~1023u;
 
 template <class S, bool F16>
 __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     k_attention(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  AttnCtl<S>& ctl = *reinterpret_cast<AttnCtl<S>*>(smem + S::kCtl);
-  const uint32_t sbase = smem_addr(smem);
+  AttnCtl<S>& ctl = *reinterpret_cast<AttnCtl<S>*>(smem);
+  const uint32_t s_q = smem_addr(smem) + kCtlBytes<S>;  // Q; then weights, ring
+  const uint32_t s_p = smem_addr(smem) + a.p_off, s_ring = smem_addr(smem) + a.ring_off;
+  const uint32_t q_slab = a.n_cols * 128u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < S::STAGES; ++i) {
+    for (int i = 0; i < a.stages; ++i) {
       mbar_init(&ctl.full[i], 1);
       mbar_init(&ctl.empty[i], 1);
     }
     mbar_init(&ctl.q_full, 1);
     mbar_init(&ctl.q_empty, 1);
-    mbar_init(&ctl.p_full, 4 * S::GROUPS);
-    mbar_init(&ctl.pv_done, 1);
+    mbar_init(&ctl.odd_full, 1);
     mbar_init(&ctl.drained, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.p_full[i], 4 * S::GROUPS);
+      mbar_init(&ctl.pv_done[i], 1);
       mbar_init(&ctl.item_full[i], 1);
       mbar_init(&ctl.item_empty[i], 4 * S::GROUPS);
     }
     ctl.status = DSPARK_OK;
     ctl.abort = 0;
-    ctl.odd_n = 0;
     fence_barrier_init();
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
@@ -386,6 +422,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             return n;
           }
           AttnReq q;
+          int h, lead_in, take;
           for (;;) {
             if (r >= r_base + 32 || r < r_base) {
               r_base = r;
@@ -395,6 +432,18 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             const int src = r - r_base;
             q.units = __shfl_sync(0xFFFFFFFFu, mine.units, src);
             if (off < q.units * a.Hkv) {
+              h = off / q.units;
+              lead_in = off - h * q.units;
+              take = static_cast<int>(min(static_cast<int64_t>(q.units - lead_in), u_end - u));
+              if (lead_in + take <= a.lead) {  // nothing but the item's lead: another CTA begins it
+                u += take;
+                off += take;
+                if (u >= u_end) {
+                  done = true;
+                  return n;
+                }
+                continue;
+              }
               q.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, src);
               q.t_rows = __shfl_sync(0xFFFFFFFFu, mine.t_rows, src);
               q.lim0 = __shfl_sync(0xFFFFFFFFu, mine.lim0, src);
@@ -410,22 +459,20 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
               return n;
             }
           }
-          const int h = off / q.units, in_head = off - h * q.units;
-          const int take = static_cast<int>(
-              min(static_cast<int64_t>(q.units - in_head), u_end - u));
+          const int in_head = max(lead_in - a.lead, 0);
           item.row0 = q.row0;
           item.r = r;
           item.kv_head = h;
           item.head0 = h * a.G + part * a.Gs;
-          item.tiles = q.end > 0 ? take : 0;
+          item.tiles = q.end > 0 ? lead_in + take - a.lead - in_head : 0;
           item.tile0 = q.begin / kTileTok + in_head;
           item.t_rows = q.t_rows;
           item.lim0 = q.lim0;
           item.begin = q.begin;
           item.end = q.end;
           item.starts = in_head == 0;
-          item.ends = in_head + take == q.units;
-          item.first = static_cast<int32_t>(((u - in_head + 1) * g - 1) / W);
+          item.ends = lead_in + take == q.units;
+          item.first = static_cast<int32_t>(((u - lead_in + a.lead + 1) * g - 1) / W);
           u += take;
           off += take;
           left = item.tiles;
@@ -447,7 +494,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       auto all_wait = [](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity)) != 0;
       };
-      uint32_t step = 0, items = 0, q_loads = 0;  // ring position; items and Q tiles so far
+      uint32_t s = 0, wraps = 0, items = 0, q_loads = 0;  // ring position; items, Q tiles so far
       bool ok = true;
       AttnItem cur_item{};
       Gen cur = next(it);
@@ -469,8 +516,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             if (!ok) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(&ctl.q_full, q_bytes);
-              for (int s = 0; s < S::HALVES; ++s)
-                tma_load_3d_to(sbase + S::kQ + s * S::NB * 128, &map_q, s * 64, cur_item.head0,
+              for (int i = 0; i < S::HALVES; ++i)
+                tma_load_3d_to(s_q + i * q_slab, &map_q, i * 64, cur_item.head0,
                                static_cast<int>(cur_item.row0), &ctl.q_full);
             }
             ++q_loads;
@@ -488,16 +535,16 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           const uint32_t bytes = __popc(loads) * rows_box * 128;
           const int y = (cur.tile * kTileTok + box * rows_box) & ((1 << a.shift) - 1);
 #pragma unroll
-          for (int kv = 0; kv < 2 && ok; ++kv, ++step) {
-            const uint32_t s = step % S::STAGES, use = step / S::STAGES;
-            if (use >= 1) ok = all_wait(&ctl.empty[s], (use - 1u) & 1u);
+          for (int kv = 0; kv < 2; ++kv) {
+            if (wraps >= 1) ok = ok && all_wait(&ctl.empty[s], (wraps - 1u) & 1u);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
             __syncwarp();
             if (cur.load)
-              tma_load_4d(sbase + S::kRing + s * S::kStage + half * S::kSlab + box * rows_box * 128,
+              tma_load_4d(s_ring + s * S::kStage + half * S::kSlab + box * rows_box * 128,
                           kv == 0 ? &map_k : &map_v, half * 64, y, cur_item.kv_head, page,
                           &ctl.full[s], policy);
+            if (++s == static_cast<uint32_t>(a.stages)) s = 0, ++wraps;
           }
         }
         cur = nxt;
@@ -517,8 +564,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         }
       }
       // leave no copy in flight into this CTA's shared memory
-      for (uint32_t i = step > S::STAGES ? step - S::STAGES : 0; i < step; ++i)
-        mbar_wait(&ctl.full[i % S::STAGES], (i / S::STAGES) & 1u);
+      for (uint32_t i = 0; i < static_cast<uint32_t>(a.stages); ++i)
+        if (i < s || wraps > 0) mbar_wait(&ctl.full[i], (i < s ? wraps : wraps - 1u) & 1u);
       if (q_loads > 0) mbar_wait(&ctl.q_full, (q_loads - 1u) & 1u);
     }
   } else if (warp == 1) {
@@ -535,21 +582,30 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       const uint64_t desc_v = attn_desc(S::kSlab, 1024, 2);
       // P: 16 rows of q contiguous per token, 16-row blocks 4,096 apart, 8-token groups 256 apart
       const uint64_t desc_p = attn_desc(4096, 256, 6);
-      uint32_t k_step = 0, items = 0, q_loads = 0, tiles = 0;  // ring position of the next K
+      uint32_t items = 0, q_loads = 0, tiles = 0, scores = 0;
+      const uint32_t stages = static_cast<uint32_t>(a.stages);
+      struct Ring {  // K tiles lie at even positions of the line of copies, V tiles at odd ones
+        uint32_t s, phase;
+      } rk{0, 0}, rv{1, 0};
+      auto two_on = [&](Ring& r) {
+        r.s += 2;
+        if (r.s >= stages) r.s -= stages, r.phase ^= 1u;
+      };
       bool ok = true;
       auto product_s = [&]() {  // S^T of the next tile
-        const uint32_t s = k_step % S::STAGES, buf = (k_step >> 1) & 1u;
-        ok = mbar_wait(&ctl.full[s], (k_step / S::STAGES) & 1u);
+        const uint32_t buf = scores & 1u;
+        ok = mbar_wait(&ctl.full[rk.s], rk.phase);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t k0 = sbase + S::kRing + s * S::kStage, q0 = sbase + S::kQ;
+        const uint32_t k0 = s_ring + rk.s * S::kStage;
 #pragma unroll
         for (int k = 0; k < S::D / 16; ++k)
           tc_mma(tmem + S::kColS + buf * S::NB, at(desc_kq, k0 + (k / 4) * S::kSlab + (k % 4) * 32),
-                 at(desc_kq, q0 + (k / 4) * S::NB * 128 + (k % 4) * 32), idesc_s, k > 0);
-        tc_commit(&ctl.empty[s]);
+                 at(desc_kq, s_q + (k / 4) * q_slab + (k % 4) * 32), idesc_s, k > 0);
+        tc_commit(&ctl.empty[rk.s]);
         tc_commit(&ctl.s_full[buf]);
-        k_step += 2;
+        two_on(rk);
+        ++scores;
       };
       while (ok) {
         const uint32_t slot = items & 1u;
@@ -563,24 +619,25 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ++q_loads;
         if (!ok) break;
         product_s();
-        for (int i = 0; i < nt && ok; ++i) {
+        for (int i = 0; i < nt && ok; ++i, ++tiles) {
           if (i + 1 < nt) product_s();
           if (!ok) break;
           if (i == max(nt - 2, 0)) tc_commit(&ctl.q_empty);  // after the item's last S
-          ok = mbar_wait(&ctl.p_full, tiles & 1u);
+          const uint32_t buf = tiles & 1u;
+          ok = mbar_wait(&ctl.p_full[buf], (tiles >> 1) & 1u);
           if (!ok) break;
-          const uint32_t v_step = 2 * tiles + 1, s = v_step % S::STAGES;
-          ok = mbar_wait(&ctl.full[s], (v_step / S::STAGES) & 1u);
+          if (i + 1 == nt) mbar_arrive(&ctl.odd_full);  // the groups' lists of the item are written
+          ok = mbar_wait(&ctl.full[rv.s], rv.phase);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t v0 = sbase + S::kRing + s * S::kStage, p0 = sbase + S::kP;
+          const uint32_t v0 = s_ring + rv.s * S::kStage, p0 = s_p + buf * a.p_bytes;
 #pragma unroll
           for (int k = 0; k < kTileTok / 16; ++k)
             tc_mma(tmem + S::kColO, at(desc_v, v0 + k * 2048), at(desc_p, p0 + k * 512), idesc_o,
                    i > 0 || k > 0);
-          tc_commit(&ctl.empty[s]);
-          tc_commit(&ctl.pv_done);
-          ++tiles;
+          tc_commit(&ctl.empty[rv.s]);
+          tc_commit(&ctl.pv_done[buf]);
+          two_on(rv);
         }
       }
       if (!ok) {
@@ -595,21 +652,22 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     // =====================================================================
     // softmax, results
     // =====================================================================
-    constexpr int kSoft = 128 * S::GROUPS;
-    const int group = (warp - 2) >> 2, quarter = warp & 3;
+    const int group = (warp - 2) >> 2, quarter = warp & 3, bar = 1 + group;
     const int gt = (quarter << 5) | lane;  // this thread's token of a tile, and lane of S and O
-    const int blocks = (a.n_cols / 16 + S::GROUPS - 1) / S::GROUPS;  // of 16 columns, per group
-    const int c0 = group * blocks * 16;    // the group's first column
+    constexpr int kBlocks = S::NC / 8;     // of 8 columns
+    const int cols = a.Gs * a.t_chunk;
+    const int blocks = (cols + 8 * S::GROUPS - 1) / (8 * S::GROUPS);  // of the group, in use
+    const int c0 = group * blocks * 8;     // the group's first column
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;  // (32 * quarter) << 16
     const uint32_t window = static_cast<uint32_t>(a.window);
     volatile int32_t* abort_flag = &ctl.abort;
-    uint32_t tiles = 0, items = 0;
+    uint32_t tiles = 0, items = 0, lists = 0;
+    uint32_t v_s = 1, v_phase = 0;         // ring position of the next V tile
     bool recorded = false;
     for (;;) {
       const uint32_t slot = items & 1u;
       bool failed = !mbar_wait(&ctl.item_full[slot], (items >> 1) & 1u);
-      if (bar_any(1, kSoft, failed || *abort_flag != 0)) {
-        failed = true;
+      if (bar_any(bar, 128, failed || *abort_flag != 0)) {
         *abort_flag = 1;
         break;
       }
@@ -617,16 +675,20 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       if (it.tiles < 0) break;
       ++items;
       const int rows = it.t_rows * a.Gs;
-      const int my_rows = max(0, min(16 * blocks, rows - c0));
-      const int nb = (my_rows + 15) >> 4;
-      for (int j = c0 + gt; j < min(c0 + 16 * blocks, a.n_cols); j += 128) {
+      const int my_rows = max(0, min(8 * blocks, rows - c0));
+      const int nb = (my_rows + 7) >> 3;
+      for (int j = c0 + gt; j < c0 + 8 * nb; j += 128) {
         // a column past the rows takes no part: all its scores are below its reference
+        const int t = j / a.Gs;
         ctl.nref[j] = j < rows ? kNoRef : -INFINITY;
-        ctl.lim[j] = j < rows ? it.lim0 + j / a.Gs : INT_MIN / 2;
+        ctl.lim[j] = j < rows ? it.lim0 + t : INT_MIN / 2;
+        ctl.at[j] = (t * a.Hq + j - t * a.Gs) * S::D;
+        ctl.fac[j] = 1.f;
       }
-      if (tid == 64) ctl.odd_n = 0;
-      bar_sync(1, kSoft);
+      if (tid == 64) ctl.odd_n[slot] = 0;
+      bar_sync(bar, 128);
       const int lim_last = it.lim0 + it.t_rows - 1;
+      const int lo_last = a.window == INT_MAX ? 0 : max(0, lim_last - a.window);
       float l[S::NC];
 #pragma unroll
       for (int j = 0; j < S::NC; ++j) l[j] = 0.f;
@@ -636,65 +698,85 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         const uint32_t buf = tiles & 1u;
         const int tok0 = (it.tile0 + i) * kTileTok, tok = tok0 + gt;
         // every token of the tile visible to every row?
-        const bool whole = tok0 + kTileTok <= it.lim0 &&
-                           (a.window == INT_MAX || tok0 >= lim_last - a.window);
+        const bool whole = tok0 + kTileTok <= it.lim0 && tok0 >= lo_last;
         failed |= !mbar_wait(&ctl.s_full[buf], (tiles >> 1) & 1u);
         tc_fence_after();
+        // scores, -inf where the row does not see the token
+        float x[S::NC];
         const uint32_t s_addr = tmem + lanes + S::kColS + buf * S::NB + c0;
-        // the scores of columns j .. j+15, -inf where the row does not see the token
-        auto scores = [&](int j, float (&x)[16]) {
-          tmem_ld16(s_addr + j, x);
-          if (!whole) {
-            const int4* lim4 = reinterpret_cast<const int4*>(&ctl.lim[c0 + j]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int4 m = lim4[k];
-              if (static_cast<uint32_t>(m.x - 1 - tok) >= window) x[4 * k] = -INFINITY;
-              if (static_cast<uint32_t>(m.y - 1 - tok) >= window) x[4 * k + 1] = -INFINITY;
-              if (static_cast<uint32_t>(m.z - 1 - tok) >= window) x[4 * k + 2] = -INFINITY;
-              if (static_cast<uint32_t>(m.w - 1 - tok) >= window) x[4 * k + 3] = -INFINITY;
-            }
-          }
-        };
-        auto exponents = [&](int j, float (&x)[16]) {
-          scores(j, x);
-          const float4* nr4 = reinterpret_cast<const float4*>(&ctl.nref[c0 + j]);
+        for (int b = 0; b < kBlocks; ++b)
+          if (b < nb) tmem_ld8(s_addr + 8 * b, x + 8 * b);
+        tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 m = nr4[k];
-            x[4 * k] = fmaf(x[4 * k], a.c, m.x);
-            x[4 * k + 1] = fmaf(x[4 * k + 1], a.c, m.y);
-            x[4 * k + 2] = fmaf(x[4 * k + 2], a.c, m.z);
-            x[4 * k + 3] = fmaf(x[4 * k + 3], a.c, m.w);
-          }
-        };
-        // With one block of columns the exponents stay in registers over the
-        // vote; with more they are read from tensor memory again.
-        float keep[16];
-        float top = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < S::NC / 16; ++b)
+        for (int b = 0; b < kBlocks; ++b)
           if (b < nb) {
-            exponents(16 * b, keep);
+            tmem_arrived(x + 8 * b);
+            if (!whole) {
+              const int4* lim4 = reinterpret_cast<const int4*>(&ctl.lim[c0 + 8 * b]);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) top = fmaxf(top, keep[k]);
-          }
-        const uint32_t prev = (tiles - 1u) & 1u;  // phase of the tile before, if there is one
-        if (bar_any(1, kSoft, top > kSlack || failed)) {
-#pragma unroll 1
-          for (int b = 0; b < nb; ++b) {
-            float x[16];
-            scores(16 * b, x);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              // floats in the order of integers; NaN takes no part
-              const int32_t f = __float_as_int(x[k] == x[k] ? x[k] : -INFINITY);
-              const int32_t o = __reduce_max_sync(0xFFFFFFFFu, f ^ ((f >> 31) & 0x7FFFFFFF));
-              if (lane == k)
-                ctl.red[quarter][c0 + 16 * b + k] = __int_as_float(o ^ ((o >> 31) & 0x7FFFFFFF));
+              for (int k = 0; k < 2; ++k) {
+                const int4 m = lim4[k];
+                float* y = x + 8 * b + 4 * k;
+                if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[0] = -INFINITY;
+                if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[1] = -INFINITY;
+                if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[2] = -INFINITY;
+                if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[3] = -INFINITY;
+              }
             }
           }
-          if (bar_any(1, kSoft, failed || *abort_flag != 0)) {
+        // exponents y = c x - m
+        auto exponent = [&](int b, float (&y)[8]) {
+          const float4* nr4 = reinterpret_cast<const float4*>(&ctl.nref[c0 + 8 * b]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float4 m = nr4[k];
+            y[4 * k] = fmaf(x[8 * b + 4 * k], a.c, m.x);
+            y[4 * k + 1] = fmaf(x[8 * b + 4 * k + 1], a.c, m.y);
+            y[4 * k + 2] = fmaf(x[8 * b + 4 * k + 2], a.c, m.z);
+            y[4 * k + 3] = fmaf(x[8 * b + 4 * k + 3], a.c, m.w);
+          }
+        };
+        bool raise = true;  // the first tile in half precision
+        if (!F16 || i > 0) {
+          if (!F16 && i == 0) {
+            // the first token that all rows see, if the tile has one
+            const int pick = max(tok0, lo_last);
+            if (pick < min(tok0 + kTileTok, it.lim0)) {
+              if (tok == pick) {
+#pragma unroll
+                for (int j = 0; j < S::NC; ++j)
+                  if (j < my_rows) {
+                    const float m = x[j] * a.c;
+                    if (fabsf(m) < kNoRef) ctl.nref[c0 + j] = -m;
+                  }
+              }
+              bar_sync(bar, 128);
+            }
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            if (b < nb) {
+              float y[8];
+              exponent(b, y);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) top = fmaxf(top, y[k]);
+            }
+          raise = bar_any(bar, 128, top > kSlack<F16> || failed);
+        }
+        if (raise) {
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            if (b < nb) {
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)  // NaN takes no part
+                v[k] = x[8 * b + k] == x[8 * b + k] ? x[8 * b + k] : -INFINITY;
+              const float m = columns_over_warp<true>(v, lane);
+              if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = m;
+            }
+          if (bar_any(bar, 128, failed || *abort_flag != 0)) {
             leave = true;
             break;
           }
@@ -705,53 +787,51 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             ctl.fac[j] = m > old ? ex2_approx(old - m) : 1.f;
             if (m > old) ctl.nref[j] = -m;
           }
-          bar_sync(1, kSoft);
+          bar_sync(bar, 128);
           if (i > 0) {
-            failed |= !mbar_wait(&ctl.pv_done, prev);
+            const uint32_t before = tiles - 1u;
+            failed |= !mbar_wait(&ctl.pv_done[before & 1u], (before >> 1) & 1u);
             tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+              if (b < nb) {
+                const float* f = &ctl.fac[c0 + 8 * b];
+                float o[8];
+                tmem_ld8(tmem + lanes + S::kColO + c0 + 8 * b, o);
+                tmem_wait_ld();
+                tmem_arrived(o);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  o[k] *= f[k];
+                  l[8 * b + k] *= f[k];
+                }
+                tmem_st8(tmem + lanes + S::kColO + c0 + 8 * b, o);
+              }
+            tmem_wait_st();
           }
-#pragma unroll
-          for (int b = 0; b < S::NC / 16; ++b)
-            if (b < nb) {
-              float f[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const int j = 16 * b + k;
-                f[k] = j < my_rows ? ctl.fac[c0 + j] : 1.f;
-                l[j] *= f[k];
-              }
-              if (i > 0) {
-                float o[16];
-                tmem_ld16(tmem + lanes + S::kColO + c0 + 16 * b, o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= f[k];
-                tmem_st16(tmem + lanes + S::kColO + c0 + 16 * b, o);
-              }
-              if constexpr (S::NC == 16) exponents(0, keep);
-            }
-          tmem_wait_st();
         }
-        // P is free once the tile before it has been multiplied
-        if (tiles > 0) failed |= !mbar_wait(&ctl.pv_done, prev);
+        // this buffer of weights is free once the tile before last has been multiplied
+        if (tiles >= 2) failed |= !mbar_wait(&ctl.pv_done[buf], ((tiles >> 1) - 1u) & 1u);
 #pragma unroll
-        for (int b = 0; b < S::NC / 16; ++b)
+        for (int b = 0; b < kBlocks; ++b)
           if (b < nb) {
-            if constexpr (S::NC > 16) exponents(16 * b, keep);
-            uint32_t p[8];
+            float y[8];
+            exponent(b, y);
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float p0 = ex2_approx(keep[k]), p1 = ex2_approx(keep[k + 1]);
-              l[16 * b + k] += p0;
-              l[16 * b + k + 1] += p1;
-              // The weights enter the second product in the inputs' type (half
-              // a step of it each, the step at most that of the output); their
-              // sum l is of the unrounded ones, whose errors do not add up.
-              p[k / 2] = pack2<F16>(p0, p1);
+            for (int k = 0; k < 8; ++k) {
+              y[k] = ex2_approx(y[k]);
+              l[8 * b + k] += y[k];
             }
-            const uint32_t row = sbase + S::kP + ((c0 >> 4) + b) * 4096 + gt * 32;
-            const uint32_t swap = (gt & 4) << 2;  // 32-byte swizzle
-            sts_u4(row + swap, p[0], p[1], p[2], p[3]);
-            sts_u4(row + (swap ^ 16u), p[4], p[5], p[6], p[7]);
+            // The weights enter the second product in the inputs' type (half a
+            // step of it each, no more than the output's own rounding); their
+            // sum l is of the unrounded ones, whose errors would not average
+            // out where a few tokens have all the weight.
+            const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
+            const uint32_t swap = static_cast<uint32_t>(gt >> 2) & 1u;  // 32-byte swizzle
+            sts_u4(s_p + buf * a.p_bytes + (chunk >> 1) * 4096u + gt * 32u +
+                       (((chunk & 1u) ^ swap) << 4),
+                   pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3]), pack2<F16>(y[4], y[5]),
+                   pack2<F16>(y[6], y[7]));
           }
         if (!whole && group == 0) {
           // Zero weights do not silence values that are not finite, and the
@@ -759,10 +839,9 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           // what only some rows see the non-finite values are taken out here
           // and added to those rows at the end.
           const bool some = tok >= it.begin && tok < it.end;
-          const bool all = tok < it.lim0 && (a.window == INT_MAX || tok >= lim_last - a.window);
-          const uint32_t v_step = 2 * tiles + 1, s = v_step % S::STAGES;
-          failed |= !mbar_wait(&ctl.full[s], (v_step / S::STAGES) & 1u);
-          const uint32_t v_row = sbase + S::kRing + s * S::kStage + gt * 128;
+          const bool all = tok < it.lim0 && tok >= lo_last;
+          failed |= !mbar_wait(&ctl.full[v_s], v_phase);
+          const uint32_t v_row = s_ring + v_s * S::kStage + gt * 128;
           if (!some) {
 #pragma unroll
             for (int q = 0; q < S::HALVES; ++q)
@@ -771,6 +850,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           } else if (!all) {
             bool odd = false;
             constexpr uint32_t kExp = F16 ? 0x7C00u : 0x7F80u;
+#pragma unroll 4
             for (int k = 0; k < 8 * S::HALVES; ++k) {
               const uint32_t addr = v_row + (k >> 3) * S::kSlab + (k & 7) * 16;
               const uint4 v = lds_u4(addr);
@@ -784,16 +864,17 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
               if (hit) sts_u4(addr, w[0], w[1], w[2], w[3]);
               odd |= hit;
             }
-            if (odd) ctl.odd[atomicAdd(&ctl.odd_n, 1)] = tok;
+            if (odd) ctl.odd[slot][atomicAdd(&ctl.odd_n[slot], 1)] = tok;
           }
         }
+        v_s += 2;
+        if (v_s >= static_cast<uint32_t>(a.stages)) v_s -= a.stages, v_phase ^= 1u;
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_full);
+        if (lane == 0) mbar_arrive(&ctl.p_full[buf]);
       }
       if (leave) {
-        failed = true;
         *abort_flag = 1;
         break;
       }
@@ -801,29 +882,23 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       // ---- the item's rows ----------------------------------------------
       const bool alone = it.starts && it.ends;
       const int64_t part_row = static_cast<int64_t>(2 * id + (it.starts ? 1 : 0)) * a.n_cols;
-      if (it.tiles > 0) {
-        failed |= !mbar_wait(&ctl.pv_done, (tiles - 1u) & 1u);
-        tc_fence_after();
-      }
 #pragma unroll
-      for (int b = 0; b < S::NC / 16; ++b)
+      for (int b = 0; b < kBlocks; ++b)
         if (b < nb) {
-          // sums over the warp's 32 tokens: halve the columns, double the tokens
+          float v[8];
 #pragma unroll
-          for (int h = 8, o = 16; h >= 1; h >>= 1, o >>= 1) {
-            const bool upper = (lane & o) != 0;
-#pragma unroll
-            for (int k = 0; k < h; ++k) {
-              const float give = upper ? l[16 * b + k] : l[16 * b + k + h];
-              const float have = upper ? l[16 * b + k + h] : l[16 * b + k];
-              l[16 * b + k] = have + __shfl_xor_sync(0xFFFFFFFFu, give, o);
-            }
-          }
-          l[16 * b] += __shfl_xor_sync(0xFFFFFFFFu, l[16 * b], 1);
-          if ((lane & 1) == 0) ctl.red[quarter][c0 + 16 * b + (lane >> 1)] = l[16 * b];
+          for (int k = 0; k < 8; ++k) v[k] = l[8 * b + k];
+          const float sum = columns_over_warp<false>(v, lane);
+          if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = sum;
         }
-      if (bar_any(1, kSoft, failed || *abort_flag != 0)) {
-        failed = true;
+      if (it.tiles > 0) {
+        const uint32_t last = tiles - 1u;
+        failed |= !mbar_wait(&ctl.odd_full, lists & 1u);
+        failed |= !mbar_wait(&ctl.pv_done[last & 1u], (last >> 1) & 1u);
+        tc_fence_after();
+        ++lists;
+      }
+      if (bar_any(bar, 128, failed || *abort_flag != 0)) {
         *abort_flag = 1;
         break;
       }
@@ -832,55 +907,61 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         const float m = -ctl.nref[j];
         if (alone) {
           const bool seen = ctl.lim[j] > 0;
-          ctl.fac[j] = 1.f / sum;
+          ctl.fac[j] = seen ? 1.f / sum : 0.f;  // no token: O is zero
           if (a.lse)
-            a.lse[(it.row0 + j / a.Gs) * a.Hq + it.head0 + j % a.Gs] =
+            a.lse[it.row0 * a.Hq + it.head0 + ctl.at[j] / S::D] =
                 seen ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
         } else {
+          ctl.fac[j] = 1.f;
           reinterpret_cast<float2*>(a.part_ml)[part_row + j] = make_float2(m, sum);
         }
       }
-      bar_sync(1, kSoft);
-      const int odd_n = ctl.odd_n;
+      bar_sync(bar, 128);
+      const int odd_n = it.tiles > 0 ? ctl.odd_n[slot] : 0;
       const bool writer = S::D == 128 || lane < 16;  // M = 64 fills 16 lanes of each warp's 32
       const int d = S::D == 128 ? gt : quarter * 16 + lane;
-      int t = c0 / a.Gs, h = c0 % a.Gs;
+      uint16_t* const out =
+          static_cast<uint16_t*>(a.out) + (it.row0 * a.Hq + it.head0) * S::D + d;
+      float* const part = a.part_o + (part_row + c0) * S::D + d;
 #pragma unroll 1
       for (int b = 0; b < nb; ++b) {
-        float o[16];
+        float o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = 0.f;
         if (it.tiles > 0) {
-          tmem_ld16(tmem + lanes + S::kColO + c0 + 16 * b, o);
+          tmem_ld8(tmem + lanes + S::kColO + c0 + 8 * b, o);
+          tmem_wait_ld();
+          tmem_arrived(o);
+        }
+        for (int q = 0; q < odd_n; ++q) {
+          const int u = ctl.odd[slot][q];
+          const int32_t page = a.table[it.r * a.stride + (u >> a.shift)];
+          if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages) || !writer) continue;
+          const uint32_t bits = static_cast<const uint16_t*>(a.v_cache)[
+              page * a.page_stride + (u & ((1 << a.shift) - 1)) * a.token_stride +
+              it.kv_head * a.head_stride + d];
+          constexpr uint32_t kExp = F16 ? 0x7C00u : 0x7F80u;
+          if ((bits & kExp) != kExp) continue;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (static_cast<uint32_t>(ctl.lim[c0 + 8 * b + k] - 1 - u) < window)
+              o[k] += half_to_float<F16>(bits);
+        }
+        const float4* f4 = reinterpret_cast<const float4*>(&ctl.fac[c0 + 8 * b]);
+        const int4* at4 = reinterpret_cast<const int4*>(&ctl.at[c0 + 8 * b]);
+        const float4 f0 = f4[0], f1 = f4[1];
+        const int4 a0 = at4[0], a1 = at4[1];
+        const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+        const int to[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+        const int live = writer ? my_rows - 8 * b : 0;  // columns of the block to write
+        if (alone) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < live) out[to[k]] = static_cast<uint16_t>(pack2<F16>(o[k] * f[k], 0.f));
         } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int j = c0 + 16 * b + k;
-          if (j < c0 + my_rows && writer) {
-            const int lim = ctl.lim[j];
-            float v = o[k];
-            for (int q = 0; q < odd_n; ++q) {
-              const int u = ctl.odd[q];
-              if (static_cast<uint32_t>(lim - 1 - u) >= window) continue;
-              const int32_t page = a.table[it.r * a.stride + (u >> a.shift)];
-              if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) continue;
-              const uint16_t bits = static_cast<const uint16_t*>(a.v_cache)[
-                  page * a.page_stride + (u & ((1 << a.shift) - 1)) * a.token_stride +
-                  it.kv_head * a.head_stride + d];
-              constexpr uint32_t kExp = F16 ? 0x7C00u : 0x7F80u;
-              if ((bits & kExp) == kExp) v += half_to_float<F16>(bits);
-            }
-            if (alone) {
-              v = lim > 0 ? v * ctl.fac[j] : 0.f;
-              const uint32_t w = pack2<F16>(v, 0.f);
-              static_cast<uint16_t*>(a.out)[((it.row0 + t) * a.Hq + it.head0 + h) * S::D + d] =
-                  static_cast<uint16_t>(w);
-            } else {
-              a.part_o[(part_row + j) * S::D + d] = v;
-            }
-          }
-          if (++h == a.Gs) h = 0, ++t;
+          for (int k = 0; k < 8; ++k)
+            if (k < live) part[(8 * b + k) * S::D] = o[k];
         }
       }
       if (it.ends && !it.starts) {
