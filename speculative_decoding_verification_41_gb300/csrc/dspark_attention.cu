@@ -85,6 +85,7 @@ int attn_shape(Launch& c, int sms) {
   if (c.a.n_cols <= 16) return attn_launch<AttnShape<D, 16, 1, 2>, F16>(c, sms);
   if (c.a.n_cols <= 32) return attn_launch<AttnShape<D, 32, 2, 1>, F16>(c, sms);
   if (c.a.n_cols <= 64) return attn_launch<AttnShape<D, 64, 4, 1>, F16>(c, sms);
+  if (c.a.n_cols <= 96) return attn_launch<AttnShape<D, 96, 3, 1>, F16>(c, sms);
   return attn_launch<AttnShape<D, 160, 4, 1>, F16>(c, sms);
 }
 

@@ -186,6 +186,20 @@ __device__ __forceinline__ float columns_over_warp(float (&v)[8], int lane) {
   }
   return v[0];
 }
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+// A wait of a whole warp: one outcome, so that its lanes stay together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity)) != 0;
+}
 __device__ __forceinline__ void bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
@@ -490,10 +504,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         --left;
         return n;
       };
-      // one outcome for the warp, so that its lanes stay together
-      auto all_wait = [](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity)) != 0;
-      };
       uint32_t s = 0, wraps = 0, items = 0, q_loads = 0;  // ring position; items, Q tiles so far
       bool ok = true;
       AttnItem cur_item{};
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         Gen nxt = done ? Gen{0, 0, false, false, false} : next(it);
         if (cur.first) {
           const uint32_t slot = items & 1u;
-          if (items >= 2) ok = all_wait(&ctl.item_empty[slot], ((items >> 1) - 1u) & 1u);
+          if (items >= 2) ok = warp_wait(&ctl.item_empty[slot], ((items >> 1) - 1u) & 1u);
           if (!ok) break;
           if (lane == 0) {
             ctl.item[slot] = cur_item;
@@ -512,7 +522,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           }
           ++items;
           if (cur.any) {
-            if (q_loads >= 1) ok = all_wait(&ctl.q_empty, (q_loads - 1u) & 1u);
+            if (q_loads >= 1) ok = warp_wait(&ctl.q_empty, (q_loads - 1u) & 1u);
             if (!ok) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(&ctl.q_full, q_bytes);
@@ -536,7 +546,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           const int y = (cur.tile * kTileTok + box * rows_box) & ((1 << a.shift) - 1);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            if (wraps >= 1) ok = ok && all_wait(&ctl.empty[s], (wraps - 1u) & 1u);
+            if (wraps >= 1) ok = ok && warp_wait(&ctl.empty[s], (wraps - 1u) & 1u);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
             __syncwarp();
@@ -557,7 +567,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       // the end of the line
       if (ok) {
         const uint32_t slot = items & 1u;
-        if (items >= 2) ok = all_wait(&ctl.item_empty[slot], ((items >> 1) - 1u) & 1u);
+        if (items >= 2) ok = warp_wait(&ctl.item_empty[slot], ((items >> 1) - 1u) & 1u);
         if (ok && lane == 0) {
           ctl.item[slot].tiles = -1;
           mbar_arrive(&ctl.item_full[slot]);
@@ -572,7 +582,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     // =====================================================================
     // products
     // =====================================================================
-    if (lane == 0 && u_begin < u_end) {
+    // The whole warp walks the line and one elected thread issues: uniform
+    // descriptors stay in uniform registers. (Walked by one thread alone an
+    // instruction cost about 100 cycles to issue, twice its execution.)
+    if (u_begin < u_end) {
+      const bool leader = elect_one();
       const uint32_t n = static_cast<uint32_t>(a.n_cols);
       const uint32_t idesc_s = attn_idesc(F16, kTileTok, n, false, false);
       const uint32_t idesc_o = attn_idesc(F16, S::D, n, true, true);
@@ -594,57 +608,64 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       bool ok = true;
       auto product_s = [&]() {  // S^T of the next tile
         const uint32_t buf = scores & 1u;
-        ok = mbar_wait(&ctl.full[rk.s], rk.phase);
+        ok = warp_wait(&ctl.full[rk.s], rk.phase);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t k0 = s_ring + rk.s * S::kStage;
+        if (leader) {
+          const uint64_t k0 = at(desc_kq, s_ring + rk.s * S::kStage), q0 = at(desc_kq, s_q);
 #pragma unroll
-        for (int k = 0; k < S::D / 16; ++k)
-          tc_mma(tmem + S::kColS + buf * S::NB, at(desc_kq, k0 + (k / 4) * S::kSlab + (k % 4) * 32),
-                 at(desc_kq, s_q + (k / 4) * q_slab + (k % 4) * 32), idesc_s, k > 0);
-        tc_commit(&ctl.empty[rk.s]);
-        tc_commit(&ctl.s_full[buf]);
+          for (int k = 0; k < S::D / 16; ++k)
+            tc_mma(tmem + S::kColS + buf * S::NB,
+                   k0 + static_cast<uint32_t>((k / 4) * (S::kSlab >> 4) + (k % 4) * 2),
+                   q0 + ((k / 4) * (q_slab >> 4) + (k % 4) * 2), idesc_s, k > 0);
+          tc_commit(&ctl.empty[rk.s]);
+          tc_commit(&ctl.s_full[buf]);
+        }
         two_on(rk);
         ++scores;
       };
       while (ok) {
         const uint32_t slot = items & 1u;
-        ok = mbar_wait(&ctl.item_full[slot], (items >> 1) & 1u);
+        ok = warp_wait(&ctl.item_full[slot], (items >> 1) & 1u);
         if (!ok) break;
-        const int nt = ctl.item[slot].tiles;
+        const int nt = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tiles, 0);
         ++items;
         if (nt < 0) break;
         if (nt == 0) continue;
-        ok = mbar_wait(&ctl.q_full, q_loads & 1u);
+        ok = warp_wait(&ctl.q_full, q_loads & 1u);
         ++q_loads;
         if (!ok) break;
         product_s();
         for (int i = 0; i < nt && ok; ++i, ++tiles) {
           if (i + 1 < nt) product_s();
           if (!ok) break;
-          if (i == max(nt - 2, 0)) tc_commit(&ctl.q_empty);  // after the item's last S
+          if (leader && i == max(nt - 2, 0)) tc_commit(&ctl.q_empty);  // after the item's last S
           const uint32_t buf = tiles & 1u;
-          ok = mbar_wait(&ctl.p_full[buf], (tiles >> 1) & 1u);
+          ok = warp_wait(&ctl.p_full[buf], (tiles >> 1) & 1u);
           if (!ok) break;
-          if (i + 1 == nt) mbar_arrive(&ctl.odd_full);  // the groups' lists of the item are written
-          ok = mbar_wait(&ctl.full[rv.s], rv.phase);
+          // the groups' lists of the item are written
+          if (leader && i + 1 == nt) mbar_arrive(&ctl.odd_full);
+          ok = warp_wait(&ctl.full[rv.s], rv.phase);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t v0 = s_ring + rv.s * S::kStage, p0 = s_p + buf * a.p_bytes;
+          if (leader) {
+            const uint64_t v0 = at(desc_v, s_ring + rv.s * S::kStage);
+            const uint64_t p0 = at(desc_p, s_p + buf * a.p_bytes);
 #pragma unroll
-          for (int k = 0; k < kTileTok / 16; ++k)
-            tc_mma(tmem + S::kColO, at(desc_v, v0 + k * 2048), at(desc_p, p0 + k * 512), idesc_o,
-                   i > 0 || k > 0);
-          tc_commit(&ctl.empty[rv.s]);
-          tc_commit(&ctl.pv_done[buf]);
+            for (int k = 0; k < kTileTok / 16; ++k)
+              tc_mma(tmem + S::kColO, v0 + static_cast<uint32_t>(k * 128),
+                     p0 + static_cast<uint32_t>(k * 32), idesc_o, k > 0 ? 1u : i > 0);
+            tc_commit(&ctl.empty[rv.s]);
+            tc_commit(&ctl.pv_done[buf]);
+          }
           two_on(rv);
         }
       }
       if (!ok) {
         set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
         *reinterpret_cast<volatile int32_t*>(&ctl.abort) = 1;
-        tc_commit(&ctl.drained);  // no product may outlive the CTA
-        mbar_wait(&ctl.drained, 0);
+        if (leader) tc_commit(&ctl.drained);  // no product may outlive the CTA
+        warp_wait(&ctl.drained, 0);
       }
     }
     __syncwarp();
@@ -671,7 +692,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         *abort_flag = 1;
         break;
       }
-      const AttnItem it = ctl.item[slot];
+      const AttnItem& it = ctl.item[slot];
       if (it.tiles < 0) break;
       ++items;
       const int rows = it.t_rows * a.Gs;
@@ -701,30 +722,51 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         const bool whole = tok0 + kTileTok <= it.lim0 && tok0 >= lo_last;
         failed |= !mbar_wait(&ctl.s_full[buf], (tiles >> 1) & 1u);
         tc_fence_after();
-        // scores, -inf where the row does not see the token
+        // Scores, -inf where the row does not see the token. A group with few
+        // columns keeps them in registers, one with many reads them from tensor
+        // memory again for the second pass.
+        constexpr bool kKeep = S::NC <= 32;
         float x[S::NC];
         const uint32_t s_addr = tmem + lanes + S::kColS + buf * S::NB + c0;
+        auto load = [&](auto from, auto to) {
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-          if (b < nb) tmem_ld8(s_addr + 8 * b, x + 8 * b);
-        tmem_wait_ld();
+          for (int b = from; b < to; ++b)
+            if (b < nb) tmem_ld8(s_addr + 8 * b, x + 8 * b);
+          tmem_wait_ld();
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-          if (b < nb) {
-            tmem_arrived(x + 8 * b);
-            if (!whole) {
-              const int4* lim4 = reinterpret_cast<const int4*>(&ctl.lim[c0 + 8 * b]);
+          for (int b = from; b < to; ++b)
+            if (b < nb) {
+              tmem_arrived(x + 8 * b);
+              if (!whole) {
+                const int4* lim4 = reinterpret_cast<const int4*>(&ctl.lim[c0 + 8 * b]);
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int4 m = lim4[k];
-                float* y = x + 8 * b + 4 * k;
-                if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[0] = -INFINITY;
-                if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[1] = -INFINITY;
-                if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[2] = -INFINITY;
-                if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[3] = -INFINITY;
+                for (int k = 0; k < 2; ++k) {
+                  const int4 m = lim4[k];
+                  float* y = x + 8 * b + 4 * k;
+                  if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[0] = -INFINITY;
+                  if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[1] = -INFINITY;
+                  if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[2] = -INFINITY;
+                  if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[3] = -INFINITY;
+                }
               }
             }
+        };
+        // f(b) for every block in use, its scores in x
+        auto each = [&](auto f) {
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+              if (b < nb) f(b);
+          } else {
+#pragma unroll
+            for (int b = 0; b < kBlocks; b += 2) {
+              load(b, b + 2 < kBlocks ? b + 2 : kBlocks);
+              if (b < nb) f(b);
+              if (b + 1 < kBlocks && b + 1 < nb) f(b + 1);
+            }
           }
+        };
+        if constexpr (kKeep) load(0, kBlocks);
         // exponents y = c x - m
         auto exponent = [&](int b, float (&y)[8]) {
           const float4* nr4 = reinterpret_cast<const float4*>(&ctl.nref[c0 + 8 * b]);
@@ -743,39 +785,36 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             // the first token that all rows see, if the tile has one
             const int pick = max(tok0, lo_last);
             if (pick < min(tok0 + kTileTok, it.lim0)) {
-              if (tok == pick) {
+              each([&](int b) {
+                if (tok == pick) {
 #pragma unroll
-                for (int j = 0; j < S::NC; ++j)
-                  if (j < my_rows) {
-                    const float m = x[j] * a.c;
-                    if (fabsf(m) < kNoRef) ctl.nref[c0 + j] = -m;
+                  for (int k = 0; k < 8; ++k) {
+                    const float m = x[8 * b + k] * a.c;
+                    if (8 * b + k < my_rows && fabsf(m) < kNoRef) ctl.nref[c0 + 8 * b + k] = -m;
                   }
-              }
+                }
+              });
               bar_sync(bar, 128);
             }
           }
           float top = -INFINITY;
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b)
-            if (b < nb) {
-              float y[8];
-              exponent(b, y);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) top = fmaxf(top, y[k]);
-            }
+          each([&](int b) {
+            float y[8];
+            exponent(b, y);
+            top = fmaxf(top, fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])),
+                                   fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7]))));
+          });
           raise = bar_any(bar, 128, top > kSlack<F16> || failed);
         }
         if (raise) {
+          each([&](int b) {
+            float v[8];
 #pragma unroll
-          for (int b = 0; b < kBlocks; ++b)
-            if (b < nb) {
-              float v[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k)  // NaN takes no part
-                v[k] = x[8 * b + k] == x[8 * b + k] ? x[8 * b + k] : -INFINITY;
-              const float m = columns_over_warp<true>(v, lane);
-              if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = m;
-            }
+            for (int k = 0; k < 8; ++k)  // NaN takes no part
+              v[k] = x[8 * b + k] == x[8 * b + k] ? x[8 * b + k] : -INFINITY;
+            const float m = columns_over_warp<true>(v, lane);
+            if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = m;
+          });
           if (bar_any(bar, 128, failed || *abort_flag != 0)) {
             leave = true;
             break;
@@ -812,27 +851,25 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         }
         // this buffer of weights is free once the tile before last has been multiplied
         if (tiles >= 2) failed |= !mbar_wait(&ctl.pv_done[buf], ((tiles >> 1) - 1u) & 1u);
+        each([&](int b) {
+          float y[8];
+          exponent(b, y);
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-          if (b < nb) {
-            float y[8];
-            exponent(b, y);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              y[k] = ex2_approx(y[k]);
-              l[8 * b + k] += y[k];
-            }
-            // The weights enter the second product in the inputs' type (half a
-            // step of it each, no more than the output's own rounding); their
-            // sum l is of the unrounded ones, whose errors would not average
-            // out where a few tokens have all the weight.
-            const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
-            const uint32_t swap = static_cast<uint32_t>(gt >> 2) & 1u;  // 32-byte swizzle
-            sts_u4(s_p + buf * a.p_bytes + (chunk >> 1) * 4096u + gt * 32u +
-                       (((chunk & 1u) ^ swap) << 4),
-                   pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3]), pack2<F16>(y[4], y[5]),
-                   pack2<F16>(y[6], y[7]));
+          for (int k = 0; k < 8; ++k) {
+            y[k] = ex2_approx(y[k]);
+            l[8 * b + k] += y[k];
           }
+          // The weights enter the second product in the inputs' type (half a
+          // step of it each, no more than the output's own rounding); their sum
+          // l is of the unrounded ones, whose errors would not average out
+          // where a few tokens have all the weight.
+          const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
+          const uint32_t swap = static_cast<uint32_t>(gt >> 2) & 1u;  // 32-byte swizzle
+          sts_u4(s_p + buf * a.p_bytes + (chunk >> 1) * 4096u + gt * 32u +
+                     (((chunk & 1u) ^ swap) << 4),
+                 pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3]), pack2<F16>(y[4], y[5]),
+                 pack2<F16>(y[6], y[7]));
+        });
         if (!whole && group == 0) {
           // Zero weights do not silence values that are not finite, and the
           // tile's rest may hold anything: what no row sees is zeroed, and of
