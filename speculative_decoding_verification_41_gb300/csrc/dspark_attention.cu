@@ -55,13 +55,15 @@ int attn_launch(Launch& c, int sms) {
   AttnArgs& a = c.a;
   a.ctas = std::max(1, std::min(sms * S::CTAS, DSPARK_PAGED_MAX_CTAS) / a.n_chunks);
   const int grid = a.ctas * a.n_chunks;
-  // Shared memory: what the queries and two buffers of weights leave is the ring's.
+  // Shared memory: what the queries and the weights leave is the rings'.
   a.p_off = kCtlBytes<S> + static_cast<uint32_t>(S::HALVES * a.n_cols * 128);
   a.p_bytes = static_cast<uint32_t>(a.n_cols / 16 * 4096);
-  a.ring_off = a.p_off + 2 * a.p_bytes;
-  a.stages = std::min<int>(kMaxStages, (kSmemCta / S::CTAS - a.ring_off) / S::kStage);
+  a.ring_off = a.p_off + S::PBUFS * a.p_bytes;
+  const int stages = std::min<int>(kMaxStages, (kSmemCta / S::CTAS - a.ring_off) / S::kStage);
+  a.k_stages = stages / 2;
+  a.v_stages = stages - a.k_stages;  // values wait for the softmax, keys do not
   a.lead = 1;
-  const size_t smem = a.ring_off + static_cast<size_t>(a.stages) * S::kStage;
+  const size_t smem = a.ring_off + static_cast<size_t>(stages) * S::kStage;
   if (launch_pdl(k_attention<S, F16>, grid, S::THREADS, smem, c.stream, c.q, c.k, c.v, a) !=
       cudaSuccess)
     return DSPARK_ERR_CUDA;
@@ -82,11 +84,11 @@ int attn_launch(Launch& c, int sms) {
 // The smallest row block that holds the rows; keys are copied once for all of them.
 template <int D, bool F16>
 int attn_shape(Launch& c, int sms) {
-  if (c.a.n_cols <= 16) return attn_launch<AttnShape<D, 16, 1, 2>, F16>(c, sms);
-  if (c.a.n_cols <= 32) return attn_launch<AttnShape<D, 32, 2, 1>, F16>(c, sms);
-  if (c.a.n_cols <= 64) return attn_launch<AttnShape<D, 64, 4, 1>, F16>(c, sms);
-  if (c.a.n_cols <= 96) return attn_launch<AttnShape<D, 96, 3, 1>, F16>(c, sms);
-  return attn_launch<AttnShape<D, 160, 4, 1>, F16>(c, sms);
+  if (c.a.n_cols <= 16) return attn_launch<AttnShape<D, 16, 1, 2, 2>, F16>(c, sms);
+  if (c.a.n_cols <= 32) return attn_launch<AttnShape<D, 32, 2, 1, 2>, F16>(c, sms);
+  if (c.a.n_cols <= 64) return attn_launch<AttnShape<D, 64, 4, 1, 2>, F16>(c, sms);
+  if (c.a.n_cols <= 96) return attn_launch<AttnShape<D, 96, 3, 1, 2>, F16>(c, sms);
+  return attn_launch<AttnShape<D, 160, 4, 1, 1>, F16>(c, sms);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -31,8 +31,9 @@
 // of it, found from the lengths on the device; a request cut by such a border leaves partial (m, l, O) rows that k_attention_join adds up in
 // the order of the tiles, so results do not depend on timing.
 //
-// Warps: 0 copies (TMA), 1 issues the products, the others, in groups of four
-// that share the rows among them, do the softmax and write the results. S and P
+// Warps: 0 copies keys and queries, 1 values (TMA), 2 issues the products; from
+// the fourth on groups of four, which share the rows among them, do the softmax
+// and write the results. S and P
 // have two buffers each: while a group is at a tile's exponents the products of
 // the next scores and of the weights before are under way.
 #pragma once
@@ -64,8 +65,8 @@ struct AttnArgs {
   int32_t B, n_tokens, Hq, Hkv, G, Gs, parts, max_new, t_chunk, n_chunks, ctas, n_cols;
   int32_t shift, num_pages, max_pages, window;  // window INT_MAX: none
   int32_t lead;     // length of an item besides its tiles
-  int32_t stages;   // of the ring
-  uint32_t p_off, p_bytes, ring_off;  // shared memory: weights (two buffers), ring
+  int32_t k_stages, v_stages;  // tiles of keys and of values in the rings
+  uint32_t p_off, p_bytes, ring_off;  // shared memory: weights, rings
   float c;  // scale * log2(e)
 };
 
@@ -128,6 +129,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 __device__ __forceinline__ void tma_load_3d_to(uint32_t dst, const CUtensorMap* map, int x, int y,
                                                int z, uint64_t* bar) {
@@ -200,6 +204,42 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity)) != 0;
 }
+// Whether a phase is complete, without waiting; one outcome for the warp.
+__device__ __forceinline__ bool warp_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xFFFFFFFFu, done) != 0;
+}
+// Pairs of floats: one instruction for two of them.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ void bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
@@ -271,11 +311,13 @@ __device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t saddr) {
 // shapes
 // ---------------------------------------------------------------------------
 constexpr int kMaxStages = 12;
+constexpr uint32_t kItems = 4;  // items planned ahead of their use, at most
 
-template <int D_, int NB_, int GROUPS_, int CTAS_>
+template <int D_, int NB_, int GROUPS_, int CTAS_, int PBUFS_>
 struct AttnShape {
   static constexpr int D = D_, NB = NB_, GROUPS = GROUPS_, CTAS = CTAS_;
-  static constexpr int THREADS = 64 + 128 * GROUPS;
+  static constexpr int PBUFS = PBUFS_;          // buffers of weights
+  static constexpr int THREADS = 128 + 128 * GROUPS;
   static constexpr int NC = (NB / 8 + GROUPS - 1) / GROUPS * 8;  // columns of a softmax group
   static constexpr int HALVES = D / 64;         // 128-byte wide slabs of a K, V or Q tile
   static constexpr uint32_t kSlab = kTileTok * 128;
@@ -286,14 +328,15 @@ struct AttnShape {
 
 template <class S>
 struct AttnCtl {
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], item_full[2], item_empty[2];
+  uint64_t full[kMaxStages], empty[kMaxStages];  // of key tiles, then of value tiles
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2];
+  uint64_t item_full[kItems], item_empty[kItems];
   uint64_t odd_full, drained;
   uint32_t tmem;
   int32_t status, abort, start_r, start_off;
   int64_t u_total;
   int64_t scan[S::THREADS / 32];
-  AttnItem item[2];
+  AttnItem item[kItems];
   // per column (row of q); a group's own
   alignas(16) float nref[S::NB + 8];    // minus the rows' references
   alignas(16) int32_t lim[S::NB + 8];   // a row sees the tokens below (and within the window)
@@ -318,7 +361,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < a.stages; ++i) {
+    for (int i = 0; i < a.k_stages + a.v_stages; ++i) {
       mbar_init(&ctl.full[i], 1);
       mbar_init(&ctl.empty[i], 1);
     }
@@ -330,6 +373,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_full[i], 4 * S::GROUPS);
       mbar_init(&ctl.pv_done[i], 1);
+    }
+    for (uint32_t i = 0; i < kItems; ++i) {
       mbar_init(&ctl.item_full[i], 1);
       mbar_init(&ctl.item_empty[i], 4 * S::GROUPS);
     }
@@ -340,7 +385,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     tma_prefetch_map(&map_k);
     tma_prefetch_map(&map_v);
   }
-  if (warp == 1) {
+  if (warp == 2) {
     tmem_alloc(&ctl.tmem, S::kTmem);
     tmem_relinquish();
   }
@@ -404,181 +449,164 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
   const int id = chunk * a.ctas + cta;  // of the record and the partial slots
   if (tid == 0 && u_begin == u_end) a.records[id].valid = 0;
 
-  if (warp == 0) {
+  if (warp < 2) {
     // =====================================================================
-    // copies
+    // copies: warp 0 keys, queries and the items' records, warp 1 values. A
+    // tile's copies cost a warp some fifty instructions, which share the SM's
+    // issue slots with the softmax: with both kinds in one warp and page ids
+    // fetched tile by tile the copies fell behind the memory.
     // =====================================================================
     if (u_begin < u_end) {
+      const bool keys = warp == 0;
       const uint64_t policy = policy_evict_first();
       const int rows_box = min(1 << a.shift, kTileTok);
       const int n_box = kTileTok / rows_box;
       const int box = lane % n_box, half = lane / n_box;
       const bool copier = half < S::HALVES;
       const uint32_t q_bytes = S::HALVES * a.Gs * a.t_chunk * 128;
+      const uint32_t box_bytes = rows_box * 128;
+      const uint32_t first_stage = keys ? 0u : static_cast<uint32_t>(a.k_stages);
+      const uint32_t end_stage =
+          keys ? static_cast<uint32_t>(a.k_stages) : static_cast<uint32_t>(a.k_stages + a.v_stages);
+      const CUtensorMap* const map = keys ? &map_k : &map_v;
+      const uint32_t dst0 = s_ring + half * S::kSlab + box * box_bytes;
       int r = ctl.start_r, off = ctl.start_off;
       int64_t u = u_begin;
       // requests r_base .. r_base+31, one per lane
       int r_base = -1000;
       AttnReq mine{};
-      AttnItem it{};
-      int left = 0, tile = 0;  // tiles of the item that are not generated yet, the next one
-      struct Gen {
-        int tile, page;
-        bool first, any, load;
-      };
-      bool done = false;
-      // the next tile of the line (uniform over the warp but for page and load)
-      auto next = [&](AttnItem& item) -> Gen {
-        Gen n{0, 0, false, false, false};
-        if (left == 0) {
-          if (u >= u_end) {
-            done = true;
-            return n;
+      uint32_t items = 0, q_loads = 0, s = first_stage, wraps = 0;
+      bool ok = true;
+      while (ok) {
+        // ---- the next item of the line
+        AttnReq q;
+        int h = 0, lead_in = 0, take = 0;
+        bool found = false;
+        while (u < u_end && r < a.B) {  // (r: lengths that changed under the call)
+          if (r >= r_base + 32 || r < r_base) {
+            r_base = r;
+            mine.units = 0;
+            mine.begin = 0;
+            if (r + lane < a.B) {
+              attn_request(a, r + lane, t0, mine);
+              if (mine.units > 0)  // the table rows of requests to come
+                prefetch_l2(a.table + (r + lane) * a.stride + (mine.begin >> a.shift));
+            }
           }
-          AttnReq q;
-          int h, lead_in, take;
-          for (;;) {
-            if (r >= r_base + 32 || r < r_base) {
-              r_base = r;
-              mine.units = 0;
-              if (r + lane < a.B) attn_request(a, r + lane, t0, mine);
-            }
-            const int src = r - r_base;
-            q.units = __shfl_sync(0xFFFFFFFFu, mine.units, src);
-            if (off < q.units * a.Hkv) {
-              h = off / q.units;
-              lead_in = off - h * q.units;
-              take = static_cast<int>(min(static_cast<int64_t>(q.units - lead_in), u_end - u));
-              if (lead_in + take <= a.lead) {  // nothing but the item's lead: another CTA begins it
-                u += take;
-                off += take;
-                if (u >= u_end) {
-                  done = true;
-                  return n;
-                }
-                continue;
-              }
-              q.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, src);
-              q.t_rows = __shfl_sync(0xFFFFFFFFu, mine.t_rows, src);
-              q.lim0 = __shfl_sync(0xFFFFFFFFu, mine.lim0, src);
-              q.begin = __shfl_sync(0xFFFFFFFFu, mine.begin, src);
-              q.end = __shfl_sync(0xFFFFFFFFu, mine.end, src);
-              break;
-            }
+          const int src = r - r_base;
+          q.units = __shfl_sync(0xFFFFFFFFu, mine.units, src);
+          if (off >= q.units * a.Hkv) {
             off -= q.units * a.Hkv;
             ++r;
-            if (r >= a.B) {  // lengths changed under the call
-              u = u_end;
-              done = true;
-              return n;
-            }
+            continue;
           }
-          const int in_head = max(lead_in - a.lead, 0);
-          item.row0 = q.row0;
-          item.r = r;
-          item.kv_head = h;
-          item.head0 = h * a.G + part * a.Gs;
-          item.tiles = q.end > 0 ? lead_in + take - a.lead - in_head : 0;
-          item.tile0 = q.begin / kTileTok + in_head;
-          item.t_rows = q.t_rows;
-          item.lim0 = q.lim0;
-          item.begin = q.begin;
-          item.end = q.end;
-          item.starts = in_head == 0;
-          item.ends = lead_in + take == q.units;
-          item.first = static_cast<int32_t>(((u - lead_in + a.lead + 1) * g - 1) / W);
+          h = off / q.units;
+          lead_in = off - h * q.units;
+          take = static_cast<int>(min(static_cast<int64_t>(q.units - lead_in), u_end - u));
           u += take;
           off += take;
-          left = item.tiles;
-          tile = item.tile0;
-          n.first = true;
-          if (left == 0) return n;
+          if (lead_in + take > a.lead) {
+            q.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, src);
+            q.t_rows = __shfl_sync(0xFFFFFFFFu, mine.t_rows, src);
+            q.lim0 = __shfl_sync(0xFFFFFFFFu, mine.lim0, src);
+            q.begin = __shfl_sync(0xFFFFFFFFu, mine.begin, src);
+            q.end = __shfl_sync(0xFFFFFFFFu, mine.end, src);
+            found = true;
+            break;
+          }  // else nothing but the item's lead: the next CTA begins it
         }
-        n.any = true;
-        n.tile = tile;
-        const int tok = tile * kTileTok + box * rows_box;
-        n.load = copier && tok < item.end && tok + rows_box > item.begin;
-        if (n.load)
-          n.page = a.table[static_cast<int64_t>(item.r) * a.stride + (tok >> a.shift)];
-        ++tile;
-        --left;
-        return n;
-      };
-      uint32_t s = 0, wraps = 0, items = 0, q_loads = 0;  // ring position; items, Q tiles so far
-      bool ok = true;
-      AttnItem cur_item{};
-      Gen cur = next(it);
-      cur_item = it;
-      while (ok && (cur.first || cur.any)) {
-        // the next tile's page ids are on their way while this one is copied
-        Gen nxt = done ? Gen{0, 0, false, false, false} : next(it);
-        if (cur.first) {
-          const uint32_t slot = items & 1u;
-          if (items >= 2) ok = warp_wait(&ctl.item_empty[slot], ((items >> 1) - 1u) & 1u);
+        if (!found) break;
+        const int in_head = max(lead_in - a.lead, 0);
+        const int tile0 = q.begin / kTileTok + in_head;
+        const int tiles = q.end > 0 ? lead_in + take - a.lead - in_head : 0;
+        const int32_t* const row = a.table + r * a.stride;
+        const int last_page = max(q.end - 1, 0) >> a.shift;
+        int page0 = (tile0 * kTileTok) >> a.shift;  // of the 32 ids that the lanes hold
+        int ids = 0, next_ids = 0;
+        if (tiles > 0) ids = row[min(page0 + lane, last_page)];
+        if (keys) {
+          const uint32_t slot = items % kItems, use = items / kItems;
+          if (use >= 1) ok = warp_wait(&ctl.item_empty[slot], (use - 1u) & 1u);
           if (!ok) break;
+          const int head0 = h * a.G + part * a.Gs;
           if (lane == 0) {
-            ctl.item[slot] = cur_item;
+            AttnItem& item = ctl.item[slot];
+            item.row0 = q.row0;
+            item.r = r;
+            item.kv_head = h;
+            item.head0 = head0;
+            item.tiles = tiles;
+            item.tile0 = tile0;
+            item.t_rows = q.t_rows;
+            item.lim0 = q.lim0;
+            item.begin = q.begin;
+            item.end = q.end;
+            item.starts = in_head == 0;
+            item.ends = lead_in + take == q.units;
+            item.first =
+                static_cast<int32_t>(((u - take - lead_in + a.lead + 1) * g - 1) / W);
             mbar_arrive(&ctl.item_full[slot]);
           }
           ++items;
-          if (cur.any) {
+          if (tiles > 0) {
             if (q_loads >= 1) ok = warp_wait(&ctl.q_empty, (q_loads - 1u) & 1u);
             if (!ok) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(&ctl.q_full, q_bytes);
               for (int i = 0; i < S::HALVES; ++i)
-                tma_load_3d_to(s_q + i * q_slab, &map_q, i * 64, cur_item.head0,
-                               static_cast<int>(cur_item.row0), &ctl.q_full);
+                tma_load_3d_to(s_q + i * q_slab, &map_q, i * 64, head0,
+                               static_cast<int>(q.row0), &ctl.q_full);
             }
             ++q_loads;
           }
         }
-        if (cur.any) {
-          int page = cur.page;
-          const bool lost = cur.load && static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages);
-          if (lost) {
-            atomicCAS(&ctl.status, static_cast<int32_t>(DSPARK_OK),
-                      static_cast<int32_t>(DSPARK_ERR_BAD_DATA));
+        // ---- its tiles
+        if (tiles > 0) next_ids = row[min(page0 + 32 + lane, last_page)];
+        int tok = tile0 * kTileTok + box * rows_box;  // this lane's box of the tile
+        for (int i = 0; i < tiles; ++i, tok += kTileTok) {
+          int rel = (tok >> a.shift) - page0;
+          if (__any_sync(0xFFFFFFFFu, rel >= 32)) {
+            page0 += 32;
+            rel -= 32;
+            ids = next_ids;
+            next_ids = row[min(page0 + 32 + lane, last_page)];
+          }
+          int page = __shfl_sync(0xFFFFFFFFu, ids, rel);
+          const bool load = copier && tok < q.end && tok + rows_box > q.begin;
+          if (load && static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) {
+            set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
             page = 0;
           }
-          const uint32_t loads = __ballot_sync(0xFFFFFFFFu, cur.load);
-          const uint32_t bytes = __popc(loads) * rows_box * 128;
-          const int y = (cur.tile * kTileTok + box * rows_box) & ((1 << a.shift) - 1);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            if (wraps >= 1) ok = ok && warp_wait(&ctl.empty[s], (wraps - 1u) & 1u);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
-            __syncwarp();
-            if (cur.load)
-              tma_load_4d(s_ring + s * S::kStage + half * S::kSlab + box * rows_box * 128,
-                          kv == 0 ? &map_k : &map_v, half * 64, y, cur_item.kv_head, page,
-                          &ctl.full[s], policy);
-            if (++s == static_cast<uint32_t>(a.stages)) s = 0, ++wraps;
-          }
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * box_bytes;
+          bool mine_ok = wraps == 0 || mbar_wait(&ctl.empty[s], (wraps - 1u) & 1u);
+          if (mine_ok && lane == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
+          ok = __all_sync(0xFFFFFFFFu, mine_ok) != 0;
+          if (!ok) break;
+          if (load)
+            tma_load_4d(dst0 + s * S::kStage, map, half * 64, tok & ((1 << a.shift) - 1), h, page,
+                        &ctl.full[s], policy);
+          if (++s == end_stage) s = first_stage, ++wraps;
         }
-        cur = nxt;
-        cur_item = it;
-      }
-      if (!ok) {
-        set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
-        *reinterpret_cast<volatile int32_t*>(&ctl.abort) = 1;
       }
       // the end of the line
-      if (ok) {
-        const uint32_t slot = items & 1u;
-        if (items >= 2) ok = warp_wait(&ctl.item_empty[slot], ((items >> 1) - 1u) & 1u);
+      if (ok && keys) {
+        const uint32_t slot = items % kItems, use = items / kItems;
+        if (use >= 1) ok = warp_wait(&ctl.item_empty[slot], (use - 1u) & 1u);
         if (ok && lane == 0) {
           ctl.item[slot].tiles = -1;
           mbar_arrive(&ctl.item_full[slot]);
         }
       }
+      if (!ok) {
+        set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
+        *reinterpret_cast<volatile int32_t*>(&ctl.abort) = 1;
+      }
       // leave no copy in flight into this CTA's shared memory
-      for (uint32_t i = 0; i < static_cast<uint32_t>(a.stages); ++i)
+      for (uint32_t i = first_stage; i < end_stage; ++i)
         if (i < s || wraps > 0) mbar_wait(&ctl.full[i], (i < s ? wraps : wraps - 1u) & 1u);
       if (q_loads > 0) mbar_wait(&ctl.q_full, (q_loads - 1u) & 1u);
     }
-  } else if (warp == 1) {
+  } else if (warp == 2) {
     // =====================================================================
     // products
     // =====================================================================
@@ -597,16 +625,16 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       // P: 16 rows of q contiguous per token, 16-row blocks 4,096 apart, 8-token groups 256 apart
       const uint64_t desc_p = attn_desc(4096, 256, 6);
       uint32_t items = 0, q_loads = 0, tiles = 0, scores = 0;
-      const uint32_t stages = static_cast<uint32_t>(a.stages);
-      struct Ring {  // K tiles lie at even positions of the line of copies, V tiles at odd ones
-        uint32_t s, phase;
-      } rk{0, 0}, rv{1, 0};
-      auto two_on = [&](Ring& r) {
-        r.s += 2;
-        if (r.s >= stages) r.s -= stages, r.phase ^= 1u;
+      struct Ring {
+        uint32_t s, phase, first, end;
+        __device__ void on() {
+          if (++s == end) s = first, phase ^= 1u;
+        }
       };
+      const uint32_t nk = a.k_stages, nv = a.v_stages;
+      Ring rk{0, 0, 0, nk}, rv{nk, 0, nk, nk + nv};
       bool ok = true;
-      auto product_s = [&]() {  // S^T of the next tile
+      auto product_s = [&](bool last) {  // S^T of the next tile; the item's last frees Q
         const uint32_t buf = scores & 1u;
         ok = warp_wait(&ctl.full[rk.s], rk.phase);
         if (!ok) return;
@@ -620,13 +648,14 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                    q0 + ((k / 4) * (q_slab >> 4) + (k % 4) * 2), idesc_s, k > 0);
           tc_commit(&ctl.empty[rk.s]);
           tc_commit(&ctl.s_full[buf]);
+          if (last) tc_commit(&ctl.q_empty);
         }
-        two_on(rk);
+        rk.on();
         ++scores;
       };
       while (ok) {
-        const uint32_t slot = items & 1u;
-        ok = warp_wait(&ctl.item_full[slot], (items >> 1) & 1u);
+        const uint32_t slot = items % kItems;
+        ok = warp_wait(&ctl.item_full[slot], (items / kItems) & 1u);
         if (!ok) break;
         const int nt = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tiles, 0);
         ++items;
@@ -635,13 +664,21 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ok = warp_wait(&ctl.q_full, q_loads & 1u);
         ++q_loads;
         if (!ok) break;
-        product_s();
+        product_s(nt == 1);
         for (int i = 0; i < nt && ok; ++i, ++tiles) {
-          if (i + 1 < nt) product_s();
-          if (!ok) break;
-          if (leader && i == max(nt - 2, 0)) tc_commit(&ctl.q_empty);  // after the item's last S
-          const uint32_t buf = tiles & 1u;
-          ok = warp_wait(&ctl.p_full[buf], (tiles >> 1) & 1u);
+          // whichever comes first, the next tile's keys or this one's weights
+          const uint32_t buf = tiles % S::PBUFS;
+          bool ahead = i + 1 == nt;
+          WaitClock clock;
+          for (;;) {
+            if (!ahead && warp_test(&ctl.full[rk.s], rk.phase)) {
+              product_s(i + 2 == nt);
+              ahead = true;
+            }
+            if (warp_test(&ctl.p_full[buf], (tiles / S::PBUFS) & 1u)) break;
+            ok = ok && !__any_sync(0xFFFFFFFFu, clock.expired());
+            if (!ok) break;
+          }
           if (!ok) break;
           // the groups' lists of the item are written
           if (leader && i + 1 == nt) mbar_arrive(&ctl.odd_full);
@@ -658,7 +695,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             tc_commit(&ctl.empty[rv.s]);
             tc_commit(&ctl.pv_done[buf]);
           }
-          two_on(rv);
+          rv.on();
+          if (!ahead) product_s(i + 2 == nt);
         }
       }
       if (!ok) {
@@ -669,11 +707,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       }
     }
     __syncwarp();
-  } else if (u_begin < u_end) {
+  } else if (warp >= 4 && u_begin < u_end) {
     // =====================================================================
     // softmax, results
     // =====================================================================
-    const int group = (warp - 2) >> 2, quarter = warp & 3, bar = 1 + group;
+    const int group = (warp - 4) >> 2, quarter = warp & 3, bar = 1 + group;
     const int gt = (quarter << 5) | lane;  // this thread's token of a tile, and lane of S and O
     constexpr int kBlocks = S::NC / 8;     // of 8 columns
     const int cols = a.Gs * a.t_chunk;
@@ -683,11 +721,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     const uint32_t window = static_cast<uint32_t>(a.window);
     volatile int32_t* abort_flag = &ctl.abort;
     uint32_t tiles = 0, items = 0, lists = 0;
-    uint32_t v_s = 1, v_phase = 0;         // ring position of the next V tile
+    const uint32_t v_end = a.k_stages + a.v_stages;
+    uint32_t v_s = a.k_stages, v_phase = 0;  // ring position of the next tile of values
+    const uint64_t c2 = pair(a.c, a.c);
     bool recorded = false;
     for (;;) {
-      const uint32_t slot = items & 1u;
-      bool failed = !mbar_wait(&ctl.item_full[slot], (items >> 1) & 1u);
+      const uint32_t slot = items % kItems, list = lists & 1u;
+      bool failed = !mbar_wait(&ctl.item_full[slot], (items / kItems) & 1u);
       if (bar_any(bar, 128, failed || *abort_flag != 0)) {
         *abort_flag = 1;
         break;
@@ -706,13 +746,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ctl.at[j] = (t * a.Hq + j - t * a.Gs) * S::D;
         ctl.fac[j] = 1.f;
       }
-      if (tid == 64) ctl.odd_n[slot] = 0;
+      if (group == 0 && gt == 0 && it.tiles > 0) ctl.odd_n[list] = 0;
       bar_sync(bar, 128);
       const int lim_last = it.lim0 + it.t_rows - 1;
       const int lo_last = a.window == INT_MAX ? 0 : max(0, lim_last - a.window);
-      float l[S::NC];
+      uint64_t l[S::NC / 2];  // sums of the columns' weights, in pairs
 #pragma unroll
-      for (int j = 0; j < S::NC; ++j) l[j] = 0.f;
+      for (int j = 0; j < S::NC / 2; ++j) l[j] = 0;
 
       bool leave = false;
       for (int i = 0; i < it.tiles; ++i, ++tiles) {
@@ -768,16 +808,14 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         };
         if constexpr (kKeep) load(0, kBlocks);
         // exponents y = c x - m
-        auto exponent = [&](int b, float (&y)[8]) {
-          const float4* nr4 = reinterpret_cast<const float4*>(&ctl.nref[c0 + 8 * b]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float4 m = nr4[k];
-            y[4 * k] = fmaf(x[8 * b + 4 * k], a.c, m.x);
-            y[4 * k + 1] = fmaf(x[8 * b + 4 * k + 1], a.c, m.y);
-            y[4 * k + 2] = fmaf(x[8 * b + 4 * k + 2], a.c, m.z);
-            y[4 * k + 3] = fmaf(x[8 * b + 4 * k + 3], a.c, m.w);
-          }
+        auto exponent = [&](int b, uint64_t (&y)[4]) {
+          const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(&ctl.nref[c0 + 8 * b]);
+          const ulonglong2 m0 = nr[0], m1 = nr[1];
+          const float* z = x + 8 * b;
+          y[0] = fma2(pair(z[0], z[1]), c2, m0.x);
+          y[1] = fma2(pair(z[2], z[3]), c2, m0.y);
+          y[2] = fma2(pair(z[4], z[5]), c2, m1.x);
+          y[3] = fma2(pair(z[6], z[7]), c2, m1.y);
         };
         bool raise = true;  // the first tile in half precision
         if (!F16 || i > 0) {
@@ -799,8 +837,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           }
           float top = -INFINITY;
           each([&](int b) {
+            uint64_t e[4];
             float y[8];
-            exponent(b, y);
+            exponent(b, e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) unpair(e[k], y[2 * k], y[2 * k + 1]);
             top = fmaxf(top, fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])),
                                    fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7]))));
           });
@@ -829,7 +870,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           bar_sync(bar, 128);
           if (i > 0) {
             const uint32_t before = tiles - 1u;
-            failed |= !mbar_wait(&ctl.pv_done[before & 1u], (before >> 1) & 1u);
+            failed |= !mbar_wait(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
             tc_fence_after();
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
@@ -840,24 +881,28 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 tmem_wait_ld();
                 tmem_arrived(o);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  o[k] *= f[k];
-                  l[8 * b + k] *= f[k];
-                }
+                for (int k = 0; k < 8; ++k) o[k] *= f[k];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
                 tmem_st8(tmem + lanes + S::kColO + c0 + 8 * b, o);
               }
             tmem_wait_st();
           }
         }
-        // this buffer of weights is free once the tile before last has been multiplied
-        if (tiles >= 2) failed |= !mbar_wait(&ctl.pv_done[buf], ((tiles >> 1) - 1u) & 1u);
+        // this buffer of weights is free once its last tile has been multiplied
+        const uint32_t pb = tiles % S::PBUFS, use = tiles / S::PBUFS;
+        if (use >= 1) failed |= !mbar_wait(&ctl.pv_done[pb], (use - 1u) & 1u);
         each([&](int b) {
+          uint64_t e[4];
           float y[8];
-          exponent(b, y);
+          exponent(b, e);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            y[k] = ex2_approx(y[k]);
-            l[8 * b + k] += y[k];
+          for (int k = 0; k < 4; ++k) {
+            unpair(e[k], y[2 * k], y[2 * k + 1]);
+            y[2 * k] = ex2_approx(y[2 * k]);
+            y[2 * k + 1] = ex2_approx(y[2 * k + 1]);
+            l[4 * b + k] = add2(l[4 * b + k], pair(y[2 * k], y[2 * k + 1]));
           }
           // The weights enter the second product in the inputs' type (half a
           // step of it each, no more than the output's own rounding); their sum
@@ -865,7 +910,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           // where a few tokens have all the weight.
           const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
           const uint32_t swap = static_cast<uint32_t>(gt >> 2) & 1u;  // 32-byte swizzle
-          sts_u4(s_p + buf * a.p_bytes + (chunk >> 1) * 4096u + gt * 32u +
+          sts_u4(s_p + pb * a.p_bytes + (chunk >> 1) * 4096u + gt * 32u +
                      (((chunk & 1u) ^ swap) << 4),
                  pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3]), pack2<F16>(y[4], y[5]),
                  pack2<F16>(y[6], y[7]));
@@ -901,15 +946,14 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
               if (hit) sts_u4(addr, w[0], w[1], w[2], w[3]);
               odd |= hit;
             }
-            if (odd) ctl.odd[slot][atomicAdd(&ctl.odd_n[slot], 1)] = tok;
+            if (odd) ctl.odd[list][atomicAdd(&ctl.odd_n[list], 1)] = tok;
           }
         }
-        v_s += 2;
-        if (v_s >= static_cast<uint32_t>(a.stages)) v_s -= a.stages, v_phase ^= 1u;
+        if (++v_s == v_end) v_s = a.k_stages, v_phase ^= 1u;
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_full[buf]);
+        if (lane == 0) mbar_arrive(&ctl.p_full[pb]);
       }
       if (leave) {
         *abort_flag = 1;
@@ -924,14 +968,14 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         if (b < nb) {
           float v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = l[8 * b + k];
+          for (int k = 0; k < 4; ++k) unpair(l[4 * b + k], v[2 * k], v[2 * k + 1]);
           const float sum = columns_over_warp<false>(v, lane);
           if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = sum;
         }
       if (it.tiles > 0) {
         const uint32_t last = tiles - 1u;
         failed |= !mbar_wait(&ctl.odd_full, lists & 1u);
-        failed |= !mbar_wait(&ctl.pv_done[last & 1u], (last >> 1) & 1u);
+        failed |= !mbar_wait(&ctl.pv_done[last % S::PBUFS], (last / S::PBUFS) & 1u);
         tc_fence_after();
         ++lists;
       }
@@ -954,7 +998,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         }
       }
       bar_sync(bar, 128);
-      const int odd_n = it.tiles > 0 ? ctl.odd_n[slot] : 0;
+      const int odd_n = it.tiles > 0 ? ctl.odd_n[list] : 0;
       const bool writer = S::D == 128 || lane < 16;  // M = 64 fills 16 lanes of each warp's 32
       const int d = S::D == 128 ? gt : quarter * 16 + lane;
       uint16_t* const out =
@@ -971,7 +1015,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           tmem_arrived(o);
         }
         for (int q = 0; q < odd_n; ++q) {
-          const int u = ctl.odd[slot][q];
+          const int u = ctl.odd[list][q];
           const int32_t page = a.table[it.r * a.stride + (u >> a.shift)];
           if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages) || !writer) continue;
           const uint32_t bits = static_cast<const uint16_t*>(a.v_cache)[
@@ -1003,7 +1047,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       }
       if (it.ends && !it.starts) {
         recorded = true;
-        if (tid == 64) {
+        if (tid == 128) {
           AttnRecord& rec = a.records[id];
           rec.valid = 1;
           rec.first = it.first;
@@ -1017,13 +1061,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.item_empty[slot]);
     }
-    if (!recorded && tid == 64) a.records[id].valid = 0;
-    if (*abort_flag != 0 && tid == 64) set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
+    if (!recorded && tid == 128) a.records[id].valid = 0;
+    if (*abort_flag != 0 && tid == 128) set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, S::kTmem);
+  if (warp == 2) tmem_dealloc(tmem, S::kTmem);
   if (tid == 0) a.records[id].status = ctl.status;
 }
 
