@@ -26,9 +26,10 @@ bool attn_map(CUtensorMap* map, bool f16, const void* base, int rank, const cuui
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Shared memory of a CTA that has its SM to itself; two share it with 1 KB each
-// for the system.
-constexpr int kSmemCta = 231424;
+// Shared memory of a CTA that has its SM to itself (227 KB), or of one of two:
+// half of 228 KB, less 1 KB each for the system.
+template <int CTAS>
+constexpr int kSmemCta = CTAS == 1 ? 232448 : 115712;
 
 struct Launch {
   CUtensorMap q, k, v;
@@ -47,7 +48,7 @@ int attn_launch(Launch& c, int sms) {
     std::lock_guard<std::mutex> lock(g_attn_mutex);
     if (!ready[dev]) {
       if (cudaFuncSetAttribute(k_attention<S, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kSmemCta / S::CTAS) != cudaSuccess)
+                               kSmemCta<S::CTAS>) != cudaSuccess)
         return DSPARK_ERR_CUDA;
       ready[dev] = true;
     }
@@ -55,14 +56,22 @@ int attn_launch(Launch& c, int sms) {
   AttnArgs& a = c.a;
   a.ctas = std::max(1, std::min(sms * S::CTAS, DSPARK_PAGED_MAX_CTAS) / a.n_chunks);
   const int grid = a.ctas * a.n_chunks;
-  // Shared memory: what the queries and the weights leave is the rings'.
-  a.p_off = kCtlBytes<S> + static_cast<uint32_t>(S::HALVES * a.n_cols * 128);
+  // Shared memory: what the queries and the weights leave is the rings'. A
+  // second tile of queries where it costs them no tile.
+  constexpr uint32_t kSmem = kSmemCta<S::CTAS>;
+  const uint32_t q_bytes = static_cast<uint32_t>(S::HALVES * a.n_cols * 128);
   a.p_bytes = static_cast<uint32_t>(a.n_cols / 16 * 4096);
-  a.ring_off = a.p_off + S::PBUFS * a.p_bytes;
-  const int stages = std::min<int>(kMaxStages, (kSmemCta / S::CTAS - a.ring_off) / S::kStage);
+  auto ring_stages = [&](int q_bufs) {
+    a.q_bufs = q_bufs;
+    a.p_off = kCtlBytes<S> + q_bufs * q_bytes;
+    a.ring_off = a.p_off + S::PBUFS * a.p_bytes;
+    return std::min<int>(kMaxStages, (kSmem - a.ring_off) / S::kStage);
+  };
+  const int stages = ring_stages(1);
+  if (ring_stages(2) < stages) ring_stages(1);
   a.k_stages = stages / 2;
   a.v_stages = stages - a.k_stages;  // values wait for the softmax, keys do not
-  a.lead = 1;
+  a.lead = 3;
   const size_t smem = a.ring_off + static_cast<size_t>(stages) * S::kStage;
   if (launch_pdl(k_attention<S, F16>, grid, S::THREADS, smem, c.stream, c.q, c.k, c.v, a) !=
       cudaSuccess)

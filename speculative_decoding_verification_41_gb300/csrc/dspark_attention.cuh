@@ -31,8 +31,8 @@
 // of it, found from the lengths on the device; a request cut by such a border leaves partial (m, l, O) rows that k_attention_join adds up in
 // the order of the tiles, so results do not depend on timing.
 //
-// Warps: 0 copies keys and queries, 1 values (TMA), 2 issues the products; from
-// the fourth on groups of four, which share the rows among them, do the softmax
+// Warps: 0 copies keys, 1 values, 3 queries (TMA), 2 issues the products; from
+// the fifth on groups of four, which share the rows among them, do the softmax
 // and write the results. S and P
 // have two buffers each: while a group is at a tile's exponents the products of
 // the next scores and of the weights before are under way.
@@ -65,6 +65,7 @@ struct AttnArgs {
   int32_t B, n_tokens, Hq, Hkv, G, Gs, parts, max_new, t_chunk, n_chunks, ctas, n_cols;
   int32_t shift, num_pages, max_pages, window;  // window INT_MAX: none
   int32_t lead;     // length of an item besides its tiles
+  int32_t q_bufs;   // tiles of queries
   int32_t k_stages, v_stages;  // tiles of keys and of values in the rings
   uint32_t p_off, p_bytes, ring_off;  // shared memory: weights, rings
   float c;  // scale * log2(e)
@@ -329,7 +330,7 @@ struct AttnShape {
 template <class S>
 struct AttnCtl {
   uint64_t full[kMaxStages], empty[kMaxStages];  // of key tiles, then of value tiles
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t odd_full, drained;
   uint32_t tmem;
@@ -365,11 +366,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       mbar_init(&ctl.full[i], 1);
       mbar_init(&ctl.empty[i], 1);
     }
-    mbar_init(&ctl.q_full, 1);
-    mbar_init(&ctl.q_empty, 1);
     mbar_init(&ctl.odd_full, 1);
     mbar_init(&ctl.drained, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.q_full[i], 1);
+      mbar_init(&ctl.q_empty[i], 1);
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_full[i], 4 * S::GROUPS);
       mbar_init(&ctl.pv_done[i], 1);
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 
   if (warp < 2) {
     // =====================================================================
-    // copies: warp 0 keys, queries and the items' records, warp 1 values. A
+    // copies: warp 0 keys and the items' records, warp 1 values. A
     // tile's copies cost a warp some fifty instructions, which share the SM's
     // issue slots with the softmax: with both kinds in one warp and page ids
     // fetched tile by tile the copies fell behind the memory.
@@ -463,7 +464,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       const int n_box = kTileTok / rows_box;
       const int box = lane % n_box, half = lane / n_box;
       const bool copier = half < S::HALVES;
-      const uint32_t q_bytes = S::HALVES * a.Gs * a.t_chunk * 128;
       const uint32_t box_bytes = rows_box * 128;
       const uint32_t first_stage = keys ? 0u : static_cast<uint32_t>(a.k_stages);
       const uint32_t end_stage =
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       // requests r_base .. r_base+31, one per lane
       int r_base = -1000;
       AttnReq mine{};
-      uint32_t items = 0, q_loads = 0, s = first_stage, wraps = 0;
+      uint32_t items = 0, s = first_stage, wraps = 0;
       bool ok = true;
       while (ok) {
         // ---- the next item of the line
@@ -528,13 +528,12 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           const uint32_t slot = items % kItems, use = items / kItems;
           if (use >= 1) ok = warp_wait(&ctl.item_empty[slot], (use - 1u) & 1u);
           if (!ok) break;
-          const int head0 = h * a.G + part * a.Gs;
           if (lane == 0) {
             AttnItem& item = ctl.item[slot];
             item.row0 = q.row0;
             item.r = r;
             item.kv_head = h;
-            item.head0 = head0;
+            item.head0 = h * a.G + part * a.Gs;
             item.tiles = tiles;
             item.tile0 = tile0;
             item.t_rows = q.t_rows;
@@ -548,17 +547,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             mbar_arrive(&ctl.item_full[slot]);
           }
           ++items;
-          if (tiles > 0) {
-            if (q_loads >= 1) ok = warp_wait(&ctl.q_empty, (q_loads - 1u) & 1u);
-            if (!ok) break;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&ctl.q_full, q_bytes);
-              for (int i = 0; i < S::HALVES; ++i)
-                tma_load_3d_to(s_q + i * q_slab, &map_q, i * 64, head0,
-                               static_cast<int>(q.row0), &ctl.q_full);
-            }
-            ++q_loads;
-          }
         }
         // ---- its tiles
         if (tiles > 0) next_ids = row[min(page0 + 32 + lane, last_page)];
@@ -604,7 +592,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       // leave no copy in flight into this CTA's shared memory
       for (uint32_t i = first_stage; i < end_stage; ++i)
         if (i < s || wraps > 0) mbar_wait(&ctl.full[i], (i < s ? wraps : wraps - 1u) & 1u);
-      if (q_loads > 0) mbar_wait(&ctl.q_full, (q_loads - 1u) & 1u);
     }
   } else if (warp == 2) {
     // =====================================================================
@@ -624,7 +611,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       const uint64_t desc_v = attn_desc(S::kSlab, 1024, 2);
       // P: 16 rows of q contiguous per token, 16-row blocks 4,096 apart, 8-token groups 256 apart
       const uint64_t desc_p = attn_desc(4096, 256, 6);
-      uint32_t items = 0, q_loads = 0, tiles = 0, scores = 0;
+      uint32_t items = 0, tiles = 0, scores = 0;
       struct Ring {
         uint32_t s, phase, first, end;
         __device__ void on() {
@@ -633,6 +620,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       };
       const uint32_t nk = a.k_stages, nv = a.v_stages;
       Ring rk{0, 0, 0, nk}, rv{nk, 0, nk, nk + nv};
+      const uint32_t nq = a.q_bufs;
+      Ring rq{nq - 1u, 1u, 0, nq};  // moved on to an item's queries before them
       bool ok = true;
       auto product_s = [&](bool last) {  // S^T of the next tile; the item's last frees Q
         const uint32_t buf = scores & 1u;
@@ -640,7 +629,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         if (!ok) return;
         tc_fence_after();
         if (leader) {
-          const uint64_t k0 = at(desc_kq, s_ring + rk.s * S::kStage), q0 = at(desc_kq, s_q);
+          const uint64_t k0 = at(desc_kq, s_ring + rk.s * S::kStage), q0 = at(desc_kq, s_q + rq.s * S::HALVES * q_slab);
 #pragma unroll
           for (int k = 0; k < S::D / 16; ++k)
             tc_mma(tmem + S::kColS + buf * S::NB,
@@ -648,7 +637,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                    q0 + ((k / 4) * (q_slab >> 4) + (k % 4) * 2), idesc_s, k > 0);
           tc_commit(&ctl.empty[rk.s]);
           tc_commit(&ctl.s_full[buf]);
-          if (last) tc_commit(&ctl.q_empty);
+          if (last) tc_commit(&ctl.q_empty[rq.s]);
         }
         rk.on();
         ++scores;
@@ -661,8 +650,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ++items;
         if (nt < 0) break;
         if (nt == 0) continue;
-        ok = warp_wait(&ctl.q_full, q_loads & 1u);
-        ++q_loads;
+        rq.on();
+        ok = warp_wait(&ctl.q_full[rq.s], rq.phase);
         if (!ok) break;
         product_s(nt == 1);
         for (int i = 0; i < nt && ok; ++i, ++tiles) {
@@ -707,7 +696,38 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       }
     }
     __syncwarp();
-  } else if (warp >= 4 && u_begin < u_end) {
+  } else if (warp == 3) {
+    // =====================================================================
+    // queries: two tiles of them where there is room, so that an item's are
+    // there when the one before it ends
+    // =====================================================================
+    if (lane == 0 && u_begin < u_end) {
+      const uint32_t bytes = S::HALVES * a.Gs * a.t_chunk * 128;
+      uint32_t items = 0, b = 0, wraps = 0;
+      bool ok = true;
+      for (;;) {
+        const uint32_t slot = items % kItems;
+        ok = mbar_wait(&ctl.item_full[slot], (items / kItems) & 1u);
+        if (!ok || ctl.item[slot].tiles < 0) break;
+        ++items;
+        if (ctl.item[slot].tiles == 0) continue;
+        if (wraps >= 1) ok = mbar_wait(&ctl.q_empty[b], (wraps - 1u) & 1u);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&ctl.q_full[b], bytes);
+        for (int i = 0; i < S::HALVES; ++i)
+          tma_load_3d_to(s_q + (b * S::HALVES + i) * q_slab, &map_q, i * 64, ctl.item[slot].head0,
+                         static_cast<int>(ctl.item[slot].row0), &ctl.q_full[b]);
+        if (++b == static_cast<uint32_t>(a.q_bufs)) b = 0, ++wraps;
+      }
+      if (!ok) {
+        set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
+        *reinterpret_cast<volatile int32_t*>(&ctl.abort) = 1;
+      }
+      for (uint32_t i = 0; i < static_cast<uint32_t>(a.q_bufs); ++i)
+        if (i < b || wraps > 0) mbar_wait(&ctl.q_full[i], (i < b ? wraps : wraps - 1u) & 1u);
+    }
+    __syncwarp();
+  } else if (u_begin < u_end) {
     // =====================================================================
     // softmax, results
     // =====================================================================
