@@ -15,6 +15,9 @@ int g_attn_sms[128];
 PFN_cuTensorMapEncodeTiled_v12000 g_attn_encode = nullptr;
 
 // A tensor of 16-bit elements in the 128-byte swizzled layout; dims[0] innermost.
+// A row of 128 elements is fetched in two halves, whose 256 bytes come together;
+// past a row of 64 lies another head's, which would be fetched for nothing (49%
+// more DRAM reads, measured with 24 heads side by side).
 bool attn_map(CUtensorMap* map, bool f16, const void* base, int rank, const cuuint64_t* dims,
               const cuuint64_t* strides, const cuuint32_t* box) {
   const cuuint32_t one[4] = {1, 1, 1, 1};
@@ -22,7 +25,8 @@ bool attn_map(CUtensorMap* map, bool f16, const void* base, int rank, const cuui
                        f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                        static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box,
                        one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       dims[0] == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                     : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -94,10 +98,10 @@ int attn_launch(Launch& c, int sms) {
 template <int D, bool F16>
 int attn_shape(Launch& c, int sms) {
   if (c.a.n_cols <= 16) return attn_launch<AttnShape<D, 16, 1, 2, 2>, F16>(c, sms);
-  if (c.a.n_cols <= 32) return attn_launch<AttnShape<D, 32, 2, 1, 2>, F16>(c, sms);
+  if (c.a.n_cols <= 32) return attn_launch<AttnShape<D, 32, 1, 2, 2>, F16>(c, sms);
   if (c.a.n_cols <= 64) return attn_launch<AttnShape<D, 64, 4, 1, 2>, F16>(c, sms);
   if (c.a.n_cols <= 96) return attn_launch<AttnShape<D, 96, 3, 1, 2>, F16>(c, sms);
-  return attn_launch<AttnShape<D, 160, 4, 1, 1>, F16>(c, sms);
+  return attn_launch<AttnShape<D, 160, 3, 1, 1>, F16>(c, sms);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -338,12 +338,14 @@ struct AttnCtl {
   int64_t u_total;
   int64_t scan[S::THREADS / 32];
   AttnItem item[kItems];
-  // per column (row of q); a group's own
-  alignas(16) float nref[S::NB + 8];    // minus the rows' references
-  alignas(16) int32_t lim[S::NB + 8];   // a row sees the tokens below (and within the window)
-  alignas(16) int32_t at[S::NB + 8];    // element of a row in out, from the item's first
-  alignas(16) float fac[S::NB + 8];     // a row's factor: of its sums, or of its result
-  float red[4][S::NB + 8];              // per warp: maxima, sums
+  // per column (row of q); a group's own. Two of what an item begins with: its
+  // slower warps may still write their results when the next one begins.
+  alignas(16) float nref[2][S::NB + 8];   // minus the rows' references
+  alignas(16) int32_t lim[2][S::NB + 8];  // a row sees the tokens below (and within the window)
+  alignas(16) int32_t at[S::NB + 8];      // element of a row in out, from the item's first
+  alignas(16) float fac[S::NB + 8];       // factor of a row's sums when its reference rises
+  int32_t new_tok[S::NB + 8];             // new token of a column
+  float red[4][S::NB + 8];                // per warp: maxima, sums
   int32_t odd_n[2], odd[2][2 * S::NB];  // tokens whose values are not finite and not for all rows
 };
 
@@ -647,6 +649,9 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ok = warp_wait(&ctl.item_full[slot], (items / kItems) & 1u);
         if (!ok) break;
         const int nt = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tiles, 0);
+        int tok0 = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tile0, 0) * kTileTok;
+        const int begin = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].begin, 0);
+        const int end = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].end, 0);
         ++items;
         if (nt < 0) break;
         if (nt == 0) continue;
@@ -654,7 +659,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ok = warp_wait(&ctl.q_full[rq.s], rq.phase);
         if (!ok) break;
         product_s(nt == 1);
-        for (int i = 0; i < nt && ok; ++i, ++tiles) {
+        for (int i = 0; i < nt && ok; ++i, ++tiles, tok0 += kTileTok) {
           // whichever comes first, the next tile's keys or this one's weights
           const uint32_t buf = tiles % S::PBUFS;
           bool ahead = i + 1 == nt;
@@ -677,10 +682,19 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           if (leader) {
             const uint64_t v0 = at(desc_v, s_ring + rv.s * S::kStage);
             const uint64_t p0 = at(desc_p, s_p + buf * a.p_bytes);
+            // the steps of 16 tokens that some row sees
+            const int k0 = max(begin - tok0, 0) >> 4, k1 = (min(end - tok0, kTileTok) + 15) >> 4;
+            if (k0 == 0 && k1 == kTileTok / 16) {
 #pragma unroll
-            for (int k = 0; k < kTileTok / 16; ++k)
-              tc_mma(tmem + S::kColO, v0 + static_cast<uint32_t>(k * 128),
-                     p0 + static_cast<uint32_t>(k * 32), idesc_o, k > 0 ? 1u : i > 0);
+              for (int k = 0; k < kTileTok / 16; ++k)
+                tc_mma(tmem + S::kColO, v0 + static_cast<uint32_t>(k * 128),
+                       p0 + static_cast<uint32_t>(k * 32), idesc_o, k > 0 ? 1u : i > 0);
+            } else {
+#pragma unroll 1
+              for (int k = k0; k < k1; ++k)
+                tc_mma(tmem + S::kColO, v0 + static_cast<uint32_t>(k * 128),
+                       p0 + static_cast<uint32_t>(k * 32), idesc_o, i > 0 || k > k0);
+            }
             tc_commit(&ctl.empty[rv.s]);
             tc_commit(&ctl.pv_done[buf]);
           }
@@ -744,36 +758,43 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     const uint32_t v_end = a.k_stages + a.v_stages;
     uint32_t v_s = a.k_stages, v_phase = 0;  // ring position of the next tile of values
     const uint64_t c2 = pair(a.c, a.c);
+    const float inv_c = 1.f / a.c;
     bool recorded = false;
+    for (int j = c0 + gt; j < min(c0 + 8 * blocks, S::NB); j += 128) {
+      const int t = j / a.Gs;
+      ctl.new_tok[j] = t;
+      ctl.at[j] = (t * a.Hq + j - t * a.Gs) * S::D;
+    }
+    bar_sync(bar, 128);
     for (;;) {
       const uint32_t slot = items % kItems, list = lists & 1u;
       bool failed = !mbar_wait(&ctl.item_full[slot], (items / kItems) & 1u);
-      if (bar_any(bar, 128, failed || *abort_flag != 0)) {
-        *abort_flag = 1;
-        break;
-      }
       const AttnItem& it = ctl.item[slot];
-      if (it.tiles < 0) break;
-      ++items;
-      const int rows = it.t_rows * a.Gs;
+      float* const nref = ctl.nref[items & 1u];
+      int32_t* const lims = ctl.lim[items & 1u];
+      const int rows = failed ? 0 : max(it.t_rows * a.Gs, 0);
       const int my_rows = max(0, min(8 * blocks, rows - c0));
       const int nb = (my_rows + 7) >> 3;
       for (int j = c0 + gt; j < c0 + 8 * nb; j += 128) {
         // a column past the rows takes no part: all its scores are below its reference
-        const int t = j / a.Gs;
-        ctl.nref[j] = j < rows ? kNoRef : -INFINITY;
-        ctl.lim[j] = j < rows ? it.lim0 + t : INT_MIN / 2;
-        ctl.at[j] = (t * a.Hq + j - t * a.Gs) * S::D;
-        ctl.fac[j] = 1.f;
+        nref[j] = j < rows ? kNoRef : -INFINITY;
+        lims[j] = j < rows ? it.lim0 + ctl.new_tok[j] : INT_MIN / 2;
       }
-      if (group == 0 && gt == 0 && it.tiles > 0) ctl.odd_n[list] = 0;
-      bar_sync(bar, 128);
+      if (group == 0 && gt == 0) ctl.odd_n[list] = 0;
+      if (bar_any(bar, 128, failed || *abort_flag != 0)) {
+        *abort_flag = 1;
+        break;
+      }
+      if (it.tiles < 0) break;
+      ++items;
       const int lim_last = it.lim0 + it.t_rows - 1;
       const int lo_last = a.window == INT_MAX ? 0 : max(0, lim_last - a.window);
       uint64_t l[S::NC / 2];  // sums of the columns' weights, in pairs
 #pragma unroll
       for (int j = 0; j < S::NC / 2; ++j) l[j] = 0;
 
+      float thr = 0.f;    // no row exceeds its reference by kSlack with scores up to this,
+      bool moved = true;  // unless references have moved since
       bool leave = false;
       for (int i = 0; i < it.tiles; ++i, ++tiles) {
         const uint32_t buf = tiles & 1u;
@@ -785,7 +806,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         // Scores, -inf where the row does not see the token. A group with few
         // columns keeps them in registers, one with many reads them from tensor
         // memory again for the second pass.
-        constexpr bool kKeep = S::NC <= 32;
+        constexpr bool kKeep = S::NC <= 32, kQuick = S::NC > 16;
         float x[S::NC];
         const uint32_t s_addr = tmem + lanes + S::kColS + buf * S::NB + c0;
         auto load = [&](auto from, auto to) {
@@ -798,7 +819,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             if (b < nb) {
               tmem_arrived(x + 8 * b);
               if (!whole) {
-                const int4* lim4 = reinterpret_cast<const int4*>(&ctl.lim[c0 + 8 * b]);
+                const int4* lim4 = reinterpret_cast<const int4*>(&lims[c0 + 8 * b]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                   const int4 m = lim4[k];
@@ -829,7 +850,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         if constexpr (kKeep) load(0, kBlocks);
         // exponents y = c x - m
         auto exponent = [&](int b, uint64_t (&y)[4]) {
-          const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(&ctl.nref[c0 + 8 * b]);
+          const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(&nref[c0 + 8 * b]);
           const ulonglong2 m0 = nr[0], m1 = nr[1];
           const float* z = x + 8 * b;
           y[0] = fma2(pair(z[0], z[1]), c2, m0.x);
@@ -837,8 +858,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           y[2] = fma2(pair(z[4], z[5]), c2, m1.x);
           y[3] = fma2(pair(z[6], z[7]), c2, m1.y);
         };
-        bool raise = true;  // the first tile in half precision
-        if (!F16 || i > 0) {
+        bool raise = F16 && i == 0;  // in half precision the first tile's maxima
+        if (!raise) {
           if (!F16 && i == 0) {
             // the first token that all rows see, if the tile has one
             const int pick = max(tok0, lo_last);
@@ -848,24 +869,40 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 #pragma unroll
                   for (int k = 0; k < 8; ++k) {
                     const float m = x[8 * b + k] * a.c;
-                    if (8 * b + k < my_rows && fabsf(m) < kNoRef) ctl.nref[c0 + 8 * b + k] = -m;
+                    if (8 * b + k < my_rows && fabsf(m) < kNoRef) nref[c0 + 8 * b + k] = -m;
                   }
                 }
               });
               bar_sync(bar, 128);
             }
           }
+          // The usual vote asks whether the largest score passes for the row of
+          // the smallest reference; only then each row is asked for itself.
           float top = -INFINITY;
-          each([&](int b) {
-            uint64_t e[4];
-            float y[8];
-            exponent(b, e);
+          bool ask = true;
+          if (kQuick && !moved) {
+            each([&](int b) {
+              const float* y = x + 8 * b;
+              const float m = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])),
+                                    fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+              top = fmaxf(top, m);
+            });
+            ask = bar_any(bar, 128, top > thr || failed);
+          }
+          if (ask) {
+            top = -INFINITY;
+            each([&](int b) {
+              uint64_t e[4];
+              exponent(b, e);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) unpair(e[k], y[2 * k], y[2 * k + 1]);
-            top = fmaxf(top, fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])),
-                                   fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7]))));
-          });
-          raise = bar_any(bar, 128, top > kSlack<F16> || failed);
+              for (int k = 0; k < 4; ++k) {
+                float y0, y1;
+                unpair(e[k], y0, y1);
+                top = fmaxf(top, fmaxf(y0, y1));
+              }
+            });
+            raise = bar_any(bar, 128, top > kSlack<F16> || failed);
+          }
         }
         if (raise) {
           each([&](int b) {
@@ -883,11 +920,12 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           for (int j = c0 + gt; j < c0 + my_rows; j += 128) {
             const float m = a.c * fmaxf(fmaxf(ctl.red[0][j], ctl.red[1][j]),
                                         fmaxf(ctl.red[2][j], ctl.red[3][j]));
-            const float old = -ctl.nref[j];
+            const float old = -nref[j];
             ctl.fac[j] = m > old ? ex2_approx(old - m) : 1.f;
-            if (m > old) ctl.nref[j] = -m;
+            if (m > old) nref[j] = -m;
           }
           bar_sync(bar, 128);
+          moved = true;
           if (i > 0) {
             const uint32_t before = tiles - 1u;
             failed |= !mbar_wait(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
@@ -942,9 +980,12 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           // and added to those rows at the end.
           const bool some = tok >= it.begin && tok < it.end;
           const bool all = tok < it.lim0 && tok >= lo_last;
-          failed |= !mbar_wait(&ctl.full[v_s], v_phase);
+          // in a step of 16 tokens that is multiplied at all
+          const bool used = (tok | 15) >= it.begin && (tok & ~15) < it.end;
+          if (used && !all) failed |= !mbar_wait(&ctl.full[v_s], v_phase);
           const uint32_t v_row = s_ring + v_s * S::kStage + gt * 128;
-          if (!some) {
+          if (!used) {
+          } else if (!some) {
 #pragma unroll
             for (int q = 0; q < S::HALVES; ++q)
 #pragma unroll
@@ -974,6 +1015,14 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.p_full[pb]);
+        if (kQuick && moved && i + 1 < it.tiles) {
+          float m = INFINITY;
+          for (int j = lane; j < my_rows; j += 32) m = fminf(m, kSlack<F16> - nref[c0 + j]);
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) m = fminf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          thr = m * inv_c;
+          moved = false;
+        }
       }
       if (leave) {
         *abort_flag = 1;
@@ -992,6 +1041,31 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           const float sum = columns_over_warp<false>(v, lane);
           if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = sum;
         }
+      if (bar_any(bar, 128, failed || *abort_flag != 0)) {
+        *abort_flag = 1;
+        break;
+      }
+      // every warp for itself: the factor of column j in lane j % 32
+      constexpr int kPer = (S::NC + 31) / 32;
+      float fac[kPer];
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const int j = c0 + 32 * q + lane;
+        fac[q] = 1.f;
+        if (32 * q + lane < my_rows) {
+          const float sum = (ctl.red[0][j] + ctl.red[1][j]) + (ctl.red[2][j] + ctl.red[3][j]);
+          const bool seen = lims[j] > 0;
+          if (alone) fac[q] = seen ? 1.f / sum : 0.f;  // no token: O is zero
+          if (quarter == 0) {
+            const float m = -nref[j];
+            if (!alone)
+              reinterpret_cast<float2*>(a.part_ml)[part_row + j] = make_float2(m, sum);
+            else if (a.lse)
+              a.lse[it.row0 * a.Hq + it.head0 + ctl.at[j] / S::D] =
+                  seen ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+          }
+        }
+      }
       if (it.tiles > 0) {
         const uint32_t last = tiles - 1u;
         failed |= !mbar_wait(&ctl.odd_full, lists & 1u);
@@ -999,25 +1073,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         tc_fence_after();
         ++lists;
       }
-      if (bar_any(bar, 128, failed || *abort_flag != 0)) {
-        *abort_flag = 1;
-        break;
-      }
-      for (int j = c0 + gt; j < c0 + my_rows; j += 128) {
-        const float sum = (ctl.red[0][j] + ctl.red[1][j]) + (ctl.red[2][j] + ctl.red[3][j]);
-        const float m = -ctl.nref[j];
-        if (alone) {
-          const bool seen = ctl.lim[j] > 0;
-          ctl.fac[j] = seen ? 1.f / sum : 0.f;  // no token: O is zero
-          if (a.lse)
-            a.lse[it.row0 * a.Hq + it.head0 + ctl.at[j] / S::D] =
-                seen ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-        } else {
-          ctl.fac[j] = 1.f;
-          reinterpret_cast<float2*>(a.part_ml)[part_row + j] = make_float2(m, sum);
-        }
-      }
-      bar_sync(bar, 128);
+      if (failed) *abort_flag = 1;  // seen by all at the next item
       const int odd_n = it.tiles > 0 ? ctl.odd_n[list] : 0;
       const bool writer = S::D == 128 || lane < 16;  // M = 64 fills 16 lanes of each warp's 32
       const int d = S::D == 128 ? gt : quarter * 16 + lane;
@@ -1045,15 +1101,16 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           if ((bits & kExp) != kExp) continue;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (static_cast<uint32_t>(ctl.lim[c0 + 8 * b + k] - 1 - u) < window)
+            if (static_cast<uint32_t>(lims[c0 + 8 * b + k] - 1 - u) < window)
               o[k] += half_to_float<F16>(bits);
         }
-        const float4* f4 = reinterpret_cast<const float4*>(&ctl.fac[c0 + 8 * b]);
         const int4* at4 = reinterpret_cast<const int4*>(&ctl.at[c0 + 8 * b]);
-        const float4 f0 = f4[0], f1 = f4[1];
         const int4 a0 = at4[0], a1 = at4[1];
-        const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
         const int to[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+        const float mine = kPer > 1 && b >= 4 ? fac[kPer - 1] : fac[0];
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = __shfl_sync(0xFFFFFFFFu, mine, (8 * b + k) & 31);
         const int live = writer ? my_rows - 8 * b : 0;  // columns of the block to write
         if (alone) {
 #pragma unroll
