@@ -169,11 +169,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
       "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
       : "memory");
 }
-// Sum or maximum of 8 columns over the warp's lanes: each step halves the
-// columns a lane holds and doubles the lanes they stand for. Lanes 4k .. 4k+3
-// return column k's.
+// Sum or maximum of 8 columns over lanes 4 apart: each step halves the columns
+// a lane holds and doubles the lanes they stand for. Lane i returns its part of
+// column i / 4.
 template <bool MAX>
-__device__ __forceinline__ float columns_over_warp(float (&v)[8], int lane) {
+__device__ __forceinline__ float fold_columns(float (&v)[8], int lane) {
 #pragma unroll
   for (int h = 4, o = 16; h >= 1; h >>= 1, o >>= 1) {
     const bool upper = (lane & o) != 0;
@@ -184,12 +184,17 @@ __device__ __forceinline__ float columns_over_warp(float (&v)[8], int lane) {
       v[k] = MAX ? fmaxf(have, got) : have + got;
     }
   }
+  return v[0];
+}
+// ... and over the four lanes of a column.
+template <bool MAX>
+__device__ __forceinline__ float over_four(float v) {
 #pragma unroll
   for (int o = 2; o >= 1; o >>= 1) {
-    const float got = __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
-    v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+    const float got = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = MAX ? fmaxf(v, got) : v + got;
   }
-  return v[0];
+  return v;
 }
 // One thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -758,7 +763,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     const uint32_t v_end = a.k_stages + a.v_stages;
     uint32_t v_s = a.k_stages, v_phase = 0;  // ring position of the next tile of values
     const uint64_t c2 = pair(a.c, a.c);
-    const float inv_c = 1.f / a.c;
     bool recorded = false;
     for (int j = c0 + gt; j < min(c0 + 8 * blocks, S::NB); j += 128) {
       const int t = j / a.Gs;
@@ -789,12 +793,19 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       ++items;
       const int lim_last = it.lim0 + it.t_rows - 1;
       const int lo_last = a.window == INT_MAX ? 0 : max(0, lim_last - a.window);
-      uint64_t l[S::NC / 2];  // sums of the columns' weights, in pairs
+      // Sums of the columns' weights: a thread's own token's, in pairs; or, where
+      // that takes too many registers, folded tile by tile into one per block.
+      constexpr bool kKeep = S::NC <= 32;
+      uint64_t l[kKeep ? S::NC / 2 : 1];
+      float lf[kKeep ? 1 : kBlocks];
+      if constexpr (kKeep) {
 #pragma unroll
-      for (int j = 0; j < S::NC / 2; ++j) l[j] = 0;
+        for (int j = 0; j < S::NC / 2; ++j) l[j] = 0;
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) lf[b] = 0.f;
+      }
 
-      float thr = 0.f;    // no row exceeds its reference by kSlack with scores up to this,
-      bool moved = true;  // unless references have moved since
       bool leave = false;
       for (int i = 0; i < it.tiles; ++i, ++tiles) {
         const uint32_t buf = tiles & 1u;
@@ -806,7 +817,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         // Scores, -inf where the row does not see the token. A group with few
         // columns keeps them in registers, one with many reads them from tensor
         // memory again for the second pass.
-        constexpr bool kKeep = S::NC <= 32, kQuick = S::NC > 16;
         float x[S::NC];
         const uint32_t s_addr = tmem + lanes + S::kColS + buf * S::NB + c0;
         auto load = [&](auto from, auto to) {
@@ -842,8 +852,9 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 #pragma unroll
             for (int b = 0; b < kBlocks; b += 2) {
               load(b, b + 2 < kBlocks ? b + 2 : kBlocks);
-              if (b < nb) f(b);
-              if (b + 1 < kBlocks && b + 1 < nb) f(b + 1);
+#pragma unroll
+              for (int k = b; k < b + 2 && k < kBlocks; ++k)
+                if (k < nb) f(k);
             }
           }
         };
@@ -876,33 +887,18 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
               bar_sync(bar, 128);
             }
           }
-          // The usual vote asks whether the largest score passes for the row of
-          // the smallest reference; only then each row is asked for itself.
           float top = -INFINITY;
-          bool ask = true;
-          if (kQuick && !moved) {
-            each([&](int b) {
-              const float* y = x + 8 * b;
-              const float m = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])),
-                                    fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-              top = fmaxf(top, m);
-            });
-            ask = bar_any(bar, 128, top > thr || failed);
-          }
-          if (ask) {
-            top = -INFINITY;
-            each([&](int b) {
-              uint64_t e[4];
-              exponent(b, e);
+          each([&](int b) {
+            uint64_t e[4];
+            exponent(b, e);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float y0, y1;
-                unpair(e[k], y0, y1);
-                top = fmaxf(top, fmaxf(y0, y1));
-              }
-            });
-            raise = bar_any(bar, 128, top > kSlack<F16> || failed);
-          }
+            for (int k = 0; k < 4; ++k) {
+              float y0, y1;
+              unpair(e[k], y0, y1);
+              top = fmaxf(top, fmaxf(y0, y1));
+            }
+          });
+          raise = bar_any(bar, 128, top > kSlack<F16> || failed);
         }
         if (raise) {
           each([&](int b) {
@@ -910,7 +906,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 #pragma unroll
             for (int k = 0; k < 8; ++k)  // NaN takes no part
               v[k] = x[8 * b + k] == x[8 * b + k] ? x[8 * b + k] : -INFINITY;
-            const float m = columns_over_warp<true>(v, lane);
+            const float m = over_four<true>(fold_columns<true>(v, lane));
             if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = m;
           });
           if (bar_any(bar, 128, failed || *abort_flag != 0)) {
@@ -925,7 +921,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             if (m > old) nref[j] = -m;
           }
           bar_sync(bar, 128);
-          moved = true;
           if (i > 0) {
             const uint32_t before = tiles - 1u;
             failed |= !mbar_wait(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
@@ -940,9 +935,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 tmem_arrived(o);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] *= f[k];
+                if constexpr (kKeep) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
+                  for (int k = 0; k < 4; ++k)
+                    l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
+                } else {
+                  lf[b] *= f[lane >> 2];
+                }
                 tmem_st8(tmem + lanes + S::kColO + c0 + 8 * b, o);
               }
             tmem_wait_st();
@@ -960,7 +959,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             unpair(e[k], y[2 * k], y[2 * k + 1]);
             y[2 * k] = ex2_approx(y[2 * k]);
             y[2 * k + 1] = ex2_approx(y[2 * k + 1]);
-            l[4 * b + k] = add2(l[4 * b + k], pair(y[2 * k], y[2 * k + 1]));
+            if constexpr (kKeep) l[4 * b + k] = add2(l[4 * b + k], pair(y[2 * k], y[2 * k + 1]));
           }
           // The weights enter the second product in the inputs' type (half a
           // step of it each, no more than the output's own rounding); their sum
@@ -972,6 +971,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                      (((chunk & 1u) ^ swap) << 4),
                  pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3]), pack2<F16>(y[4], y[5]),
                  pack2<F16>(y[6], y[7]));
+          if constexpr (!kKeep) lf[b] += fold_columns<false>(y, lane);
         });
         if (!whole && group == 0) {
           // Zero weights do not silence values that are not finite, and the
@@ -1015,14 +1015,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.p_full[pb]);
-        if (kQuick && moved && i + 1 < it.tiles) {
-          float m = INFINITY;
-          for (int j = lane; j < my_rows; j += 32) m = fminf(m, kSlack<F16> - nref[c0 + j]);
-#pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) m = fminf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-          thr = m * inv_c;
-          moved = false;
-        }
       }
       if (leave) {
         *abort_flag = 1;
@@ -1035,10 +1027,15 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
         if (b < nb) {
-          float v[8];
+          float sum;
+          if constexpr (kKeep) {
+            float v[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) unpair(l[4 * b + k], v[2 * k], v[2 * k + 1]);
-          const float sum = columns_over_warp<false>(v, lane);
+            for (int k = 0; k < 4; ++k) unpair(l[4 * b + k], v[2 * k], v[2 * k + 1]);
+            sum = over_four<false>(fold_columns<false>(v, lane));
+          } else {
+            sum = over_four<false>(lf[b]);
+          }
           if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = sum;
         }
       if (bar_any(bar, 128, failed || *abort_flag != 0)) {
