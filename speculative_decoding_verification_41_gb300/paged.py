@@ -60,7 +60,7 @@ def _load():
                                                i32, i32, vp, vp, vp, vp, sz, vp]
         for name in EXPORTED:
             getattr(lib, name).restype = ctypes.c_int
-        _fns = lib
+        _fns = {name: getattr(lib, name) for name in EXPORTED}
     return _fns
 
 
@@ -70,53 +70,77 @@ def paged_attention_workspace_bytes(Hq: int, Hkv: int, max_new: int, D: int) -> 
     return ((PAGED_MAX_CTAS * 64 + 255) & ~255) + 2 * PAGED_MAX_CTAS * rows * (4 * D + 8)
 
 
-def _want(name: str, t: torch.Tensor, dtype, device, shape=None):
+# A call takes a few microseconds on the GPU, so its checks and marshalling on
+# the host are kept to the ones it needs: torch.cuda.current_stream() alone, which
+# makes a Stream object, costs more than all of a call's pointer arguments.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device = torch._C._cuda_getDevice
+_I32, _I64 = torch.int32, torch.int64
+
+
+def _index(name: str, t) -> int:
+    """The device number of the call's first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libdspark has no CPU path)")
+    return t.get_device()
+
+
+def _want(name: str, t: torch.Tensor, dtype, index: int, shape=None):
     """A contiguous CUDA tensor of this type, place and shape."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous() and (shape is None or t.shape == shape)):
+        return
+    device = torch.device("cuda", index)
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libdspark has no CPU path)")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _table(block_table: torch.Tensor, B: int, device):
+def _table(block_table: torch.Tensor, B: int, index: int):
+    """Stride and width of a block table's rows."""
     if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
         raise ValueError("block_table must be a CUDA tensor (libdspark has no CPU path)")
-    if block_table.dtype != torch.int32 or block_table.device != device:
-        raise ValueError(f"block_table must be torch.int32 on {device}")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    if block_table.dtype is not _I32 or block_table.get_device() != index:
+        raise ValueError(f"block_table must be torch.int32 on cuda:{index}")
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
         raise ValueError(f"block_table must be [{B}, max_pages]")
-    width = block_table.shape[1]
+    width = shape[1]
     stride, inner = block_table.stride()
     if inner != 1 and width > 1 and B > 0:
         raise ValueError("rows of block_table must be contiguous")
     return (stride if B > 1 else width), width
 
 
-def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, device):
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-            raise ValueError(f"{name} must be a CUDA tensor on {device}")
-        if t.dim() != 4 or t.stride(3) != 1:
-            raise ValueError(f"{name} must be [pages, page_size, heads, D] with contiguous D")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, index: int):
+    """Shape, strides and type number of the two caches."""
+    if not isinstance(v_cache, torch.Tensor) or v_cache.get_device() != index:
+        raise ValueError(f"v_cache must be a CUDA tensor on cuda:{index}")
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or stride[3] != 1:
+        raise ValueError("caches must be [pages, page_size, heads, D] with contiguous D")
+    if v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    if k_cache.dtype not in _DTYPES or v_cache.dtype != k_cache.dtype:
+    dtype = _DTYPES.get(k_cache.dtype)
+    if dtype is None or v_cache.dtype is not k_cache.dtype:
         raise ValueError(f"caches must be bfloat16 or float16 alike, got {k_cache.dtype} and "
                          f"{v_cache.dtype}")
+    return shape, stride, dtype
 
 
-def _on(stream, device):
+def _on(stream, index: int) -> int:
     """The stream's handle; a stream of another device than the tensors' is refused."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
-    return s
+    if stream is None:
+        return _raw_stream(index)
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    return stream.cuda_stream
 
 
 def _kept(buffers, stream):
@@ -127,23 +151,23 @@ def _kept(buffers, stream):
                 t.record_stream(stream)
 
 
-def _call(name: str, device, *args):
-    fn = getattr(_load(), name)
-    if torch.cuda.current_device() == device.index:
+def _call(name: str, index: int, *args):
+    fn = _fns[name] if _fns is not None else _load()[name]
+    if _get_device() == index:
         rc = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args)
     if rc != 0:
         raise DsparkError(name, rc)
 
 
-def _checked(name: str, status: torch.Tensor, check: bool, stream):
-    if check:
-        stream.synchronize()
-        st = int(status.item())
-        if st != 0:
-            raise DsparkError(f"{name} (device)", st)
+def _checked(name: str, status: torch.Tensor, index: int, stream):
+    """Wait for the call and raise on a status that is not OK."""
+    (stream or torch.cuda.current_stream(index)).synchronize()
+    st = int(status.item())
+    if st != 0:
+        raise DsparkError(f"{name} (device)", st)
 
 
 class ReserveBuffers:
@@ -175,15 +199,15 @@ def dspark_pages_reserve(context_len: torch.Tensor, new_len: torch.Tensor,
     with extra = 1), draft_off [B+1] int64 (its draft_row_off), slot_map and
     positions [max_tokens], free_count [1], device_status [1] (device tensors).
     With check=True the call synchronises and raises on a non-OK device status."""
-    dev = context_len.device
-    _want("context_len", context_len, torch.int32, None)
+    dev = _index("context_len", context_len)
     B = context_len.numel()
-    _want("new_len", new_len, torch.int32, dev, context_len.shape)
+    _want("context_len", context_len, _I32, dev, (B,))
+    _want("new_len", new_len, _I32, dev, (B,))
     stride, width = _table(block_table, B, dev)
-    _want("free_pages", free_pages, torch.int32, dev)
-    _want("free_count", free_count, torch.int32, dev, (1,))
-    buf = buffers or ReserveBuffers(B, max_tokens, dev)
-    if (buf.B, buf.max_tokens) != (B, max_tokens):
+    _want("free_pages", free_pages, _I32, dev)
+    _want("free_count", free_count, _I32, dev, (1,))
+    buf = buffers or ReserveBuffers(B, max_tokens, context_len.device)
+    if buf.B != B or buf.max_tokens != max_tokens:
         raise ValueError("buffers were made for another shape")
     s = _on(stream, dev)
     if buffers is None:
@@ -193,8 +217,9 @@ def dspark_pages_reserve(context_len: torch.Tensor, new_len: torch.Tensor,
           free_pages.data_ptr(), free_count.data_ptr(), max_tokens, buf.context_len.data_ptr(),
           buf.row_off.data_ptr(), buf.draft_off.data_ptr(), buf.slot_map.data_ptr(),
           buf.positions.data_ptr(), buf.free_count.data_ptr(), buf.device_status.data_ptr(),
-          s.cuda_stream)
-    _checked("dspark_pages_reserve", buf.device_status, check, s)
+          s)
+    if check:
+        _checked("dspark_pages_reserve", buf.device_status, dev, stream)
     return {"context_len": buf.context_len, "row_off": buf.row_off, "draft_off": buf.draft_off,
             "slot_map": buf.slot_map, "positions": buf.positions, "free_count": buf.free_count,
             "device_status": buf.device_status}
@@ -221,15 +246,15 @@ def dspark_pages_release(context_len: torch.Tensor, reserved_len: torch.Tensor,
     pages past them go back on free_pages, in place (include/dspark_paged.h).
 
     Returns context_len [B], free_count [1], device_status [1] (device tensors)."""
-    dev = context_len.device
-    _want("context_len", context_len, torch.int32, None)
+    dev = _index("context_len", context_len)
     B = context_len.numel()
-    _want("reserved_len", reserved_len, torch.int32, dev, context_len.shape)
-    _want("kept_len", kept_len, torch.int32, dev, context_len.shape)
+    _want("context_len", context_len, _I32, dev, (B,))
+    _want("reserved_len", reserved_len, _I32, dev, (B,))
+    _want("kept_len", kept_len, _I32, dev, (B,))
     stride, width = _table(block_table, B, dev)
-    _want("free_pages", free_pages, torch.int32, dev)
-    _want("free_count", free_count, torch.int32, dev, (1,))
-    buf = buffers or ReleaseBuffers(B, dev)
+    _want("free_pages", free_pages, _I32, dev)
+    _want("free_count", free_count, _I32, dev, (1,))
+    buf = buffers or ReleaseBuffers(B, context_len.device)
     if buf.B != B:
         raise ValueError("buffers were made for another shape")
     s = _on(stream, dev)
@@ -239,8 +264,9 @@ def dspark_pages_release(context_len: torch.Tensor, reserved_len: torch.Tensor,
           kept_len.data_ptr(), extra, B, page_size, free_pages.numel(), block_table.data_ptr(),
           stride, width, free_pages.data_ptr(), free_count.data_ptr(),
           buf.context_len.data_ptr(), buf.free_count.data_ptr(), buf.device_status.data_ptr(),
-          s.cuda_stream)
-    _checked("dspark_pages_release", buf.device_status, check, s)
+          s)
+    if check:
+        _checked("dspark_pages_release", buf.device_status, dev, stream)
     return {"context_len": buf.context_len, "free_count": buf.free_count,
             "device_status": buf.device_status}
 
@@ -253,35 +279,34 @@ def dspark_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
     slot_map[i] of the caches, in place; negative slots are skipped
     (include/dspark_paged.h). slot_map may be longer than n (a reservation's whole
     map): its first n entries count. Returns device_status [1]."""
-    dev = k_cache.device
-    _cache(k_cache, v_cache, dev)
-    for name, t in (("k", k), ("v", v)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on {dev}")
-        if t.dtype != k_cache.dtype:
-            raise ValueError(f"{name} must be {k_cache.dtype}, got {t.dtype}")
-        if t.dim() != 3 or t.stride(2) != 1 or t.shape[1:] != k_cache.shape[2:]:
-            raise ValueError(f"{name} must be [n, {k_cache.shape[2]}, {k_cache.shape[3]}] with "
-                             "contiguous rows")
-    if k.shape != v.shape or k.stride() != v.stride():
+    dev = _index("k_cache", k_cache)
+    (pages, page_size, Hkv, D), (sp, st, sh, _), dtype = _cache(k_cache, v_cache, dev)
+    for name, x in (("k", k), ("v", v)):
+        if not isinstance(x, torch.Tensor) or x.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    shape, strides = k.shape, k.stride()
+    if len(shape) != 3 or strides[2] != 1 or shape[1] != Hkv or shape[2] != D:
+        raise ValueError(f"k must be [n, {Hkv}, {D}] with contiguous rows")
+    if k.dtype is not k_cache.dtype or v.dtype is not k.dtype:
+        raise ValueError(f"k and v must be {k_cache.dtype}, got {k.dtype} and {v.dtype}")
+    if v.shape != shape or v.stride() != strides:
         raise ValueError("k and v must have the same shape and strides")
-    n, Hkv, D = k.shape
-    _want("slot_map", slot_map, torch.int32, dev)
+    n = shape[0]
+    _want("slot_map", slot_map, _I32, dev)
     if slot_map.numel() < n:
         raise ValueError(f"slot_map has {slot_map.numel()} entries for {n} rows")
     s = _on(stream, dev)
     if device_status is None:
-        device_status = torch.empty(1, dtype=torch.int32, device=dev)
+        device_status = torch.empty(1, dtype=_I32, device=k_cache.device)
         if stream is not None:
             device_status.record_stream(stream)
     else:
-        _want("device_status", device_status, torch.int32, dev, (1,))
-    sp, st, sh, _ = k_cache.stride()
-    _call("dspark_kv_append", dev, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-          slot_map.data_ptr(), n, Hkv, D, _DTYPES[k.dtype], k_cache.data_ptr(),
-          v_cache.data_ptr(), sp, st, sh, k_cache.shape[1], k_cache.shape[0],
-          device_status.data_ptr(), s.cuda_stream)
-    _checked("dspark_kv_append", device_status, check, s)
+        _want("device_status", device_status, _I32, dev, (1,))
+    _call("dspark_kv_append", dev, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
+          slot_map.data_ptr(), n, Hkv, D, dtype, k_cache.data_ptr(), v_cache.data_ptr(), sp, st,
+          sh, page_size, pages, device_status.data_ptr(), s)
+    if check:
+        _checked("dspark_kv_append", device_status, dev, stream)
     return {"device_status": device_status}
 
 
@@ -292,8 +317,7 @@ class AttentionBuffers:
     def __init__(self, n_tokens: int, Hq: int, Hkv: int, D: int, max_new: int, dtype, device,
                  with_lse: bool = False):
         dev = torch.device(device)
-        self.shape = (n_tokens, Hq, D)
-        self.out = torch.empty(self.shape, dtype=dtype, device=dev)
+        self.out = torch.empty(n_tokens, Hq, D, dtype=dtype, device=dev)
         self.lse = torch.empty(n_tokens, Hq, dtype=torch.float32, device=dev) if with_lse else None
         self.device_status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.workspace = torch.empty(paged_attention_workspace_bytes(Hq, Hkv, max_new, D),
@@ -313,37 +337,38 @@ def dspark_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
 
     Returns out [n_tokens, Hq, D], lse [n_tokens, Hq] float32 (or None) and
     device_status [1] (device tensors)."""
-    dev = k_cache.device
-    _cache(k_cache, v_cache, dev)
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.device != dev:
-        raise ValueError(f"q must be a CUDA tensor on {dev}")
-    if q.dtype != k_cache.dtype:
+    dev = _index("k_cache", k_cache)
+    (pages, page_size, Hkv, D), (sp, st, sh, _), dtype = _cache(k_cache, v_cache, dev)
+    if not isinstance(q, torch.Tensor) or q.get_device() != dev:
+        raise ValueError(f"q must be a CUDA tensor on cuda:{dev}")
+    if q.dtype is not k_cache.dtype:
         raise ValueError(f"q must be {k_cache.dtype}, got {q.dtype}")
-    pages, page_size, Hkv, D = k_cache.shape
-    if q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != D:
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 3 or strides[2] != 1 or shape[2] != D:
         raise ValueError(f"q must be [n_tokens, heads, {D}] with contiguous rows")
-    n, Hq, _ = q.shape
-    _want("context_len", context_len, torch.int32, dev)
+    n, Hq, _ = shape
     B = context_len.numel()
-    _want("row_off", row_off, torch.int64, dev, (B + 1,))
+    _want("context_len", context_len, _I32, dev, (B,))
+    _want("row_off", row_off, _I64, dev, (B + 1,))
     stride, width = _table(block_table, B, dev)
     if Hkv < 1 or Hq < 1 or Hq % Hkv != 0 or max_new < 1:
         raise ValueError(f"{Hq} query heads on {Hkv} key heads, max_new {max_new}")
-    buf = buffers or AttentionBuffers(n, Hq, Hkv, D, max_new, q.dtype, dev, with_lse)
-    if buf.shape != (n, Hq, D) or buf.out.dtype != q.dtype:
+    buf = buffers or AttentionBuffers(n, Hq, Hkv, D, max_new, q.dtype, q.device, with_lse)
+    out = buf.out
+    if out.shape != shape or out.dtype is not q.dtype:
         raise ValueError("buffers were made for another shape or type")
     if with_lse and buf.lse is None:
         raise ValueError("buffers were made without lse (AttentionBuffers(..., with_lse=True))")
     s = _on(stream, dev)
     if buffers is None:
         _kept(buf, stream)
-    sp, st, sh, _ = k_cache.stride()
-    _call("dspark_paged_attention", dev, q.data_ptr(), q.stride(0), q.stride(1),
+    _call("dspark_paged_attention", dev, q.data_ptr(), strides[0], strides[1],
           k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, page_size, pages,
           block_table.data_ptr(), stride, width, context_len.data_ptr(), row_off.data_ptr(), B, n,
-          Hq, Hkv, D, max_new, scale, window, _DTYPES[q.dtype], buf.out.data_ptr(),
+          Hq, Hkv, D, max_new, scale, window, dtype, out.data_ptr(),
           buf.lse.data_ptr() if with_lse else None, buf.device_status.data_ptr(),
-          buf.workspace.data_ptr(), buf.workspace.numel(), s.cuda_stream)
-    _checked("dspark_paged_attention", buf.device_status, check, s)
-    return {"out": buf.out, "lse": buf.lse if with_lse else None,
+          buf.workspace.data_ptr(), buf.workspace.numel(), s)
+    if check:
+        _checked("dspark_paged_attention", buf.device_status, dev, stream)
+    return {"out": out, "lse": buf.lse if with_lse else None,
             "device_status": buf.device_status}

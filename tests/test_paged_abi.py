@@ -20,7 +20,8 @@ from tests import _paged
 @pytest.fixture(scope="module")
 def lib():
     cuda_build.build()
-    return paged._load()
+    paged._load()
+    return binding.load()
 
 
 def test_header_declares_the_exported_calls(lib):
