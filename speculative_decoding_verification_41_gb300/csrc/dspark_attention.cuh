@@ -77,9 +77,8 @@ struct AttnRecord {
   int32_t valid, first, status, rows;
   int64_t row0;
   int32_t head0, lim0;
-  int32_t pad[8];
 };
-static_assert(sizeof(AttnRecord) == 64, "AttnRecord layout");
+static_assert(sizeof(AttnRecord) == 32, "AttnRecord layout");
 
 // One piece of work: tiles [tile0, tile0 + tiles) of a request's key head.
 struct AttnItem {
@@ -1164,19 +1163,35 @@ struct JoinArgs {
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const JoinArgs a) {
-  __shared__ uint32_t s_valid[(DSPARK_PAGED_MAX_CTAS + 31) / 32], s_bad[(DSPARK_PAGED_MAX_CTAS + 31) / 32];
+  constexpr int kWords = (DSPARK_PAGED_MAX_CTAS + 31) / 32;
+  constexpr int kEach = (kWords + kJoinWarps - 1) / kJoinWarps;  // records per thread
+  constexpr int V = D / 32;                                      // floats per lane
+  constexpr int kBatch = 8;                                      // pieces in flight per warp
+  __shared__ uint32_t s_valid[kWords], s_bad[kWords];
+  __shared__ AttnRecord s_rec;
   __shared__ float s_acc[kJoinWarps][D];
-  __shared__ float s_sum[kJoinWarps];
+  __shared__ float2 s_ml[kJoinWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
+  // All records at once (one trip to the cache), then the one that is asked for.
   const int words = (a.n + 31) / 32;
-  for (int w = warp; w < words; w += kJoinWarps) {
-    const int i = w * 32 + lane;
-    const bool in = i < a.n;
-    const uint32_t v = __ballot_sync(0xFFFFFFFFu, in && a.records[i].valid != 0);
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, in && a.records[i].status != DSPARK_OK);
-    if (lane == 0) s_valid[w] = v, s_bad[w] = b;
+  int4 rec[kEach][2];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = (warp + k * kJoinWarps) * 32 + lane;
+    rec[k][0] = rec[k][1] = make_int4(0, 0, 0, 0);
+    if (i < a.n) {
+      rec[k][0] = reinterpret_cast<const int4*>(a.records + i)[0];
+      rec[k][1] = reinterpret_cast<const int4*>(a.records + i)[1];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const uint32_t v = __ballot_sync(0xFFFFFFFFu, rec[k][0].x != 0);
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, rec[k][0].z != DSPARK_OK);
+    if (lane == 0 && warp + k * kJoinWarps < words)
+      s_valid[warp + k * kJoinWarps] = v, s_bad[warp + k * kJoinWarps] = b;
   }
   __syncthreads();
   if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
@@ -1197,52 +1212,86 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const JoinAr
     want -= c;
   }
   if (id < 0) return;
-  const AttnRecord rec = a.records[id];
-  const int chunk0 = id / a.ctas * a.ctas, pieces = id - chunk0 - rec.first + 1;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if ((warp + k * kJoinWarps) * 32 + lane == id) {
+      reinterpret_cast<int4*>(&s_rec)[0] = rec[k][0];
+      reinterpret_cast<int4*>(&s_rec)[1] = rec[k][1];
+    }
+  __syncthreads();
+  const AttnRecord r = s_rec;
+  const int chunk0 = id / a.ctas * a.ctas, pieces = id - chunk0 - r.first + 1;
   const int row = blockIdx.y * (kJoinWarps / a.per_row) + warp / a.per_row;
   const int sub = warp % a.per_row;
-  constexpr int V = D / 32;  // floats per lane
-  float acc[V], sum = 0.f, top = -INFINITY;
+  // Sums of 2^(m - top) l and O over the warp's pieces, a batch at a time: its
+  // maxima and rows are fetched together, and the sums so far are scaled.
+  float acc[V] = {}, sum = 0.f, top = -INFINITY;
+  if (row < r.rows) {
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+    for (int k0 = sub; k0 < pieces; k0 += kBatch * a.per_row) {
+      float2 p[kBatch];
+      float o[kBatch][V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) acc[k] = 0.f;
-  auto slot = [&](int k) {
-    return (2 * static_cast<int64_t>(chunk0 + rec.first + k) + (k == 0 ? 1 : 0)) * a.n_cols + row;
-  };
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-  if (row < rec.rows) {
-    for (int k = lane; k < pieces; k += 32) top = fmaxf(top, ml[slot(k)].x);
-    top = warp_max(top);
-#pragma unroll 4
-    for (int k = sub; k < pieces; k += a.per_row) {
-      const int64_t s = slot(k);
-      const float2 p = ml[s];
-      const float w = ex2_approx(p.x - top);
-      sum = fmaf(w, p.y, sum);
-      const float* o = a.part_o + s * D + lane * V;
+      for (int q = 0; q < kBatch; ++q) {
+        const int k = k0 + q * a.per_row;
+        p[q] = make_float2(-INFINITY, 0.f);
+        if (k < pieces) {
+          const int64_t s =
+              (2 * static_cast<int64_t>(chunk0 + r.first + k) + (k == 0 ? 1 : 0)) * a.n_cols + row;
+          p[q] = ml[s];
+          const float* from = a.part_o + s * D + lane * V;
+          if constexpr (V == 4)
+            *reinterpret_cast<float4*>(o[q]) = *reinterpret_cast<const float4*>(from);
+          else
+            *reinterpret_cast<float2*>(o[q]) = *reinterpret_cast<const float2*>(from);
+        }
+      }
+      float now = top;
 #pragma unroll
-      for (int q = 0; q < V; ++q) acc[q] = fmaf(w, o[q], acc[q]);
+      for (int q = 0; q < kBatch; ++q) now = fmaxf(now, p[q].x);
+      const float f = top == -INFINITY ? 0.f : ex2_approx(top - now);
+      sum *= f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= f;
+      top = now;
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q)
+        if (k0 + q * a.per_row < pieces) {
+          const float w = ex2_approx(p[q].x - top);
+          sum = fmaf(w, p[q].y, sum);
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] = fmaf(w, o[q][v], acc[v]);
+        }
     }
   }
   if (a.per_row > 1) {
 #pragma unroll
-    for (int q = 0; q < V; ++q) s_acc[warp][lane * V + q] = acc[q];
-    if (lane == 0) s_sum[warp] = sum;
+    for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
+    if (lane == 0) s_ml[warp] = make_float2(top, sum);
     __syncthreads();
-    if (sub == 0)
-      for (int w = 1; w < a.per_row; ++w) {
-        sum += s_sum[warp + w];
+    if (sub == 0) {
+      for (int w = 1; w < a.per_row; ++w) top = fmaxf(top, s_ml[warp + w].x);
+      sum = 0.f;
 #pragma unroll
-        for (int q = 0; q < V; ++q) acc[q] += s_acc[warp + w][lane * V + q];
+      for (int v = 0; v < V; ++v) acc[v] = 0.f;
+      for (int w = 0; w < a.per_row; ++w) {
+        const float2 p = s_ml[warp + w];
+        if (p.x == -INFINITY) continue;  // a warp without pieces
+        const float f = ex2_approx(p.x - top);
+        sum = fmaf(f, p.y, sum);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(f, s_acc[warp + w][lane * V + v], acc[v]);
       }
+    }
   }
-  if (row < rec.rows && sub == 0) {
-    const bool seen = rec.lim0 + row / a.Gs > 0;
-    const int64_t at = (rec.row0 + row / a.Gs) * a.Hq + rec.head0 + row % a.Gs;
+  if (row < r.rows && sub == 0) {
+    const bool seen = r.lim0 + row / a.Gs > 0;
+    const int64_t at = (r.row0 + row / a.Gs) * a.Hq + r.head0 + row % a.Gs;
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + lane * V);
     const float inv = 1.f / sum;
 #pragma unroll
-    for (int q = 0; q < V; q += 2)
-      out[q / 2] = seen ? pack2<F16>(acc[q] * inv, acc[q + 1] * inv) : 0u;
+    for (int v = 0; v < V; v += 2)
+      out[v / 2] = seen ? pack2<F16>(acc[v] * inv, acc[v + 1] * inv) : 0u;
     if (a.lse && lane == 0) a.lse[at] = seen ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
 }
