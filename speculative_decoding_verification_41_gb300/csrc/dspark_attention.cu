@@ -101,7 +101,7 @@ int attn_shape(Launch& c, int sms) {
   if (c.a.n_cols <= 32) return attn_launch<AttnShape<D, 32, 1, 2, 2>, F16>(c, sms);
   if (c.a.n_cols <= 64) return attn_launch<AttnShape<D, 64, 4, 1, 2>, F16>(c, sms);
   if (c.a.n_cols <= 96) return attn_launch<AttnShape<D, 96, 3, 1, 2>, F16>(c, sms);
-  return attn_launch<AttnShape<D, 160, 4, 1, 1>, F16>(c, sms);
+  return attn_launch<AttnShape<D, 160, 3, 1, 1>, F16>(c, sms);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

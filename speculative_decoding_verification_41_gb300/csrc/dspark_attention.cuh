@@ -794,10 +794,10 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       const int lo_last = a.window == INT_MAX ? 0 : max(0, lim_last - a.window);
       // Sums of the columns' weights: a thread's own token's, in pairs; or, where
       // that takes too many registers, folded tile by tile into one per block.
-      constexpr bool kKeep = S::NC <= 32;
-      uint64_t l[kKeep ? S::NC / 2 : 1];
-      float lf[kKeep ? 1 : kBlocks];
-      if constexpr (kKeep) {
+      constexpr bool kPairs = S::NC <= 32;
+      uint64_t l[kPairs ? S::NC / 2 : 1];
+      float lf[kPairs ? 1 : kBlocks];
+      if constexpr (kPairs) {
 #pragma unroll
         for (int j = 0; j < S::NC / 2; ++j) l[j] = 0;
       } else {
@@ -813,51 +813,35 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         const bool whole = tok0 + kTileTok <= it.lim0 && tok0 >= lo_last;
         failed |= !mbar_wait(&ctl.s_full[buf], (tiles >> 1) & 1u);
         tc_fence_after();
-        // Scores, -inf where the row does not see the token. A group with few
-        // columns keeps them in registers, one with many reads them from tensor
-        // memory again for the second pass.
+        // scores, -inf where the row does not see the token
         float x[S::NC];
         const uint32_t s_addr = tmem + lanes + S::kColS + buf * S::NB + c0;
-        auto load = [&](auto from, auto to) {
 #pragma unroll
-          for (int b = from; b < to; ++b)
-            if (b < nb) tmem_ld8(s_addr + 8 * b, x + 8 * b);
-          tmem_wait_ld();
+        for (int b = 0; b < kBlocks; ++b)
+          if (b < nb) tmem_ld8(s_addr + 8 * b, x + 8 * b);
+        tmem_wait_ld();
 #pragma unroll
-          for (int b = from; b < to; ++b)
-            if (b < nb) {
-              tmem_arrived(x + 8 * b);
-              if (!whole) {
-                const int4* lim4 = reinterpret_cast<const int4*>(&lims[c0 + 8 * b]);
+        for (int b = 0; b < kBlocks; ++b)
+          if (b < nb) {
+            tmem_arrived(x + 8 * b);
+            if (!whole) {
+              const int4* lim4 = reinterpret_cast<const int4*>(&lims[c0 + 8 * b]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int4 m = lim4[k];
-                  float* y = x + 8 * b + 4 * k;
-                  if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[0] = -INFINITY;
-                  if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[1] = -INFINITY;
-                  if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[2] = -INFINITY;
-                  if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[3] = -INFINITY;
-                }
+              for (int k = 0; k < 2; ++k) {
+                const int4 m = lim4[k];
+                float* y = x + 8 * b + 4 * k;
+                if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[0] = -INFINITY;
+                if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[1] = -INFINITY;
+                if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[2] = -INFINITY;
+                if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[3] = -INFINITY;
               }
             }
-        };
-        // f(b) for every block in use, its scores in x
-        auto each = [&](auto f) {
-          if constexpr (kKeep) {
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-              if (b < nb) f(b);
-          } else {
-#pragma unroll
-            for (int b = 0; b < kBlocks; b += 2) {
-              load(b, b + 2 < kBlocks ? b + 2 : kBlocks);
-#pragma unroll
-              for (int k = b; k < b + 2 && k < kBlocks; ++k)
-                if (k < nb) f(k);
-            }
           }
+        auto each = [&](auto f) {  // f(b) for every block in use
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            if (b < nb) f(b);
         };
-        if constexpr (kKeep) load(0, kBlocks);
         // exponents y = c x - m
         auto exponent = [&](int b, uint64_t (&y)[4]) {
           const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(&nref[c0 + 8 * b]);
@@ -934,7 +918,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 tmem_arrived(o);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] *= f[k];
-                if constexpr (kKeep) {
+                if constexpr (kPairs) {
 #pragma unroll
                   for (int k = 0; k < 4; ++k)
                     l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
@@ -958,7 +942,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             unpair(e[k], y[2 * k], y[2 * k + 1]);
             y[2 * k] = ex2_approx(y[2 * k]);
             y[2 * k + 1] = ex2_approx(y[2 * k + 1]);
-            if constexpr (kKeep) l[4 * b + k] = add2(l[4 * b + k], pair(y[2 * k], y[2 * k + 1]));
+            if constexpr (kPairs) l[4 * b + k] = add2(l[4 * b + k], pair(y[2 * k], y[2 * k + 1]));
           }
           // The weights enter the second product in the inputs' type (half a
           // step of it each, no more than the output's own rounding); their sum
@@ -970,7 +954,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                      (((chunk & 1u) ^ swap) << 4),
                  pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3]), pack2<F16>(y[4], y[5]),
                  pack2<F16>(y[6], y[7]));
-          if constexpr (!kKeep) lf[b] += fold_columns<false>(y, lane);
+          if constexpr (!kPairs) lf[b] += fold_columns<false>(y, lane);
         });
         if (!whole && group == 0) {
           // Zero weights do not silence values that are not finite, and the
@@ -1027,7 +1011,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       for (int b = 0; b < kBlocks; ++b)
         if (b < nb) {
           float sum;
-          if constexpr (kKeep) {
+          if constexpr (kPairs) {
             float v[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) unpair(l[4 * b + k], v[2 * k], v[2 * k + 1]);
