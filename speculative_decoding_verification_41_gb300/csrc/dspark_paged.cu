@@ -91,7 +91,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_pages_reserve(const Reserv
   __shared__ Sum3 warp_sums[kPagedWarps];
   __shared__ uint32_t s_tok[kPagedThreads], s_page[kPagedThreads];  // inclusive, in this step
   __shared__ int32_t s_ctx[kPagedThreads];
+  __shared__ uint32_t s_first, s_why;
   const int tid = threadIdx.x;
+  if (tid == 0) s_why = 0;
   pdl_wait();  // predecessor grid complete, its writes visible
   pdl_trigger();
   const bool books = blockIdx.x == 0;
@@ -132,9 +134,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_pages_reserve(const Reserv
     const bool refused = own.tok > 0 && (closed || no_row || no_page);
     // What does not fit is a suffix of the requests with new tokens: the sums
     // up to the last one served are those of the whole step where all fit.
+    s_tok[tid] = in.tok;
+    s_page[tid] = in.page;
+    s_ctx[tid] = ctx;
     uint32_t served = kPagedThreads;
     if (__syncthreads_or(refused)) {
-      __shared__ uint32_t s_first;
       if (tid == 0) s_first = kPagedThreads;
       __syncthreads();
       if (refused) atomicMin(&s_first, static_cast<uint32_t>(tid));
@@ -144,16 +148,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_pages_reserve(const Reserv
         many = no_row;
         dry = no_page;
       }
-    }
-    if (static_cast<uint32_t>(tid) >= served) own = Sum3{0, 0, 0};
-    s_tok[tid] = in.tok;
-    s_page[tid] = in.page;
-    s_ctx[tid] = ctx;
-    if (served < kPagedThreads && static_cast<uint32_t>(tid) + 1u == served) warp_sums[0] = in;
-    __syncthreads();
-    if (served < kPagedThreads) {
+      if (static_cast<uint32_t>(tid) + 1u == served) warp_sums[0] = in;
+      __syncthreads();
       all = served > 0 ? warp_sums[0] : Sum3{0, 0, 0};
-      if (static_cast<uint32_t>(tid) >= served) in = all;
+      if (static_cast<uint32_t>(tid) >= served) own = Sum3{0, 0, 0}, in = all;
       closed = true;
     }
     const int n_req = static_cast<int>(min(served, static_cast<uint32_t>(a.B - base)));
@@ -170,6 +168,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_pages_reserve(const Reserv
           bad |= static_cast<uint32_t>(p) >= static_cast<uint32_t>(a.num_pages);
         }
       }
+#pragma unroll 8
       for (uint32_t i = tid; i < all.page; i += kPagedThreads) {
         const int32_t p = a.stack[avail - 1u - (carry.page + i)];
         bad |= static_cast<uint32_t>(p) >= static_cast<uint32_t>(a.num_pages);
@@ -231,16 +230,25 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_pages_reserve(const Reserv
       }
     }
     carry = add(carry, all);
-    __syncthreads();  // the step's sums are read no more
+    if (base + kPagedThreads < a.B) __syncthreads();  // the step's sums are read no more
   }
   // rows past the last token
-  for (uint32_t t = max(t0, carry.tok) + tid; t < t1; t += kPagedThreads) {
-    a.slots[t] = -1;
-    if (a.pos) a.pos[t] = -1;
+  const uint32_t pad = max(t0, carry.tok);
+  for (uint32_t g = (pad & ~3u) + 4u * tid; g < t1; g += 4u * kPagedThreads) {
+    if (a.vec && g >= pad && g + 4u <= t1) {
+      *reinterpret_cast<int4*>(a.slots + g) = make_int4(-1, -1, -1, -1);
+      if (a.pos) *reinterpret_cast<int4*>(a.pos + g) = make_int4(-1, -1, -1, -1);
+    } else {
+      for (uint32_t t = max(g, pad); t < min(g + 4u, t1); ++t) {
+        a.slots[t] = -1;
+        if (a.pos) a.pos[t] = -1;
+      }
+    }
   }
   if (books) {
-    const int any_bad = __syncthreads_or(bad), any_many = __syncthreads_or(many),
-              any_dry = __syncthreads_or(dry);
+    if (bad || many || dry) atomicOr(&s_why, (bad ? 1u : 0u) | (many ? 2u : 0u) | (dry ? 4u : 0u));
+    __syncthreads();
+    const uint32_t any_bad = s_why & 1u, any_many = s_why & 2u, any_dry = s_why & 4u;
     if (tid == 0) {
       a.row_off[0] = 0;
       if (a.draft_off) a.draft_off[0] = 0;
@@ -330,8 +338,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_pages_release(const Releas
   }
 }
 
-// A CTA takes groups of whole rows of about 1,024 16-byte pieces: four loads of
-// keys and four of values in flight per thread before the first store. CTA 0
+// A CTA takes a group of whole rows of about 1,024 16-byte pieces: four loads of
+// keys and four of values in flight per thread before the first store. CTAs that
+// end and begin keep the memory busier than CTAs that loop: 100,000 rows of 8 x
+// 128 in 114 us (6.7 TB/s) against 133 us with eight looping CTAs per SM. CTA 0
 // only judges the slots, so that one CTA writes the status.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendPieces = 4;
@@ -507,7 +517,7 @@ extern "C" int dspark_kv_append(const void* k, const void* v, int64_t row_stride
   a.shift = page_shift(page_size), a.n_slots = num_pages * page_size;
   a.rows = std::max(1, kAppendPieces * kAppendThreads / a.pieces);
   const int64_t groups = static_cast<int64_t>(DSPARK_CEILDIV(n, a.rows));
-  const int grid = 1 + static_cast<int>(std::min<int64_t>(groups, 152 * 8));
+  const int grid = 1 + static_cast<int>(std::min<int64_t>(groups, 1 << 20));
   if (launch_pdl(k_kv_append, grid, kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream),
                  a) != cudaSuccess ||
       cudaGetLastError() != cudaSuccess)
