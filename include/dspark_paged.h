@@ -191,7 +191,10 @@ int dspark_kv_append(const void* k, const void* v, int64_t row_stride, int64_t i
  *   context_len   [B] int32, 0 .. max_pages * page_size.
  *   row_off       [B+1] int64, ascending from >= 0 to <= n_tokens. Rows outside
  *                 every request are not written.
- *   Hq, Hkv       Hq a multiple of Hkv; D = 64 or 128; max_new >= 1.
+ *   Hq, Hkv       Hq a multiple of Hkv; D = 64 or 128; max_new >= 1. A key head's
+ *                 (Hq / Hkv) * max_new query rows are served in passes of up to
+ *                 DSPARK_PAGED_MAX_ROWS, side by side; more passes than the device
+ *                 has SMs, or max_pages * page_size * Hkv past 2^37, are refused.
  *   scale         finite, > 0.
  *   window        visible tokens per new token, itself included; 0: all.
  * Outputs

@@ -145,6 +145,7 @@ extern "C" int dspark_paged_attention(
       page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0 || num_pages < 1 ||
       static_cast<int64_t>(num_pages) * page_size > INT32_MAX || max_pages < 1 ||
       static_cast<int64_t>(max_pages) * page_size > INT32_MAX - 2 * kTileTok ||
+      static_cast<int64_t>(max_pages) * page_size / kTileTok * Hkv > INT32_MAX / 2 ||
       table_stride < max_pages || !device_status)
     return DSPARK_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
