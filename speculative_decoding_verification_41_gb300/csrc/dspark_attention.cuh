@@ -17,10 +17,11 @@
 // in range for every score s serves, and one that some score reaches keeps the
 // largest weight at 1 or more. A tile whose scores exceed their rows' references
 // by less than kSlack (log2) is used as it is: that is one vote per tile instead
-// of a maximum over 128 tokens for every row. Bf16 weights have binary32's range,
-// so there a row starts with the score of one token that it sees, whichever, and
-// a slack of 2^60; half precision ends at 2^16 and starts with the first tile's
-// maxima. When a vote fails, the maxima are taken, m raised and O and l scaled.
+// of a maximum over 128 tokens for every row. A row starts with its maximum over
+// the first tile (a score of one token would do for the range of bf16, and costs
+// as much, but leaves the largest weight a rounding that a weight of 1 has not:
+// 1.5 times the output's own rounding error in all, against 1.1 to 1.3). When a
+// vote fails, the maxima are taken, m raised and O and l scaled.
 //
 // Bound. Every cached key and value is read once: 4 D bytes per token and key
 // head against 4 D R flops, so up to R of about 280 the copy rate of HBM bounds
@@ -28,14 +29,15 @@
 // across requests; (2) work split evenly over the CTAs whatever the lengths:
 // all (request, head) items form one line, each as long as its tiles and `lead`
 // more for what it costs to begin and end one; CTA c of C takes [cW/C, (c+1)W/C)
-// of it, found from the lengths on the device; a request cut by such a border leaves partial (m, l, O) rows that k_attention_join adds up in
-// the order of the tiles, so results do not depend on timing.
+// of it, found from the lengths on the device; a request cut by such a border
+// leaves partial (m, l, O) rows that k_attention_join adds up in the order of
+// the tiles, so results do not depend on timing.
 //
 // Warps: 0 copies keys, 1 values, 3 queries (TMA), 2 issues the products; from
 // the fifth on groups of four, which share the rows among them, do the softmax
-// and write the results. S and P
-// have two buffers each: while a group is at a tile's exponents the products of
-// the next scores and of the weights before are under way.
+// and write the results. S and P have two buffers each (P of the widest block
+// one): while a group is at a tile's exponents the products of the next scores
+// and of the weights before are under way.
 #pragma once
 
 #include <climits>
@@ -852,24 +854,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           y[2] = fma2(pair(z[4], z[5]), c2, m1.x);
           y[3] = fma2(pair(z[6], z[7]), c2, m1.y);
         };
-        bool raise = F16 && i == 0;  // in half precision the first tile's maxima
+        bool raise = i == 0;  // the first tile's maxima
         if (!raise) {
-          if (!F16 && i == 0) {
-            // the first token that all rows see, if the tile has one
-            const int pick = max(tok0, lo_last);
-            if (pick < min(tok0 + kTileTok, it.lim0)) {
-              each([&](int b) {
-                if (tok == pick) {
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    const float m = x[8 * b + k] * a.c;
-                    if (8 * b + k < my_rows && fabsf(m) < kNoRef) nref[c0 + 8 * b + k] = -m;
-                  }
-                }
-              });
-              bar_sync(bar, 128);
-            }
-          }
           float top = -INFINITY;
           each([&](int b) {
             uint64_t e[4];

@@ -151,15 +151,16 @@ def _kept(buffers, stream):
                 t.record_stream(stream)
 
 
-def _call(name: str, index: int, *args):
-    fn = _fns[name] if _fns is not None else _load()[name]
+def _fn(name: str, index: int):
+    """The library's function, called on the tensors' device."""
+    fn = (_fns or _load())[name]
     if _get_device() == index:
-        rc = fn(*args)
-    else:
+        return fn
+
+    def there(*args):
         with torch.cuda.device(index):
-            rc = fn(*args)
-    if rc != 0:
-        raise DsparkError(name, rc)
+            return fn(*args)
+    return there
 
 
 def _checked(name: str, status: torch.Tensor, index: int, stream):
@@ -212,17 +213,21 @@ def dspark_pages_reserve(context_len: torch.Tensor, new_len: torch.Tensor,
     s = _on(stream, dev)
     if buffers is None:
         _kept(buf, stream)
-    _call("dspark_pages_reserve", dev, context_len.data_ptr(), new_len.data_ptr(), extra, B,
-          page_size, free_pages.numel(), block_table.data_ptr(), stride, width,
-          free_pages.data_ptr(), free_count.data_ptr(), max_tokens, buf.context_len.data_ptr(),
-          buf.row_off.data_ptr(), buf.draft_off.data_ptr(), buf.slot_map.data_ptr(),
-          buf.positions.data_ptr(), buf.free_count.data_ptr(), buf.device_status.data_ptr(),
-          s)
+    out_len, row_off, draft_off = buf.context_len, buf.row_off, buf.draft_off
+    slot_map, positions = buf.slot_map, buf.positions
+    left, status = buf.free_count, buf.device_status
+    rc = _fn("dspark_pages_reserve", dev)(
+        context_len.data_ptr(), new_len.data_ptr(), extra, B, page_size, free_pages.numel(),
+        block_table.data_ptr(), stride, width, free_pages.data_ptr(), free_count.data_ptr(),
+        max_tokens, out_len.data_ptr(), row_off.data_ptr(), draft_off.data_ptr(),
+        slot_map.data_ptr(), positions.data_ptr(), left.data_ptr(), status.data_ptr(), s)
+    if rc != 0:
+        raise DsparkError("dspark_pages_reserve", rc)
     if check:
-        _checked("dspark_pages_reserve", buf.device_status, dev, stream)
-    return {"context_len": buf.context_len, "row_off": buf.row_off, "draft_off": buf.draft_off,
-            "slot_map": buf.slot_map, "positions": buf.positions, "free_count": buf.free_count,
-            "device_status": buf.device_status}
+        _checked("dspark_pages_reserve", status, dev, stream)
+    return {"context_len": out_len, "row_off": row_off, "draft_off": draft_off,
+            "slot_map": slot_map, "positions": positions, "free_count": left,
+            "device_status": status}
 
 
 class ReleaseBuffers:
@@ -260,15 +265,16 @@ def dspark_pages_release(context_len: torch.Tensor, reserved_len: torch.Tensor,
     s = _on(stream, dev)
     if buffers is None:
         _kept(buf, stream)
-    _call("dspark_pages_release", dev, context_len.data_ptr(), reserved_len.data_ptr(),
-          kept_len.data_ptr(), extra, B, page_size, free_pages.numel(), block_table.data_ptr(),
-          stride, width, free_pages.data_ptr(), free_count.data_ptr(),
-          buf.context_len.data_ptr(), buf.free_count.data_ptr(), buf.device_status.data_ptr(),
-          s)
+    out_len, left, status = buf.context_len, buf.free_count, buf.device_status
+    rc = _fn("dspark_pages_release", dev)(
+        context_len.data_ptr(), reserved_len.data_ptr(), kept_len.data_ptr(), extra, B, page_size,
+        free_pages.numel(), block_table.data_ptr(), stride, width, free_pages.data_ptr(),
+        free_count.data_ptr(), out_len.data_ptr(), left.data_ptr(), status.data_ptr(), s)
+    if rc != 0:
+        raise DsparkError("dspark_pages_release", rc)
     if check:
-        _checked("dspark_pages_release", buf.device_status, dev, stream)
-    return {"context_len": buf.context_len, "free_count": buf.free_count,
-            "device_status": buf.device_status}
+        _checked("dspark_pages_release", status, dev, stream)
+    return {"context_len": out_len, "free_count": left, "device_status": status}
 
 
 def dspark_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
@@ -302,9 +308,12 @@ def dspark_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
             device_status.record_stream(stream)
     else:
         _want("device_status", device_status, _I32, dev, (1,))
-    _call("dspark_kv_append", dev, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
-          slot_map.data_ptr(), n, Hkv, D, dtype, k_cache.data_ptr(), v_cache.data_ptr(), sp, st,
-          sh, page_size, pages, device_status.data_ptr(), s)
+    rc = _fn("dspark_kv_append", dev)(
+        k.data_ptr(), v.data_ptr(), strides[0], strides[1], slot_map.data_ptr(), n, Hkv, D, dtype,
+        k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, page_size, pages,
+        device_status.data_ptr(), s)
+    if rc != 0:
+        raise DsparkError("dspark_kv_append", rc)
     if check:
         _checked("dspark_kv_append", device_status, dev, stream)
     return {"device_status": device_status}
@@ -362,13 +371,15 @@ def dspark_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     s = _on(stream, dev)
     if buffers is None:
         _kept(buf, stream)
-    _call("dspark_paged_attention", dev, q.data_ptr(), strides[0], strides[1],
-          k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, page_size, pages,
-          block_table.data_ptr(), stride, width, context_len.data_ptr(), row_off.data_ptr(), B, n,
-          Hq, Hkv, D, max_new, scale, window, dtype, out.data_ptr(),
-          buf.lse.data_ptr() if with_lse else None, buf.device_status.data_ptr(),
-          buf.workspace.data_ptr(), buf.workspace.numel(), s)
+    lse, status, workspace = buf.lse if with_lse else None, buf.device_status, buf.workspace
+    rc = _fn("dspark_paged_attention", dev)(
+        q.data_ptr(), strides[0], strides[1], k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh,
+        page_size, pages, block_table.data_ptr(), stride, width, context_len.data_ptr(),
+        row_off.data_ptr(), B, n, Hq, Hkv, D, max_new, scale, window, dtype, out.data_ptr(),
+        lse.data_ptr() if with_lse else None, status.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), s)
+    if rc != 0:
+        raise DsparkError("dspark_paged_attention", rc)
     if check:
-        _checked("dspark_paged_attention", buf.device_status, dev, stream)
-    return {"out": out, "lse": buf.lse if with_lse else None,
-            "device_status": buf.device_status}
+        _checked("dspark_paged_attention", status, dev, stream)
+    return {"out": out, "lse": lse, "device_status": status}
