@@ -200,7 +200,9 @@ int dspark_kv_append(const void* k, const void* v, int64_t row_stride, int64_t i
  * Outputs
  *   out           [n_tokens][Hq][D] dtype, contiguous.
  *   lse           [n_tokens][Hq] float32 or NULL (natural logarithm).
- *   device_status [1] int32 (required).
+ *   device_status [1] int32 (required): DSPARK_OK or a data error;
+ *                 DSPARK_ERR_TOO_LARGE (nothing computed) for a batch of 2^31
+ *                 units or more (128 tokens of a key head each).
  *   workspace     at least DSPARK_PAGED_ATTENTION_WS_BYTES(Hq, Hkv, max_new, D)
  *                 bytes, 256-byte aligned; no initial contents needed.
  * q, k_cache, v_cache and out must be 16-byte aligned and all strides multiples

@@ -102,6 +102,25 @@ struct AttnReq {  // a request, as the partition sees it
   int32_t t_rows, lim0, begin, end;
 };
 
+// The line of all units, cut into one part per CTA: the first `more` parts are
+// one unit longer. CTAs past `parts` have none.
+constexpr uint32_t kMaxUnits = INT_MAX;
+struct Line {
+  uint32_t units = 0, parts = 0, per = 0, more = 0;
+  __device__ Line() {}
+  __device__ Line(uint32_t n, int ctas) : units(n) {
+    parts = min(n, static_cast<uint32_t>(ctas));
+    if (parts > 0) per = n / parts, more = n - per * parts;
+  }
+  __device__ uint32_t begin(uint32_t c) const {
+    return c >= parts ? units : c * per + min(c, more);
+  }
+  __device__ int32_t owner(uint32_t u) const {  // of unit u
+    const uint32_t longer = more * (per + 1u);
+    return static_cast<int32_t>(u < longer ? u / (per + 1u) : more + (u - longer) / per);
+  }
+};
+
 __device__ __forceinline__ bool attn_request(const AttnArgs& a, int r, int t0, AttnReq& q) {
   const int64_t o0 = a.row_off[r], o1 = a.row_off[r + 1];
   const int32_t len = a.ctx[r];
@@ -341,8 +360,7 @@ struct AttnCtl {
   uint64_t odd_full, drained;
   uint32_t tmem;
   int32_t status, abort, start_r, start_off;
-  int64_t u_total;
-  int64_t scan[S::THREADS / 32];
+  uint32_t scan[S::THREADS / 32];
   AttnItem item[kItems];
   // per column (row of q); a group's own. Two of what an item begins with: its
   // slower warps may still write their results when the next one begins.
@@ -402,41 +420,47 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
   pdl_trigger();
 
   // ---- this CTA's part of the line of units ------------------------------
-  const int chunk = blockIdx.x % a.n_chunks, cta = blockIdx.x / a.n_chunks;
-  const int part = chunk % a.parts, t0 = chunk / a.parts * a.t_chunk;
+  int chunk = 0, cta = blockIdx.x, part = 0, t0 = 0;
+  if (a.n_chunks > 1) {
+    chunk = blockIdx.x % a.n_chunks, cta = blockIdx.x / a.n_chunks;
+    part = chunk % a.parts, t0 = chunk / a.parts * a.t_chunk;
+  }
+  Line line;
   {
-    const int per = (a.B + S::THREADS - 1) / S::THREADS;
+    const int per = (a.B + S::THREADS - 1) / S::THREADS;  // requests per thread
     const int r0 = min(tid * per, a.B), r1 = min(r0 + per, a.B);
-    int64_t sum = 0;
+    uint32_t sum = 0;
     bool bad = false;
-    AttnReq q;
+    AttnReq q{};
 #pragma unroll 4
     for (int r = r0; r < r1; ++r) {
       bad |= !attn_request(a, r, t0, q);
-      sum += static_cast<int64_t>(q.units) * a.Hkv;
+      sum = min(sum + static_cast<uint32_t>(q.units * a.Hkv), kMaxUnits);
     }
-    int64_t in = sum;
+    uint32_t in = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, in, o);
-      if (lane >= o) in += u;
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, in, o);
+      if (lane >= o) in = min(in + u, kMaxUnits);
     }
     if (lane == 31) ctl.scan[warp] = in;
     tc_fence_before();
     const int any_bad = __syncthreads_or(bad);
     tc_fence_after();
-    int64_t before = in - sum, total = 0;
+    uint32_t before = in - sum, total = 0;
+#pragma unroll
     for (int w = 0; w < S::THREADS / 32; ++w) {
-      if (w < warp) before += ctl.scan[w];
-      total += ctl.scan[w];
+      const uint32_t v = ctl.scan[w];
+      if (w < warp) before = min(before + v, kMaxUnits);
+      total = min(total + v, kMaxUnits);
     }
-    const int64_t g = min(static_cast<int64_t>(a.ctas), total);
-    const int64_t u0 = cta < g ? cta * total / g : total;
+    line = Line(total < kMaxUnits ? total : 0u, a.ctas);
+    const uint32_t u0 = line.begin(cta);
     if (u0 >= before && u0 < before + sum) {
-      int64_t u = before;
+      uint32_t u = before;
       for (int r = r0; r < r1; ++r) {
-        attn_request(a, r, t0, q);
-        const int64_t n = static_cast<int64_t>(q.units) * a.Hkv;
+        if (per > 1) attn_request(a, r, t0, q);
+        const uint32_t n = static_cast<uint32_t>(q.units * a.Hkv);
         if (u0 < u + n) {
           ctl.start_r = r;
           ctl.start_off = static_cast<int32_t>(u0 - u);
@@ -446,14 +470,12 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       }
     }
     if (tid == 0) {
-      ctl.u_total = total;
+      if (total == kMaxUnits) ctl.status = DSPARK_ERR_TOO_LARGE;
       if (any_bad) ctl.status = DSPARK_ERR_BAD_DATA;
     }
   }
   __syncthreads();
-  const int64_t W = ctl.u_total;
-  const int64_t g = min(static_cast<int64_t>(a.ctas), W);
-  const int64_t u_begin = cta < g ? cta * W / g : W, u_end = cta < g ? (cta + 1) * W / g : W;
+  const uint32_t u_begin = line.begin(cta), u_end = line.begin(cta + 1);
   const uint32_t tmem = ctl.tmem;
   const int id = chunk * a.ctas + cta;  // of the record and the partial slots
   if (tid == 0 && u_begin == u_end) a.records[id].valid = 0;
@@ -479,7 +501,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       const CUtensorMap* const map = keys ? &map_k : &map_v;
       const uint32_t dst0 = s_ring + half * S::kSlab + box * box_bytes;
       int r = ctl.start_r, off = ctl.start_off;
-      int64_t u = u_begin;
+      uint32_t u = u_begin;
       // requests r_base .. r_base+31, one per lane
       int r_base = -1000;
       AttnReq mine{};
@@ -510,7 +532,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           }
           h = off / q.units;
           lead_in = off - h * q.units;
-          take = static_cast<int>(min(static_cast<int64_t>(q.units - lead_in), u_end - u));
+          take = static_cast<int>(min(static_cast<uint32_t>(q.units - lead_in), u_end - u));
           u += take;
           off += take;
           if (lead_in + take > a.lead) {
@@ -550,8 +572,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             item.end = q.end;
             item.starts = in_head == 0;
             item.ends = lead_in + take == q.units;
-            item.first =
-                static_cast<int32_t>(((u - take - lead_in + a.lead + 1) * g - 1) / W);
+            item.first = line.owner(u - take - lead_in + a.lead);
             mbar_arrive(&ctl.item_full[slot]);
           }
           ++items;
