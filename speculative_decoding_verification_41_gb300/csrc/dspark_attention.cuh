@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     }
     for (uint32_t i = 0; i < kItems; ++i) {
       mbar_init(&ctl.item_full[i], 1);
-      mbar_init(&ctl.item_empty[i], 4 * S::GROUPS);
+      mbar_init(&ctl.item_empty[i], 4 * S::GROUPS + 2);  // softmax warps, products, queries
     }
     ctl.status = DSPARK_OK;
     ctl.abort = 0;
@@ -685,6 +685,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         int tok0 = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tile0, 0) * kTileTok;
         const int begin = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].begin, 0);
         const int end = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].end, 0);
+        if (nt >= 0 && leader) mbar_arrive(&ctl.item_empty[slot]);
         ++items;
         if (nt < 0) break;
         if (nt == 0) continue;
@@ -757,13 +758,16 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ok = mbar_wait(&ctl.item_full[slot], (items / kItems) & 1u);
         if (!ok || ctl.item[slot].tiles < 0) break;
         ++items;
-        if (ctl.item[slot].tiles == 0) continue;
+        const int tiles = ctl.item[slot].tiles, head0 = ctl.item[slot].head0;
+        const int row0 = static_cast<int>(ctl.item[slot].row0);
+        mbar_arrive(&ctl.item_empty[slot]);
+        if (tiles == 0) continue;
         if (wraps >= 1) ok = mbar_wait(&ctl.q_empty[b], (wraps - 1u) & 1u);
         if (!ok) break;
         mbar_arrive_expect_tx(&ctl.q_full[b], bytes);
         for (int i = 0; i < S::HALVES; ++i)
-          tma_load_3d_to(s_q + (b * S::HALVES + i) * q_slab, &map_q, i * 64, ctl.item[slot].head0,
-                         static_cast<int>(ctl.item[slot].row0), &ctl.q_full[b]);
+          tma_load_3d_to(s_q + (b * S::HALVES + i) * q_slab, &map_q, i * 64, head0, row0,
+                         &ctl.q_full[b]);
         if (++b == static_cast<uint32_t>(a.q_bufs)) b = 0, ++wraps;
       }
       if (!ok) {
