@@ -1,6 +1,8 @@
 """The paged key-value cache around a speculative step (include/dspark_paged.h),
-through ctypes: argument checks and marshalling only, every step runs in the
-CUDA kernels of libdspark.so.
+argument checks and marshalling only, every step runs in the CUDA kernels of
+libdspark.so. A call with its buffers goes through the _paged_binding module
+(csrc/paged_binding.cpp), which makes the same checks in a fraction of the time;
+what does not pass them there comes back to the ones here, and through ctypes.
 
   dspark_pages_reserve(...)    pages, slots, positions and row offsets of new tokens
   dspark_kv_append(...)        their keys and values into the cache
@@ -41,6 +43,24 @@ binding.STATUS_NAMES[DSPARK_ERR_NO_PAGES] = "DSPARK_ERR_NO_PAGES"
 _DTYPES = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16}
 
 _fns = None
+_ext = None
+
+
+def _native():
+    """The _paged_binding module, with libdspark's functions bound. Raises if it has not been
+    built: there is no fallback."""
+    global _ext
+    if _ext is None:
+        fns = _load()
+        try:
+            from . import _paged_binding
+        except ImportError as e:
+            raise RuntimeError("the _paged_binding module is not built or does not fit this "
+                               "Python and torch; run `python -c 'import __graft_entry__ as g; "
+                               f"g.build()'` ({e})") from e
+        _paged_binding.bind(*(ctypes.cast(fns[name], ctypes.c_void_p).value for name in EXPORTED))
+        _ext = _paged_binding
+    return _ext
 
 
 def _load():
@@ -70,9 +90,6 @@ def paged_attention_workspace_bytes(Hq: int, Hkv: int, max_new: int, D: int) -> 
     return ((PAGED_MAX_CTAS * 64 + 255) & ~255) + 2 * PAGED_MAX_CTAS * rows * (4 * D + 8)
 
 
-# A call takes a few microseconds on the GPU, so its checks and marshalling on
-# the host are kept to the ones it needs: torch.cuda.current_stream() alone, which
-# makes a Stream object, costs more than all of a call's pointer arguments.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _get_device = torch._C._cuda_getDevice
 _I32, _I64 = torch.int32, torch.int64
@@ -143,6 +160,13 @@ def _on(stream, index: int) -> int:
     return stream.cuda_stream
 
 
+def _handle(stream, t):
+    """A given stream's handle for the usual path; None: the current stream."""
+    if stream is None:
+        return None
+    return _on(stream, t.get_device() if isinstance(t, torch.Tensor) else -1)
+
+
 def _kept(buffers, stream):
     """Memory that the call allocated stays the stream's until its work is done."""
     if stream is not None:
@@ -163,9 +187,9 @@ def _fn(name: str, index: int):
     return there
 
 
-def _checked(name: str, status: torch.Tensor, index: int, stream):
+def _checked(name: str, status: torch.Tensor, stream):
     """Wait for the call and raise on a status that is not OK."""
-    (stream or torch.cuda.current_stream(index)).synchronize()
+    (stream or torch.cuda.current_stream(status.device)).synchronize()
     st = int(status.item())
     if st != 0:
         raise DsparkError(f"{name} (device)", st)
@@ -200,34 +224,42 @@ def dspark_pages_reserve(context_len: torch.Tensor, new_len: torch.Tensor,
     with extra = 1), draft_off [B+1] int64 (its draft_row_off), slot_map and
     positions [max_tokens], free_count [1], device_status [1] (device tensors).
     With check=True the call synchronises and raises on a non-OK device status."""
-    dev = _index("context_len", context_len)
-    B = context_len.numel()
-    _want("context_len", context_len, _I32, dev, (B,))
-    _want("new_len", new_len, _I32, dev, (B,))
-    stride, width = _table(block_table, B, dev)
-    _want("free_pages", free_pages, _I32, dev)
-    _want("free_count", free_count, _I32, dev, (1,))
-    buf = buffers or ReserveBuffers(B, max_tokens, context_len.device)
-    if buf.B != B or buf.max_tokens != max_tokens:
-        raise ValueError("buffers were made for another shape")
-    s = _on(stream, dev)
-    if buffers is None:
-        _kept(buf, stream)
-    out_len, row_off, draft_off = buf.context_len, buf.row_off, buf.draft_off
-    slot_map, positions = buf.slot_map, buf.positions
-    left, status = buf.free_count, buf.device_status
-    rc = _fn("dspark_pages_reserve", dev)(
-        context_len.data_ptr(), new_len.data_ptr(), extra, B, page_size, free_pages.numel(),
-        block_table.data_ptr(), stride, width, free_pages.data_ptr(), free_count.data_ptr(),
-        max_tokens, out_len.data_ptr(), row_off.data_ptr(), draft_off.data_ptr(),
-        slot_map.data_ptr(), positions.data_ptr(), left.data_ptr(), status.data_ptr(), s)
+    buf, rc = buffers, None
+    if buf is not None:
+        rc = (_ext or _native()).reserve(
+            context_len, new_len, block_table, free_pages, free_count, page_size, max_tokens,
+            extra, buf.context_len, buf.row_off, buf.draft_off, buf.slot_map, buf.positions,
+            buf.free_count, buf.device_status, _handle(stream, context_len))
+    if rc is None:
+        dev = _index("context_len", context_len)
+        B = context_len.numel()
+        _want("context_len", context_len, _I32, dev, (B,))
+        _want("new_len", new_len, _I32, dev, (B,))
+        stride, width = _table(block_table, B, dev)
+        _want("free_pages", free_pages, _I32, dev)
+        _want("free_count", free_count, _I32, dev, (1,))
+        s = _on(stream, dev)
+        if buf is None:
+            buf = ReserveBuffers(B, max_tokens, context_len.device)
+            _kept(buf, stream)
+        for name, dtype, n in (("context_len", _I32, B), ("row_off", _I64, B + 1),
+                               ("draft_off", _I64, B + 1), ("slot_map", _I32, max_tokens),
+                               ("positions", _I32, max_tokens), ("free_count", _I32, 1),
+                               ("device_status", _I32, 1)):
+            _want(f"buffers.{name}", getattr(buf, name), dtype, dev, (n,))
+        rc = _fn("dspark_pages_reserve", dev)(
+            context_len.data_ptr(), new_len.data_ptr(), extra, B, page_size, free_pages.numel(),
+            block_table.data_ptr(), stride, width, free_pages.data_ptr(), free_count.data_ptr(),
+            max_tokens, buf.context_len.data_ptr(), buf.row_off.data_ptr(),
+            buf.draft_off.data_ptr(), buf.slot_map.data_ptr(), buf.positions.data_ptr(),
+            buf.free_count.data_ptr(), buf.device_status.data_ptr(), s)
     if rc != 0:
         raise DsparkError("dspark_pages_reserve", rc)
     if check:
-        _checked("dspark_pages_reserve", status, dev, stream)
-    return {"context_len": out_len, "row_off": row_off, "draft_off": draft_off,
-            "slot_map": slot_map, "positions": positions, "free_count": left,
-            "device_status": status}
+        _checked("dspark_pages_reserve", buf.device_status, stream)
+    return {"context_len": buf.context_len, "row_off": buf.row_off, "draft_off": buf.draft_off,
+            "slot_map": buf.slot_map, "positions": buf.positions, "free_count": buf.free_count,
+            "device_status": buf.device_status}
 
 
 class ReleaseBuffers:
@@ -251,30 +283,38 @@ def dspark_pages_release(context_len: torch.Tensor, reserved_len: torch.Tensor,
     pages past them go back on free_pages, in place (include/dspark_paged.h).
 
     Returns context_len [B], free_count [1], device_status [1] (device tensors)."""
-    dev = _index("context_len", context_len)
-    B = context_len.numel()
-    _want("context_len", context_len, _I32, dev, (B,))
-    _want("reserved_len", reserved_len, _I32, dev, (B,))
-    _want("kept_len", kept_len, _I32, dev, (B,))
-    stride, width = _table(block_table, B, dev)
-    _want("free_pages", free_pages, _I32, dev)
-    _want("free_count", free_count, _I32, dev, (1,))
-    buf = buffers or ReleaseBuffers(B, context_len.device)
-    if buf.B != B:
-        raise ValueError("buffers were made for another shape")
-    s = _on(stream, dev)
-    if buffers is None:
-        _kept(buf, stream)
-    out_len, left, status = buf.context_len, buf.free_count, buf.device_status
-    rc = _fn("dspark_pages_release", dev)(
-        context_len.data_ptr(), reserved_len.data_ptr(), kept_len.data_ptr(), extra, B, page_size,
-        free_pages.numel(), block_table.data_ptr(), stride, width, free_pages.data_ptr(),
-        free_count.data_ptr(), out_len.data_ptr(), left.data_ptr(), status.data_ptr(), s)
+    buf, rc = buffers, None
+    if buf is not None:
+        rc = (_ext or _native()).release(
+            context_len, reserved_len, kept_len, block_table, free_pages, free_count, page_size,
+            extra, buf.context_len, buf.free_count, buf.device_status,
+            _handle(stream, context_len))
+    if rc is None:
+        dev = _index("context_len", context_len)
+        B = context_len.numel()
+        _want("context_len", context_len, _I32, dev, (B,))
+        _want("reserved_len", reserved_len, _I32, dev, (B,))
+        _want("kept_len", kept_len, _I32, dev, (B,))
+        stride, width = _table(block_table, B, dev)
+        _want("free_pages", free_pages, _I32, dev)
+        _want("free_count", free_count, _I32, dev, (1,))
+        s = _on(stream, dev)
+        if buf is None:
+            buf = ReleaseBuffers(B, context_len.device)
+            _kept(buf, stream)
+        for name, n in (("context_len", B), ("free_count", 1), ("device_status", 1)):
+            _want(f"buffers.{name}", getattr(buf, name), _I32, dev, (n,))
+        rc = _fn("dspark_pages_release", dev)(
+            context_len.data_ptr(), reserved_len.data_ptr(), kept_len.data_ptr(), extra, B,
+            page_size, free_pages.numel(), block_table.data_ptr(), stride, width,
+            free_pages.data_ptr(), free_count.data_ptr(), buf.context_len.data_ptr(),
+            buf.free_count.data_ptr(), buf.device_status.data_ptr(), s)
     if rc != 0:
         raise DsparkError("dspark_pages_release", rc)
     if check:
-        _checked("dspark_pages_release", status, dev, stream)
-    return {"context_len": out_len, "free_count": left, "device_status": status}
+        _checked("dspark_pages_release", buf.device_status, stream)
+    return {"context_len": buf.context_len, "free_count": buf.free_count,
+            "device_status": buf.device_status}
 
 
 def dspark_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
@@ -285,37 +325,42 @@ def dspark_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
     slot_map[i] of the caches, in place; negative slots are skipped
     (include/dspark_paged.h). slot_map may be longer than n (a reservation's whole
     map): its first n entries count. Returns device_status [1]."""
-    dev = _index("k_cache", k_cache)
-    (pages, page_size, Hkv, D), (sp, st, sh, _), dtype = _cache(k_cache, v_cache, dev)
-    for name, x in (("k", k), ("v", v)):
-        if not isinstance(x, torch.Tensor) or x.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-    shape, strides = k.shape, k.stride()
-    if len(shape) != 3 or strides[2] != 1 or shape[1] != Hkv or shape[2] != D:
-        raise ValueError(f"k must be [n, {Hkv}, {D}] with contiguous rows")
-    if k.dtype is not k_cache.dtype or v.dtype is not k.dtype:
-        raise ValueError(f"k and v must be {k_cache.dtype}, got {k.dtype} and {v.dtype}")
-    if v.shape != shape or v.stride() != strides:
-        raise ValueError("k and v must have the same shape and strides")
-    n = shape[0]
-    _want("slot_map", slot_map, _I32, dev)
-    if slot_map.numel() < n:
-        raise ValueError(f"slot_map has {slot_map.numel()} entries for {n} rows")
-    s = _on(stream, dev)
-    if device_status is None:
-        device_status = torch.empty(1, dtype=_I32, device=k_cache.device)
-        if stream is not None:
-            device_status.record_stream(stream)
-    else:
-        _want("device_status", device_status, _I32, dev, (1,))
-    rc = _fn("dspark_kv_append", dev)(
-        k.data_ptr(), v.data_ptr(), strides[0], strides[1], slot_map.data_ptr(), n, Hkv, D, dtype,
-        k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, page_size, pages,
-        device_status.data_ptr(), s)
+    rc = None
+    if device_status is not None:
+        rc = (_ext or _native()).append(k, v, slot_map, k_cache, v_cache, device_status,
+                                        _handle(stream, k_cache))
+    if rc is None:
+        dev = _index("k_cache", k_cache)
+        (pages, page_size, Hkv, D), (sp, st, sh, _), dtype = _cache(k_cache, v_cache, dev)
+        for name, x in (("k", k), ("v", v)):
+            if not isinstance(x, torch.Tensor) or x.get_device() != dev:
+                raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
+        shape, strides = k.shape, k.stride()
+        if len(shape) != 3 or strides[2] != 1 or shape[1] != Hkv or shape[2] != D:
+            raise ValueError(f"k must be [n, {Hkv}, {D}] with contiguous rows")
+        if k.dtype is not k_cache.dtype or v.dtype is not k.dtype:
+            raise ValueError(f"k and v must be {k_cache.dtype}, got {k.dtype} and {v.dtype}")
+        if v.shape != shape or v.stride() != strides:
+            raise ValueError("k and v must have the same shape and strides")
+        n = shape[0]
+        _want("slot_map", slot_map, _I32, dev)
+        if slot_map.numel() < n:
+            raise ValueError(f"slot_map has {slot_map.numel()} entries for {n} rows")
+        s = _on(stream, dev)
+        if device_status is None:
+            device_status = torch.empty(1, dtype=_I32, device=k_cache.device)
+            if stream is not None:
+                device_status.record_stream(stream)
+        else:
+            _want("device_status", device_status, _I32, dev, (1,))
+        rc = _fn("dspark_kv_append", dev)(
+            k.data_ptr(), v.data_ptr(), strides[0], strides[1], slot_map.data_ptr(), n, Hkv, D,
+            dtype, k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, page_size, pages,
+            device_status.data_ptr(), s)
     if rc != 0:
         raise DsparkError("dspark_kv_append", rc)
     if check:
-        _checked("dspark_kv_append", device_status, dev, stream)
+        _checked("dspark_kv_append", device_status, stream)
     return {"device_status": device_status}
 
 
@@ -346,40 +391,49 @@ def dspark_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
 
     Returns out [n_tokens, Hq, D], lse [n_tokens, Hq] float32 (or None) and
     device_status [1] (device tensors)."""
-    dev = _index("k_cache", k_cache)
-    (pages, page_size, Hkv, D), (sp, st, sh, _), dtype = _cache(k_cache, v_cache, dev)
-    if not isinstance(q, torch.Tensor) or q.get_device() != dev:
-        raise ValueError(f"q must be a CUDA tensor on cuda:{dev}")
-    if q.dtype is not k_cache.dtype:
-        raise ValueError(f"q must be {k_cache.dtype}, got {q.dtype}")
-    shape, strides = q.shape, q.stride()
-    if len(shape) != 3 or strides[2] != 1 or shape[2] != D:
-        raise ValueError(f"q must be [n_tokens, heads, {D}] with contiguous rows")
-    n, Hq, _ = shape
-    B = context_len.numel()
-    _want("context_len", context_len, _I32, dev, (B,))
-    _want("row_off", row_off, _I64, dev, (B + 1,))
-    stride, width = _table(block_table, B, dev)
-    if Hkv < 1 or Hq < 1 or Hq % Hkv != 0 or max_new < 1:
-        raise ValueError(f"{Hq} query heads on {Hkv} key heads, max_new {max_new}")
-    buf = buffers or AttentionBuffers(n, Hq, Hkv, D, max_new, q.dtype, q.device, with_lse)
-    out = buf.out
-    if out.shape != shape or out.dtype is not q.dtype:
-        raise ValueError("buffers were made for another shape or type")
-    if with_lse and buf.lse is None:
-        raise ValueError("buffers were made without lse (AttentionBuffers(..., with_lse=True))")
-    s = _on(stream, dev)
-    if buffers is None:
-        _kept(buf, stream)
-    lse, status, workspace = buf.lse if with_lse else None, buf.device_status, buf.workspace
-    rc = _fn("dspark_paged_attention", dev)(
-        q.data_ptr(), strides[0], strides[1], k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh,
-        page_size, pages, block_table.data_ptr(), stride, width, context_len.data_ptr(),
-        row_off.data_ptr(), B, n, Hq, Hkv, D, max_new, scale, window, dtype, out.data_ptr(),
-        lse.data_ptr() if with_lse else None, status.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), s)
+    buf, rc = buffers, None
+    if buf is not None:
+        if with_lse and buf.lse is None:
+            raise ValueError("buffers were made without lse (AttentionBuffers(..., with_lse=True))")
+        rc = (_ext or _native()).attention(
+            q, k_cache, v_cache, block_table, context_len, row_off, scale, max_new, window,
+            buf.out, buf.lse if with_lse else None, buf.device_status, buf.workspace,
+            _handle(stream, k_cache))
+    if rc is None:
+        dev = _index("k_cache", k_cache)
+        (pages, page_size, Hkv, D), (sp, st, sh, _), dtype = _cache(k_cache, v_cache, dev)
+        if not isinstance(q, torch.Tensor) or q.get_device() != dev:
+            raise ValueError(f"q must be a CUDA tensor on cuda:{dev}")
+        if q.dtype is not k_cache.dtype:
+            raise ValueError(f"q must be {k_cache.dtype}, got {q.dtype}")
+        shape, strides = q.shape, q.stride()
+        if len(shape) != 3 or strides[2] != 1 or shape[2] != D:
+            raise ValueError(f"q must be [n_tokens, heads, {D}] with contiguous rows")
+        n, Hq, _ = shape
+        B = context_len.numel()
+        _want("context_len", context_len, _I32, dev, (B,))
+        _want("row_off", row_off, _I64, dev, (B + 1,))
+        stride, width = _table(block_table, B, dev)
+        if Hkv < 1 or Hq < 1 or Hq % Hkv != 0 or max_new < 1:
+            raise ValueError(f"{Hq} query heads on {Hkv} key heads, max_new {max_new}")
+        s = _on(stream, dev)
+        if buf is None:
+            buf = AttentionBuffers(n, Hq, Hkv, D, max_new, q.dtype, q.device, with_lse)
+            _kept(buf, stream)
+        _want("buffers.out", buf.out, q.dtype, dev, shape)
+        if with_lse:
+            _want("buffers.lse", buf.lse, torch.float32, dev, (n, Hq))
+        _want("buffers.device_status", buf.device_status, _I32, dev, (1,))
+        _want("buffers.workspace", buf.workspace, torch.uint8, dev)
+        rc = _fn("dspark_paged_attention", dev)(
+            q.data_ptr(), strides[0], strides[1], k_cache.data_ptr(), v_cache.data_ptr(), sp, st,
+            sh, page_size, pages, block_table.data_ptr(), stride, width, context_len.data_ptr(),
+            row_off.data_ptr(), B, n, Hq, Hkv, D, max_new, scale, window, dtype,
+            buf.out.data_ptr(), buf.lse.data_ptr() if with_lse else None,
+            buf.device_status.data_ptr(), buf.workspace.data_ptr(), buf.workspace.numel(), s)
     if rc != 0:
         raise DsparkError("dspark_paged_attention", rc)
     if check:
-        _checked("dspark_paged_attention", status, dev, stream)
-    return {"out": out, "lse": lse, "device_status": status}
+        _checked("dspark_paged_attention", buf.device_status, stream)
+    return {"out": buf.out, "lse": buf.lse if with_lse else None,
+            "device_status": buf.device_status}

@@ -26,10 +26,14 @@ def dev():
     return torch.device("cuda:0")
 
 
-def call(a, **kw):
+def call(a, buffers=None, **kw):
+    """With buffers of its own unless given some: the usual path of the binding."""
+    n, Hq, D = a.q.shape
+    buffers = buffers or paged.AttentionBuffers(n, Hq, a.k_cache.shape[2], D, a.max_new, a.q.dtype,
+                                                a.q.device, with_lse=True)
     return paged.dspark_paged_attention(a.q, a.k_cache, a.v_cache, a.table, a.context_len,
                                         a.row_off, scale=a.scale, max_new=a.max_new,
-                                        window=a.window, with_lse=True, **kw)
+                                        window=a.window, with_lse=True, buffers=buffers, **kw)
 
 
 def check(a, o=None, rows=None):
@@ -231,6 +235,10 @@ def test_strides_streams_and_graphs(dev):
     side = torch.cuda.Stream(dev)
     o = call(a, stream=side)
     side.synchronize()
+    assert torch.equal(o["out"], want["out"])
+    o = paged.dspark_paged_attention(a.q, a.k_cache, a.v_cache, a.table, a.context_len, a.row_off,
+                                     scale=a.scale, max_new=a.max_new, with_lse=True, stream=side)
+    side.synchronize()
     assert torch.equal(o["out"], want["out"]) and torch.equal(o["lse"], want["lse"])
     buf = paged.AttentionBuffers(5, 8, 2, 128, a.max_new, torch.bfloat16, dev, with_lse=True)
     call(a, buffers=buf)
@@ -309,6 +317,40 @@ def test_past_32_bit_offsets(dev):
     a = _paged.Attention(q, big, big, table, torch.tensor([311], dtype=torch.int32, device=dev),
                          torch.tensor([0, 3], device=dev), D ** -0.5, 3, 0)
     check(a)
+
+
+def test_binding(dev):
+    """Outputs that the call allocates itself are the ones of given buffers, and tensors that are
+    not the call's are refused on either path before anything is launched."""
+    a = _paged.make_attention([50, 300], [2, 1], 4, 2, 64, 16, torch.bfloat16, seed=1, device=dev)
+    want = call(a)
+    args = [a.q, a.k_cache, a.v_cache, a.table, a.context_len, a.row_off]
+    opts = dict(scale=a.scale, max_new=a.max_new, with_lse=True)
+    o = paged.dspark_paged_attention(*args, **opts)
+    torch.cuda.synchronize()
+    assert torch.equal(o["out"], want["out"]) and torch.equal(o["lse"], want["lse"])
+    buf = paged.AttentionBuffers(3, 4, 2, 64, 2, torch.bfloat16, dev, with_lse=True)
+    marks = buf.out.fill_(7.0)
+    bad = [(0, a.q.half()), (0, a.q.cpu()), (0, a.q[:, :3]), (0, a.q.transpose(1, 2)), (0, None),
+           (1, a.k_cache.half()), (1, a.k_cache.transpose(2, 3)), (2, a.v_cache[:-1]),
+           (2, a.v_cache.clone().transpose(1, 2).contiguous().transpose(1, 2)),
+           (3, a.table.long()), (3, a.table[:1]), (3, a.table.cpu()), (4, a.context_len[:1]),
+           (4, a.context_len.long()), (5, a.row_off[:2]), (5, a.row_off.int())]
+    for i, x in bad:
+        for given in (None, buf):
+            with pytest.raises(ValueError):
+                paged.dspark_paged_attention(*args[:i], x, *args[i + 1:], **opts, buffers=given)
+    for given in (paged.AttentionBuffers(2, 4, 2, 64, 2, torch.bfloat16, dev, with_lse=True),
+                  paged.AttentionBuffers(3, 4, 2, 64, 2, torch.float16, dev, with_lse=True),
+                  paged.AttentionBuffers(3, 4, 2, 64, 2, torch.bfloat16, dev)):
+        with pytest.raises(ValueError):
+            paged.dspark_paged_attention(*args, **opts, buffers=given)
+    for wrong in (dict(scale=0.0), dict(window=-1)):
+        for given in (None, buf):
+            with pytest.raises(paged.DsparkError):
+                paged.dspark_paged_attention(*args, **{**opts, **wrong}, buffers=given)
+    torch.cuda.synchronize()
+    assert bool((marks == 7.0).all())
 
 
 def test_nothing_to_do(dev):

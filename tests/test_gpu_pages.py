@@ -133,6 +133,54 @@ def test_reserve_bad_data(dev):
         same(run_reserve(dev, ctx, new, table, stack, n_free, 16, 500, 1), ref)
 
 
+def test_buffers_and_refusals(dev):
+    """Given buffers hold what allocated ones do; what is not the calls' is refused either way."""
+    B, tokens = 70, 3000
+    ctx, new, table, stack, count, pages, width = make(B, 16, 200, 40, 9, 1, spare=9)
+    args = [t32(ctx, dev), t32(new, dev), t32(table, dev), t32(stack, dev), t32([count], dev)]
+    opts = dict(page_size=16, max_tokens=tokens, extra=1)
+    want = paged.dspark_pages_reserve(*args, **opts)
+    buf = paged.ReserveBuffers(B, tokens, dev)
+    got = paged.dspark_pages_reserve(*args, **opts, buffers=buf)
+    torch.cuda.synchronize()
+    assert all(torch.equal(want[k], got[k]) for k in want)
+    kept = torch.zeros(B, dtype=torch.int32, device=dev)
+    rel = [args[0], want["context_len"], kept, args[2]]
+    a, b = args[3].clone(), args[3].clone()
+    want_r = paged.dspark_pages_release(*rel, a, want["free_count"], page_size=16, extra=1)
+    got_r = paged.dspark_pages_release(*rel, b, want["free_count"], page_size=16, extra=1,
+                                       buffers=paged.ReleaseBuffers(B, dev))
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and all(torch.equal(want_r[k], got_r[k]) for k in want_r)
+    for i, x in [(0, args[0].long()), (0, args[0].cpu()), (1, args[1][1:]), (2, args[2].long()),
+                 (2, args[2][:, ::2]), (2, args[2][1:]), (3, args[3].float()), (4, args[3]),
+                 (4, None)]:
+        for given in (None, buf):
+            with pytest.raises(ValueError):
+                paged.dspark_pages_reserve(*args[:i], x, *args[i + 1:], **opts, buffers=given)
+    for given in (paged.ReserveBuffers(B + 1, tokens, dev), paged.ReserveBuffers(B, 5, dev)):
+        with pytest.raises(ValueError):
+            paged.dspark_pages_reserve(*args, **opts, buffers=given)
+    with pytest.raises(ValueError):
+        paged.dspark_pages_release(*rel, a, want["free_count"], page_size=16,
+                                   buffers=paged.ReleaseBuffers(B - 1, dev))
+    for given in (None, buf):
+        with pytest.raises(paged.DsparkError):
+            paged.dspark_pages_reserve(*args, **{**opts, "page_size": 24}, buffers=given)
+    cache = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16, device=dev)
+    k = torch.ones(3, 2, 64, dtype=torch.bfloat16, device=dev)
+    slots, st = t32([1, 2, 3], dev), t32([9], dev)
+    assert paged.dspark_kv_append(k, k, slots, cache, cache, device_status=st)["device_status"] is st
+    assert int(st.item()) == 0
+    for bad in [(k.half(), k, slots, cache, cache), (k, k[:2], slots, cache, cache),
+                (k, k, slots[:2], cache, cache), (k, k, slots.long(), cache, cache),
+                (k, k, slots, cache, cache[:3]), (k[:, :1], k[:, :1], slots, cache, cache),
+                (k, None, slots, cache, cache), (k.cpu(), k.cpu(), slots, cache, cache)]:
+        for given in (None, st):
+            with pytest.raises(ValueError):
+                paged.dspark_kv_append(*bad, device_status=given)
+
+
 @pytest.mark.parametrize("B", [3, 1500])
 def test_in_place_lengths(dev, B):
     """context_out over context_len and the count over itself: the outputs of separate buffers."""
