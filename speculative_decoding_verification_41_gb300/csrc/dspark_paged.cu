@@ -174,19 +174,28 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_pages_reserve(const Reserv
         bad |= static_cast<uint32_t>(p) >= static_cast<uint32_t>(a.num_pages);
       }
     }
+    // new pages, a block of them per CTA in turn (a small call's all in CTA 0)
+    for (uint32_t i = blockIdx.x * kPagedThreads + tid; i < all.page;
+         i += gridDim.x * kPagedThreads) {
+      const int q = first_above(s_page, n_req, i);
+      const uint32_t before = q > 0 ? s_page[q - 1] : 0u;
+      const uint32_t have = (static_cast<uint32_t>(s_ctx[q]) + mask) >> a.shift;
+      a.table[static_cast<int64_t>(base + q) * a.stride + have + (i - before)] =
+          a.stack[avail - 1u - (carry.page + i)];
+    }
     // Rows of this step's requests in the CTA's range: one per thread where that
     // does for all (a decoding step: one chain of search, page id, store), else
-    // four in a row, which share a search and are stored together (prompts: 9.1 us
-    // against 12.9 for 2 M rows; a step of 64 requests 3.1 against 4.2).
+    // four in a row, which share a search and are stored together (2 M rows: 12.9 us
+    // one by one; a step of 64 requests: 3.1 us one by one, 4.2 in fours).
     const uint32_t lo = max(t0, carry.tok), hi = min(t1, carry.tok + all.tok);
-    // page id and position of row x of this step, in request q
-    auto page_of = [&](uint32_t x, int q, uint32_t& p) {
+    // where the page id of row x of this step is, x in request q, and its position
+    auto page_of = [&](uint32_t x, int q, uint32_t& p) -> const int32_t* {
       const uint32_t c = static_cast<uint32_t>(s_ctx[q]);
       p = c + (x - (q > 0 ? s_tok[q - 1] : 0u));
       const uint32_t have = (c + mask) >> a.shift, blk = p >> a.shift;
-      return blk < have ? a.table[static_cast<int64_t>(base + q) * a.stride + blk]
-                        : a.stack[avail - 1u - (carry.page + (q > 0 ? s_page[q - 1] : 0u) +
-                                                (blk - have))];
+      return blk < have ? a.table + static_cast<int64_t>(base + q) * a.stride + blk
+                        : a.stack + (avail - 1u - (carry.page + (q > 0 ? s_page[q - 1] : 0u) +
+                                                   (blk - have)));
     };
     auto slot_of = [&](int32_t page, uint32_t p) {
       return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages)
@@ -197,27 +206,30 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_pages_reserve(const Reserv
       const uint32_t t = t0 + tid;
       if (t >= lo && t < hi) {
         uint32_t p;
-        const int32_t page = page_of(t - carry.tok, first_above(s_tok, n_req, t - carry.tok), p);
+        const int32_t page = *page_of(t - carry.tok, first_above(s_tok, n_req, t - carry.tok), p);
         a.slots[t] = slot_of(page, p);
         if (a.pos) a.pos[t] = static_cast<int32_t>(p);
       }
     } else {
       for (uint32_t g = (lo & ~3u) + 4u * tid; g < hi; g += 4u * kPagedThreads) {
-        int32_t slot[4];
+        int32_t slot[4], page[4];
         uint32_t pos[4];
+        const int32_t* from[4];
         int q = -1;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t t = g + k;
-          if (t < lo || t >= hi) continue;
-          const uint32_t x = t - carry.tok;
+          const uint32_t t = min(max(g + k, lo), hi - 1u), x = t - carry.tok;
           if (q < 0)
             q = first_above(s_tok, n_req, x);
           else
             while (s_tok[q] <= x) ++q;
-          const int32_t page = page_of(x, q, pos[k]);
-          slot[k] = slot_of(page, pos[k]);
+          from[k] = page_of(x, q, pos[k]);
         }
+        // mostly one page, and one trip to the cache
+#pragma unroll
+        for (int k = 0; k < 4; ++k) page[k] = *from[k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) slot[k] = slot_of(page[k], pos[k]);
         if (a.vec && g >= lo && g + 4u <= hi) {
           *reinterpret_cast<int4*>(a.slots + g) = make_int4(slot[0], slot[1], slot[2], slot[3]);
           if (a.pos)
@@ -231,15 +243,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) k_pages_reserve(const Reserv
             }
         }
       }
-    }
-    // new pages, a block of them per CTA in turn (a small call's all in CTA 0)
-    for (uint32_t i = blockIdx.x * kPagedThreads + tid; i < all.page;
-         i += gridDim.x * kPagedThreads) {
-      const int q = first_above(s_page, n_req, i);
-      const uint32_t before = q > 0 ? s_page[q - 1] : 0u;
-      const uint32_t have = (static_cast<uint32_t>(s_ctx[q]) + mask) >> a.shift;
-      a.table[static_cast<int64_t>(base + q) * a.stride + have + (i - before)] =
-          a.stack[avail - 1u - (carry.page + i)];
     }
     carry = add(carry, all);
     if (base + kPagedThreads < a.B) __syncthreads();  // the step's sums are read no more
