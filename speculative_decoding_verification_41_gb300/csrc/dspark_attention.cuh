@@ -14,14 +14,15 @@
 // walks the rows: its weights P land in shared memory as 16-byte stores.
 //
 // The reference m of a row need not be its running maximum: any m with 2^(c s - m)
-// in range for every score s serves, and one that some score reaches keeps the
-// largest weight at 1 or more. A tile whose scores exceed their rows' references
-// by less than kSlack (log2) is used as it is: that is one vote per tile instead
-// of a maximum over 128 tokens for every row. A row starts with its maximum over
-// the first tile (a score of one token would do for the range of bf16, and costs
-// as much, but leaves the largest weight a rounding that a weight of 1 has not:
-// 1.5 times the output's own rounding error in all, against 1.1 to 1.3). When a
-// vote fails, the maxima are taken, m raised and O and l scaled.
+// in range for every score s serves, and one that lies a whole number of powers of
+// two from some score keeps that score's weight free of rounding. A tile whose
+// scores exceed their rows' references by no more than kHighest (log2) is used as
+// it is: that is one vote per tile instead of a maximum over 128 tokens for every
+// row. A row starts with its maximum over the first tile (a score of one token
+// would do for the range of bf16, and costs as much, but leaves the largest weight
+// a rounding that a power of two has not: 1.5 times the output's own rounding error
+// in all, against 1.1 to 1.3). When a vote fails, the maxima are taken, m raised
+// and O and l scaled.
 //
 // Bound. Every cached key and value is read once: 4 D bytes per token and key
 // head against 4 D R flops, so up to R of about 280 the copy rate of HBM bounds
@@ -40,6 +41,7 @@
 // and of the weights before are under way.
 #pragma once
 
+#include <cfloat>
 #include <climits>
 
 #include "../../include/dspark_paged.h"
@@ -49,15 +51,34 @@ namespace dspark {
 
 constexpr int kTileTok = 128;
 constexpr float kNoRef = 1e38f;  // minus the reference of a row that has seen no token yet
-// How far (log2) a score may exceed its row's reference.
+// Exponents (log2) of a row's weights: the largest one when its reference is set
+// (kBase), and the largest before it is raised (kHighest). Half precision ends at
+// 2^16 and has its full 11 bits down to 2^-14, so its weights use the upper end: with a
+// largest weight of 1 a row with one token 17 nats above 2,000 others lost 3% of
+// their sum in the second product and none of it in l. Seven powers of two of room
+// seldom need a raise (136 rows, scores of 2 nats' deviation: 1% of the time, against
+// 13% with four), and weights down to 2^-23 of the largest keep their bits. A row with a peak, a tile's maximum far
+// above one of its four quarters' (kPeak), is the one that needs more, and the one
+// whose maximum is not likely to grow: its weights keep theirs down to 2^-28.
 template <bool F16>
-constexpr float kSlack = F16 ? 14.f : 60.f;
+constexpr float kBase = F16 ? 9.f : 0.f;
+template <bool F16>
+constexpr float kPeakBase = F16 ? 14.f : 0.f;
+constexpr float kPeak = 8.f;
+template <bool F16>
+constexpr float kHighest = F16 ? 15.9f : 60.f;
 // Rows of few, with many tiles to come, take every new maximum: a largest weight
-// of exactly 1 has no rounding, and the output is off by 1.1 to 1.2 times its own
-// rounding (1.3 to 1.45 with the slack). New maxima grow rare along a context, and
-// a block of up to 16 rows waits for memory anyway; short pieces and wider blocks
-// would pay (measured: a tenth for 9 tiles, 3% for 32 rows, a fifth for 64).
+// that is a power of two has no rounding, and the output is off by 1.1 to 1.2 times
+// its own rounding (1.3 to 1.45 with the room above). New maxima grow rare along a
+// context, and a block of up to 16 rows waits for memory anyway; short pieces and
+// wider blocks would pay (measured: a tenth for 9 tiles, 3% for 32 rows, a fifth
+// for 64).
 constexpr int kExactRows = 16, kExactTiles = 16;
+template <bool F16>
+constexpr float kExactBase = F16 ? 15.f : 0.f;
+// A maximum of this size or more is the reference itself: its product with c is
+// rounded to a 64th or less finely, and the room above kBase has to hold that too.
+constexpr float kNoShift = 262144.f;
 
 struct AttnArgs {
   const int32_t* table;
@@ -309,6 +330,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// m + log2(sum): the sum's exponent joins m, whose opposite it nearly is where the
+// reference lies far from the row's largest score.
+__device__ __forceinline__ float plus_log2(float m, float sum) {
+  const uint32_t bits = __float_as_uint(sum);
+  const int e = static_cast<int>(bits >> 23) - 127;
+  if (!(sum >= FLT_MIN && sum <= FLT_MAX)) return m + log2f(sum);
+  return (m + static_cast<float>(e)) + log2f(__uint_as_float(bits - (static_cast<uint32_t>(e) << 23)));
 }
 template <bool F16>
 __device__ __forceinline__ float half_to_float(uint32_t bits16) {
@@ -838,7 +867,10 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         for (int b = 0; b < kBlocks; ++b) lf[b] = 0.f;
       }
 
-      const float slack = S::NB <= kExactRows && it.tiles >= kExactTiles ? 0.f : kSlack<F16>;
+      const bool exact = S::NB <= kExactRows && it.tiles >= kExactTiles;
+      const float base = exact ? kExactBase<F16> : kBase<F16>;
+      const float peak_base = exact ? kExactBase<F16> : kPeakBase<F16>;
+      const float highest = exact ? kExactBase<F16> : kHighest<F16>;
       bool leave = false;
       for (int i = 0; i < it.tiles; ++i, ++tiles) {
         const uint32_t buf = tiles & 1u;
@@ -899,7 +931,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
               top = fmaxf(top, fmaxf(y0, y1));
             }
           });
-          raise = bar_any(bar, 128, top > slack || failed);
+          raise = bar_any(bar, 128, top > highest || failed);
         }
         if (raise) {
           each([&](int b) {
@@ -915,11 +947,17 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             break;
           }
           for (int j = c0 + gt; j < c0 + my_rows; j += 128) {
-            const float m = a.c * fmaxf(fmaxf(ctl.red[0][j], ctl.red[1][j]),
-                                        fmaxf(ctl.red[2][j], ctl.red[3][j]));
-            const float old = -nref[j];
-            ctl.fac[j] = m > old ? ex2_approx(old - m) : 1.f;
-            if (m > old) nref[j] = -m;
+            float top = -INFINITY, low = INFINITY;  // of the quarters that hold a token
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float v = ctl.red[w][j];
+              top = fmaxf(top, v);
+              if (v > -INFINITY) low = fminf(low, v);
+            }
+            const float m = a.c * top, down = a.c * (top - low) > kPeak ? peak_base : base;
+            const float ref = fabsf(m) < kNoShift ? m - down : m, old = -nref[j];
+            ctl.fac[j] = ref > old ? ex2_approx(old - ref) : 1.f;
+            if (ref > old) nref[j] = -ref;
           }
           bar_sync(bar, 128);
           if (i > 0) {
@@ -1060,7 +1098,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
               reinterpret_cast<float2*>(a.part_ml)[part_row + j] = make_float2(m, sum);
             else if (a.lse)
               a.lse[it.row0 * a.Hq + it.head0 + ctl.at[j] / S::D] =
-                  seen ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+                  seen ? plus_log2(m, sum) * 0.69314718055994531f : -INFINITY;
           }
         }
       }
@@ -1294,7 +1332,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attention_join(const JoinAr
 #pragma unroll
     for (int v = 0; v < V; v += 2)
       out[v / 2] = seen ? pack2<F16>(acc[v] * inv, acc[v + 1] * inv) : 0u;
-    if (a.lse && lane == 0) a.lse[at] = seen ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    if (a.lse && lane == 0) a.lse[at] = seen ? plus_log2(top, sum) * 0.69314718055994531f : -INFINITY;
   }
 }
 
