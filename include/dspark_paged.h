@@ -178,8 +178,9 @@ int dspark_kv_append(const void* k, const void* v, int64_t row_stride, int64_t i
  * Products of 16-bit inputs are accumulated in binary32 on the tensor cores;
  * the maximum, the sum and the output are binary32; the weights e^{s - m} are
  * rounded to the inputs' type for the second product (their sum is not). m is near
- * the row's largest score; for half precision some nats below it, so that weights
- * keep their bits down to e^-16 of the largest (where scale * |s| is below 2^17). The
+ * the row's largest score: for half precision some nats below it, so that weights
+ * keep their bits down to e^-16 of the largest (where scale * |s| is below 2^17);
+ * for bf16 at or above it, so that no weight exceeds 1. The
  * output is rounded once. Results depend on the inputs alone, not on timing.
  *
  * Arguments

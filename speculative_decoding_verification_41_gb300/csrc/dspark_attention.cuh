@@ -57,19 +57,22 @@ constexpr float kNoRef = 1e38f;  // minus the reference of a row that has seen n
 // largest weight of 1 a row with one token 17 nats above 2,000 others lost 3% of
 // their sum in the second product and none of it in l. Seven powers of two of room
 // seldom need a raise (136 rows, scores of 2 nats' deviation: 1% of the time, against
-// 13% with four), and weights down to 2^-23 of the largest keep their bits. A row with a peak, a tile's maximum far
-// above one of its four quarters' (kPeak), is the one that needs more, and the one
-// whose maximum is not likely to grow: its weights keep theirs down to 2^-28.
+// 13% with four), and weights down to 2^-23 of the largest keep their bits. A row
+// with a peak, a tile's maximum far above one of its four quarters' (kPeak), is the
+// one that needs more, and the one whose maximum is not likely to grow: its weights
+// keep theirs down to 2^-28. bf16 has the range of binary32, which the sums of
+// weights times values must not leave where the values themselves are near its end:
+// no weight exceeds 1, and the room lies below.
 template <bool F16>
-constexpr float kBase = F16 ? 9.f : 0.f;
+constexpr float kBase = F16 ? 9.f : -8.f;
 template <bool F16>
-constexpr float kPeakBase = F16 ? 14.f : 0.f;
+constexpr float kPeakBase = F16 ? 14.f : -8.f;
 constexpr float kPeak = 8.f;
 template <bool F16>
-constexpr float kHighest = F16 ? 15.9f : 60.f;
+constexpr float kHighest = F16 ? 15.9f : 0.f;
 // Rows of few, with many tiles to come, take every new maximum: a largest weight
 // that is a power of two has no rounding, and the output is off by 1.1 to 1.2 times
-// its own rounding (1.3 to 1.45 with the room above). New maxima grow rare along a
+// its own rounding (1.25 to 1.4 with the room above). New maxima grow rare along a
 // context, and a block of up to 16 rows waits for memory anyway; short pieces and
 // wider blocks would pay (measured: a tenth for 9 tiles, 3% for 32 rows, a fifth
 // for 64).

@@ -126,3 +126,23 @@ def test_peaks_everywhere_in_a_tile(dev, dtype, G, T, L, first, drop):
     off = np.abs(got - want)
     assert (off <= tol).all(), f"off by {(off / tol).max():.2f} of the bound"
     assert (np.abs(got_lse - lse) <= lse_tol).all()
+
+
+@pytest.mark.parametrize("G,T", BLOCKS)
+@pytest.mark.parametrize("L,rise", [(700, 40.0), (2300, 40.0), (2300, 9.0)])
+def test_values_near_the_end_of_the_range(dev, G, T, L, rise):
+    """bf16 values of 2^110 and scores that rise along the context (from nothing to `rise` nats past
+    the first half): every partial sum in the formula's order of magnitude is in binary32's range."""
+    D = 128
+    g = torch.Generator().manual_seed(L)
+    q, k = torch.randn(T, G, D, generator=g) * 0.1, torch.randn(L, 1, D, generator=g)
+    q[:, :, 0], k[:, :, 0] = 1.0, 0.0
+    k[L // 2:, :, 0] = rise * D ** 0.5
+    v = (torch.randn(L, 1, D, generator=g) * 0.25 + 1.0) * 2.0 ** 110
+    q, k, v = (x.to(torch.bfloat16) for x in (q, k, v))
+    want, lse, tol, lse_tol = exact(q, k, v, D ** -0.5, 0.0)
+    got, got_lse = attend(dev, q, k, v, 320, 16, D ** -0.5)
+    assert np.isfinite(got).all()
+    off = np.abs(got - want)
+    assert (off <= tol).all(), f"off by {(off / tol).max():.2f} of the bound"
+    assert (np.abs(got_lse - lse) <= lse_tol).all()
