@@ -149,6 +149,22 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def made_on(stream, make):
+    """make(), which allocates tensors (one, or an object's), for a call on `stream` (None: the
+    current one). They are allocated there, so that nothing queued elsewhere writes them after the
+    call has (their own zeroing, or work on memory that was theirs before), and stay allocated
+    until the current stream, where they are likely to be read, has come past their release."""
+    if stream is None:
+        return make()
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        made = make()
+    for t in [made] if isinstance(made, torch.Tensor) else vars(made).values():
+        if isinstance(t, torch.Tensor):
+            t.record_stream(caller)
+    return made
+
+
 def _require_cuda(name: str, t: torch.Tensor, dtype=None, device=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libdspark has no CPU path)")

@@ -23,7 +23,7 @@ from typing import Optional
 import torch
 
 from . import binding
-from .binding import DSPARK_BF16, DsparkError
+from .binding import DSPARK_BF16, DsparkError, made_on
 
 HEADER = os.path.join(binding.ROOT, "include", "dspark_paged.h")
 EXPORTED = ("dspark_pages_reserve", "dspark_pages_release", "dspark_kv_append",
@@ -167,14 +167,6 @@ def _handle(stream, t):
     return _on(stream, t.get_device() if isinstance(t, torch.Tensor) else -1)
 
 
-def _kept(buffers, stream):
-    """Memory that the call allocated stays the stream's until its work is done."""
-    if stream is not None:
-        for t in vars(buffers).values():
-            if isinstance(t, torch.Tensor):
-                t.record_stream(stream)
-
-
 def _fn(name: str, index: int):
     """The library's function, called on the tensors' device."""
     fn = (_fns or _load())[name]
@@ -240,8 +232,7 @@ def dspark_pages_reserve(context_len: torch.Tensor, new_len: torch.Tensor,
         _want("free_count", free_count, _I32, dev, (1,))
         s = _on(stream, dev)
         if buf is None:
-            buf = ReserveBuffers(B, max_tokens, context_len.device)
-            _kept(buf, stream)
+            buf = made_on(stream, lambda: ReserveBuffers(B, max_tokens, context_len.device))
         for name, dtype, n in (("context_len", _I32, B), ("row_off", _I64, B + 1),
                                ("draft_off", _I64, B + 1), ("slot_map", _I32, max_tokens),
                                ("positions", _I32, max_tokens), ("free_count", _I32, 1),
@@ -300,8 +291,7 @@ def dspark_pages_release(context_len: torch.Tensor, reserved_len: torch.Tensor,
         _want("free_count", free_count, _I32, dev, (1,))
         s = _on(stream, dev)
         if buf is None:
-            buf = ReleaseBuffers(B, context_len.device)
-            _kept(buf, stream)
+            buf = made_on(stream, lambda: ReleaseBuffers(B, context_len.device))
         for name, n in (("context_len", B), ("free_count", 1), ("device_status", 1)):
             _want(f"buffers.{name}", getattr(buf, name), _I32, dev, (n,))
         rc = _fn("dspark_pages_release", dev)(
@@ -348,9 +338,8 @@ def dspark_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
             raise ValueError(f"slot_map has {slot_map.numel()} entries for {n} rows")
         s = _on(stream, dev)
         if device_status is None:
-            device_status = torch.empty(1, dtype=_I32, device=k_cache.device)
-            if stream is not None:
-                device_status.record_stream(stream)
+            device_status = made_on(
+                stream, lambda: torch.empty(1, dtype=_I32, device=k_cache.device))
         else:
             _want("device_status", device_status, _I32, dev, (1,))
         rc = _fn("dspark_kv_append", dev)(
@@ -418,8 +407,8 @@ def dspark_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
             raise ValueError(f"{Hq} query heads on {Hkv} key heads, max_new {max_new}")
         s = _on(stream, dev)
         if buf is None:
-            buf = AttentionBuffers(n, Hq, Hkv, D, max_new, q.dtype, q.device, with_lse)
-            _kept(buf, stream)
+            buf = made_on(stream, lambda: AttentionBuffers(n, Hq, Hkv, D, max_new, q.dtype,
+                                                           q.device, with_lse))
         _want("buffers.out", buf.out, q.dtype, dev, shape)
         if with_lse:
             _want("buffers.lse", buf.lse, torch.float32, dev, (n, Hq))
