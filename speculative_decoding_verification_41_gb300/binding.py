@@ -238,7 +238,8 @@ def dspark_verify(target_logits: torch.Tensor, draft_logits: torch.Tensor,
         raise ValueError("uniforms must be [B, gamma+1] and verify_len [B]")
     if with_rates and events is not None:
         raise ValueError("with_rates and events are separate entry points")
-    buf = buffers or VerifyBuffers(B, gamma, V, dev, with_probs, with_rates)
+    buf = buffers or made_on(stream, lambda: VerifyBuffers(B, gamma, V, dev, with_probs,
+                                                           with_rates))
     if (buf.B, buf.gamma, buf.V) != (B, gamma, V):
         raise ValueError("buffers were made for another shape")
     if with_rates and buf.rates is None:
@@ -308,11 +309,12 @@ def dspark_acceptance(target_logits: torch.Tensor, draft_logits: torch.Tensor,
         _require_cuda("draft_row_off", draft_row_off, torch.int64, dev)
     B = verify_len.shape[0]
     V = target_logits.shape[-1]
-    out = rates if rates is not None else torch.empty(B, gamma, dtype=torch.float32, device=dev)
-    ws_bytes = acceptance_workspace_bytes(B, gamma, V)
-    ws = workspace if workspace is not None else torch.empty(ws_bytes, dtype=torch.uint8,
-                                                             device=dev)
-    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    out = rates if rates is not None else made_on(
+        stream, lambda: torch.empty(B, gamma, dtype=torch.float32, device=dev))
+    ws = workspace if workspace is not None else made_on(
+        stream, lambda: torch.empty(acceptance_workspace_bytes(B, gamma, V), dtype=torch.uint8,
+                                    device=dev))
+    status = made_on(stream, lambda: torch.zeros(1, dtype=torch.int32, device=dev))
     lib = load()
     with torch.cuda.device(dev):
         rc = lib.dspark_acceptance(_ptr(target_logits), _ptr(draft_logits), _ptr(verify_len),
@@ -350,7 +352,7 @@ def dspark_schedule(confidences: torch.Tensor, step_time_ms: torch.Tensor, *,
     _require_cuda("confidences", confidences, torch.float32)
     _require_cuda("step_time_ms", step_time_ms, torch.float64, dev)
     R, gamma = confidences.shape
-    buf = buffers or ScheduleBuffers(R, gamma, dev)
+    buf = buffers or made_on(stream, lambda: ScheduleBuffers(R, gamma, dev))
     lib = load()
     with torch.cuda.device(dev):
         rc = lib.dspark_schedule(_ptr(confidences), _ptr(step_time_ms), step_time_ms.numel(), R,
@@ -383,7 +385,7 @@ def dspark_schedule_capacity(confidences: torch.Tensor, step_time_ms: torch.Tens
     _require_cuda("confidences", confidences, torch.float32)
     _require_cuda("step_time_ms", step_time_ms, torch.float64, dev)
     R, gamma = confidences.shape
-    buf = buffers or ScheduleBuffers(R, gamma, dev)
+    buf = buffers or made_on(stream, lambda: ScheduleBuffers(R, gamma, dev))
     lib = load()
     with torch.cuda.device(dev):
         rc = lib.dspark_schedule_capacity(
@@ -406,7 +408,7 @@ def dspark_schedule_topk(confidences: torch.Tensor, capacity: torch.Tensor, *,
     _require_cuda("confidences", confidences, torch.float32)
     _require_cuda("capacity", capacity, torch.int32, dev)
     R, gamma = confidences.shape
-    buf = buffers or ScheduleBuffers(R, gamma, dev)
+    buf = buffers or made_on(stream, lambda: ScheduleBuffers(R, gamma, dev))
     lib = load()
     with torch.cuda.device(dev):
         rc = lib.dspark_schedule_topk(_ptr(confidences), _ptr(capacity), R, gamma,
@@ -428,9 +430,10 @@ def dspark_schedule_threshold(confidences: torch.Tensor, threshold: float, *,
     dev = confidences.device
     _require_cuda("confidences", confidences, torch.float32)
     R, gamma = confidences.shape
-    ell = verify_len if verify_len is not None else torch.empty(R, dtype=torch.int32, device=dev)
-    st = device_status if device_status is not None else torch.zeros(1, dtype=torch.int32,
-                                                                      device=dev)
+    ell = verify_len if verify_len is not None else made_on(
+        stream, lambda: torch.empty(R, dtype=torch.int32, device=dev))
+    st = device_status if device_status is not None else made_on(
+        stream, lambda: torch.zeros(1, dtype=torch.int32, device=dev))
     lib = load()
     with torch.cuda.device(dev):
         rc = lib.dspark_schedule_threshold(_ptr(confidences), float(threshold), R, gamma,
@@ -473,15 +476,17 @@ def dspark_draft_markov(base_logits: torch.Tensor, w1: torch.Tensor, w2t: torch.
     r = w1.shape[1]
     if anchors.shape != (B,) or uniforms.shape != (B, gamma):
         raise ValueError("anchors must be [B] and uniforms [B, gamma]")
-    out = draft_logits if draft_logits is not None else torch.empty_like(base_logits)
+    out = draft_logits if draft_logits is not None else made_on(
+        stream, lambda: torch.empty_like(base_logits))
     _require_cuda("draft_logits", out, torch.bfloat16, dev)
     if out.shape != base_logits.shape:
         raise ValueError("draft_logits must be [B, gamma, V]")
-    tok = draft_tokens if draft_tokens is not None else torch.empty(B, gamma, dtype=torch.int32,
-                                                                     device=dev)
-    ws = workspace if workspace is not None else torch.empty(
-        max(draft_workspace_bytes(B, r, V), 256), dtype=torch.uint8, device=dev)
-    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    tok = draft_tokens if draft_tokens is not None else made_on(
+        stream, lambda: torch.empty(B, gamma, dtype=torch.int32, device=dev))
+    ws = workspace if workspace is not None else made_on(
+        stream, lambda: torch.empty(max(draft_workspace_bytes(B, r, V), 256), dtype=torch.uint8,
+                                    device=dev))
+    status = made_on(stream, lambda: torch.zeros(1, dtype=torch.int32, device=dev))
     lib = load()
     args = (_ptr(base_logits), _ptr(w1), _ptr(w2t), _ptr(anchors), _ptr(uniforms),
             float(temperature), B, gamma, V, r, _ptr(out), _ptr(tok), _ptr(status), _ptr(ws),
@@ -514,8 +519,8 @@ def wait_selftest(which: int, device="cuda", stream=None) -> dict:
     completes. Returns the device status it left (DSPARK_ERR_TIMEOUT expected)
     and the seconds the call took on the device."""
     dev = torch.device(device)
-    status = torch.zeros(1, dtype=torch.int32, device=dev)
-    sync = torch.zeros(2, dtype=torch.int32, device=dev)
+    status = made_on(stream, lambda: torch.zeros(1, dtype=torch.int32, device=dev))
+    sync = made_on(stream, lambda: torch.zeros(2, dtype=torch.int32, device=dev))
     lib = load()
     with torch.cuda.device(dev):
         st = stream if stream is not None else torch.cuda.current_stream(dev)

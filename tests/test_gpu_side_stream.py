@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from speculative_decoding_verification_41_gb300 import build as cuda_build
-from speculative_decoding_verification_41_gb300 import paged
+from speculative_decoding_verification_41_gb300 import binding, paged, workloads
 from tests import _paged
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +87,54 @@ def test_paged_outputs_survive(dev):
     torch.cuda.synchronize()
     o = behind(dev, call, [4 * B, 8 * B + 8, 8 * B + 8, 3600, 3600, 4, 4])
     assert all(torch.equal(o[k], want[k]) for k in want)
+
+
+def test_the_method_s_calls(dev):
+    """The verification, its rates, the scheduler's calls and the drafter: on sound inputs the
+    outputs of the same call on the current stream, on bad ones its status."""
+    t = workloads.make_tiny(dev)
+    bad_len = t.verify_len.clone()
+    bad_len[1] = t.gamma + 3
+    conf = torch.from_numpy(workloads.make_confidences(8, 4, seed=3)).to(dev)
+    bad_conf = conf.clone()
+    bad_conf[2, 1] = float("nan")
+    T = torch.from_numpy(workloads.step_time_profile(8 * 5 + 1, base_ms=1.0, slope_ms=0.05)).to(dev)
+    d = workloads.make_markov_draft(3, 4, 1000, 64, temperature=0.7, seed=1, device=dev)
+    bad_anchors = d.anchors.clone()
+    bad_anchors[0] = -1
+    K = torch.tensor([9], dtype=torch.int32, device=dev)
+
+    def verify(ell):
+        return lambda s: binding.dspark_verify(t.target_logits, t.draft_logits, t.draft_tokens,
+                                               ell, t.uniforms, t.temperature, stream=s)
+
+    def rates(ell):
+        return lambda s: binding.dspark_acceptance(t.target_logits, t.draft_logits, ell,
+                                                   t.temperature, t.gamma, stream=s)
+
+    def draft(anchors):
+        return lambda s: binding.dspark_draft_markov(d.base_logits, d.w1, d.w2t, anchors,
+                                                     d.uniforms, d.temperature, stream=s)
+
+    pairs = [(verify(t.verify_len), verify(bad_len)), (rates(t.verify_len), rates(bad_len)),
+             (draft(d.anchors), draft(bad_anchors))]
+    pairs += [(lambda s, c=c: c(conf, s), lambda s, c=c: c(bad_conf, s)) for c in (
+        lambda x, s: binding.dspark_schedule(x, T, stream=s),
+        lambda x, s: binding.dspark_schedule_capacity(x, T, stream=s),
+        lambda x, s: binding.dspark_schedule_topk(x, K, stream=s),
+        lambda x, s: binding.dspark_schedule_threshold(x, 0.5, stream=s))]
+    sizes = [512] * 8 + [binding.verify_workspace_bytes(t.B, t.gamma, 32),
+                         binding.acceptance_workspace_bytes(t.B, t.gamma, 32),
+                         binding.draft_workspace_bytes(3, 64, 1000), 24000]
+    written = {"accepted_len", "emitted_tokens", "probs", "rates", "draft_logits", "draft_tokens",
+               "verify_len"}
+    for good, bad in pairs:
+        want = good(None)
+        torch.cuda.synchronize()
+        o = behind(dev, good, sizes)
+        assert int(o["device_status"].item()) == 0
+        assert any(k in written for k in o)
+        assert all(torch.equal(o[k], want[k]) for k in o if k in written)
+        want = int(bad(None)["device_status"].item())
+        assert want != 0
+        assert int(behind(dev, bad, sizes)["device_status"].item()) == want
