@@ -105,11 +105,19 @@ def speculative_step(cache: PagedCache, target: ToyTarget, anchors: torch.Tensor
                      verify_len: torch.Tensor, uniforms: torch.Tensor, temperature: float) -> dict:
     """One target pass over each request's anchor and its first verify_len[r] drafts, the
     verification, and the roll back. draft_tokens [B, gamma], draft_logits [B, gamma, V].
-    Returns dspark_verify's outputs; the next anchors are emitted_tokens at accepted_len."""
+
+    Returns dspark_verify's outputs, and
+      served [B] bool: which requests got rows. The others (out of pages or of room in their
+        block table, reserve_status says why) are as they were before the step: their anchor is
+        still to be run, their accepted_len is 0, their emitted_tokens are -1, and device_status is
+        DSPARK_ERR_BAD_DATA because of them;
+      next_anchors [B]: emitted_tokens at accepted_len, the same anchor where not served;
+      reserve_status [1]: dspark_pages_reserve's status."""
     B, gamma = draft_tokens.shape
     dev = anchors.device
     rows = cache.reserve(verify_len)
     row_off = rows["row_off"]
+    served = row_off[1:] > row_off[:-1]
     # the token of every row: position 0 of a request is its anchor
     i = torch.arange(B * cache.max_new, device=dev)
     r = torch.searchsorted(row_off[1:], i, right=True).clamp(max=B - 1)
@@ -122,7 +130,9 @@ def speculative_step(cache: PagedCache, target: ToyTarget, anchors: torch.Tensor
         logits, draft_logits.reshape(B * gamma, -1), draft_tokens, verify_len, uniforms,
         temperature, row_off, torch.arange(B + 1, device=dev, dtype=torch.int64) * gamma)
     cache.release(out["accepted_len"])
-    return out
+    last = out["emitted_tokens"].gather(1, out["accepted_len"].long()[:, None])[:, 0]
+    return {**out, "served": served, "next_anchors": torch.where(served, last, anchors),
+            "reserve_status": rows["device_status"].clone()}
 
 
 def demo(B: int = 32, gamma: int = 4, V: int = 4096, steps: int = 8, device="cuda") -> dict:
@@ -145,9 +155,8 @@ def demo(B: int = 32, gamma: int = 4, V: int = 4096, steps: int = 8, device="cud
         out = speculative_step(cache, target, anchors, draft["draft_tokens"],
                                draft["draft_logits"], ell,
                                torch.rand(B, gamma + 1, generator=g, device=dev), 1.0)
-        m = out["accepted_len"].long()
-        anchors = out["emitted_tokens"].gather(1, m[:, None])[:, 0].contiguous()
-        emitted += int(m.sum().item()) + B
+        anchors = out["next_anchors"]
+        emitted += int((out["accepted_len"].long() + out["served"]).sum().item())
     held = int(((cache.context_len + 15) // 16).sum().item())
     return {"tokens": emitted, "cached": int(cache.context_len.sum().item()),
             "pages_held": held, "pages_free": int(cache.free_count.item()),
