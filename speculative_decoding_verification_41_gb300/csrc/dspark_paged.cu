@@ -20,7 +20,9 @@ namespace {
 
 constexpr int kPagedThreads = 1024;         // requests per step of the sums
 constexpr int kPagedWarps = kPagedThreads / 32;
-constexpr uint32_t kCap = 1u << 30;          // sums saturate here: above every limit they meet
+// Sums saturate here, above every limit they meet (max_tokens may be 2^30); two of
+// them still add within 32 bits.
+constexpr uint32_t kCap = (1u << 30) + 1u;
 constexpr int kTokensPerCta = 1024;          // slot-map rows per filling CTA, at least
 
 struct Sum3 {
