@@ -25,10 +25,14 @@ decltype(&dspark_paged_attention) g_attention;
 const at::Tensor* tensor(PyObject* o) {
   return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr;
 }
-// a contiguous tensor of this type on CUDA device `dev` (numel < 0: any size)
-bool plain(const at::Tensor* t, at::ScalarType type, int dev, int64_t numel = -1) {
+// a contiguous tensor of this type on CUDA device `dev`
+bool plain(const at::Tensor* t, at::ScalarType type, int dev) {
   return t && t->scalar_type() == type && t->is_cuda() && t->get_device() == dev &&
-         t->is_contiguous() && (numel < 0 || t->numel() == numel);
+         t->is_contiguous();
+}
+// ... of this shape
+bool plain(const at::Tensor* t, at::ScalarType type, int dev, at::IntArrayRef shape) {
+  return plain(t, type, dev) && t->sizes() == shape;
 }
 template <typename T>
 T* data(const at::Tensor* t) {
@@ -116,7 +120,7 @@ PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CUstream_st* s;
   REFUSE_UNLESS(B <= INT32_MAX && small(a[5], page_size) && small(a[6], max_tokens) &&
                 small(a[7], extra) && max_tokens >= 0);
-  REFUSE_UNLESS(plain(t[0], at::kInt, dev) && plain(t[1], at::kInt, dev, B) &&
+  REFUSE_UNLESS(plain(t[0], at::kInt, dev, B) && plain(t[1], at::kInt, dev, B) &&
                 table(t[2], dev, B, stride, width) && plain(t[3], at::kInt, dev) &&
                 t[3]->numel() <= INT32_MAX && plain(t[4], at::kInt, dev, 1) &&
                 plain(t[8], at::kInt, dev, B) && plain(t[9], at::kLong, dev, B + 1) &&
@@ -144,7 +148,7 @@ PyObject* release(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t stride;
   CUstream_st* s;
   REFUSE_UNLESS(B <= INT32_MAX && small(a[6], page_size) && small(a[7], extra));
-  REFUSE_UNLESS(plain(t[0], at::kInt, dev) && plain(t[1], at::kInt, dev, B) &&
+  REFUSE_UNLESS(plain(t[0], at::kInt, dev, B) && plain(t[1], at::kInt, dev, B) &&
                 plain(t[2], at::kInt, dev, B) && table(t[3], dev, B, stride, width) &&
                 plain(t[4], at::kInt, dev) && t[4]->numel() <= INT32_MAX &&
                 plain(t[5], at::kInt, dev, 1) && plain(t[8], at::kInt, dev, B) &&
@@ -208,10 +212,10 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 q.size(2) == c.D && q.scalar_type() == t[1]->scalar_type() &&
                 q.size(0) <= INT32_MAX && q.size(1) <= INT32_MAX && c.heads >= 1 &&
                 q.size(1) >= 1 && q.size(1) % c.heads == 0);
-  REFUSE_UNLESS(B <= INT32_MAX && plain(t[4], at::kInt, dev) && plain(t[5], at::kLong, dev, B + 1) &&
-                table(t[3], dev, B, stride, width) && plain(t[9], q.scalar_type(), dev) &&
-                t[9]->sizes() == q.sizes() &&
-                (a[10] == Py_None || plain(t[10], at::kFloat, dev, q.size(0) * q.size(1))) &&
+  REFUSE_UNLESS(B <= INT32_MAX && plain(t[4], at::kInt, dev, B) &&
+                plain(t[5], at::kLong, dev, B + 1) && table(t[3], dev, B, stride, width) &&
+                plain(t[9], q.scalar_type(), dev, q.sizes()) &&
+                (a[10] == Py_None || plain(t[10], at::kFloat, dev, {q.size(0), q.size(1)})) &&
                 plain(t[11], at::kInt, dev, 1) && plain(t[12], at::kByte, dev) && here(dev) &&
                 stream_of(a[13], dev, s));
   return done(g_attention(
