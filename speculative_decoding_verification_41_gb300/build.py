@@ -5,6 +5,7 @@ from __future__ import annotations
 import concurrent.futures
 import os
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +17,7 @@ SOURCES = ["dspark_verify.cu", "dspark_schedule.cu", "dspark_draft.cu", "dspark_
            "dspark_attention.cu"]
 BINDING_SOURCE = os.path.join(CSRC, "paged_binding.cpp")
 BINDING_PATH = os.path.join(PKG, "_paged_binding.so")
+BINDING_STAMP = os.path.join(BUILD_DIR, "paged_binding.stamp")
 HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith(".cuh"))
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
@@ -25,6 +27,22 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", 
 def _nvcc() -> str:
     cand = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
     return cand if os.path.exists(cand) else "nvcc"
+
+
+def _binding_abi() -> str:
+    """What the module's machine code is tied to: this Python, and this torch's C++ classes."""
+    import torch
+    return "\n".join([sysconfig.get_config_var("EXT_SUFFIX") or "", sys.version, torch.__version__,
+                      str(torch.version.git_version), str(int(torch.compiled_with_cxx11_abi()))])
+
+
+def binding_fits() -> bool:
+    """Whether the module that is there was compiled for the Python and torch that run."""
+    try:
+        with open(BINDING_STAMP) as f:
+            return os.path.exists(BINDING_PATH) and f.read() == _binding_abi()
+    except OSError:
+        return False
 
 
 def _build_binding() -> None:
@@ -43,10 +61,12 @@ def _build_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for {BINDING_SOURCE}:\n{r.stderr}")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_abi())
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+    if not os.path.exists(LIB_PATH) or not binding_fits():
         return True
     t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]

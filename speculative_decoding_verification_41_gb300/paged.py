@@ -22,7 +22,7 @@ from typing import Optional
 
 import torch
 
-from . import binding
+from . import binding, build
 from .binding import DSPARK_BF16, DsparkError, made_on
 
 HEADER = os.path.join(binding.ROOT, "include", "dspark_paged.h")
@@ -52,12 +52,10 @@ def _native():
     global _ext
     if _ext is None:
         fns = _load()
-        try:
-            from . import _paged_binding
-        except ImportError as e:
-            raise RuntimeError("the _paged_binding module is not built or does not fit this "
-                               "Python and torch; run `python -c 'import __graft_entry__ as g; "
-                               f"g.build()'` ({e})") from e
+        if not build.binding_fits():  # its machine code knows one torch's tensors
+            raise RuntimeError("the _paged_binding module is not built, or not for this Python and "
+                               "torch; run `python -c 'import __graft_entry__ as g; g.build()'`")
+        from . import _paged_binding
         _paged_binding.bind(*(ctypes.cast(fns[name], ctypes.c_void_p).value for name in EXPORTED))
         _ext = _paged_binding
     return _ext
