@@ -153,7 +153,7 @@ int dspark_pages_release(const int32_t* context_len, const int32_t* reserved_len
  *                 strides for both.
  *   n >= 0 rows, Hkv >= 1 heads, D = 64 or 128.
  *   k_cache, v_cache, page_stride, token_stride, head_stride: the cache.
- *   All pointers 16-byte aligned, all strides multiples of 8 elements.
+ *   All pointers 16-byte aligned, all strides multiples of 8 elements, >= 0.
  * No workspace; one launch.
  */
 int dspark_kv_append(const void* k, const void* v, int64_t row_stride, int64_t in_head_stride,
@@ -208,7 +208,7 @@ int dspark_kv_append(const void* k, const void* v, int64_t row_stride, int64_t i
  *   workspace     at least DSPARK_PAGED_ATTENTION_WS_BYTES(Hq, Hkv, max_new, D)
  *                 bytes, 256-byte aligned; no initial contents needed.
  * q, k_cache, v_cache and out must be 16-byte aligned and all strides multiples
- * of 8 elements (tensor memory access); otherwise DSPARK_ERR_INVALID_ARG.
+ * of 8 elements, >= 0 (tensor memory access); otherwise DSPARK_ERR_INVALID_ARG.
  */
 int dspark_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
                            const void* k_cache, const void* v_cache, int64_t page_stride,

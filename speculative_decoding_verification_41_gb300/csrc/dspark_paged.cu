@@ -522,6 +522,8 @@ extern "C" int dspark_kv_append(const void* k, const void* v, int64_t row_stride
       (dtype != DSPARK_BF16 && dtype != DSPARK_F16) || !pool_ok(0, page_size, num_pages, 1, 1) ||
       !device_status || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) ||
       !aligned16(v_cache) || (n > 0 && (!k || !v || !slot_map || !k_cache || !v_cache)) ||
+      row_stride < 0 || in_head_stride < 0 || page_stride < 0 || token_stride < 0 ||
+      head_stride < 0 ||
       ((row_stride | in_head_stride | page_stride | token_stride | head_stride) & 7) != 0)
     return DSPARK_ERR_INVALID_ARG;
   AppendArgs a{};
