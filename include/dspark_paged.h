@@ -98,7 +98,8 @@ extern "C" {
  *   free_count_out [1] int32. May be free_count itself.
  *   device_status  [1] int32 (required).
  * Calling it again with the same inputs gives the same outputs (unless they
- * overwrite the inputs). No workspace; one launch.
+ * overwrite the inputs). No workspace; one launch, and a second one of one CTA where
+ * an output is written over an input.
  */
 int dspark_pages_reserve(const int32_t* context_len, const int32_t* new_len, int32_t extra,
                          int32_t B, int32_t page_size, int32_t num_pages, int32_t* block_table,
@@ -131,7 +132,8 @@ int dspark_pages_reserve(const int32_t* context_len, const int32_t* new_len, int
  *   context_out   [B] int32: tokens kept. May be context_len or reserved_len.
  *   free_count_out [1] int32. May be free_count itself.
  * Calling it again with the same inputs gives the same outputs (unless they
- * overwrite the inputs). No workspace; one launch.
+ * overwrite the inputs). No workspace; one launch, and a second one of one CTA where
+ * an output is written over an input.
  */
 int dspark_pages_release(const int32_t* context_len, const int32_t* reserved_len,
                          const int32_t* kept_len, int32_t extra, int32_t B, int32_t page_size,

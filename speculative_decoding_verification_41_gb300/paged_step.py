@@ -52,6 +52,8 @@ class PagedCache:
                                device_status=self._append_status)
 
     def attend(self, q: torch.Tensor) -> torch.Tensor:
+        """Attention of the step's rows. The result is a buffer that the next call for rows of this
+        shape overwrites (another layer's): copy what has to outlive it."""
         n, Hq, D = q.shape
         if self._attention is None or self._attention.out.shape != q.shape:
             self._attention = paged.AttentionBuffers(n, Hq, self.k.shape[2], D, self.max_new,
@@ -67,7 +69,8 @@ class PagedCache:
                                    page_size=self.page_size, extra=extra, buffers=self._kept)
 
     def statuses(self) -> list:
-        """The calls' device status words (synchronises)."""
+        """The cache's calls' device status words (synchronises): reserve, append, release and, once
+        it has run, the attention. The verification's is in speculative_step's result."""
         words = [self.rows.device_status, self._append_status, self._kept.device_status]
         if self._attention is not None:
             words.append(self._attention.device_status)
