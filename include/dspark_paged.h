@@ -197,8 +197,10 @@ int dspark_kv_append(const void* k, const void* v, int64_t row_stride, int64_t i
  *                 every request are not written.
  *   Hq, Hkv       Hq a multiple of Hkv; D = 64 or 128; max_new >= 1. A key head's
  *                 (Hq / Hkv) * max_new query rows are served in passes of up to
- *                 DSPARK_PAGED_MAX_ROWS, side by side; more passes than the device
- *                 has SMs, or max_pages * page_size * Hkv past 2^37, are refused.
+ *                 DSPARK_PAGED_MAX_ROWS, side by side, which share the device
+ *                 evenly: long prompts belong in calls of their own, without
+ *                 requests of few new tokens. More passes than the device has SMs,
+ *                 or max_pages * page_size * Hkv past 2^37, are refused.
  *   scale         finite, > 0.
  *   window        visible tokens per new token, itself included; 0: all.
  * Outputs
