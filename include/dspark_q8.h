@@ -1,0 +1,180 @@
+/*
+ * dspark_q8.h -- the paged key-value cache (dspark_paged.h) held in 8 bits, and
+ * rotary positions, in libdspark (one GB300 GPU, sm_103a). Half the bytes of the
+ * 16-bit cache, which are what bounds the attention.
+ *
+ * Between the projections of a layer and its attention stand, in this order:
+ *   dspark_rotary              positions into the queries;
+ *   dspark_kv_append_q8        positions into the keys, keys and values into the cache;
+ *   dspark_paged_attention_q8  attention of the new tokens over the cache;
+ * and dspark_kv_gather_q8 reads stored tokens back in 16 bits. Pages are reserved
+ * and released as for the 16-bit cache (dspark_pages_reserve, dspark_pages_release).
+ *
+ * The cache. Codes are e4m3 numbers (1 sign, 4 exponent and 3 mantissa bits,
+ * largest 448, no infinities, 0x7F and 0xFF are NaN), laid out like the 16-bit
+ * cache: code of token t of page p, head h, element d at byte p*page_stride +
+ * t*token_stride + h*head_stride + d. A page's tokens form page_size / block
+ * blocks of `block` tokens (a power of two, 1..page_size), and each block and head
+ * has a binary32 scale for its keys and one for its values, at element
+ * p*scale_page_stride + (t / block)*scale_block_stride + h*scale_head_stride of
+ * k_scale and v_scale. A stored element is code * scale.
+ *
+ * Conventions are those of dspark.h and dspark_paged.h: caller-owned device
+ * pointers, no allocation, no synchronisation, host errors as return codes before
+ * anything is launched, data errors in *device_status, CUDA-graph capturable after
+ * one call outside a capture.
+ */
+#ifndef DSPARK_Q8_H
+#define DSPARK_Q8_H
+
+#include "dspark_paged.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Pairs of elements that a rotation turns: (j, j + rot_dim/2), or (2j, 2j + 1). */
+#define DSPARK_ROTARY_HALF 0
+#define DSPARK_ROTARY_INTERLEAVED 1
+
+/* A rotation by positions: pair j of a head's first rot_dim elements turns by
+ * 2 pi * (position * turns[j] mod 2^64) / 2^64, and is multiplied by gain:
+ *   (a, b) -> gain * (a cos - b sin, b cos + a sin).
+ * turns[j] is the pair's part of a full turn per position, as a 64-bit fraction:
+ * the product wraps where the angle does, so far positions lose nothing. */
+typedef struct {
+  const uint64_t* turns; /* device, [rot_dim / 2] */
+  int32_t rot_dim;       /* a multiple of 16, 16 .. D */
+  int32_t pairs;         /* DSPARK_ROTARY_HALF or DSPARK_ROTARY_INTERLEAVED */
+  float gain;            /* finite; 1 unless the angles are scaled for long contexts */
+} dspark_rotation;
+
+/*
+ * dspark_rotary -- row i, all its heads, turned by positions[i]. Elements past
+ * rot_dim are copied. Rows with a negative position (dspark_pages_reserve's padding)
+ * are not written. Computed in binary32, rounded once.
+ *
+ * Arguments
+ *   x             [n][heads][D] dtype (DSPARK_BF16, DSPARK_F16), strides
+ *                 row_stride, head_stride in elements, D contiguous.
+ *   positions     [n] int32.
+ *   rotation      host pointer, read during the call.
+ *   inverse       0, or 1: by the opposite angle (with the same gain). This is the
+ *                 transposed map: a gradient with respect to the result becomes one
+ *                 with respect to x.
+ *   n >= 0, 1 <= heads <= 65536, D = 64 or 128.
+ *   out           [n][heads][D] dtype, strides out_row_stride, out_head_stride; x
+ *                 itself (with its strides) or disjoint.
+ *   x and out 16-byte aligned, strides multiples of 8 elements, >= 0.
+ * No workspace, no data errors; one launch.
+ */
+int dspark_rotary(const void* x, int64_t row_stride, int64_t head_stride,
+                  const int32_t* positions, const dspark_rotation* rotation, int32_t inverse,
+                  int32_t n, int32_t heads, int32_t D, int32_t dtype, void* out,
+                  int64_t out_row_stride, int64_t out_head_stride, struct CUstream_st* stream);
+
+/*
+ * dspark_kv_append_q8 -- keys and values of new tokens into the 8-bit cache: row i
+ * of k and v goes to slot slot_map[i]; rows with a negative slot are skipped; a slot
+ * of num_pages * page_size or more is skipped and sets DSPARK_ERR_BAD_DATA.
+ *
+ * Scales. Let a be the largest finite magnitude among the rows written to a block,
+ * for a head, and e the smallest integer, at least -126, with a <= 448 * 2^e.
+ *   - A block whose first token is among the rows begins anew: its scale is 2^e,
+ *     and what its other tokens held is lost.
+ *   - Another block keeps its scale s if a <= 448 * s; if not, its scale becomes
+ *     2^e and its other tokens' codes are rounded again at that scale (a scale that is
+ *     not positive and finite counts as none: nothing is rounded again).
+ * So a rejected token's larger scale stays, and a token is rounded again when a larger
+ * one joins its block; between powers of two that costs only what falls below the
+ * smallest normal code. Codes are x / scale rounded to nearest even; infinities and
+ * NaN become NaN and do not count in a.
+ *
+ * Rows of one block must be neighbours in slot_map (as dspark_pages_reserve gives
+ * them), in any order; a block that is written by rows with others in between has
+ * unspecified codes and scales. Slots that occur twice leave either row.
+ *
+ * Arguments
+ *   k, v          dtype (DSPARK_BF16, DSPARK_F16): head h of row i at element
+ *                 i*row_stride + h*in_head_stride, D contiguous; the same strides.
+ *   rotation, positions  NULL, or the keys are turned first (as by dspark_rotary,
+ *                 in binary32, not rounded in between): positions [n] int32. Rows with
+ *                 a negative position are skipped.
+ *   n >= 0 rows, Hkv >= 1 heads, D = 64 or 128.
+ *   k_cache, v_cache  the codes, the same strides (bytes, multiples of 16, >= 0).
+ *   k_scale, v_scale  the scales, the same strides (elements, >= 0).
+ *   k, v, k_cache and v_cache 16-byte aligned; row_stride and in_head_stride
+ *   multiples of 8 elements, >= 0.
+ * No workspace; one launch.
+ */
+int dspark_kv_append_q8(const void* k, const void* v, int64_t row_stride,
+                        int64_t in_head_stride, const dspark_rotation* rotation,
+                        const int32_t* positions, const int32_t* slot_map, int32_t n,
+                        int32_t Hkv, int32_t D, int32_t dtype, void* k_cache, void* v_cache,
+                        int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                        float* k_scale, float* v_scale, int64_t scale_page_stride,
+                        int64_t scale_block_stride, int64_t scale_head_stride, int32_t block,
+                        int32_t page_size, int32_t num_pages, int32_t* device_status,
+                        struct CUstream_st* stream);
+
+/*
+ * dspark_kv_gather_q8 -- stored tokens back in 16 bits: row i of k and v is the
+ * token of slot slot_map[i], code * scale rounded once to dtype (exact in bf16 for
+ * scales that are powers of two, but for results below its range). Rows with a negative
+ * slot are not written; a slot of num_pages * page_size or more is skipped and sets
+ * DSPARK_ERR_BAD_DATA. A slot may occur any number of times.
+ * Arguments as for dspark_kv_append_q8, with k and v written.
+ * No workspace; one launch.
+ */
+int dspark_kv_gather_q8(const void* k_cache, const void* v_cache, int64_t page_stride,
+                        int64_t token_stride, int64_t head_stride, const float* k_scale,
+                        const float* v_scale, int64_t scale_page_stride,
+                        int64_t scale_block_stride, int64_t scale_head_stride, int32_t block,
+                        int32_t page_size, int32_t num_pages, const int32_t* slot_map, int32_t n,
+                        int32_t Hkv, int32_t D, int32_t dtype, void* k, void* v,
+                        int64_t row_stride, int64_t out_head_stride, int32_t* device_status,
+                        struct CUstream_st* stream);
+
+/*
+ * dspark_paged_attention_q8 -- dspark_paged_attention over the 8-bit cache: the same
+ * requests, rows, visibility and outputs, with K = code * k_scale and V = code *
+ * v_scale.
+ *
+ * Queries are split into e4m3 numbers whose sum they are (all their bits down to
+ * 2^-9 of the row's largest element for bf16, 2^-6 for half precision, and 2^-17 of
+ * it at least), so scores are sums of exact products in binary32. The weights
+ * e^{s - m} v_scale / 2^r are cut to 9 bits (bf16 queries) or rounded to 11 (half
+ * precision) for the second product (their sum is not), where m is some nats below the
+ * row's largest score and 2^r at most four times the largest v_scale so far: they
+ * keep these bits down to 2^-18 (half precision: 2^-15) of the largest one, five powers
+ * of two further where that is a peak, and lose them below. Sums and outputs are
+ * binary32, and the output is rounded once.
+ * Results depend on the inputs alone, not on timing.
+ *
+ * A cached code, or a scale, that a row does not see never reaches it. A scale that
+ * is not finite and positive where a visible token lies sets DSPARK_ERR_BAD_DATA (that
+ * request's rows are unspecified).
+ *
+ * Arguments as for dspark_paged_attention, but
+ *   k_cache, v_cache  codes; page_stride, token_stride and head_stride in bytes,
+ *                 multiples of 16, >= 0.
+ *   k_scale, v_scale  the scales, the same strides (elements, >= 0).
+ *   q, out        dtype DSPARK_BF16 or DSPARK_F16. A pass over a request's keys serves
+ *                 up to 96 query rows of a key head (bf16) or 80 (half precision).
+ */
+int dspark_paged_attention_q8(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_cache,
+    const void* v_cache, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+    const float* k_scale, const float* v_scale, int64_t scale_page_stride,
+    int64_t scale_block_stride, int64_t scale_head_stride, int32_t block, int32_t page_size,
+    int32_t num_pages, const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+    const int32_t* context_len, const int64_t* row_off, int32_t B, int32_t n_tokens, int32_t Hq,
+    int32_t Hkv, int32_t D, int32_t max_new, float scale, int32_t window, int32_t dtype, void* out,
+    float* lse, int32_t* device_status, void* workspace, size_t workspace_bytes,
+    struct CUstream_st* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DSPARK_Q8_H */

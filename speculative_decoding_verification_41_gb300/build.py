@@ -14,11 +14,11 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libdspark.so")
 SOURCES = ["dspark_verify.cu", "dspark_schedule.cu", "dspark_draft.cu", "dspark_paged.cu",
-           "dspark_attention.cu"]
+           "dspark_attention.cu", "dspark_q8.cu", "dspark_attention_q8.cu"]
 BINDING_SOURCE = os.path.join(CSRC, "paged_binding.cpp")
 BINDING_PATH = os.path.join(PKG, "_paged_binding.so")
 BINDING_STAMP = os.path.join(BUILD_DIR, "paged_binding.stamp")
-HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith(".cuh"))
+HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")))
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", f"-I{os.path.join(ROOT, 'include')}"]
@@ -70,7 +70,7 @@ def _stale() -> bool:
         return True
     t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps += [os.path.join(ROOT, "include", h) for h in ("dspark.h", "dspark_testing.h", "dspark_paged.h")]
+    deps += [os.path.join(ROOT, "include", h) for h in ("dspark.h", "dspark_testing.h", "dspark_paged.h", "dspark_q8.h")]
     deps += [os.path.abspath(__file__), BINDING_SOURCE]
     return any(os.path.getmtime(d) > t for d in deps)
 

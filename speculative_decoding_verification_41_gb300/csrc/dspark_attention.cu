@@ -2,17 +2,12 @@
 // launches (the kernels and their reasons are in dspark_attention.cuh).
 #include <algorithm>
 #include <cmath>
-#include <cudaTypedefs.h>
-#include <mutex>
 
 #include "dspark_attention.cuh"
+#include "dspark_attention_host.h"
 
 namespace dspark {
 namespace {
-
-std::mutex g_attn_mutex;
-int g_attn_sms[128];
-PFN_cuTensorMapEncodeTiled_v12000 g_attn_encode = nullptr;
 
 // A tensor of 16-bit elements in the 128-byte swizzled layout; dims[0] innermost.
 // A row of 128 elements is fetched in two halves, whose 256 bytes come together;
@@ -29,11 +24,6 @@ bool attn_map(CUtensorMap* map, bool f16, const void* base, int rank, const cuui
                                      : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-// Shared memory of a CTA that has its SM to itself (227 KB), or of one of two:
-// half of 228 KB, less 1 KB each for the system.
-template <int CTAS>
-constexpr int kSmemCta = CTAS == 1 ? 232448 : 115712;
 
 struct Launch {
   CUtensorMap q, k, v;
@@ -102,28 +92,6 @@ int attn_shape(Launch& c, int sms) {
   if (c.a.n_cols <= 64) return attn_launch<AttnShape<D, 64, 4, 1, 2>, F16>(c, sms);
   if (c.a.n_cols <= 96) return attn_launch<AttnShape<D, 96, 3, 1, 2>, F16>(c, sms);
   return attn_launch<AttnShape<D, 160, 3, 1, 1>, F16>(c, sms);
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int attn_setup(int& sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return DSPARK_ERR_CUDA;
-  std::lock_guard<std::mutex> lock(g_attn_mutex);
-  if (!g_attn_encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn)
-      return DSPARK_ERR_CUDA;
-    g_attn_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  if (g_attn_sms[dev] == 0 &&
-      cudaDeviceGetAttribute(&g_attn_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return DSPARK_ERR_CUDA;
-  sms = g_attn_sms[dev];
-  return DSPARK_OK;
 }
 
 }  // namespace

@@ -1,0 +1,194 @@
+// dspark_attention_q8.cu -- dspark_paged_attention_q8: checks, tensor maps, shapes and
+// launches (the kernels and their reasons are in dspark_attention_q8.cuh and
+// dspark_attention.cuh).
+#include <algorithm>
+#include <cmath>
+
+#include "dspark_attention_host.h"
+#include "dspark_attention_q8.cuh"
+
+namespace dspark {
+namespace {
+
+// Codes of the cache; a box is a row of D bytes of up to 128 tokens.
+bool q8_map(CUtensorMap* map, const void* base, int D, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return g_attn_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
+                       strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct LaunchQ8 {
+  CUtensorMap k, v;
+  AttnQ8Args a;
+  JoinArgs j;
+  int items;
+  cudaStream_t stream;
+};
+
+template <class S>
+int q8_launch(LaunchQ8& c, int sms) {
+  static bool ready[128];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return DSPARK_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(g_attn_mutex);
+    if (!ready[dev]) {
+      if (cudaFuncSetAttribute(k_attention_q8<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kSmemCta<S::CTAS>) != cudaSuccess)
+        return DSPARK_ERR_CUDA;
+      ready[dev] = true;
+    }
+  }
+  AttnQ8Args& a = c.a;
+  a.ctas = std::max(1, std::min(sms * S::CTAS, DSPARK_PAGED_MAX_CTAS) / a.n_chunks);
+  const int grid = a.ctas * a.n_chunks;
+  // Shared memory: what the queries, the weights and the scales leave is the rings'. A
+  // second tile of queries where it costs them no tile.
+  constexpr uint32_t kSmem = kSmemCta<S::CTAS>;
+  const uint32_t q_bytes = static_cast<uint32_t>(S::QP * S::D * a.n_cols);
+  a.part_bytes = static_cast<uint32_t>(a.n_cols / 16 * 2048);
+  a.p_bytes = S::PP * a.part_bytes;
+  auto ring_stages = [&](int q_bufs) {
+    a.q_bufs = q_bufs;
+    a.p_off = kQ8CtlBytes<S> + q_bufs * q_bytes;
+    a.scale_off = a.p_off + S::PBUFS * a.p_bytes;
+    auto ring_at = [&](int v_stages) {
+      return (a.scale_off + v_stages * 8u * a.n_scales + 1023u) & ~1023u;
+    };
+    int stages = kQ8MaxStages;
+    while (stages > 2 && ring_at(stages - stages / 2) + stages * S::kStage > kSmem) --stages;
+    a.ring_off = ring_at(stages - stages / 2);
+    return stages;
+  };
+  const int stages = ring_stages(1);
+  if (ring_stages(2) < stages) ring_stages(1);
+  a.k_stages = stages / 2;
+  a.v_stages = stages - a.k_stages;  // values wait for the softmax, keys do not
+  a.lead = 3;
+  const size_t smem = a.ring_off + static_cast<size_t>(stages) * S::kStage;
+  if (smem > kSmem) return DSPARK_ERR_INVALID_ARG;
+  if (launch_pdl(k_attention_q8<S>, grid, S::THREADS, smem, c.stream, c.k, c.v, a) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  JoinArgs& j = c.j;
+  j.n = grid;
+  j.ctas = a.ctas;
+  // Few requests: each is cut into many pieces, which eight warps share per row.
+  j.per_row = c.items * 8 <= grid ? kJoinWarps : 1;
+  const int rows = kJoinWarps / j.per_row;
+  if (launch_pdl(k_attention_join<S::D, S::F16>,
+                 dim3(std::min(c.items, grid), (a.n_cols + rows - 1) / rows), kJoinWarps * 32, 0,
+                 c.stream, j) != cudaSuccess ||
+      cudaGetLastError() != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  return DSPARK_OK;
+}
+
+// Rows that a pass can serve: two buffers of scores and the parts of the outputs fill the
+// 512 columns of tensor memory.
+constexpr int q8_max_rows(bool f16) { return f16 ? 80 : 96; }
+
+// The smallest row block that holds the rows; keys are copied once for all of them.
+template <int D, bool F16>
+int q8_shape(LaunchQ8& c, int sms) {
+  if (c.a.n_cols <= 16) return q8_launch<AttnQ8Shape<D, F16, 16, 1, 2, 2>>(c, sms);
+  if (c.a.n_cols <= 32) return q8_launch<AttnQ8Shape<D, F16, 32, 1, 2, 2>>(c, sms);
+  if (c.a.n_cols <= 64) return q8_launch<AttnQ8Shape<D, F16, 64, 4, 1, 2>>(c, sms);
+  return q8_launch<AttnQ8Shape<D, F16, q8_max_rows(F16), 3, 1, 2>>(c, sms);
+}
+
+}  // namespace
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" int dspark_paged_attention_q8(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_cache,
+    const void* v_cache, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+    const float* k_scale, const float* v_scale, int64_t scale_page_stride,
+    int64_t scale_block_stride, int64_t scale_head_stride, int32_t block, int32_t page_size,
+    int32_t num_pages, const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+    const int32_t* context_len, const int64_t* row_off, int32_t B, int32_t n_tokens, int32_t Hq,
+    int32_t Hkv, int32_t D, int32_t max_new, float scale, int32_t window, int32_t dtype, void* out,
+    float* lse, int32_t* device_status, void* workspace, size_t workspace_bytes,
+    struct CUstream_st* stream) {
+  if (B < 0 || n_tokens < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq > 65536 ||
+      (D != 64 && D != 128) || max_new < 1 || max_new > (1 << 20) || !std::isfinite(scale) ||
+      !(scale > 0.f) || window < 0 || (dtype != DSPARK_BF16 && dtype != DSPARK_F16) ||
+      page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0 || num_pages < 1 ||
+      block < 1 || block > page_size || (block & (block - 1)) != 0 ||
+      static_cast<int64_t>(num_pages) * page_size > INT32_MAX || max_pages < 1 ||
+      static_cast<int64_t>(max_pages) * page_size > INT32_MAX - 2 * kTileTok ||
+      static_cast<int64_t>(max_pages) * page_size / kTileTok * Hkv > INT32_MAX / 2 ||
+      table_stride < max_pages || !device_status)
+    return DSPARK_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (B == 0 || n_tokens == 0)  // no rows
+    return cudaMemsetAsync(device_status, 0, 4, st) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !context_len ||
+      !row_off || !out || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(out) || q_row_stride < 0 || q_head_stride < 0 || page_stride < 0 ||
+      token_stride < 0 || head_stride < 0 || scale_page_stride < 0 || scale_block_stride < 0 ||
+      scale_head_stride < 0 || ((q_row_stride | q_head_stride) & 7) != 0 ||
+      ((page_stride | token_stride | head_stride) & 15) != 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < DSPARK_PAGED_ATTENTION_WS_BYTES(Hq, Hkv, max_new, D))
+    return DSPARK_ERR_WORKSPACE;
+  int sms = 0;
+  const int rc = attn_setup(sms);
+  if (rc != DSPARK_OK) return rc;
+
+  LaunchQ8 c{};
+  AttnQ8Args& a = c.a;
+  a.G = Hq / Hkv;
+  a.parts = 1;  // of a group of query heads, if it has more than fit
+  const bool f16 = dtype == DSPARK_F16;
+  const int max_rows = q8_max_rows(f16);
+  while (a.G % a.parts != 0 || a.G / a.parts > max_rows) ++a.parts;
+  a.Gs = a.G / a.parts;
+  const int fit = max_rows / a.Gs;
+  const int t_chunks = (max_new + fit - 1) / fit;
+  a.t_chunk = (max_new + t_chunks - 1) / t_chunks;
+  a.n_chunks = a.parts * t_chunks;
+  if (a.n_chunks > sms) return DSPARK_ERR_INVALID_ARG;
+  a.n_cols = (a.Gs * a.t_chunk + 15) / 16 * 16;
+  a.table = block_table, a.ctx = context_len, a.row_off = row_off, a.out = out, a.lse = lse;
+  a.v_cache = v_cache, a.stride = table_stride, a.page_stride = page_stride;
+  a.token_stride = token_stride, a.head_stride = head_stride, a.B = B, a.n_tokens = n_tokens;
+  a.Hq = Hq, a.Hkv = Hkv, a.max_new = max_new, a.num_pages = num_pages, a.max_pages = max_pages;
+  a.q = static_cast<const uint16_t*>(q), a.q_row = q_row_stride, a.q_head = q_head_stride;
+  a.k_scale = k_scale, a.v_scale = v_scale, a.scale_page = scale_page_stride;
+  a.scale_block = scale_block_stride, a.scale_head = scale_head_stride;
+  while ((1 << a.shift) < page_size) ++a.shift;
+  while ((1 << a.b_shift) < block) ++a.b_shift;
+  a.n_scales = kTileTok / std::min(block, kTileTok);
+  a.window = window > 0 ? window : INT_MAX;
+  a.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.records = reinterpret_cast<AttnRecord*>(ws);
+  ws += DSPARK_ALIGN256(DSPARK_PAGED_MAX_CTAS * sizeof(AttnRecord));
+  a.part_ml = reinterpret_cast<float*>(ws);
+  ws += static_cast<size_t>(2 * DSPARK_PAGED_MAX_CTAS) * a.n_cols * 8;
+  a.part_o = reinterpret_cast<float*>(ws);
+  c.j.records = a.records, c.j.part_ml = a.part_ml, c.j.part_o = a.part_o, c.j.out = out;
+  c.j.lse = lse, c.j.status = device_status, c.j.n_cols = a.n_cols, c.j.Hq = Hq, c.j.Gs = a.Gs;
+  c.items = static_cast<int>(
+      std::min<int64_t>(static_cast<int64_t>(B) * Hkv * a.n_chunks, DSPARK_PAGED_MAX_CTAS));
+  c.stream = st;
+
+  const cuuint64_t cd[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page_size),
+                            static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(num_pages)};
+  const cuuint64_t cs[3] = {static_cast<cuuint64_t>(token_stride),
+                            static_cast<cuuint64_t>(head_stride),
+                            static_cast<cuuint64_t>(page_stride)};
+  const cuuint32_t cb[4] = {static_cast<cuuint32_t>(D),
+                            static_cast<cuuint32_t>(std::min(page_size, kTileTok)), 1, 1};
+  if (!q8_map(&c.k, k_cache, D, cd, cs, cb) || !q8_map(&c.v, v_cache, D, cd, cs, cb))
+    return DSPARK_ERR_INVALID_ARG;
+  if (D == 64) return f16 ? q8_shape<64, true>(c, sms) : q8_shape<64, false>(c, sms);
+  return f16 ? q8_shape<128, true>(c, sms) : q8_shape<128, false>(c, sms);
+}

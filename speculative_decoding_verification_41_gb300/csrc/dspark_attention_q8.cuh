@@ -1,0 +1,1074 @@
+// dspark_attention_q8.cuh -- attention of each request's newest tokens over its pages
+// of 8-bit codes (dspark_paged_attention_q8, include/dspark_q8.h), sm_103a.
+//
+// Mathematics. As dspark_attention.cuh, whose split of the work, items, references and
+// join it shares, with keys ks_u K_u and values vs_u V_u: codes K, V in e4m3 and a scale
+// each per token u (of its block and head). In tiles of 128 tokens
+//   S^T = K Q^T            (128 tokens x R rows, tcgen05 kind::f8f6f4, f32)
+//   P^T = vs 2^(t - m),     t = S^T ks c_r,  l += 2^(t - m)
+//   O^T += V^T P^T          (D x R)
+// The codes enter the instruction as they lie in the cache. For that Q and P, which have
+// more bits than an 8-bit number, are split into 8-bit numbers whose sum they are:
+//   Q: each row times a power of two (its largest element in [2^7, 2^8)), then 2 e4m3
+//      parts (bf16: 8 bits) or 3 (half precision: 11), nearest first; the row's
+//      opposite power of two joins c_r.
+//   P: rounded to half precision, whose upper byte is an e5m2 number: that byte, the
+//      upper byte of the rest, and so on: 3 bits each, 3 parts (9 bits) for bf16
+//      outputs, 4 (all 11) for half precision. Each part is a product of its own
+//      (columns side by side, one pass over V for up to 256 of them), so the last one
+//      can be scaled: times 2^4 (2^6), its smallest number is 2^-20 (2^-22).
+// The parts of Q are passes over the same columns and add up in the same sums.
+//
+// A scale of a value is relative to 2^rv, rv chosen like a row's reference (from the
+// first tile, with room above, and raised when a larger one comes), so that weights keep
+// the upper end of half precision's range.
+//
+// Bound. 2 D bytes per token and key head: 11 cycles of an SM's part of HBM for D = 128.
+// The tensor cores read K once per part of Q and V once per 256 columns.
+#pragma once
+
+#include "dspark_attention.cuh"
+#include "dspark_q8.cuh"
+
+namespace dspark {
+
+struct AttnQ8Args : AttnArgs {
+  const uint16_t* q;
+  const float *k_scale, *v_scale;
+  int64_t q_row, q_head;                       // elements
+  int64_t scale_page, scale_block, scale_head;  // elements
+  int32_t b_shift;                             // tokens of a block
+  int32_t n_scales;                            // scales of a tile: 128 tokens', or 1
+  uint32_t part_bytes;                         // of one part of the weights
+  uint32_t scale_off;                          // shared memory: [stage of values][2][n_scales]
+};
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor: D f32, A e4m3, B e4m3 (0) or e5m2 (1); ta, tb as in attn_idesc
+__host__ __device__ constexpr uint32_t attn_idesc_f8(uint32_t b_format, int M, int N, bool ta,
+                                                     bool tb) {
+  return (1u << 4) | (b_format << 10) | ((ta ? 1u : 0u) << 15) | ((tb ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on `bar` when this thread's copies so far have landed (counted in its phase).
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts_u2(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// A part of four half precision numbers (two words): their upper bytes.
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) {
+  return __byte_perm(a, b, 0x7531);
+}
+// What the upper bytes of a pair leave: exact, the rest's bits are the lower ones.
+__device__ __forceinline__ uint32_t without_upper(uint32_t a) {
+  return sub_f16x2(a, a & 0xFF00FF00u);
+}
+
+constexpr int kQ8MaxStages = 16;
+// Room (log2) above the first tile's largest value scale.
+constexpr int kScaleRoom = 1;
+// Weights of three parts are cut, not rounded: by 2^-9 of their power of two on average,
+// which is 0.7213 * 2^-9 of the weight itself (the mean of 1/m for m spread over its
+// logarithm in [1, 2)). They are made larger by as much, which leaves a weight that is a
+// power of two, like a row's largest one can be, free of rounding.
+constexpr float kCut = 1.f + 0.7213f / 512.f;
+
+template <int D_, bool F16_, int NB_, int GROUPS_, int CTAS_, int PBUFS_>
+struct AttnQ8Shape {
+  static constexpr int D = D_, NB = NB_, GROUPS = GROUPS_, CTAS = CTAS_;
+  static constexpr bool F16 = F16_;
+  static constexpr int PBUFS = PBUFS_;
+  static constexpr int QP = F16 ? 3 : 2, PP = F16 ? 4 : 3;  // parts of Q and of P
+  static constexpr int LAST = F16 ? 6 : 4;                  // scale (log2) of P's last part
+  static constexpr int THREADS = 128 + 128 * GROUPS;
+  static constexpr int NC = (NB / 8 + GROUPS - 1) / GROUPS * 8;
+  static constexpr uint32_t kStage = kTileTok * D;
+  static constexpr uint32_t kColS = 0, kColO = 2 * NB;
+  static constexpr int kCols = (2 + PP) * NB;
+  static constexpr uint32_t kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;  // of rows of D bytes
+  static_assert(kCols <= 512 && CTAS * kTmem <= 512, "tensor memory");
+};
+
+template <class S>
+struct AttnQ8Ctl {
+  uint64_t full[kQ8MaxStages], empty[kQ8MaxStages];  // of key tiles, then of value tiles
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t item_full[kItems], item_empty[kItems], factors[kItems];
+  uint64_t odd_full, drained;
+  uint32_t tmem;
+  int32_t status, abort, start_r, start_off;
+  uint32_t scan[S::THREADS / 32];
+  AttnItem item[kItems];
+  // per column (row of q); a group's own. Two of what an item begins with: its
+  // slower warps may still write their results when the next one begins.
+  alignas(16) float nref[2][S::NB + 8];   // minus the rows' references
+  alignas(16) int32_t lim[2][S::NB + 8];  // a row sees the tokens below (and within the window)
+  alignas(16) int32_t at[S::NB + 8];      // element of a row in out, from the item's first
+  alignas(16) float fac[S::NB + 8];       // factor of a row's sums when its reference rises
+  alignas(16) float cq[kItems][S::NB + 8];  // per item: scale * log2(e) over the row's power of two
+  int32_t vexp[S::GROUPS][4];             // per warp of a group: exponent of the largest value scale
+  int32_t new_tok[S::NB + 8];             // new token of a column
+  float red[4][S::NB + 8];                // per warp: maxima, sums
+  int32_t odd_n[2], odd[2][2 * S::NB];  // tokens whose values are not finite and not for all rows
+};
+
+template <class S>
+constexpr uint32_t kQ8CtlBytes = (static_cast<uint32_t>(sizeof(AttnQ8Ctl<S>)) + 1023u) & ~1023u;
+
+template <class S>
+__global__ void __launch_bounds__(S::THREADS, S::CTAS)
+    k_attention_q8(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ AttnQ8Args a) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  AttnQ8Ctl<S>& ctl = *reinterpret_cast<AttnQ8Ctl<S>*>(smem);
+  const uint32_t s_q = smem_addr(smem) + kQ8CtlBytes<S>;  // Q; then weights, scales, ring
+  const uint32_t s_p = smem_addr(smem) + a.p_off, s_ring = smem_addr(smem) + a.ring_off;
+  const uint32_t s_scale = smem_addr(smem) + a.scale_off;
+  const uint32_t q_part = a.n_cols * static_cast<uint32_t>(S::D);  // bytes of a part of Q
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < a.k_stages + a.v_stages; ++i) {
+      mbar_init(&ctl.full[i], i < a.k_stages ? 1 : 33);  // values: and a warp's copies of scales
+      mbar_init(&ctl.empty[i], 1);
+    }
+    mbar_init(&ctl.odd_full, 1);
+    mbar_init(&ctl.drained, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.q_full[i], 1);
+      mbar_init(&ctl.q_empty[i], 1);
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.p_full[i], 4 * S::GROUPS);
+      mbar_init(&ctl.pv_done[i], 1);
+    }
+    for (uint32_t i = 0; i < kItems; ++i) {
+      mbar_init(&ctl.item_full[i], 1);
+      mbar_init(&ctl.factors[i], 1);
+      mbar_init(&ctl.item_empty[i], 4 * S::GROUPS + 2);  // softmax warps, products, queries
+    }
+    ctl.status = DSPARK_OK;
+    ctl.abort = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&map_k);
+    tma_prefetch_map(&map_v);
+  }
+  if (warp == 2) {
+    tmem_alloc(&ctl.tmem, S::kTmem);
+    tmem_relinquish();
+  }
+  pdl_wait();  // predecessor grid complete, its writes visible
+  pdl_trigger();
+
+  // ---- this CTA's part of the line of units ------------------------------
+  int chunk = 0, cta = blockIdx.x, part = 0, t0 = 0;
+  if (a.n_chunks > 1) {
+    chunk = blockIdx.x % a.n_chunks, cta = blockIdx.x / a.n_chunks;
+    part = chunk % a.parts, t0 = chunk / a.parts * a.t_chunk;
+  }
+  Line line;
+  {
+    const int per = (a.B + S::THREADS - 1) / S::THREADS;  // requests per thread
+    const int r0 = min(tid * per, a.B), r1 = min(r0 + per, a.B);
+    uint32_t sum = 0;
+    bool bad = false;
+    AttnReq q{};
+#pragma unroll 4
+    for (int r = r0; r < r1; ++r) {
+      bad |= !attn_request(a, r, t0, q);
+      sum = min(sum + static_cast<uint32_t>(q.units * a.Hkv), kMaxUnits);
+    }
+    uint32_t in = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, in, o);
+      if (lane >= o) in = min(in + u, kMaxUnits);
+    }
+    if (lane == 31) ctl.scan[warp] = in;
+    tc_fence_before();
+    const int any_bad = __syncthreads_or(bad);
+    tc_fence_after();
+    uint32_t before = in - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < S::THREADS / 32; ++w) {
+      const uint32_t v = ctl.scan[w];
+      if (w < warp) before = min(before + v, kMaxUnits);
+      total = min(total + v, kMaxUnits);
+    }
+    line = Line(total < kMaxUnits ? total : 0u, a.ctas);
+    const uint32_t u0 = line.begin(cta);
+    if (u0 >= before && u0 < before + sum) {
+      uint32_t u = before;
+      for (int r = r0; r < r1; ++r) {
+        if (per > 1) attn_request(a, r, t0, q);
+        const uint32_t n = static_cast<uint32_t>(q.units * a.Hkv);
+        if (u0 < u + n) {
+          ctl.start_r = r;
+          ctl.start_off = static_cast<int32_t>(u0 - u);
+          break;
+        }
+        u += n;
+      }
+    }
+    if (tid == 0) {
+      if (total == kMaxUnits) ctl.status = DSPARK_ERR_TOO_LARGE;
+      if (any_bad) ctl.status = DSPARK_ERR_BAD_DATA;
+    }
+  }
+  __syncthreads();
+  const uint32_t u_begin = line.begin(cta), u_end = line.begin(cta + 1);
+  const uint32_t tmem = ctl.tmem;
+  const int id = chunk * a.ctas + cta;  // of the record and the partial slots
+  if (tid == 0 && u_begin == u_end) a.records[id].valid = 0;
+
+  if (warp < 2) {
+    // =====================================================================
+    // copies: warp 0 keys and the items' records, warp 1 values. A
+    // tile's copies cost a warp some fifty instructions, which share the SM's
+    // issue slots with the softmax: with both kinds in one warp and page ids
+    // fetched tile by tile the copies fell behind the memory.
+    // =====================================================================
+    if (u_begin < u_end) {
+      const bool keys = warp == 0;
+      const uint64_t policy = policy_evict_first();
+      const int rows_box = min(1 << a.shift, kTileTok);
+      const int n_box = kTileTok / rows_box;
+      const int box = lane % n_box;
+      const bool copier = lane < n_box;
+      const uint32_t box_bytes = rows_box * S::D;
+      const uint32_t first_stage = keys ? 0u : static_cast<uint32_t>(a.k_stages);
+      const uint32_t end_stage =
+          keys ? static_cast<uint32_t>(a.k_stages) : static_cast<uint32_t>(a.k_stages + a.v_stages);
+      const CUtensorMap* const map = keys ? &map_k : &map_v;
+      const uint32_t dst0 = s_ring + box * box_bytes;
+      int r = ctl.start_r, off = ctl.start_off;
+      uint32_t u = u_begin;
+      // requests r_base .. r_base+31, one per lane
+      int r_base = -1000;
+      AttnReq mine{};
+      uint32_t items = 0, s = first_stage, wraps = 0;
+      bool ok = true;
+      while (ok) {
+        // ---- the next item of the line
+        AttnReq q;
+        int h = 0, lead_in = 0, take = 0;
+        bool found = false;
+        while (u < u_end && r < a.B) {  // (r: lengths that changed under the call)
+          if (r >= r_base + 32 || r < r_base) {
+            r_base = r;
+            mine.units = 0;
+            mine.begin = 0;
+            if (r + lane < a.B) {
+              attn_request(a, r + lane, t0, mine);
+              if (mine.units > 0)  // the table rows of requests to come
+                prefetch_l2(a.table + (r + lane) * a.stride + (mine.begin >> a.shift));
+            }
+          }
+          const int src = r - r_base;
+          q.units = __shfl_sync(0xFFFFFFFFu, mine.units, src);
+          if (off >= q.units * a.Hkv) {
+            off -= q.units * a.Hkv;
+            ++r;
+            continue;
+          }
+          h = off / q.units;
+          lead_in = off - h * q.units;
+          take = static_cast<int>(min(static_cast<uint32_t>(q.units - lead_in), u_end - u));
+          u += take;
+          off += take;
+          if (lead_in + take > a.lead) {
+            q.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, src);
+            q.t_rows = __shfl_sync(0xFFFFFFFFu, mine.t_rows, src);
+            q.lim0 = __shfl_sync(0xFFFFFFFFu, mine.lim0, src);
+            q.begin = __shfl_sync(0xFFFFFFFFu, mine.begin, src);
+            q.end = __shfl_sync(0xFFFFFFFFu, mine.end, src);
+            found = true;
+            break;
+          }  // else nothing but the item's lead: the next CTA begins it
+        }
+        if (!found) break;
+        const int in_head = max(lead_in - a.lead, 0);
+        const int tile0 = q.begin / kTileTok + in_head;
+        const int tiles = q.end > 0 ? lead_in + take - a.lead - in_head : 0;
+        const int32_t* const row = a.table + r * a.stride;
+        const int last_page = max(q.end - 1, 0) >> a.shift;
+        int page0 = (tile0 * kTileTok) >> a.shift;  // of the 32 ids that the lanes hold
+        int ids = 0, next_ids = 0;
+        if (tiles > 0) ids = row[min(page0 + lane, last_page)];
+        if (keys) {
+          const uint32_t slot = items % kItems, use = items / kItems;
+          if (use >= 1) ok = warp_wait(&ctl.item_empty[slot], (use - 1u) & 1u);
+          if (!ok) break;
+          if (lane == 0) {
+            AttnItem& item = ctl.item[slot];
+            item.row0 = q.row0;
+            item.r = r;
+            item.kv_head = h;
+            item.head0 = h * a.G + part * a.Gs;
+            item.tiles = tiles;
+            item.tile0 = tile0;
+            item.t_rows = q.t_rows;
+            item.lim0 = q.lim0;
+            item.begin = q.begin;
+            item.end = q.end;
+            item.starts = in_head == 0;
+            item.ends = lead_in + take == q.units;
+            item.first = line.owner(u - take - lead_in + a.lead);
+            mbar_arrive(&ctl.item_full[slot]);
+          }
+          ++items;
+        }
+        // ---- its tiles
+        if (tiles > 0) next_ids = row[min(page0 + 32 + lane, last_page)];
+        int tok = tile0 * kTileTok + box * rows_box;  // this lane's box of the tile
+        for (int i = 0; i < tiles; ++i, tok += kTileTok) {
+          int rel = (tok >> a.shift) - page0;
+          if (__any_sync(0xFFFFFFFFu, rel >= 32)) {
+            page0 += 32;
+            rel -= 32;
+            ids = next_ids;
+            next_ids = row[min(page0 + 32 + lane, last_page)];
+          }
+          int page = __shfl_sync(0xFFFFFFFFu, ids, rel);
+          const bool load = copier && tok < q.end && tok + rows_box > q.begin;
+          if (load && static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) {
+            set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
+            page = 0;
+          }
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * box_bytes;
+          bool mine_ok = wraps == 0 || mbar_wait(&ctl.empty[s], (wraps - 1u) & 1u);
+          if (mine_ok && lane == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
+          ok = __all_sync(0xFFFFFFFFu, mine_ok) != 0;
+          if (!ok) break;
+          if (load)
+            tma_load_4d(dst0 + s * S::kStage, map, 0, tok & ((1 << a.shift) - 1), h, page,
+                        &ctl.full[s], policy);
+          if (!keys) {
+            // the scales of the tile's keys and values travel with its values, whose stage
+            // is held until the softmax is done with the tile
+            const int tile_tok = (tile0 + i) * kTileTok;
+            const uint32_t to = s_scale + (s - first_stage) * (8u * a.n_scales);
+            for (int j0 = 0; j0 < a.n_scales; j0 += 32) {
+              const int j = j0 + lane;
+              const int t = tile_tok + (j < a.n_scales ? j << a.b_shift : 0);
+              const int id = __shfl_sync(0xFFFFFFFFu, ids, (t >> a.shift) - page0);
+              // a block that starts before the first token that is seen may hold it
+              if (j < a.n_scales && t < q.end && t + (1 << a.b_shift) > q.begin &&
+                  static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages)) {
+                const int64_t from = id * a.scale_page +
+                                     ((t & ((1 << a.shift) - 1)) >> a.b_shift) * a.scale_block +
+                                     h * a.scale_head;
+                cp_async4(to + 4u * j, a.k_scale + from);
+                cp_async4(to + 4u * (a.n_scales + j), a.v_scale + from);
+              }
+            }
+            cp_async_arrive(&ctl.full[s]);
+          }
+          if (++s == end_stage) s = first_stage, ++wraps;
+        }
+      }
+      // the end of the line
+      if (ok && keys) {
+        const uint32_t slot = items % kItems, use = items / kItems;
+        if (use >= 1) ok = warp_wait(&ctl.item_empty[slot], (use - 1u) & 1u);
+        if (ok && lane == 0) {
+          ctl.item[slot].tiles = -1;
+          mbar_arrive(&ctl.item_full[slot]);
+        }
+      }
+      if (!ok) {
+        set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
+        *reinterpret_cast<volatile int32_t*>(&ctl.abort) = 1;
+      }
+      // leave no copy in flight into this CTA's shared memory
+      for (uint32_t i = first_stage; i < end_stage; ++i)
+        if (i < s || wraps > 0) mbar_wait(&ctl.full[i], (i < s ? wraps : wraps - 1u) & 1u);
+    }
+  } else if (warp == 2) {
+    // =====================================================================
+    // products
+    // =====================================================================
+    // The whole warp walks the line and one elected thread issues: uniform
+    // descriptors stay in uniform registers. (Walked by one thread alone an
+    // instruction cost about 100 cycles to issue, twice its execution.)
+    if (u_begin < u_end) {
+      const bool leader = elect_one();
+      const uint32_t n = static_cast<uint32_t>(a.n_cols);
+      const uint32_t idesc_s = attn_idesc_f8(0, kTileTok, n, false, false);
+      // the parts of P in one product or, past 256 columns, in two
+      const uint32_t parts_a = S::PP * n <= 256 ? S::PP : 2, n_a = parts_a * n;
+      const uint32_t idesc_o = attn_idesc_f8(1, S::D, n_a, true, true);
+      const uint32_t idesc_o2 = attn_idesc_f8(1, S::D, S::PP * n - n_a, true, true);
+      const bool two = parts_a < S::PP;
+      // K and Q: rows of D bytes, 8-row groups together
+      const uint64_t desc_kq = attn_desc(16, 8 * S::D, S::kSwizzle);
+      // V: a token's D bytes together, 8-token groups after one another
+      const uint64_t desc_v = attn_desc(S::kStage, 8 * S::D, S::kSwizzle);
+      // P: 16 rows of q contiguous per token, 16-row blocks 2,048 apart, 8-token groups 128
+      // apart, no swizzle (there the leading offset is that of the tokens)
+      const uint64_t desc_p = attn_desc(128, 2048, 0);
+      uint32_t items = 0, tiles = 0, scores = 0;
+      struct Ring {
+        uint32_t s, phase, first, end;
+        __device__ void on() {
+          if (++s == end) s = first, phase ^= 1u;
+        }
+      };
+      const uint32_t nk = a.k_stages, nv = a.v_stages;
+      Ring rk{0, 0, 0, nk}, rv{nk, 0, nk, nk + nv};
+      const uint32_t nq = a.q_bufs;
+      Ring rq{nq - 1u, 1u, 0, nq};  // moved on to an item's queries before them
+      bool ok = true;
+      auto product_s = [&](bool last) {  // S^T of the next tile; the item's last frees Q
+        const uint32_t buf = scores & 1u;
+        ok = warp_wait(&ctl.full[rk.s], rk.phase);
+        if (!ok) return;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t k0 = at(desc_kq, s_ring + rk.s * S::kStage);
+          const uint64_t q0 = at(desc_kq, s_q + rq.s * S::QP * q_part);
+#pragma unroll
+          for (int p = 0; p < S::QP; ++p)
+#pragma unroll
+            for (int k = 0; k < S::D / 32; ++k)
+              tc_mma_f8(tmem + S::kColS + buf * S::NB, k0 + static_cast<uint32_t>(2 * k),
+                        q0 + (p * (q_part >> 4) + 2 * k), idesc_s, p > 0 || k > 0);
+          tc_commit(&ctl.empty[rk.s]);
+          tc_commit(&ctl.s_full[buf]);
+          if (last) tc_commit(&ctl.q_empty[rq.s]);
+        }
+        rk.on();
+        ++scores;
+      };
+      while (ok) {
+        const uint32_t slot = items % kItems;
+        ok = warp_wait(&ctl.item_full[slot], (items / kItems) & 1u);
+        if (!ok) break;
+        const int nt = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tiles, 0);
+        int tok0 = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tile0, 0) * kTileTok;
+        const int begin = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].begin, 0);
+        const int end = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].end, 0);
+        if (nt >= 0 && leader) mbar_arrive(&ctl.item_empty[slot]);
+        ++items;
+        if (nt < 0) break;
+        if (nt == 0) continue;
+        rq.on();
+        ok = warp_wait(&ctl.q_full[rq.s], rq.phase);
+        if (!ok) break;
+        product_s(nt == 1);
+        for (int i = 0; i < nt && ok; ++i, ++tiles, tok0 += kTileTok) {
+          // whichever comes first, the next tile's keys or this one's weights
+          const uint32_t buf = tiles % S::PBUFS;
+          bool ahead = i + 1 == nt;
+          WaitClock clock;
+          for (;;) {
+            if (!ahead && warp_test(&ctl.full[rk.s], rk.phase)) {
+              product_s(i + 2 == nt);
+              ahead = true;
+            }
+            if (warp_test(&ctl.p_full[buf], (tiles / S::PBUFS) & 1u)) break;
+            ok = ok && !__any_sync(0xFFFFFFFFu, clock.expired());
+            if (!ok) break;
+          }
+          if (!ok) break;
+          // the groups' lists of the item are written
+          if (leader && i + 1 == nt) mbar_arrive(&ctl.odd_full);
+          ok = warp_wait(&ctl.full[rv.s], rv.phase);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t v0 = at(desc_v, s_ring + rv.s * S::kStage);
+            const uint64_t p0 = at(desc_p, s_p + buf * a.p_bytes);
+            // the steps of 32 tokens that some row sees
+            const int k0 = max(begin - tok0, 0) >> 5, k1 = (min(end - tok0, kTileTok) + 31) >> 5;
+            constexpr uint32_t kStep = 32 * S::D >> 4;  // of V
+            auto product_o = [&](uint32_t col, uint64_t p, uint32_t idesc) {
+              if (k0 == 0 && k1 == kTileTok / 32) {
+#pragma unroll
+                for (int k = 0; k < kTileTok / 32; ++k)
+                  tc_mma_f8(tmem + S::kColO + col, v0 + static_cast<uint32_t>(k * kStep),
+                            p + static_cast<uint32_t>(k * 32), idesc, k > 0 ? 1u : i > 0);
+              } else {
+#pragma unroll 1
+                for (int k = k0; k < k1; ++k)
+                  tc_mma_f8(tmem + S::kColO + col, v0 + static_cast<uint32_t>(k * kStep),
+                            p + static_cast<uint32_t>(k * 32), idesc, i > 0 || k > k0);
+              }
+            };
+            product_o(0, p0, idesc_o);
+            if (two) product_o(n_a, p0 + parts_a * (a.part_bytes >> 4), idesc_o2);
+            tc_commit(&ctl.empty[rv.s]);
+            tc_commit(&ctl.pv_done[buf]);
+          }
+          rv.on();
+          if (!ahead) product_s(i + 2 == nt);
+        }
+      }
+      if (!ok) {
+        set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
+        *reinterpret_cast<volatile int32_t*>(&ctl.abort) = 1;
+        if (leader) tc_commit(&ctl.drained);  // no product may outlive the CTA
+        warp_wait(&ctl.drained, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // =====================================================================
+    // queries: a group of lanes has a row in registers, 8 elements a lane, scales
+    // it and writes its parts. Two tiles of them where there is room, so that an
+    // item's are there when the one before it ends.
+    // =====================================================================
+    if (u_begin < u_end) {
+      constexpr int LPR = S::D / 8, kRows = 32 / LPR, kDeep = 4;
+      const int sub = lane / LPR, l = lane % LPR;
+      uint32_t items = 0, b = 0, wraps = 0;
+      bool ok = true;
+      for (;;) {
+        const uint32_t slot = items % kItems;
+        ok = warp_wait(&ctl.item_full[slot], (items / kItems) & 1u);
+        if (!ok) break;
+        const AttnItem& it = ctl.item[slot];
+        const int tiles = __shfl_sync(0xFFFFFFFFu, it.tiles, 0);
+        if (tiles < 0) break;
+        const int rows = min(it.t_rows * a.Gs, a.n_cols);
+        const uint16_t* const q0 = a.q + it.row0 * a.q_row + it.head0 * a.q_head + 8 * l;
+        ++items;
+        if (tiles > 0) {
+          if (wraps >= 1) ok = warp_wait(&ctl.q_empty[b], (wraps - 1u) & 1u);
+          if (!ok) break;
+          const uint32_t to = s_q + b * S::QP * q_part;
+          for (int j0 = sub; j0 < a.n_cols; j0 += kRows * kDeep) {
+            uint4 w[kDeep];
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+              const int j = j0 + k * kRows, t = j / a.Gs;
+              w[k] = make_uint4(0, 0, 0, 0);
+              if (j < rows)
+                w[k] = *reinterpret_cast<const uint4*>(q0 + t * a.q_row + (j - t * a.Gs) * a.q_head);
+            }
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+              const int j = j0 + k * kRows;
+              const uint32_t own[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+              float x[8];
+              uint32_t top = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 p = word_to_f32<S::F16>(own[e]);
+                x[2 * e] = p.x, x[2 * e + 1] = p.y;
+                top = max(top, max(__float_as_uint(p.x) & 0x7FFFFFFFu,
+                                   __float_as_uint(p.y) & 0x7FFFFFFFu));
+              }
+#pragma unroll
+              for (int o = LPR / 2; o >= 1; o >>= 1)
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+              // exponent of the largest element; rows below 2^-100 keep their size
+              const int e = max(static_cast<int>(top >> 23) - 127, -100);
+              const float f = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)  // not finite: NaN
+                x[i] = fabsf(x[i]) < INFINITY ? x[i] * f : NAN;
+              const uint32_t chunk = static_cast<uint32_t>(l) >> 1;
+              const uint32_t swap = S::D == 128 ? j & 7u : (static_cast<uint32_t>(j) >> 1) & 3u;
+              const uint32_t addr = to + j * S::D + ((chunk ^ swap) << 4) + (l & 1) * 8;
+#pragma unroll
+              for (int p = 0; p < S::QP; ++p) {
+                const uint32_t lo = e4m3x4(x[0], x[1], x[2], x[3]);
+                const uint32_t hi = e4m3x4(x[4], x[5], x[6], x[7]);
+                if (j < a.n_cols) sts_u2(addr + p * q_part, lo, hi);
+                if (p + 1 < S::QP) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float2 v = e4m3x2_to_f32((i < 2 ? lo : hi) >> (16 * (i & 1)));
+                    x[2 * i] -= v.x, x[2 * i + 1] -= v.y;
+                  }
+                }
+              }
+              if (l == 0 && j < a.n_cols)
+                ctl.cq[slot][j] = a.c * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+            }
+          }
+          fence_proxy_async();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (tiles > 0) mbar_arrive(&ctl.q_full[b]);
+          mbar_arrive(&ctl.factors[slot]);
+          mbar_arrive(&ctl.item_empty[slot]);
+        }
+        if (tiles > 0 && ++b == static_cast<uint32_t>(a.q_bufs)) b = 0, ++wraps;
+      }
+      if (!ok) {
+        set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
+        *reinterpret_cast<volatile int32_t*>(&ctl.abort) = 1;
+      }
+    }
+    __syncwarp();
+  } else if (u_begin < u_end) {
+    // =====================================================================
+    // softmax, results
+    // =====================================================================
+    const int group = (warp - 4) >> 2, quarter = warp & 3, bar = 1 + group;
+    const int gt = (quarter << 5) | lane;  // this thread's token of a tile, and lane of S and O
+    constexpr int kBlocks = S::NC / 8;     // of 8 columns
+    const int cols = a.Gs * a.t_chunk;
+    const int blocks = (cols + 8 * S::GROUPS - 1) / (8 * S::GROUPS);  // of the group, in use
+    const int c0 = group * blocks * 8;     // the group's first column
+    const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;  // (32 * quarter) << 16
+    const uint32_t window = static_cast<uint32_t>(a.window);
+    volatile int32_t* abort_flag = &ctl.abort;
+    uint32_t tiles = 0, items = 0, lists = 0;
+    const uint32_t v_end = a.k_stages + a.v_stages;
+    uint32_t v_s = a.k_stages, v_phase = 0;  // ring position of the next tile of values
+    int rv = 0;                              // weights stand for 2^-rv of their values
+    bool recorded = false;
+    for (int j = c0 + gt; j < min(c0 + 8 * blocks, S::NB); j += 128) {
+      const int t = j / a.Gs;
+      ctl.new_tok[j] = t;
+      ctl.at[j] = (t * a.Hq + j - t * a.Gs) * S::D;
+    }
+    bar_sync(bar, 128);
+    for (;;) {
+      const uint32_t slot = items % kItems, list = lists & 1u;
+      bool failed = !mbar_wait(&ctl.item_full[slot], (items / kItems) & 1u);
+      const AttnItem& it = ctl.item[slot];
+      if (!failed && it.tiles > 0) failed = !mbar_wait(&ctl.factors[slot], (items / kItems) & 1u);
+      const float* const cq = ctl.cq[slot];
+      float* const nref = ctl.nref[items & 1u];
+      int32_t* const lims = ctl.lim[items & 1u];
+      const int rows = failed ? 0 : max(it.t_rows * a.Gs, 0);
+      const int my_rows = max(0, min(8 * blocks, rows - c0));
+      const int nb = (my_rows + 7) >> 3;
+      for (int j = c0 + gt; j < c0 + 8 * nb; j += 128) {
+        // a column past the rows takes no part: all its scores are below its reference
+        nref[j] = j < rows ? kNoRef : -INFINITY;
+        lims[j] = j < rows ? it.lim0 + ctl.new_tok[j] : INT_MIN / 2;
+      }
+      if (group == 0 && gt == 0) ctl.odd_n[list] = 0;
+      if (bar_any(bar, 128, failed || *abort_flag != 0)) {
+        *abort_flag = 1;
+        break;
+      }
+      if (it.tiles < 0) break;
+      ++items;
+      const int lim_last = it.lim0 + it.t_rows - 1;
+      const int lo_last = a.window == INT_MAX ? 0 : max(0, lim_last - a.window);
+      // Sums of the columns' weights: a thread's own token's, in pairs; or, where
+      // that takes too many registers, folded tile by tile into one per block.
+      constexpr bool kPairs = S::NC <= 32;
+      uint64_t l[kPairs ? S::NC / 2 : 1];
+      float lf[kPairs ? 1 : kBlocks];
+      if constexpr (kPairs) {
+#pragma unroll
+        for (int j = 0; j < S::NC / 2; ++j) l[j] = 0;
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) lf[b] = 0.f;
+      }
+
+      const bool exact = S::NB <= kExactRows && it.tiles >= kExactTiles;
+      // weights are half precision numbers, whatever the outputs' type
+      const float base = exact ? kExactBase<true> : kBase<true>;
+      const float peak_base = exact ? kExactBase<true> : kPeakBase<true>;
+      const float highest = exact ? kExactBase<true> : kHighest<true>;
+      bool leave = false;
+      for (int i = 0; i < it.tiles; ++i, ++tiles) {
+        const uint32_t buf = tiles & 1u;
+        const int tok0 = (it.tile0 + i) * kTileTok, tok = tok0 + gt;
+        // every token of the tile visible to every row?
+        const bool whole = tok0 + kTileTok <= it.lim0 && tok0 >= lo_last;
+        // this token's scales; what no row sees has none
+        const bool some = tok >= it.begin && tok < it.end;
+        failed |= !mbar_wait(&ctl.full[v_s], v_phase);
+        float ks = 0.f, vs = 0.f;
+        if (some) {
+          const uint32_t from =
+              s_scale + (v_s - a.k_stages) * (8u * a.n_scales) + 4u * (gt >> min(a.b_shift, 7));
+          ks = lds_f32(from);
+          vs = lds_f32(from + 4u * a.n_scales);
+          if (!is_scale(ks) || !is_scale(vs)) {
+            set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
+            ks = vs = 1.f;
+          }
+        }
+        const int vexp = static_cast<int>(__float_as_uint(vs) >> 23) - 126;  // vs < 2^vexp
+        failed |= !mbar_wait(&ctl.s_full[buf], (tiles >> 1) & 1u);
+        tc_fence_after();
+        // scores, -inf where the row does not see the token
+        float x[S::NC];
+        const uint32_t s_addr = tmem + lanes + S::kColS + buf * S::NB + c0;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+          if (b < nb) tmem_ld8(s_addr + 8 * b, x + 8 * b);
+        tmem_wait_ld();
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+          if (b < nb) {
+            tmem_arrived(x + 8 * b);
+            // in powers of two: t = s ks cq
+            const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[c0 + 8 * b]);
+            const ulonglong2 f0 = cq4[0], f1 = cq4[1];
+            const uint64_t ks2 = pair(ks, ks), f[4] = {f0.x, f0.y, f1.x, f1.y};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float* y = x + 8 * b + 2 * k;
+              unpair(mul2(pair(y[0], y[1]), mul2(f[k], ks2)), y[0], y[1]);
+            }
+            if (!whole) {
+              const int4* lim4 = reinterpret_cast<const int4*>(&lims[c0 + 8 * b]);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int4 m = lim4[k];
+                float* y = x + 8 * b + 4 * k;
+                if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[0] = -INFINITY;
+                if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[1] = -INFINITY;
+                if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[2] = -INFINITY;
+                if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[3] = -INFINITY;
+              }
+            }
+          }
+        auto each = [&](auto f) {  // f(b) for every block in use
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            if (b < nb) f(b);
+        };
+        // exponents t - m
+        auto exponent = [&](int b, uint64_t (&y)[4]) {
+          const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(&nref[c0 + 8 * b]);
+          const ulonglong2 m0 = nr[0], m1 = nr[1];
+          const float* z = x + 8 * b;
+          y[0] = add2(pair(z[0], z[1]), m0.x);
+          y[1] = add2(pair(z[2], z[3]), m0.y);
+          y[2] = add2(pair(z[4], z[5]), m1.x);
+          y[3] = add2(pair(z[6], z[7]), m1.y);
+        };
+        bool raise = i == 0;  // the first tile's maxima
+        if (!raise) {
+          float top = -INFINITY;
+          each([&](int b) {
+            uint64_t e[4];
+            exponent(b, e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float y0, y1;
+              unpair(e[k], y0, y1);
+              top = fmaxf(top, fmaxf(y0, y1));
+            }
+          });
+          raise = bar_any(bar, 128, top > highest || vexp > rv || failed);
+        }
+        if (raise) {
+          each([&](int b) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)  // NaN takes no part
+              v[k] = x[8 * b + k] == x[8 * b + k] ? x[8 * b + k] : -INFINITY;
+            const float m = over_four<true>(fold_columns<true>(v, lane));
+            if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = m;
+          });
+          const int warp_vexp = __reduce_max_sync(0xFFFFFFFFu, vexp);
+          if (lane == 0) ctl.vexp[group][quarter] = warp_vexp;
+          if (bar_any(bar, 128, failed || *abort_flag != 0)) {
+            leave = true;
+            break;
+          }
+          const int* const ve = ctl.vexp[group];
+          const int top_vexp = max(max(ve[0], ve[1]), max(ve[2], ve[3]));
+          const int old_rv = rv;
+          if (i == 0 || top_vexp > rv) rv = min(max(top_vexp + kScaleRoom, -100), 120);
+          const float down_v = i == 0 ? 1.f : exp2f(static_cast<float>(old_rv - rv));
+          for (int j = c0 + gt; j < c0 + my_rows; j += 128) {
+            float top = -INFINITY, low = INFINITY;  // of the quarters that hold a token
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float v = ctl.red[w][j];
+              top = fmaxf(top, v);
+              if (v > -INFINITY) low = fminf(low, v);
+            }
+            const float m = top, down = top - low > kPeak ? peak_base : base;
+            const float ref = fabsf(m) < kNoShift ? m - down : m, old = -nref[j];
+            ctl.fac[j] = ref > old ? ex2_approx(old - ref) : 1.f;
+            if (ref > old) nref[j] = -ref;
+          }
+          bar_sync(bar, 128);
+          if (i > 0) {
+            const uint32_t before = tiles - 1u;
+            failed |= !mbar_wait(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+              if (b < nb) {
+                const float* f = &ctl.fac[c0 + 8 * b];
+#pragma unroll
+                for (int p = 0; p < S::PP; ++p) {
+                  const uint32_t at_o = tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b;
+                  float o[8];
+                  tmem_ld8(at_o, o);
+                  tmem_wait_ld();
+                  tmem_arrived(o);
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) o[k] *= f[k] * down_v;
+                  tmem_st8(at_o, o);
+                }
+                if constexpr (kPairs) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
+                } else {
+                  lf[b] *= f[lane >> 2];
+                }
+              }
+            tmem_wait_st();
+          }
+        }
+        // this buffer of weights is free once its last tile has been multiplied
+        const uint32_t pb = tiles % S::PBUFS, use = tiles / S::PBUFS;
+        const float vr = vs * __uint_as_float(static_cast<uint32_t>(127 - rv) << 23) *
+                         (S::PP == 3 ? kCut : 1.f);
+        const uint64_t vr2 = pair(vr, vr);
+        if (use >= 1) failed |= !mbar_wait(&ctl.pv_done[pb], (use - 1u) & 1u);
+        each([&](int b) {
+          uint64_t e[4];
+          float y[8];
+          exponent(b, e);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            unpair(e[k], y[2 * k], y[2 * k + 1]);
+            y[2 * k] = ex2_approx(y[2 * k]);
+            y[2 * k + 1] = ex2_approx(y[2 * k + 1]);
+            if constexpr (kPairs) l[4 * b + k] = add2(l[4 * b + k], pair(y[2 * k], y[2 * k + 1]));
+          }
+          // The weights enter the second product cut to their parts' bits (no more than
+          // the output's own rounding); their sum l is of the unrounded ones.
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float p0, p1;
+            unpair(mul2(pair(y[2 * k], y[2 * k + 1]), vr2), p0, p1);
+            h[k] = pack2<true>(p0, p1);
+          }
+          const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
+          const uint32_t to =
+              s_p + pb * a.p_bytes + (chunk >> 1) * 2048u + gt * 16u + (chunk & 1u) * 8u;
+#pragma unroll
+          for (int p = 0; p < S::PP; ++p) {
+            if (p > 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                h[k] = without_upper(h[k]);
+                if (p == S::PP - 1) h[k] = mul_f16x2(h[k], S::LAST == 4 ? 0x4C004C00u : 0x54005400u);
+              }
+            }
+            sts_u2(to + p * a.part_bytes, upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]));
+          }
+          if constexpr (!kPairs) lf[b] += fold_columns<false>(y, lane);
+        });
+        if (!whole && group == 0) {
+          // Zero weights do not silence values that are not finite, and the
+          // tile's rest may hold anything: what no row sees is zeroed, and of
+          // what only some rows see the non-finite values are taken out here
+          // and added to those rows at the end.
+          const bool all = tok < it.lim0 && tok >= lo_last;
+          // in a step of 32 tokens that is multiplied at all
+          const bool used = (tok | 31) >= it.begin && (tok & ~31) < it.end;
+          const uint32_t v_row = s_ring + v_s * S::kStage + gt * S::D;
+          if (!used) {
+          } else if (!some) {
+#pragma unroll
+            for (int k = 0; k < S::D / 16; ++k) sts_u4(v_row + k * 16, 0, 0, 0, 0);
+          } else if (!all) {
+            bool odd = false;
+#pragma unroll 4
+            for (int k = 0; k < S::D / 16; ++k) {
+              const uint4 v = lds_u4(v_row + k * 16);
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              bool hit = false;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                // bit 7 of each byte that is NaN (lower seven bits all set)
+                const uint32_t nan = ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                w[q] &= ~(nan | (nan - (nan >> 7)));
+                hit |= nan != 0;
+              }
+              if (hit) sts_u4(v_row + k * 16, w[0], w[1], w[2], w[3]);
+              odd |= hit;
+            }
+            if (odd) ctl.odd[list][atomicAdd(&ctl.odd_n[list], 1)] = tok;
+          }
+        }
+        if (++v_s == v_end) v_s = a.k_stages, v_phase ^= 1u;
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p_full[pb]);
+      }
+      if (leave) {
+        *abort_flag = 1;
+        break;
+      }
+
+      // ---- the item's rows ----------------------------------------------
+      const bool alone = it.starts && it.ends;
+      const int64_t part_row = static_cast<int64_t>(2 * id + (it.starts ? 1 : 0)) * a.n_cols;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+        if (b < nb) {
+          float sum;
+          if constexpr (kPairs) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) unpair(l[4 * b + k], v[2 * k], v[2 * k + 1]);
+            sum = over_four<false>(fold_columns<false>(v, lane));
+          } else {
+            sum = over_four<false>(lf[b]);
+          }
+          if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = sum;
+        }
+      if (bar_any(bar, 128, failed || *abort_flag != 0)) {
+        *abort_flag = 1;
+        break;
+      }
+      // every warp for itself: the factor of column j in lane j % 32
+      constexpr int kPer = (S::NC + 31) / 32;
+      float fac[kPer];
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const int j = c0 + 32 * q + lane;
+        fac[q] = 1.f;
+        if (32 * q + lane < my_rows) {
+          const float sum = (ctl.red[0][j] + ctl.red[1][j]) + (ctl.red[2][j] + ctl.red[3][j]);
+          const bool seen = lims[j] > 0;
+          if (alone) fac[q] = seen ? 1.f / sum : 0.f;  // no token: O is zero
+          if (quarter == 0) {
+            const float m = -nref[j];
+            if (!alone)
+              reinterpret_cast<float2*>(a.part_ml)[part_row + j] = make_float2(m, sum);
+            else if (a.lse)
+              a.lse[it.row0 * a.Hq + it.head0 + ctl.at[j] / S::D] =
+                  seen ? plus_log2(m, sum) * 0.69314718055994531f : -INFINITY;
+          }
+        }
+      }
+      if (it.tiles > 0) {
+        const uint32_t last = tiles - 1u;
+        failed |= !mbar_wait(&ctl.odd_full, lists & 1u);
+        failed |= !mbar_wait(&ctl.pv_done[last % S::PBUFS], (last / S::PBUFS) & 1u);
+        tc_fence_after();
+        ++lists;
+      }
+      if (failed) *abort_flag = 1;  // seen by all at the next item
+      const int odd_n = it.tiles > 0 ? ctl.odd_n[list] : 0;
+      const bool writer = S::D == 128 || lane < 16;  // M = 64 fills 16 lanes of each warp's 32
+      const int d = S::D == 128 ? gt : quarter * 16 + lane;
+      uint16_t* const out =
+          static_cast<uint16_t*>(a.out) + (it.row0 * a.Hq + it.head0) * S::D + d;
+      const float unit = __uint_as_float(static_cast<uint32_t>(rv + 127) << 23);
+      float* const part = a.part_o + (part_row + c0) * S::D + d;
+#pragma unroll 1
+      for (int b = 0; b < nb; ++b) {
+        float o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = 0.f;
+        if (it.tiles > 0) {
+          float parts[S::PP][8];
+#pragma unroll
+          for (int p = 0; p < S::PP; ++p)
+            tmem_ld8(tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b, parts[p]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int p = 0; p < S::PP; ++p) tmem_arrived(parts[p]);
+          constexpr float kLast = 1.f / (1 << S::LAST);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            o[k] = parts[S::PP - 1][k] * kLast;
+#pragma unroll
+            for (int p = S::PP - 2; p >= 0; --p) o[k] += parts[p][k];
+            o[k] *= unit;
+          }
+        }
+        for (int q = 0; q < odd_n; ++q) {
+          const int u = ctl.odd[list][q];
+          const int32_t page = a.table[it.r * a.stride + (u >> a.shift)];
+          if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages) || !writer) continue;
+          const uint32_t code = static_cast<const uint8_t*>(a.v_cache)[
+              page * a.page_stride + (u & ((1 << a.shift) - 1)) * a.token_stride +
+              it.kv_head * a.head_stride + d];
+          if ((code & 0x7Fu) != 0x7Fu) continue;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (static_cast<uint32_t>(lims[c0 + 8 * b + k] - 1 - u) < window) o[k] = NAN;
+        }
+        const int4* at4 = reinterpret_cast<const int4*>(&ctl.at[c0 + 8 * b]);
+        const int4 a0 = at4[0], a1 = at4[1];
+        const int to[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+        const float mine = kPer > 1 && b >= 4 ? fac[kPer - 1] : fac[0];
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = __shfl_sync(0xFFFFFFFFu, mine, (8 * b + k) & 31);
+        const int live = writer ? my_rows - 8 * b : 0;  // columns of the block to write
+        if (alone) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < live) out[to[k]] = static_cast<uint16_t>(pack2<S::F16>(o[k] * f[k], 0.f));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < live) part[(8 * b + k) * S::D] = o[k];
+        }
+      }
+      if (it.ends && !it.starts) {
+        recorded = true;
+        if (tid == 128) {
+          AttnRecord& rec = a.records[id];
+          rec.valid = 1;
+          rec.first = it.first;
+          rec.rows = rows;
+          rec.row0 = it.row0;
+          rec.head0 = it.head0;
+          rec.lim0 = it.lim0;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.item_empty[slot]);
+    }
+    if (!recorded && tid == 128) a.records[id].valid = 0;
+    if (*abort_flag != 0 && tid == 128) set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, S::kTmem);
+  if (tid == 0) a.records[id].status = ctl.status;
+}
+
+}  // namespace dspark

@@ -28,6 +28,9 @@ from .binding import DSPARK_BF16, DsparkError, made_on
 HEADER = os.path.join(binding.ROOT, "include", "dspark_paged.h")
 EXPORTED = ("dspark_pages_reserve", "dspark_pages_release", "dspark_kv_append",
             "dspark_paged_attention")
+# of the 8-bit cache (include/dspark_q8.h, paged_q8.py)
+EXPORTED_Q8 = ("dspark_rotary", "dspark_kv_append_q8", "dspark_kv_gather_q8",
+               "dspark_paged_attention_q8")
 
 
 def _header_const(name: str) -> int:
@@ -56,7 +59,8 @@ def _native():
             raise RuntimeError("the _paged_binding module is not built, or not for this Python and "
                                "torch; run `python -c 'import __graft_entry__ as g; g.build()'`")
         from . import _paged_binding
-        _paged_binding.bind(*(ctypes.cast(fns[name], ctypes.c_void_p).value for name in EXPORTED))
+        _paged_binding.bind(*(ctypes.cast(fns[name], ctypes.c_void_p).value
+                              for name in EXPORTED + EXPORTED_Q8))
         _ext = _paged_binding
     return _ext
 
@@ -76,9 +80,20 @@ def _load():
         lib.dspark_paged_attention.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, i32, i32, vp,
                                                i64, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32,
                                                i32, i32, vp, vp, vp, vp, sz, vp]
-        for name in EXPORTED:
+        lib.dspark_rotary.argtypes = [vp, i64, i64, vp, vp, i32, i32, i32, i32, i32, vp, i64, i64,
+                                      vp]
+        lib.dspark_kv_append_q8.argtypes = [vp, vp, i64, i64, vp, vp, vp, i32, i32, i32, i32, vp,
+                                            vp, i64, i64, i64, vp, vp, i64, i64, i64, i32, i32, i32,
+                                            vp, vp]
+        lib.dspark_kv_gather_q8.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, i64, i64, i32, i32,
+                                            i32, vp, i32, i32, i32, i32, vp, vp, i64, i64, vp, vp]
+        lib.dspark_paged_attention_q8.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, vp, vp, i64,
+                                                  i64, i64, i32, i32, i32, vp, i64, i32, vp, vp,
+                                                  i32, i32, i32, i32, i32, i32, f32, i32, i32, vp,
+                                                  vp, vp, vp, sz, vp]
+        for name in EXPORTED + EXPORTED_Q8:
             getattr(lib, name).restype = ctypes.c_int
-        _fns = {name: getattr(lib, name) for name in EXPORTED}
+        _fns = {name: getattr(lib, name) for name in EXPORTED + EXPORTED_Q8}
     return _fns
 
 

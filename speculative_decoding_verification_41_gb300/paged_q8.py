@@ -1,0 +1,356 @@
+"""The paged key-value cache in 8 bits, and rotary positions (include/dspark_q8.h):
+argument checks and marshalling only, every step runs in the CUDA kernels of
+libdspark.so. A call with its buffers goes through the _paged_binding module
+(csrc/paged_binding.cpp), which makes the same checks in a fraction of the time;
+what does not pass them there comes back to the ones here, and through ctypes.
+
+  RotaryTable(...)                the angles of a rotation, also stretched for long contexts
+  dspark_rotary(...)              positions into queries (or keys)
+  dspark_kv_append_q8(...)        keys (turned on the way, if wanted) and values into the cache
+  dspark_kv_gather_q8(...)        stored tokens back in 16 bits
+  dspark_paged_attention_q8(...)  attention of the new tokens over the cache
+
+Caches are [num_pages, page_size, heads, D] tensors of torch.float8_e4m3fn of any
+strides with contiguous D, scales [num_pages, page_size / block, heads] float32 tensors
+of any strides: a stored element is its code times its block's scale. Pages are reserved
+and released as for the 16-bit cache (paged.py).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+from typing import Optional
+
+import torch
+
+from . import binding, paged
+from .binding import DSPARK_BF16, DsparkError, made_on
+from .paged import (DSPARK_F16, AttentionBuffers, _checked, _fn, _handle, _index, _on, _table,
+                    _want)
+
+HEADER = os.path.join(binding.ROOT, "include", "dspark_q8.h")
+EXPORTED = paged.EXPORTED_Q8
+E4M3 = torch.float8_e4m3fn
+_DTYPES = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16}
+_I32 = torch.int32
+_native = paged._native
+
+
+class RotaryTable:
+    """The rotation of a head's first rot_dim elements: pair j turns by position * f_j with
+    f_j = base^(-2j / rot_dim), stretched for contexts longer than original_len by
+
+      "linear"  f_j / factor;
+      "ntk"     base * factor^(rot_dim / (rot_dim - 2)) in base's place (the fastest pair keeps
+                its angle, the slowest one's is divided by factor);
+      "yarn"    by parts: pairs that turn more than `fast` times in original_len positions keep
+                their angle, those of less than `slow` turns are divided by factor, with a ramp
+                over the turns in between; sines and cosines times 0.1 ln(factor) + 1.
+
+    interleaved: pairs are (2j, 2j + 1), else (j, j + rot_dim / 2). gain: the factor of sines and
+    cosines, if another than the scaling's own. A table of other angles is made with
+    RotaryTable.of(angles in radians per position)."""
+
+    def __init__(self, rot_dim: int, *, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, original_len: int = 0,
+                 fast: float = 32.0, slow: float = 1.0, gain: Optional[float] = None,
+                 device="cuda"):
+        if rot_dim < 16 or rot_dim % 16 != 0 or rot_dim > 128:
+            raise ValueError(f"rot_dim must be a multiple of 16 up to 128, got {rot_dim}")
+        if scaling not in ("none", "linear", "ntk", "yarn"):
+            raise ValueError(f"scaling must be none, linear, ntk or yarn, got {scaling!r}")
+        if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
+            raise ValueError(f"base and factor must be positive, got {base} and {factor}")
+        if scaling == "ntk":
+            base *= factor ** (rot_dim / (rot_dim - 2))
+        f = [base ** (-2.0 * j / rot_dim) for j in range(rot_dim // 2)]
+        own_gain = 1.0
+        if scaling == "linear":
+            f = [x / factor for x in f]
+        elif scaling == "yarn":
+            if original_len < 1 or not fast > slow:
+                raise ValueError("yarn needs original_len >= 1 and fast > slow")
+            turns = [original_len * x / (2 * math.pi) for x in f]
+            keep = [min(max((t - slow) / (fast - slow), 0.0), 1.0) for t in turns]
+            f = [k * x + (1 - k) * x / factor for k, x in zip(keep, f)]
+            own_gain = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+        self._set(f, interleaved, own_gain if gain is None else gain, device)
+
+    @classmethod
+    def of(cls, angles, *, interleaved: bool = False, gain: float = 1.0,
+           device="cuda") -> "RotaryTable":
+        """A table of these angles per position (radians, rot_dim / 2 numbers)."""
+        angles = [float(x) for x in angles]
+        if len(angles) < 8 or len(angles) % 8 != 0 or len(angles) > 64:
+            raise ValueError(f"a multiple of 8 angles up to 64, got {len(angles)}")
+        self = cls.__new__(cls)
+        self._set(angles, interleaved, gain, device)
+        return self
+
+    def _set(self, angles, interleaved, gain, device):
+        if not all(math.isfinite(x) for x in angles) or not math.isfinite(gain):
+            raise ValueError("angles and gain must be finite")
+        self.angles, self.rot_dim, self.interleaved = angles, 2 * len(angles), bool(interleaved)
+        self.gain = float(gain)
+        # parts of a full turn per position as 64-bit fractions
+        fractions = [round(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for x in angles]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in fractions],
+                                  dtype=torch.int64, device=device)
+        self.c = _Rotation(self.turns.data_ptr(), self.rot_dim, int(self.interleaved), self.gain)
+        self.address = ctypes.addressof(self.c)
+
+
+class _Rotation(ctypes.Structure):
+    """dspark_rotation"""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("pairs", ctypes.c_int32), ("gain", ctypes.c_float)]
+
+
+def _rotation(name: str, table: RotaryTable, index: int) -> int:
+    if not isinstance(table, RotaryTable):
+        raise ValueError(f"{name} must be a RotaryTable")
+    if table.turns.get_device() != index:
+        raise ValueError(f"{name} is on {table.turns.device}, the tensors on cuda:{index}")
+    return table.address
+
+
+def _rows(name: str, t, index: int, heads: Optional[int], D: int, dtype=None):
+    """[n, heads, D] of a 16-bit type with contiguous rows; its type number."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+    number = _DTYPES.get(t.dtype)
+    if number is None or (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{name} must be {dtype or 'bfloat16 or float16'}, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != D \
+            or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [n, {heads or 'heads'}, {D}] with contiguous rows, got "
+                         f"{tuple(t.shape)}")
+    return number
+
+
+def _cache_q8(k_cache, v_cache, k_scale, v_scale, index: int):
+    """Shape and strides of the two caches, strides of their scales and tokens of a block."""
+    for name, t, dtype in (("k_cache", k_cache, E4M3), ("v_cache", v_cache, E4M3),
+                           ("k_scale", k_scale, torch.float32),
+                           ("v_scale", v_scale, torch.float32)):
+        if not isinstance(t, torch.Tensor) or t.get_device() != index:
+            raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or stride[3] != 1:
+        raise ValueError("caches must be [pages, page_size, heads, D] with contiguous D")
+    if v_cache.shape != shape or v_cache.stride() != stride:
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    blocks = k_scale.shape[1] if k_scale.dim() == 3 else 0
+    if blocks < 1 or shape[1] % blocks != 0 or k_scale.shape != (shape[0], blocks, shape[2]):
+        raise ValueError(f"k_scale must be [{shape[0]}, page_size / block, {shape[2]}], got "
+                         f"{tuple(k_scale.shape)}")
+    if v_scale.shape != k_scale.shape or v_scale.stride() != k_scale.stride():
+        raise ValueError("k_scale and v_scale must have the same shape and strides")
+    return shape, stride, k_scale.stride(), shape[1] // blocks
+
+
+def dspark_rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable, *,
+                  out: Optional[torch.Tensor] = None, inverse: bool = False, stream=None) -> dict:
+    """Row i of x ([n, heads, D], any strides, contiguous D), all its heads, turned by
+    positions[i] (include/dspark_q8.h); rows with a negative position are not written. positions
+    may be longer than n: its first n entries count. out may be x. inverse turns the other way:
+    a gradient with respect to the result becomes one with respect to x.
+
+    Returns out [n, heads, D]."""
+    rc = None
+    if out is not None and isinstance(table, RotaryTable):
+        rc = (paged._ext or _native()).rotary(x, positions, table.turns, table.address, inverse,
+                                              out, _handle(stream, x))
+    if rc is None:
+        dev = _index("x", x)
+        D = x.shape[-1]
+        dtype = _rows("x", x, dev, None, D)
+        n, heads, _ = x.shape
+        _want("positions", positions, _I32, dev)
+        if positions.numel() < n:
+            raise ValueError(f"positions has {positions.numel()} entries for {n} rows")
+        rotation = _rotation("table", table, dev)
+        s = _on(stream, dev)
+        if out is None:
+            out = made_on(stream, lambda: torch.empty(n, heads, D, dtype=x.dtype, device=x.device))
+        else:
+            _rows("out", out, dev, heads, D, x.dtype)
+            if out.shape[0] != n:
+                raise ValueError(f"out must be [{n}, {heads}, {D}], got {tuple(out.shape)}")
+        rc = _fn("dspark_rotary", dev)(
+            x.data_ptr(), x.stride(0), x.stride(1), positions.data_ptr(), rotation,
+            1 if inverse else 0, n, heads, D, dtype, out.data_ptr(), out.stride(0), out.stride(1),
+            s)
+    if rc != 0:
+        raise DsparkError("dspark_rotary", rc)
+    return {"out": out}
+
+
+def _status(device_status, stream, dev: int, device) -> torch.Tensor:
+    if device_status is None:
+        return made_on(stream, lambda: torch.empty(1, dtype=_I32, device=device))
+    _want("device_status", device_status, _I32, dev, (1,))
+    return device_status
+
+
+def dspark_kv_append_q8(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
+                        k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                        v_scale: torch.Tensor, *, rotary: Optional[RotaryTable] = None,
+                        positions: Optional[torch.Tensor] = None,
+                        device_status: Optional[torch.Tensor] = None, stream=None,
+                        check: bool = False) -> dict:
+    """Row i of k and v ([n, heads, D], any strides alike, contiguous D) into slot slot_map[i] of
+    the caches, with the scales of the blocks it joins, in place; negative slots are skipped
+    (include/dspark_q8.h). With `rotary`, k is turned by positions[i] on the way. slot_map and
+    positions may be longer than n. Rows of one block must be neighbours in slot_map, as a
+    reservation gives them. Returns device_status [1]."""
+    rc = None
+    if device_status is not None and (rotary is None or isinstance(rotary, RotaryTable)):
+        rc = (paged._ext or _native()).append_q8(
+            k, v, slot_map, k_cache, v_cache, k_scale, v_scale,
+            None if rotary is None else rotary.turns, 0 if rotary is None else rotary.address,
+            None if rotary is None else positions, device_status, _handle(stream, k_cache))
+    if rc is None:
+        dev = _index("k_cache", k_cache)
+        (pages, page_size, Hkv, D), (sp, st, sh, _), sc, block = _cache_q8(k_cache, v_cache,
+                                                                           k_scale, v_scale, dev)
+        dtype = _rows("k", k, dev, Hkv, D)
+        _rows("v", v, dev, Hkv, D, k.dtype)
+        if v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError("k and v must have the same shape and strides")
+        n = k.shape[0]
+        _want("slot_map", slot_map, _I32, dev)
+        if slot_map.numel() < n:
+            raise ValueError(f"slot_map has {slot_map.numel()} entries for {n} rows")
+        rotation = at = None
+        if rotary is not None:
+            rotation = _rotation("rotary", rotary, dev)
+            _want("positions", positions, _I32, dev)
+            if positions.numel() < n:
+                raise ValueError(f"positions has {positions.numel()} entries for {n} rows")
+            at = positions.data_ptr()
+        s = _on(stream, dev)
+        device_status = _status(device_status, stream, dev, k_cache.device)
+        rc = _fn("dspark_kv_append_q8", dev)(
+            k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), rotation, at,
+            slot_map.data_ptr(), n, Hkv, D, dtype, k_cache.data_ptr(), v_cache.data_ptr(), sp, st,
+            sh, k_scale.data_ptr(), v_scale.data_ptr(), *sc, block, page_size, pages,
+            device_status.data_ptr(), s)
+    if rc != 0:
+        raise DsparkError("dspark_kv_append_q8", rc)
+    if check:
+        _checked("dspark_kv_append_q8", device_status, stream)
+    return {"device_status": device_status}
+
+
+class _KeysValues:
+    def __init__(self, n: int, heads: int, D: int, dtype, device):
+        self.k, self.v = (torch.zeros(n, heads, D, dtype=dtype, device=device) for _ in range(2))
+
+
+def dspark_kv_gather_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                        v_scale: torch.Tensor, slot_map: torch.Tensor, *,
+                        dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
+                        v: Optional[torch.Tensor] = None,
+                        device_status: Optional[torch.Tensor] = None, stream=None,
+                        check: bool = False) -> dict:
+    """The tokens of these slots back in 16 bits (include/dspark_q8.h): row i of k and v, [n,
+    heads, D] of k's type, or new tensors of `dtype` with a row per entry of slot_map. Rows with a
+    negative slot are not written (in new tensors they are zero).
+
+    Returns k, v, device_status [1]."""
+    rc = None
+    if k is not None and device_status is not None:
+        rc = (paged._ext or _native()).gather_q8(k_cache, v_cache, k_scale, v_scale, slot_map, k,
+                                                 v, device_status, _handle(stream, k_cache))
+    if rc is None:
+        dev = _index("k_cache", k_cache)
+        (pages, page_size, Hkv, D), (sp, st, sh, _), sc, block = _cache_q8(k_cache, v_cache,
+                                                                           k_scale, v_scale, dev)
+        _want("slot_map", slot_map, _I32, dev)
+        s = _on(stream, dev)
+        if (k is None) != (v is None):
+            raise ValueError("k and v are given together or not at all")
+        if k is None:
+            if dtype not in _DTYPES:
+                raise ValueError(f"dtype must be bfloat16 or float16, got {dtype}")
+            made = made_on(stream, lambda: _KeysValues(slot_map.numel(), Hkv, D, dtype,
+                                                       k_cache.device))
+            k, v = made.k, made.v
+        number = _rows("k", k, dev, Hkv, D)
+        _rows("v", v, dev, Hkv, D, k.dtype)
+        if v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError("k and v must have the same shape and strides")
+        n = k.shape[0]
+        if slot_map.numel() < n:
+            raise ValueError(f"slot_map has {slot_map.numel()} entries for {n} rows")
+        device_status = _status(device_status, stream, dev, k_cache.device)
+        rc = _fn("dspark_kv_gather_q8", dev)(
+            k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, k_scale.data_ptr(),
+            v_scale.data_ptr(), *sc, block, page_size, pages, slot_map.data_ptr(), n, Hkv, D,
+            number, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+            device_status.data_ptr(), s)
+    if rc != 0:
+        raise DsparkError("dspark_kv_gather_q8", rc)
+    if check:
+        _checked("dspark_kv_gather_q8", device_status, stream)
+    return {"k": k, "v": v, "device_status": device_status}
+
+
+def dspark_paged_attention_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              k_scale: torch.Tensor, v_scale: torch.Tensor,
+                              block_table: torch.Tensor, context_len: torch.Tensor,
+                              row_off: torch.Tensor, *, scale: float, max_new: int,
+                              window: int = 0, with_lse: bool = False,
+                              buffers: Optional[AttentionBuffers] = None, stream=None,
+                              check: bool = False) -> dict:
+    """dspark_paged_attention (paged.py) over the 8-bit cache: the same requests, rows, windows
+    and buffers (include/dspark_q8.h). q is [n_tokens, Hq, D] bfloat16 or float16.
+
+    Returns out [n_tokens, Hq, D] of q's type, lse [n_tokens, Hq] float32 (or None) and
+    device_status [1] (device tensors)."""
+    buf, rc = buffers, None
+    if buf is not None:
+        if with_lse and buf.lse is None:
+            raise ValueError("buffers were made without lse (AttentionBuffers(..., with_lse=True))")
+        rc = (paged._ext or _native()).attention_q8(
+            q, k_cache, v_cache, k_scale, v_scale, block_table, context_len, row_off, scale,
+            max_new, window, buf.out, buf.lse if with_lse else None, buf.device_status,
+            buf.workspace, _handle(stream, k_cache))
+    if rc is None:
+        dev = _index("k_cache", k_cache)
+        (pages, page_size, Hkv, D), (sp, st, sh, _), sc, block = _cache_q8(k_cache, v_cache,
+                                                                           k_scale, v_scale, dev)
+        dtype = _rows("q", q, dev, None, D)
+        n, Hq, _ = shape = q.shape
+        B = context_len.numel()
+        _want("context_len", context_len, _I32, dev, (B,))
+        _want("row_off", row_off, torch.int64, dev, (B + 1,))
+        stride, width = _table(block_table, B, dev)
+        if Hkv < 1 or Hq < 1 or Hq % Hkv != 0 or max_new < 1:
+            raise ValueError(f"{Hq} query heads on {Hkv} key heads, max_new {max_new}")
+        s = _on(stream, dev)
+        if buf is None:
+            buf = made_on(stream, lambda: AttentionBuffers(n, Hq, Hkv, D, max_new, q.dtype,
+                                                           q.device, with_lse))
+        _want("buffers.out", buf.out, q.dtype, dev, shape)
+        if with_lse:
+            _want("buffers.lse", buf.lse, torch.float32, dev, (n, Hq))
+        _want("buffers.device_status", buf.device_status, _I32, dev, (1,))
+        _want("buffers.workspace", buf.workspace, torch.uint8, dev)
+        rc = _fn("dspark_paged_attention_q8", dev)(
+            q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), sp, st,
+            sh, k_scale.data_ptr(), v_scale.data_ptr(), *sc, block, page_size, pages,
+            block_table.data_ptr(), stride, width, context_len.data_ptr(), row_off.data_ptr(), B, n,
+            Hq, Hkv, D, max_new, scale, window, dtype, buf.out.data_ptr(),
+            buf.lse.data_ptr() if with_lse else None, buf.device_status.data_ptr(),
+            buf.workspace.data_ptr(), buf.workspace.numel(), s)
+    if rc != 0:
+        raise DsparkError("dspark_paged_attention_q8", rc)
+    if check:
+        _checked("dspark_paged_attention_q8", buf.device_status, stream)
+    return {"out": buf.out, "lse": buf.lse if with_lse else None,
+            "device_status": buf.device_status}
