@@ -151,6 +151,7 @@ struct Line {
   }
 };
 
+template <int TILE = kTileTok>  // tokens of a tile
 __device__ __forceinline__ bool attn_request(const AttnArgs& a, int r, int t0, AttnReq& q) {
   const int64_t o0 = a.row_off[r], o1 = a.row_off[r + 1];
   const int32_t len = a.ctx[r];
@@ -166,7 +167,7 @@ __device__ __forceinline__ bool attn_request(const AttnArgs& a, int r, int t0, A
   q.end = max(0, q.lim0 + q.t_rows - 1);
   q.begin = min(q.end, max(0, q.lim0 > a.window ? q.lim0 - a.window : 0));
   // an item without tiles still has rows to write: it counts as one
-  q.units = a.lead + (q.end > 0 ? (q.end + kTileTok - 1) / kTileTok - q.begin / kTileTok : 1);
+  q.units = a.lead + (q.end > 0 ? (q.end + TILE - 1) / TILE - q.begin / TILE : 1);
   return true;
 }
 

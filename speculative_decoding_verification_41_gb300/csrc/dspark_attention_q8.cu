@@ -38,24 +38,24 @@ int q8_launch(LaunchQ8& c, int sms) {
     std::lock_guard<std::mutex> lock(g_attn_mutex);
     if (!ready[dev]) {
       if (cudaFuncSetAttribute(k_attention_q8<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kSmemCta<S::CTAS>) != cudaSuccess)
+                               kSmemCta<1>) != cudaSuccess)
         return DSPARK_ERR_CUDA;
       ready[dev] = true;
     }
   }
   AttnQ8Args& a = c.a;
-  a.ctas = std::max(1, std::min(sms * S::CTAS, DSPARK_PAGED_MAX_CTAS) / a.n_chunks);
+  a.ctas = std::max(1, std::min(sms, DSPARK_PAGED_MAX_CTAS) / a.n_chunks);
   const int grid = a.ctas * a.n_chunks;
   // Shared memory: what the queries, the weights and the scales leave is the rings'. A
   // second tile of queries where it costs them no tile.
-  constexpr uint32_t kSmem = kSmemCta<S::CTAS>;
+  constexpr uint32_t kSmem = kSmemCta<1>;
   const uint32_t q_bytes = static_cast<uint32_t>(S::QP * S::D * a.n_cols);
   a.part_bytes = static_cast<uint32_t>(a.n_cols / 16 * 2048);
   a.p_bytes = S::PP * a.part_bytes;
   auto ring_stages = [&](int q_bufs) {
     a.q_bufs = q_bufs;
     a.p_off = kQ8CtlBytes<S> + q_bufs * q_bytes;
-    a.scale_off = a.p_off + S::PBUFS * a.p_bytes;
+    a.scale_off = a.p_off + S::PBUFS * S::HALVES * a.p_bytes;
     auto ring_at = [&](int v_stages) {
       return (a.scale_off + v_stages * 8u * a.n_scales + 1023u) & ~1023u;
     };
@@ -89,15 +89,16 @@ int q8_launch(LaunchQ8& c, int sms) {
 
 // Rows that a pass can serve: two buffers of scores and the parts of the outputs fill the
 // 512 columns of tensor memory.
-constexpr int q8_max_rows(bool f16) { return f16 ? 80 : 96; }
+constexpr int kMaxRows = 80;
 
 // The smallest row block that holds the rows; keys are copied once for all of them.
 template <int D, bool F16>
 int q8_shape(LaunchQ8& c, int sms) {
-  if (c.a.n_cols <= 16) return q8_launch<AttnQ8Shape<D, F16, 16, 1, 2, 2>>(c, sms);
-  if (c.a.n_cols <= 32) return q8_launch<AttnQ8Shape<D, F16, 32, 1, 2, 2>>(c, sms);
-  if (c.a.n_cols <= 64) return q8_launch<AttnQ8Shape<D, F16, 64, 4, 1, 2>>(c, sms);
-  return q8_launch<AttnQ8Shape<D, F16, q8_max_rows(F16), 3, 1, 2>>(c, sms);
+  if (c.a.n_cols <= 16) return q8_launch<AttnQ8Shape<D, F16, 16, 1, false, 2>>(c, sms);
+  if (c.a.n_cols <= 32) return q8_launch<AttnQ8Shape<D, F16, 32, 2, false, 2>>(c, sms);
+  if (c.a.n_cols <= 48) return q8_launch<AttnQ8Shape<D, F16, 48, 3, false, F16 ? 1 : 2>>(c, sms);
+  if (c.a.n_cols <= 64) return q8_launch<AttnQ8Shape<D, F16, 64, 2, true, 2>>(c, sms);
+  return q8_launch<AttnQ8Shape<D, F16, kMaxRows, 3, true, 2>>(c, sms);
 }
 
 }  // namespace
@@ -121,7 +122,7 @@ extern "C" int dspark_paged_attention_q8(
       page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0 || num_pages < 1 ||
       block < 1 || block > page_size || (block & (block - 1)) != 0 ||
       static_cast<int64_t>(num_pages) * page_size > INT32_MAX || max_pages < 1 ||
-      static_cast<int64_t>(max_pages) * page_size > INT32_MAX - 2 * kTileTok ||
+      static_cast<int64_t>(max_pages) * page_size > INT32_MAX - 2 * kQ8Tile ||
       static_cast<int64_t>(max_pages) * page_size / kTileTok * Hkv > INT32_MAX / 2 ||
       table_stride < max_pages || !device_status)
     return DSPARK_ERR_INVALID_ARG;
@@ -147,10 +148,9 @@ extern "C" int dspark_paged_attention_q8(
   a.G = Hq / Hkv;
   a.parts = 1;  // of a group of query heads, if it has more than fit
   const bool f16 = dtype == DSPARK_F16;
-  const int max_rows = q8_max_rows(f16);
-  while (a.G % a.parts != 0 || a.G / a.parts > max_rows) ++a.parts;
+  while (a.G % a.parts != 0 || a.G / a.parts > kMaxRows) ++a.parts;
   a.Gs = a.G / a.parts;
-  const int fit = max_rows / a.Gs;
+  const int fit = kMaxRows / a.Gs;
   const int t_chunks = (max_new + fit - 1) / fit;
   a.t_chunk = (max_new + t_chunks - 1) / t_chunks;
   a.n_chunks = a.parts * t_chunks;
@@ -165,7 +165,7 @@ extern "C" int dspark_paged_attention_q8(
   a.scale_block = scale_block_stride, a.scale_head = scale_head_stride;
   while ((1 << a.shift) < page_size) ++a.shift;
   while ((1 << a.b_shift) < block) ++a.b_shift;
-  a.n_scales = kTileTok / std::min(block, kTileTok);
+  a.n_scales = kQ8Tile / std::min(block, kQ8Tile);
   a.window = window > 0 ? window : INT_MAX;
   a.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -186,7 +186,7 @@ extern "C" int dspark_paged_attention_q8(
                             static_cast<cuuint64_t>(head_stride),
                             static_cast<cuuint64_t>(page_stride)};
   const cuuint32_t cb[4] = {static_cast<cuuint32_t>(D),
-                            static_cast<cuuint32_t>(std::min(page_size, kTileTok)), 1, 1};
+                            static_cast<cuuint32_t>(std::min(page_size, kQ8Tile)), 1, 1};
   if (!q8_map(&c.k, k_cache, D, cd, cs, cb) || !q8_map(&c.v, v_cache, D, cd, cs, cb))
     return DSPARK_ERR_INVALID_ARG;
   if (D == 64) return f16 ? q8_shape<64, true>(c, sms) : q8_shape<64, false>(c, sms);

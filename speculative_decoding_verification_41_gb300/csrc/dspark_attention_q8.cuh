@@ -84,6 +84,51 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// N times 8 consecutive f32 columns of this thread's lane. The loads and the wait for them
+// are one statement: a register that a load is still to write must not be moved, spilled or
+// given to another value before, which the compiler cannot know.
+template <int N>
+__device__ __forceinline__ void tmem_read(const uint32_t (&at)[N], float (&v)[N][8]) {
+  if constexpr (N == 1)
+    asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]), "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7])
+      : "r"(at[0])
+      : "memory");
+  if constexpr (N == 2)
+    asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]), "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]), "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]), "=&f"(v[1][7])
+      : "r"(at[0]), "r"(at[1])
+      : "memory");
+  if constexpr (N == 3)
+    asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%24];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%25];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%26];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]), "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]), "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]), "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]), "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7])
+      : "r"(at[0]), "r"(at[1]), "r"(at[2])
+      : "memory");
+  if constexpr (N == 4)
+    asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]), "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]), "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]), "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]), "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7]), "=&f"(v[3][0]), "=&f"(v[3][1]), "=&f"(v[3][2]), "=&f"(v[3][3]), "=&f"(v[3][4]), "=&f"(v[3][5]), "=&f"(v[3][6]), "=&f"(v[3][7])
+      : "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3])
+      : "memory");
+}
 // A part of four half precision numbers (two words): their upper bytes.
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) {
   return __byte_perm(a, b, 0x7531);
@@ -94,6 +139,10 @@ __device__ __forceinline__ uint32_t without_upper(uint32_t a) {
 }
 
 constexpr int kQ8MaxStages = 16;
+// Tokens of a tile of the line: two instructions of 128. A tile's way through the barriers
+// and the copies takes each warp some 1,000 cycles whatever its work, which is why it is
+// twice the instruction's.
+constexpr int kQ8Tile = 2 * kTileTok;
 // Room (log2) above the first tile's largest value scale.
 constexpr int kScaleRoom = 1;
 // Weights of three parts are cut, not rounded: by 2^-9 of their power of two on average,
@@ -102,21 +151,27 @@ constexpr int kScaleRoom = 1;
 // power of two, like a row's largest one can be, free of rounding.
 constexpr float kCut = 1.f + 0.7213f / 512.f;
 
-template <int D_, bool F16_, int NB_, int GROUPS_, int CTAS_, int PBUFS_>
+// SPLIT: a tile's weights are made and multiplied in two units, one per 128 tokens, and the
+// parts of P but the last add up in one accumulator: for the rows whose weights and outputs
+// would not fit otherwise. PBUFS: buffers of a unit's weights. There are two of a tile's scores.
+template <int D_, bool F16_, int NB_, int GROUPS_, bool SPLIT_, int PBUFS_>
 struct AttnQ8Shape {
-  static constexpr int D = D_, NB = NB_, GROUPS = GROUPS_, CTAS = CTAS_;
-  static constexpr bool F16 = F16_;
-  static constexpr int PBUFS = PBUFS_;
-  static constexpr int QP = F16 ? 3 : 2, PP = F16 ? 4 : 3;  // parts of Q and of P
-  static constexpr int LAST = F16 ? 6 : 4;                  // scale (log2) of P's last part
+  static constexpr int D = D_, NB = NB_, GROUPS = GROUPS_, PBUFS = PBUFS_;
+  static constexpr bool F16 = F16_, SPLIT = SPLIT_;
+  static constexpr int UNITS = SPLIT ? 2 : 1, HALVES = 2 / UNITS;  // of a tile; 128s of a unit
+  static constexpr int QP = F16 ? 3 : 2, PP = F16 ? 4 : 3;         // parts of Q and of P
+  static constexpr int LAST = F16 ? 6 : 4;                         // scale (log2) of P's last part
+  static constexpr int ACCS = SPLIT ? 2 : PP;                      // accumulators of the outputs
   static constexpr int THREADS = 128 + 128 * GROUPS;
-  static constexpr int NC = (NB / 8 + GROUPS - 1) / GROUPS * 8;
-  static constexpr uint32_t kStage = kTileTok * D;
-  static constexpr uint32_t kColS = 0, kColO = 2 * NB;
-  static constexpr int kCols = (2 + PP) * NB;
-  static constexpr uint32_t kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static constexpr int NC = (NB / 8 + GROUPS - 1) / GROUPS * 8;  // columns of a softmax group
+  static constexpr int WIDTH = NC * GROUPS;  // columns of all groups, NB and more
+  static constexpr uint32_t kStage = kQ8Tile * D;
+  static constexpr int kCols = (4 + ACCS) * NB;
+  static constexpr uint32_t kColS = 0, kColO = 4 * NB;
+  static constexpr uint32_t kTmem = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;  // of rows of D bytes
-  static_assert(kCols <= 512 && CTAS * kTmem <= 512, "tensor memory");
+  static_assert(kCols <= 512, "tensor memory");
+  static_assert(NC <= 32, "sums of a thread's columns in registers");
 };
 
 template <class S>
@@ -131,14 +186,14 @@ struct AttnQ8Ctl {
   AttnItem item[kItems];
   // per column (row of q); a group's own. Two of what an item begins with: its
   // slower warps may still write their results when the next one begins.
-  alignas(16) float nref[2][S::NB + 8];   // minus the rows' references
-  alignas(16) int32_t lim[2][S::NB + 8];  // a row sees the tokens below (and within the window)
-  alignas(16) int32_t at[S::NB + 8];      // element of a row in out, from the item's first
-  alignas(16) float fac[S::NB + 8];       // factor of a row's sums when its reference rises
-  alignas(16) float cq[kItems][S::NB + 8];  // per item: scale * log2(e) over the row's power of two
+  alignas(16) float nref[2][S::WIDTH];   // minus the rows' references
+  alignas(16) int32_t lim[2][S::WIDTH];  // a row sees the tokens below (and within the window)
+  alignas(16) int32_t at[S::WIDTH];      // element of a row in out, from the item's first
+  alignas(16) float fac[S::WIDTH];       // factor of a row's sums when its reference rises
+  alignas(16) float cq[kItems][S::WIDTH];  // per item: scale * log2(e) over the row's power of two
   int32_t vexp[S::GROUPS][4];             // per warp of a group: exponent of the largest value scale
-  int32_t new_tok[S::NB + 8];             // new token of a column
-  float red[4][S::NB + 8];                // per warp: maxima, sums
+  int32_t new_tok[S::WIDTH];             // new token of a column
+  float red[4][S::WIDTH];                // per warp: maxima, sums
   int32_t odd_n[2], odd[2][2 * S::NB];  // tokens whose values are not finite and not for all rows
 };
 
@@ -146,7 +201,7 @@ template <class S>
 constexpr uint32_t kQ8CtlBytes = (static_cast<uint32_t>(sizeof(AttnQ8Ctl<S>)) + 1023u) & ~1023u;
 
 template <class S>
-__global__ void __launch_bounds__(S::THREADS, S::CTAS)
+__global__ void __launch_bounds__(S::THREADS, 1)
     k_attention_q8(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ AttnQ8Args a) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -204,7 +259,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     AttnReq q{};
 #pragma unroll 4
     for (int r = r0; r < r1; ++r) {
-      bad |= !attn_request(a, r, t0, q);
+      bad |= !attn_request<kQ8Tile>(a, r, t0, q);
       sum = min(sum + static_cast<uint32_t>(q.units * a.Hkv), kMaxUnits);
     }
     uint32_t in = sum;
@@ -229,7 +284,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     if (u0 >= before && u0 < before + sum) {
       uint32_t u = before;
       for (int r = r0; r < r1; ++r) {
-        if (per > 1) attn_request(a, r, t0, q);
+        if (per > 1) attn_request<kQ8Tile>(a, r, t0, q);
         const uint32_t n = static_cast<uint32_t>(q.units * a.Hkv);
         if (u0 < u + n) {
           ctl.start_r = r;
@@ -260,8 +315,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     if (u_begin < u_end) {
       const bool keys = warp == 0;
       const uint64_t policy = policy_evict_first();
-      const int rows_box = min(1 << a.shift, kTileTok);
-      const int n_box = kTileTok / rows_box;
+      const int rows_box = min(1 << a.shift, kQ8Tile);
+      const int n_box = kQ8Tile / rows_box;
       const int box = lane % n_box;
       const bool copier = lane < n_box;
       const uint32_t box_bytes = rows_box * S::D;
@@ -288,7 +343,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             mine.units = 0;
             mine.begin = 0;
             if (r + lane < a.B) {
-              attn_request(a, r + lane, t0, mine);
+              attn_request<kQ8Tile>(a, r + lane, t0, mine);
               if (mine.units > 0)  // the table rows of requests to come
                 prefetch_l2(a.table + (r + lane) * a.stride + (mine.begin >> a.shift));
             }
@@ -317,11 +372,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         }
         if (!found) break;
         const int in_head = max(lead_in - a.lead, 0);
-        const int tile0 = q.begin / kTileTok + in_head;
+        const int tile0 = q.begin / kQ8Tile + in_head;
         const int tiles = q.end > 0 ? lead_in + take - a.lead - in_head : 0;
         const int32_t* const row = a.table + r * a.stride;
         const int last_page = max(q.end - 1, 0) >> a.shift;
-        int page0 = (tile0 * kTileTok) >> a.shift;  // of the 32 ids that the lanes hold
+        int page0 = (tile0 * kQ8Tile) >> a.shift;  // of the 32 ids that the lanes hold
         int ids = 0, next_ids = 0;
         if (tiles > 0) ids = row[min(page0 + lane, last_page)];
         if (keys) {
@@ -349,51 +404,60 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         }
         // ---- its tiles
         if (tiles > 0) next_ids = row[min(page0 + 32 + lane, last_page)];
-        int tok = tile0 * kTileTok + box * rows_box;  // this lane's box of the tile
-        for (int i = 0; i < tiles; ++i, tok += kTileTok) {
-          int rel = (tok >> a.shift) - page0;
-          if (__any_sync(0xFFFFFFFFu, rel >= 32)) {
+        const int in_page = (1 << a.shift) - 1, head_box = box * rows_box;
+        int tile_tok = tile0 * kQ8Tile, rel = ((tile_tok + head_box) >> a.shift) - page0;
+        uint32_t dst = dst0 + s * S::kStage;
+        const float* const ks0 = a.k_scale + h * a.scale_head;
+        const float* const vs0 = a.v_scale + h * a.scale_head;
+        for (int i = 0; i < tiles; ++i) {
+          if (((tile_tok >> a.shift) - page0) >= 32) {  // a window of ids holds whole tiles
             page0 += 32;
             rel -= 32;
             ids = next_ids;
             next_ids = row[min(page0 + 32 + lane, last_page)];
           }
           int page = __shfl_sync(0xFFFFFFFFu, ids, rel);
-          const bool load = copier && tok < q.end && tok + rows_box > q.begin;
-          if (load && static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) {
-            set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
-            page = 0;
+          const int tok = tile_tok + head_box;  // this lane's box of the tile
+          bool load = copier;
+          uint32_t bytes = S::kStage;
+          if (tile_tok < q.begin || tile_tok + kQ8Tile > q.end) {
+            load = copier && tok < q.end && tok + rows_box > q.begin;
+            bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * box_bytes;
           }
-          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * box_bytes;
-          bool mine_ok = wraps == 0 || mbar_wait(&ctl.empty[s], (wraps - 1u) & 1u);
-          if (mine_ok && lane == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
-          ok = __all_sync(0xFFFFFFFFu, mine_ok) != 0;
-          if (!ok) break;
-          if (load)
-            tma_load_4d(dst0 + s * S::kStage, map, 0, tok & ((1 << a.shift) - 1), h, page,
-                        &ctl.full[s], policy);
+          if (wraps > 0 && !warp_test(&ctl.empty[s], (wraps - 1u) & 1u)) {
+            ok = warp_wait(&ctl.empty[s], (wraps - 1u) & 1u);
+            if (!ok) break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
+          if (load) {
+            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) {
+              set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
+              page = 0;
+            }
+            tma_load_4d(dst, map, 0, tok & in_page, h, page, &ctl.full[s], policy);
+          }
           if (!keys) {
             // the scales of the tile's keys and values travel with its values, whose stage
             // is held until the softmax is done with the tile
-            const int tile_tok = (tile0 + i) * kTileTok;
             const uint32_t to = s_scale + (s - first_stage) * (8u * a.n_scales);
+#pragma unroll 1
             for (int j0 = 0; j0 < a.n_scales; j0 += 32) {
-              const int j = j0 + lane;
-              const int t = tile_tok + (j < a.n_scales ? j << a.b_shift : 0);
-              const int id = __shfl_sync(0xFFFFFFFFu, ids, (t >> a.shift) - page0);
+              const int j = j0 + lane, t = tile_tok + (j << a.b_shift);
+              const int id = __shfl_sync(0xFFFFFFFFu, ids, min((t >> a.shift) - page0, 31));
               // a block that starts before the first token that is seen may hold it
               if (j < a.n_scales && t < q.end && t + (1 << a.b_shift) > q.begin &&
                   static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages)) {
-                const int64_t from = id * a.scale_page +
-                                     ((t & ((1 << a.shift) - 1)) >> a.b_shift) * a.scale_block +
-                                     h * a.scale_head;
-                cp_async4(to + 4u * j, a.k_scale + from);
-                cp_async4(to + 4u * (a.n_scales + j), a.v_scale + from);
+                const int64_t from = id * a.scale_page + ((t & in_page) >> a.b_shift) * a.scale_block;
+                cp_async4(to + 4u * j, ks0 + from);
+                cp_async4(to + 4u * (a.n_scales + j), vs0 + from);
               }
             }
             cp_async_arrive(&ctl.full[s]);
           }
-          if (++s == end_stage) s = first_stage, ++wraps;
+          tile_tok += kQ8Tile;
+          rel = ((tile_tok + head_box) >> a.shift) - page0;
+          dst += S::kStage;
+          if (++s == end_stage) s = first_stage, dst = dst0 + first_stage * S::kStage, ++wraps;
         }
       }
       // the end of the line
@@ -424,11 +488,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       const bool leader = elect_one();
       const uint32_t n = static_cast<uint32_t>(a.n_cols);
       const uint32_t idesc_s = attn_idesc_f8(0, kTileTok, n, false, false);
-      // the parts of P in one product or, past 256 columns, in two
-      const uint32_t parts_a = S::PP * n <= 256 ? S::PP : 2, n_a = parts_a * n;
-      const uint32_t idesc_o = attn_idesc_f8(1, S::D, n_a, true, true);
-      const uint32_t idesc_o2 = attn_idesc_f8(1, S::D, S::PP * n - n_a, true, true);
-      const bool two = parts_a < S::PP;
+      // the parts of P side by side or, split, one after another
+      const uint32_t idesc_o = attn_idesc_f8(1, S::D, S::SPLIT ? n : S::PP * n, true, true);
       // K and Q: rows of D bytes, 8-row groups together
       const uint64_t desc_kq = attn_desc(16, 8 * S::D, S::kSwizzle);
       // V: a token's D bytes together, 8-token groups after one another
@@ -436,7 +497,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       // P: 16 rows of q contiguous per token, 16-row blocks 2,048 apart, 8-token groups 128
       // apart, no swizzle (there the leading offset is that of the tokens)
       const uint64_t desc_p = attn_desc(128, 2048, 0);
-      uint32_t items = 0, tiles = 0, scores = 0;
       struct Ring {
         uint32_t s, phase, first, end;
         __device__ void on() {
@@ -447,90 +507,140 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       Ring rk{0, 0, 0, nk}, rv{nk, 0, nk, nk + nv};
       const uint32_t nq = a.q_bufs;
       Ring rq{nq - 1u, 1u, 0, nq};  // moved on to an item's queries before them
-      bool ok = true;
-      auto product_s = [&](bool last) {  // S^T of the next tile; the item's last frees Q
-        const uint32_t buf = scores & 1u;
-        ok = warp_wait(&ctl.full[rk.s], rk.phase);
-        if (!ok) return;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t k0 = at(desc_kq, s_ring + rk.s * S::kStage);
-          const uint64_t q0 = at(desc_kq, s_q + rq.s * S::QP * q_part);
-#pragma unroll
-          for (int p = 0; p < S::QP; ++p)
-#pragma unroll
-            for (int k = 0; k < S::D / 32; ++k)
-              tc_mma_f8(tmem + S::kColS + buf * S::NB, k0 + static_cast<uint32_t>(2 * k),
-                        q0 + (p * (q_part >> 4) + 2 * k), idesc_s, p > 0 || k > 0);
-          tc_commit(&ctl.empty[rk.s]);
-          tc_commit(&ctl.s_full[buf]);
-          if (last) tc_commit(&ctl.q_empty[rq.s]);
-        }
-        rk.on();
-        ++scores;
-      };
-      while (ok) {
-        const uint32_t slot = items % kItems;
-        ok = warp_wait(&ctl.item_full[slot], (items / kItems) & 1u);
-        if (!ok) break;
-        const int nt = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tiles, 0);
-        int tok0 = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tile0, 0) * kTileTok;
-        const int begin = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].begin, 0);
-        const int end = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].end, 0);
-        if (nt >= 0 && leader) mbar_arrive(&ctl.item_empty[slot]);
-        ++items;
-        if (nt < 0) break;
-        if (nt == 0) continue;
-        rq.on();
-        ok = warp_wait(&ctl.q_full[rq.s], rq.phase);
-        if (!ok) break;
-        product_s(nt == 1);
-        for (int i = 0; i < nt && ok; ++i, ++tiles, tok0 += kTileTok) {
-          // whichever comes first, the next tile's keys or this one's weights
-          const uint32_t buf = tiles % S::PBUFS;
-          bool ahead = i + 1 == nt;
-          WaitClock clock;
-          for (;;) {
-            if (!ahead && warp_test(&ctl.full[rk.s], rk.phase)) {
-              product_s(i + 2 == nt);
-              ahead = true;
+      // Two places in the line of tiles. Scores run ahead of the weights by up to two tiles,
+      // into the next item too; whichever is possible is done.
+      uint32_t s_items = 0, s_done = 0;       // scores: items begun, tiles done
+      int s_tiles = 0;                        // tiles of the item to come
+      int s_tok = 0, s_begin = 0, s_stop = 0; // the next tile's first token, those that are seen
+      bool s_end = false, s_queries = false;  // no more items; the item's queries are there
+      uint32_t o_items = 0, o_done = 0, o_units = 0, o_sub = 0;  // outputs: tiles, units done
+      int o_tiles = 0, tok0 = 0, begin = 0, end = 0;
+      bool first = true, ok = true;
+      WaitClock clock;
+      for (;;) {
+        bool done = false;
+        if (!s_end && s_done < o_done + 2u) {
+          if (s_tiles == 0) {
+            const uint32_t slot = s_items % kItems;
+            if (warp_test(&ctl.item_full[slot], (s_items / kItems) & 1u)) {
+              s_tiles = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tiles, 0);
+              s_tok = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tile0, 0) * kQ8Tile;
+              s_begin = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].begin, 0);
+              s_stop = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].end, 0);
+              ++s_items;
+              s_end = s_tiles < 0;
+              s_queries = false;
+              if (s_tiles > 0) rq.on();
+              done = true;
             }
-            if (warp_test(&ctl.p_full[buf], (tiles / S::PBUFS) & 1u)) break;
-            ok = ok && !__any_sync(0xFFFFFFFFu, clock.expired());
-            if (!ok) break;
-          }
-          if (!ok) break;
-          // the groups' lists of the item are written
-          if (leader && i + 1 == nt) mbar_arrive(&ctl.odd_full);
-          ok = warp_wait(&ctl.full[rv.s], rv.phase);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            const uint64_t v0 = at(desc_v, s_ring + rv.s * S::kStage);
-            const uint64_t p0 = at(desc_p, s_p + buf * a.p_bytes);
-            // the steps of 32 tokens that some row sees
-            const int k0 = max(begin - tok0, 0) >> 5, k1 = (min(end - tok0, kTileTok) + 31) >> 5;
-            constexpr uint32_t kStep = 32 * S::D >> 4;  // of V
-            auto product_o = [&](uint32_t col, uint64_t p, uint32_t idesc) {
-              if (k0 == 0 && k1 == kTileTok / 32) {
+          } else if (!s_queries) {
+            s_queries = warp_test(&ctl.q_full[rq.s], rq.phase);
+            done = s_queries;
+          } else if (warp_test(&ctl.full[rk.s], rk.phase)) {
+            tc_fence_after();
+            --s_tiles;
+            if (leader) {
+              const uint64_t q0 = at(desc_kq, s_q + rq.s * S::QP * q_part);
+              auto half = [&](uint32_t h) {
+                const uint64_t k0 = at(desc_kq, s_ring + rk.s * S::kStage + h * (kTileTok * S::D));
+                const uint32_t col = S::kColS + ((s_done & 1u) * 2u + h) * S::NB;
 #pragma unroll
-                for (int k = 0; k < kTileTok / 32; ++k)
-                  tc_mma_f8(tmem + S::kColO + col, v0 + static_cast<uint32_t>(k * kStep),
-                            p + static_cast<uint32_t>(k * 32), idesc, k > 0 ? 1u : i > 0);
-              } else {
-#pragma unroll 1
-                for (int k = k0; k < k1; ++k)
-                  tc_mma_f8(tmem + S::kColO + col, v0 + static_cast<uint32_t>(k * kStep),
-                            p + static_cast<uint32_t>(k * 32), idesc, i > 0 || k > k0);
-              }
-            };
-            product_o(0, p0, idesc_o);
-            if (two) product_o(n_a, p0 + parts_a * (a.part_bytes >> 4), idesc_o2);
-            tc_commit(&ctl.empty[rv.s]);
-            tc_commit(&ctl.pv_done[buf]);
+                for (int p = 0; p < S::QP; ++p)
+#pragma unroll
+                  for (int k = 0; k < S::D / 32; ++k)
+                    tc_mma_f8(tmem + col, k0 + static_cast<uint32_t>(2 * k),
+                              q0 + (p * (q_part >> 4) + 2 * k), idesc_s, p > 0 || k > 0);
+              };
+              if (s_begin < s_tok + kTileTok) half(0);
+              if (s_stop > s_tok + kTileTok) half(1);
+              tc_commit(&ctl.empty[rk.s]);
+              tc_commit(&ctl.s_full[s_done & 1u]);
+              if (s_tiles == 0) tc_commit(&ctl.q_empty[rq.s]);
+            }
+            rk.on();
+            ++s_done;
+            s_tok += kQ8Tile;
+            done = true;
           }
-          rv.on();
-          if (!ahead) product_s(i + 2 == nt);
+        }
+        if (o_tiles == 0) {
+          if (o_items < s_items) {
+            const uint32_t slot = o_items % kItems;
+            o_tiles = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tiles, 0);
+            if (o_tiles < 0) break;
+            tok0 = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].tile0, 0) * kQ8Tile;
+            begin = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].begin, 0);
+            end = __shfl_sync(0xFFFFFFFFu, ctl.item[slot].end, 0);
+            if (leader) mbar_arrive(&ctl.item_empty[slot]);
+            ++o_items;
+            first = true;
+            done = true;
+          }
+        } else if (o_done < s_done) {
+          const uint32_t buf = o_units % S::PBUFS;
+          if (warp_test(&ctl.p_full[buf], (o_units / S::PBUFS) & 1u)) {
+            const bool last = o_sub + 1u == S::UNITS;  // unit of the tile
+            // the groups' lists of the item are written
+            if (leader && last && o_tiles == 1) mbar_arrive(&ctl.odd_full);
+            ok = warp_wait(&ctl.full[rv.s], rv.phase);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (uint32_t g = 0; g < S::HALVES; ++g) {
+              const uint32_t h = S::SPLIT ? o_sub : g;
+              const int tok = tok0 + static_cast<int>(h) * kTileTok;
+              // the steps of 32 tokens that some row sees
+              const int k0 = max(begin - tok, 0) >> 5, k1 = (min(end - tok, kTileTok) + 31) >> 5;
+              if (k0 >= k1) continue;
+              if (leader) {
+                const uint64_t v0 = at(desc_v, s_ring + rv.s * S::kStage + h * (kTileTok * S::D));
+                const uint64_t p0 = at(desc_p, s_p + (buf * S::HALVES + g) * a.p_bytes);
+                constexpr uint32_t kStep = 32 * S::D >> 4;  // of V
+                auto product_o = [&](uint32_t col, uint64_t p, bool fresh) {
+                  if (k0 == 0 && k1 == kTileTok / 32) {
+#pragma unroll
+                    for (int k = 0; k < kTileTok / 32; ++k)
+                      tc_mma_f8(tmem + S::kColO + col, v0 + static_cast<uint32_t>(k * kStep),
+                                p + static_cast<uint32_t>(k * 32), idesc_o, k > 0 || !fresh);
+                  } else {
+#pragma unroll 1
+                    for (int k = k0; k < k1; ++k)
+                      tc_mma_f8(tmem + S::kColO + col, v0 + static_cast<uint32_t>(k * kStep),
+                                p + static_cast<uint32_t>(k * 32), idesc_o, k > k0 || !fresh);
+                  }
+                };
+                if constexpr (S::SPLIT) {
+#pragma unroll 1
+                  for (int p = 0; p + 1 < S::PP; ++p)
+                    product_o(0, p0 + p * (a.part_bytes >> 4), first && p == 0);
+                  product_o(n, p0 + (S::PP - 1) * (a.part_bytes >> 4), first);
+                } else {
+                  product_o(0, p0, first);
+                }
+              }
+              first = false;
+            }
+            if (leader) {
+              if (last) tc_commit(&ctl.empty[rv.s]);
+              tc_commit(&ctl.pv_done[buf]);
+            }
+            ++o_units;
+            ++o_sub;
+            if (last) {
+              rv.on();
+              o_sub = 0;
+              ++o_done;
+              --o_tiles;
+              tok0 += kQ8Tile;
+            }
+            done = true;
+          }
+        }
+        if (done) {
+          clock = WaitClock();
+        } else if (__any_sync(0xFFFFFFFFu, clock.expired())) {
+          ok = false;
+          break;
         }
       }
       if (!ok) {
@@ -545,11 +655,18 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     // =====================================================================
     // queries: a group of lanes has a row in registers, 8 elements a lane, scales
     // it and writes its parts. Two tiles of them where there is room, so that an
-    // item's are there when the one before it ends.
+    // item's are there when the one before it ends. Rows past an item's keep what
+    // they hold (their columns take no part), from the start zeros. One warp does this
+    // beside 16 and more tiles of 80 rows only if nothing in it waits: four rows
+    // of each group at once, the next ones' loads before the arithmetic of these,
+    // two elements an instruction (a loop without these took 74,000 cycles for 80
+    // rows, 3 times as long as their 16 tiles).
     // =====================================================================
     if (u_begin < u_end) {
-      constexpr int LPR = S::D / 8, kRows = 32 / LPR, kDeep = 4;
+      constexpr int LPR = S::D / 8, kRows = 32 / LPR, kDeep = 4, kBatch = kRows * kDeep;
       const int sub = lane / LPR, l = lane % LPR;
+      const uint32_t gs_inv = (65536u + a.Gs - 1u) / a.Gs;  // j / Gs = j * gs_inv >> 16 for j < 160
+      for (uint32_t i = lane * 16u; i < a.q_bufs * S::QP * q_part; i += 512u) sts_u4(s_q + i, 0, 0, 0, 0);
       uint32_t items = 0, b = 0, wraps = 0;
       bool ok = true;
       for (;;) {
@@ -563,58 +680,82 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         const uint16_t* const q0 = a.q + it.row0 * a.q_row + it.head0 * a.q_head + 8 * l;
         ++items;
         if (tiles > 0) {
+          auto load = [&](int j0, uint4 (&w)[kDeep]) {
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+              const int j = j0 + k * kRows + sub;
+              const int t = static_cast<int>(static_cast<uint32_t>(j) * gs_inv >> 16);
+              w[k] = make_uint4(0, 0, 0, 0);
+              if (j < rows)
+                w[k] = __ldg(reinterpret_cast<const uint4*>(q0 + t * a.q_row + (j - t * a.Gs) * a.q_head));
+            }
+          };
+          uint4 next[kDeep];
+          load(0, next);
           if (wraps >= 1) ok = warp_wait(&ctl.q_empty[b], (wraps - 1u) & 1u);
           if (!ok) break;
           const uint32_t to = s_q + b * S::QP * q_part;
-          for (int j0 = sub; j0 < a.n_cols; j0 += kRows * kDeep) {
-            uint4 w[kDeep];
+          for (int j0 = 0; j0 < rows; j0 += kBatch) {
+            uint32_t v[kDeep][4], top[kDeep];
 #pragma unroll
             for (int k = 0; k < kDeep; ++k) {
-              const int j = j0 + k * kRows, t = j / a.Gs;
-              w[k] = make_uint4(0, 0, 0, 0);
-              if (j < rows)
-                w[k] = *reinterpret_cast<const uint4*>(q0 + t * a.q_row + (j - t * a.Gs) * a.q_head);
+              v[k][0] = next[k].x, v[k][1] = next[k].y, v[k][2] = next[k].z, v[k][3] = next[k].w;
+              uint32_t m = 0;  // the largest magnitudes, as 16-bit patterns
+#pragma unroll
+              for (int e = 0; e < 4; ++e) m = __vmaxu2(m, v[k][e] & 0x7FFF7FFFu);
+              top[k] = max(m & 0xFFFFu, m >> 16);
+            }
+            if (j0 + kBatch < rows) load(j0 + kBatch, next);
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1)
+#pragma unroll
+              for (int k = 0; k < kDeep; ++k) top[k] = max(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], o));
+            uint32_t part[S::QP][kDeep][2];
+            int e[kDeep];
+            bool odd = false;
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+              odd |= top[k] >= (S::F16 ? 0x7C00u : 0x7F80u);
+              // exponent of the largest element; rows below 2^-100 keep their size
+              const uint32_t bits = __float_as_uint(word_to_f32<S::F16>(top[k]).x);
+              e[k] = max(static_cast<int>(bits >> 23) - 127, -100);
+              const float f = __uint_as_float(static_cast<uint32_t>(7 - e[k] + 127) << 23);
+              uint32_t h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 x = word_to_f32<S::F16>(v[k][i]);
+                h[i] = pack2<true>(x.x * f, x.y * f);
+              }
+              if (odd) {  // what is not finite: NaN
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 x = word_to_f32<S::F16>(v[k][i]);
+                  h[i] = pack2<true>(fabsf(x.x) < INFINITY ? x.x * f : NAN,
+                                     fabsf(x.y) < INFINITY ? x.y * f : NAN);
+                }
+              }
+#pragma unroll
+              for (int p = 0; p < S::QP; ++p) {
+                uint32_t c[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  c[i] = f16x2_to_e4m3x2(h[i]);
+                  if (p + 1 < S::QP) h[i] = sub_f16x2(h[i], e4m3x2_to_f16x2(c[i]));
+                }
+                part[p][k][0] = c[0] | (c[1] << 16);
+                part[p][k][1] = c[2] | (c[3] << 16);
+              }
             }
 #pragma unroll
             for (int k = 0; k < kDeep; ++k) {
-              const int j = j0 + k * kRows;
-              const uint32_t own[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-              float x[8];
-              uint32_t top = 0;
+              const uint32_t j = j0 + k * kRows + sub;
+              if (j >= static_cast<uint32_t>(a.n_cols)) continue;
+              const uint32_t swap = S::D == 128 ? j & 7u : (j >> 1) & 3u;
+              const uint32_t addr = to + j * S::D + (((static_cast<uint32_t>(l) >> 1) ^ swap) << 4) + (l & 1) * 8;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 p = word_to_f32<S::F16>(own[e]);
-                x[2 * e] = p.x, x[2 * e + 1] = p.y;
-                top = max(top, max(__float_as_uint(p.x) & 0x7FFFFFFFu,
-                                   __float_as_uint(p.y) & 0x7FFFFFFFu));
-              }
-#pragma unroll
-              for (int o = LPR / 2; o >= 1; o >>= 1)
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-              // exponent of the largest element; rows below 2^-100 keep their size
-              const int e = max(static_cast<int>(top >> 23) - 127, -100);
-              const float f = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)  // not finite: NaN
-                x[i] = fabsf(x[i]) < INFINITY ? x[i] * f : NAN;
-              const uint32_t chunk = static_cast<uint32_t>(l) >> 1;
-              const uint32_t swap = S::D == 128 ? j & 7u : (static_cast<uint32_t>(j) >> 1) & 3u;
-              const uint32_t addr = to + j * S::D + ((chunk ^ swap) << 4) + (l & 1) * 8;
-#pragma unroll
-              for (int p = 0; p < S::QP; ++p) {
-                const uint32_t lo = e4m3x4(x[0], x[1], x[2], x[3]);
-                const uint32_t hi = e4m3x4(x[4], x[5], x[6], x[7]);
-                if (j < a.n_cols) sts_u2(addr + p * q_part, lo, hi);
-                if (p + 1 < S::QP) {
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const float2 v = e4m3x2_to_f32((i < 2 ? lo : hi) >> (16 * (i & 1)));
-                    x[2 * i] -= v.x, x[2 * i + 1] -= v.y;
-                  }
-                }
-              }
-              if (l == 0 && j < a.n_cols)
-                ctl.cq[slot][j] = a.c * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+              for (int p = 0; p < S::QP; ++p) sts_u2(addr + p * q_part, part[p][k][0], part[p][k][1]);
+              if (l == 0)
+                ctl.cq[slot][j] = a.c * __uint_as_float(static_cast<uint32_t>(e[k] - 7 + 127) << 23);
             }
           }
           fence_proxy_async();
@@ -646,7 +787,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;  // (32 * quarter) << 16
     const uint32_t window = static_cast<uint32_t>(a.window);
     volatile int32_t* abort_flag = &ctl.abort;
-    uint32_t tiles = 0, items = 0, lists = 0;
+    uint32_t done = 0, units = 0, items = 0, lists = 0;  // tiles, units
     const uint32_t v_end = a.k_stages + a.v_stages;
     uint32_t v_s = a.k_stages, v_phase = 0;  // ring position of the next tile of values
     int rv = 0;                              // weights stand for 2^-rv of their values
@@ -665,7 +806,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       const float* const cq = ctl.cq[slot];
       float* const nref = ctl.nref[items & 1u];
       int32_t* const lims = ctl.lim[items & 1u];
-      const int rows = failed ? 0 : max(it.t_rows * a.Gs, 0);
+      // (the item that ends the line has nothing but its mark)
+      const int rows = failed || it.tiles < 0 ? 0 : it.t_rows * a.Gs;
       const int my_rows = max(0, min(8 * blocks, rows - c0));
       const int nb = (my_rows + 7) >> 3;
       for (int j = c0 + gt; j < c0 + 8 * nb; j += 128) {
@@ -682,254 +824,269 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
       ++items;
       const int lim_last = it.lim0 + it.t_rows - 1;
       const int lo_last = a.window == INT_MAX ? 0 : max(0, lim_last - a.window);
-      // Sums of the columns' weights: a thread's own token's, in pairs; or, where
-      // that takes too many registers, folded tile by tile into one per block.
-      constexpr bool kPairs = S::NC <= 32;
-      uint64_t l[kPairs ? S::NC / 2 : 1];
-      float lf[kPairs ? 1 : kBlocks];
-      if constexpr (kPairs) {
+      uint64_t l[S::NC / 2];  // sums of the columns' weights over the thread's tokens, in pairs
 #pragma unroll
-        for (int j = 0; j < S::NC / 2; ++j) l[j] = 0;
-      } else {
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) lf[b] = 0.f;
-      }
+      for (int j = 0; j < S::NC / 2; ++j) l[j] = 0;
 
-      const bool exact = S::NB <= kExactRows && it.tiles >= kExactTiles;
-      // weights are half precision numbers, whatever the outputs' type
-      const float base = exact ? kExactBase<true> : kBase<true>;
-      const float peak_base = exact ? kExactBase<true> : kPeakBase<true>;
-      const float highest = exact ? kExactBase<true> : kHighest<true>;
       bool leave = false;
-      for (int i = 0; i < it.tiles; ++i, ++tiles) {
-        const uint32_t buf = tiles & 1u;
-        const int tok0 = (it.tile0 + i) * kTileTok, tok = tok0 + gt;
-        // every token of the tile visible to every row?
-        const bool whole = tok0 + kTileTok <= it.lim0 && tok0 >= lo_last;
-        // this token's scales; what no row sees has none
-        const bool some = tok >= it.begin && tok < it.end;
+      for (int i = 0; i < it.tiles; ++i, ++done) {
+        const uint32_t sbuf = done & 1u;
+        const int tok0 = (it.tile0 + i) * kQ8Tile;
+        // of each 128 tokens: whether all are visible to every row, whether some are to some;
+        // this thread's token, its scales (what no row sees has none)
+        bool whole[2], live[2], some[2];
+        float ks[2], vs[2];
         failed |= !mbar_wait(&ctl.full[v_s], v_phase);
-        float ks = 0.f, vs = 0.f;
-        if (some) {
-          const uint32_t from =
-              s_scale + (v_s - a.k_stages) * (8u * a.n_scales) + 4u * (gt >> min(a.b_shift, 7));
-          ks = lds_f32(from);
-          vs = lds_f32(from + 4u * a.n_scales);
-          if (!is_scale(ks) || !is_scale(vs)) {
-            set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
-            ks = vs = 1.f;
-          }
-        }
-        const int vexp = static_cast<int>(__float_as_uint(vs) >> 23) - 126;  // vs < 2^vexp
-        failed |= !mbar_wait(&ctl.s_full[buf], (tiles >> 1) & 1u);
-        tc_fence_after();
-        // scores, -inf where the row does not see the token
-        float x[S::NC];
-        const uint32_t s_addr = tmem + lanes + S::kColS + buf * S::NB + c0;
+        const uint32_t row_v = s_ring + v_s * S::kStage + gt * S::D;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-          if (b < nb) tmem_ld8(s_addr + 8 * b, x + 8 * b);
-        tmem_wait_ld();
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-          if (b < nb) {
-            tmem_arrived(x + 8 * b);
-            // in powers of two: t = s ks cq
-            const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[c0 + 8 * b]);
-            const ulonglong2 f0 = cq4[0], f1 = cq4[1];
-            const uint64_t ks2 = pair(ks, ks), f[4] = {f0.x, f0.y, f1.x, f1.y};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float* y = x + 8 * b + 2 * k;
-              unpair(mul2(pair(y[0], y[1]), mul2(f[k], ks2)), y[0], y[1]);
+        for (int h = 0; h < 2; ++h) {
+          const int from = tok0 + h * kTileTok, tok = from + gt;
+          whole[h] = from + kTileTok <= it.lim0 && from >= lo_last;
+          live[h] = from < it.end && from + kTileTok > it.begin;
+          some[h] = tok >= it.begin && tok < it.end;
+          ks[h] = vs[h] = 0.f;
+          if (some[h]) {
+            const uint32_t at_s = s_scale + (v_s - a.k_stages) * (8u * a.n_scales) +
+                                  4u * ((h * kTileTok + gt) >> min(a.b_shift, 8));
+            ks[h] = lds_f32(at_s);
+            vs[h] = lds_f32(at_s + 4u * a.n_scales);
+            if (!is_scale(ks[h]) || !is_scale(vs[h])) {
+              set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
+              ks[h] = vs[h] = 1.f;
             }
-            if (!whole) {
-              const int4* lim4 = reinterpret_cast<const int4*>(&lims[c0 + 8 * b]);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int4 m = lim4[k];
-                float* y = x + 8 * b + 4 * k;
-                if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[0] = -INFINITY;
-                if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[1] = -INFINITY;
-                if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[2] = -INFINITY;
-                if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[3] = -INFINITY;
-              }
-            }
-          }
-        auto each = [&](auto f) {  // f(b) for every block in use
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b)
-            if (b < nb) f(b);
-        };
-        // exponents t - m
-        auto exponent = [&](int b, uint64_t (&y)[4]) {
-          const ulonglong2* nr = reinterpret_cast<const ulonglong2*>(&nref[c0 + 8 * b]);
-          const ulonglong2 m0 = nr[0], m1 = nr[1];
-          const float* z = x + 8 * b;
-          y[0] = add2(pair(z[0], z[1]), m0.x);
-          y[1] = add2(pair(z[2], z[3]), m0.y);
-          y[2] = add2(pair(z[4], z[5]), m1.x);
-          y[3] = add2(pair(z[6], z[7]), m1.y);
-        };
-        bool raise = i == 0;  // the first tile's maxima
-        if (!raise) {
-          float top = -INFINITY;
-          each([&](int b) {
-            uint64_t e[4];
-            exponent(b, e);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float y0, y1;
-              unpair(e[k], y0, y1);
-              top = fmaxf(top, fmaxf(y0, y1));
-            }
-          });
-          raise = bar_any(bar, 128, top > highest || vexp > rv || failed);
-        }
-        if (raise) {
-          each([&](int b) {
-            float v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)  // NaN takes no part
-              v[k] = x[8 * b + k] == x[8 * b + k] ? x[8 * b + k] : -INFINITY;
-            const float m = over_four<true>(fold_columns<true>(v, lane));
-            if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = m;
-          });
-          const int warp_vexp = __reduce_max_sync(0xFFFFFFFFu, vexp);
-          if (lane == 0) ctl.vexp[group][quarter] = warp_vexp;
-          if (bar_any(bar, 128, failed || *abort_flag != 0)) {
-            leave = true;
-            break;
-          }
-          const int* const ve = ctl.vexp[group];
-          const int top_vexp = max(max(ve[0], ve[1]), max(ve[2], ve[3]));
-          const int old_rv = rv;
-          if (i == 0 || top_vexp > rv) rv = min(max(top_vexp + kScaleRoom, -100), 120);
-          const float down_v = i == 0 ? 1.f : exp2f(static_cast<float>(old_rv - rv));
-          for (int j = c0 + gt; j < c0 + my_rows; j += 128) {
-            float top = -INFINITY, low = INFINITY;  // of the quarters that hold a token
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float v = ctl.red[w][j];
-              top = fmaxf(top, v);
-              if (v > -INFINITY) low = fminf(low, v);
-            }
-            const float m = top, down = top - low > kPeak ? peak_base : base;
-            const float ref = fabsf(m) < kNoShift ? m - down : m, old = -nref[j];
-            ctl.fac[j] = ref > old ? ex2_approx(old - ref) : 1.f;
-            if (ref > old) nref[j] = -ref;
-          }
-          bar_sync(bar, 128);
-          if (i > 0) {
-            const uint32_t before = tiles - 1u;
-            failed |= !mbar_wait(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
-            tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-              if (b < nb) {
-                const float* f = &ctl.fac[c0 + 8 * b];
-#pragma unroll
-                for (int p = 0; p < S::PP; ++p) {
-                  const uint32_t at_o = tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b;
-                  float o[8];
-                  tmem_ld8(at_o, o);
-                  tmem_wait_ld();
-                  tmem_arrived(o);
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) o[k] *= f[k] * down_v;
-                  tmem_st8(at_o, o);
-                }
-                if constexpr (kPairs) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
-                } else {
-                  lf[b] *= f[lane >> 2];
-                }
-              }
-            tmem_wait_st();
-          }
-        }
-        // this buffer of weights is free once its last tile has been multiplied
-        const uint32_t pb = tiles % S::PBUFS, use = tiles / S::PBUFS;
-        const float vr = vs * __uint_as_float(static_cast<uint32_t>(127 - rv) << 23) *
-                         (S::PP == 3 ? kCut : 1.f);
-        const uint64_t vr2 = pair(vr, vr);
-        if (use >= 1) failed |= !mbar_wait(&ctl.pv_done[pb], (use - 1u) & 1u);
-        each([&](int b) {
-          uint64_t e[4];
-          float y[8];
-          exponent(b, e);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            unpair(e[k], y[2 * k], y[2 * k + 1]);
-            y[2 * k] = ex2_approx(y[2 * k]);
-            y[2 * k + 1] = ex2_approx(y[2 * k + 1]);
-            if constexpr (kPairs) l[4 * b + k] = add2(l[4 * b + k], pair(y[2 * k], y[2 * k + 1]));
-          }
-          // The weights enter the second product cut to their parts' bits (no more than
-          // the output's own rounding); their sum l is of the unrounded ones.
-          uint32_t h[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float p0, p1;
-            unpair(mul2(pair(y[2 * k], y[2 * k + 1]), vr2), p0, p1);
-            h[k] = pack2<true>(p0, p1);
-          }
-          const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
-          const uint32_t to =
-              s_p + pb * a.p_bytes + (chunk >> 1) * 2048u + gt * 16u + (chunk & 1u) * 8u;
-#pragma unroll
-          for (int p = 0; p < S::PP; ++p) {
-            if (p > 0) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                h[k] = without_upper(h[k]);
-                if (p == S::PP - 1) h[k] = mul_f16x2(h[k], S::LAST == 4 ? 0x4C004C00u : 0x54005400u);
-              }
-            }
-            sts_u2(to + p * a.part_bytes, upper_bytes(h[0], h[1]), upper_bytes(h[2], h[3]));
-          }
-          if constexpr (!kPairs) lf[b] += fold_columns<false>(y, lane);
-        });
-        if (!whole && group == 0) {
-          // Zero weights do not silence values that are not finite, and the
-          // tile's rest may hold anything: what no row sees is zeroed, and of
-          // what only some rows see the non-finite values are taken out here
-          // and added to those rows at the end.
-          const bool all = tok < it.lim0 && tok >= lo_last;
-          // in a step of 32 tokens that is multiplied at all
-          const bool used = (tok | 31) >= it.begin && (tok & ~31) < it.end;
-          const uint32_t v_row = s_ring + v_s * S::kStage + gt * S::D;
-          if (!used) {
-          } else if (!some) {
-#pragma unroll
-            for (int k = 0; k < S::D / 16; ++k) sts_u4(v_row + k * 16, 0, 0, 0, 0);
-          } else if (!all) {
-            bool odd = false;
-#pragma unroll 4
-            for (int k = 0; k < S::D / 16; ++k) {
-              const uint4 v = lds_u4(v_row + k * 16);
-              uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              bool hit = false;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                // bit 7 of each byte that is NaN (lower seven bits all set)
-                const uint32_t nan = ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                w[q] &= ~(nan | (nan - (nan >> 7)));
-                hit |= nan != 0;
-              }
-              if (hit) sts_u4(v_row + k * 16, w[0], w[1], w[2], w[3]);
-              odd |= hit;
-            }
-            if (odd) ctl.odd[list][atomicAdd(&ctl.odd_n[list], 1)] = tok;
           }
         }
         if (++v_s == v_end) v_s = a.k_stages, v_phase ^= 1u;
+        failed |= !mbar_wait(&ctl.s_full[sbuf], (done >> 1) & 1u);
+        tc_fence_after();
+        const uint32_t s_tile = tmem + lanes + S::kColS + sbuf * (2 * S::NB) + c0;
+#pragma unroll 1
+       for (int unit = 0; unit < S::UNITS; ++unit, ++units) {
+        const uint32_t pb = units % S::PBUFS, use = units / S::PBUFS;
+        const bool begins = i == 0 && unit == 0;
+        const uint32_t s_addr = s_tile + unit * S::NB;  // (the unit's first 128)
+        auto pick = [&](auto& x, int g) { return S::SPLIT ? (unit ? x[1] : x[0]) : x[g]; };
+        int vexp = -126;  // vs < 2^vexp
+#pragma unroll
+        for (int g = 0; g < S::HALVES; ++g)
+          vexp = max(vexp, static_cast<int>(__float_as_uint(pick(vs, g)) >> 23) - 126);
+        // -inf where the row does not see the token
+        auto hide = [&](int b, int g, float (&y)[8]) {
+          const int4* lim4 = reinterpret_cast<const int4*>(&lims[c0 + 8 * b]);
+          const int tok = tok0 + (S::SPLIT ? unit : g) * kTileTok + gt;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int4 m = lim4[k];
+            if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[4 * k] = -INFINITY;
+            if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[4 * k + 1] = -INFINITY;
+            if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[4 * k + 2] = -INFINITY;
+            if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[4 * k + 3] = -INFINITY;
+          }
+        };
+        // The weights are made with the references so far, the check that they stay in range
+        // comes with them: a unit whose weights leave it raises the references and makes them again.
+        uint64_t sum[S::NC / 2];  // of the unit's weights
+        bool raise = begins;      // the first unit's maxima
+        for (;;) {
+          if (raise) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+              if (b < nb) {
+                const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[c0 + 8 * b]);
+                const ulonglong2 f0 = cq4[0], f1 = cq4[1];
+                const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < S::HALVES; ++g) {
+                  if (!pick(live, g)) continue;
+                  float z[1][8];
+                  const uint32_t from[1] = {s_addr + g * S::NB + 8 * b};
+                  tmem_read<1>(from, z);
+                  float(&y)[8] = z[0];
+                  const uint64_t ks2 = pair(pick(ks, g), pick(ks, g));
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    unpair(mul2(mul2(pair(y[2 * k], y[2 * k + 1]), f[k]), ks2), y[2 * k], y[2 * k + 1]);
+                  if (!pick(whole, g)) hide(b, g, y);
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) v[k] = fmaxf(v[k], y[k]);  // NaN takes no part
+                }
+                const float m = over_four<true>(fold_columns<true>(v, lane));
+                if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = m;
+              }
+            const int warp_vexp = __reduce_max_sync(0xFFFFFFFFu, vexp);
+            if (lane == 0) ctl.vexp[group][quarter] = warp_vexp;
+            if (bar_any(bar, 128, failed || *abort_flag != 0)) {
+              leave = true;
+              break;
+            }
+            const int* const ve = ctl.vexp[group];
+            const int top_vexp = max(max(ve[0], ve[1]), max(ve[2], ve[3]));
+            const int old_rv = rv;
+            if (begins || top_vexp > rv) rv = min(max(top_vexp + kScaleRoom, -100), 120);
+            const float down_v = begins ? 1.f : exp2f(static_cast<float>(old_rv - rv));
+            for (int j = c0 + gt; j < c0 + my_rows; j += 128) {
+              float top = -INFINITY, low = INFINITY;  // of the quarters that hold a token
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const float v = ctl.red[w][j];
+                top = fmaxf(top, v);
+                if (v > -INFINITY) low = fminf(low, v);
+              }
+              // weights are half precision numbers, whatever the outputs' type
+              const float down = top - low > kPeak ? kPeakBase<true> : kBase<true>;
+              const float ref = fabsf(top) < kNoShift ? top - down : top, old = -nref[j];
+              ctl.fac[j] = ref > old ? ex2_approx(old - ref) : 1.f;
+              if (ref > old) nref[j] = -ref;
+            }
+            bar_sync(bar, 128);
+            if (!begins) {
+              const uint32_t before = units - 1u;
+              failed |= !mbar_wait(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
+              tc_fence_after();
+#pragma unroll
+              for (int b = 0; b < kBlocks; ++b)
+                if (b < nb) {
+                  const float* f = &ctl.fac[c0 + 8 * b];
+#pragma unroll
+                  for (int p = 0; p < S::ACCS; ++p) {
+                    const uint32_t at_o = tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b;
+                    float z[1][8];
+                    const uint32_t from[1] = {at_o};
+                    tmem_read<1>(from, z);
+                    float(&o)[8] = z[0];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] *= f[k] * down_v;
+                    tmem_st8(at_o, o);
+                  }
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
+                }
+              tmem_wait_st();
+            }
+          }
+          uint64_t ks2[S::HALVES], vr2[S::HALVES];
+#pragma unroll
+          for (int g = 0; g < S::HALVES; ++g) {
+            const float vr = pick(vs, g) * __uint_as_float(static_cast<uint32_t>(127 - rv) << 23) *
+                             (S::PP == 3 ? kCut : 1.f);
+            vr2[g] = pair(vr, vr), ks2[g] = pair(pick(ks, g), pick(ks, g));
+          }
+          // this buffer of weights is free once its last unit has been multiplied
+          if (use >= 1 && !(raise && !begins)) failed |= !mbar_wait(&ctl.pv_done[pb], (use - 1u) & 1u);
+          uint32_t hot = 0;  // the largest weights
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            if (b < nb) {
+              float x[S::HALVES][8];
+              uint32_t from[S::HALVES];
+#pragma unroll
+              for (int g = 0; g < S::HALVES; ++g) from[g] = s_addr + g * S::NB + 8 * b;
+              tmem_read<S::HALVES>(from, x);
+              const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[c0 + 8 * b]);
+              const ulonglong2* nr4 = reinterpret_cast<const ulonglong2*>(&nref[c0 + 8 * b]);
+              const ulonglong2 f0 = cq4[0], f1 = cq4[1], m0 = nr4[0], m1 = nr4[1];
+              const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y}, m[4] = {m0.x, m0.y, m1.x, m1.y};
+              const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
+#pragma unroll
+              for (int g = 0; g < S::HALVES; ++g) {
+                float* const z = x[g];
+                if (!pick(live, g)) {
+                  if (g == 0)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum[4 * b + k] = 0;
+                  continue;
+                }
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // t - m, t = s cq ks
+                  unpair(fma2(mul2(pair(z[2 * k], z[2 * k + 1]), f[k]), ks2[g], m[k]), y[2 * k],
+                         y[2 * k + 1]);
+                if (!pick(whole, g)) hide(b, g, y);
+                // The weights enter the second product cut to their parts' bits (no more
+                // than the output's own rounding); their sum l is of the unrounded ones.
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint64_t e = pair(ex2_approx(y[2 * k]), ex2_approx(y[2 * k + 1]));
+                  sum[4 * b + k] = g == 0 ? e : add2(sum[4 * b + k], e);
+                  float p0, p1;
+                  unpair(mul2(e, vr2[g]), p0, p1);
+                  w[k] = pack2<true>(p0, p1);
+                }
+                hot = max_f16x2(max_f16x2(hot, w[0]), max_f16x2(max_f16x2(w[1], w[2]), w[3]));
+                const uint32_t to = s_p + (pb * S::HALVES + g) * a.p_bytes + (chunk >> 1) * 2048u +
+                                    gt * 16u + (chunk & 1u) * 8u;
+#pragma unroll
+                for (int p = 0; p < S::PP; ++p) {
+                  if (p > 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      w[k] = without_upper(w[k]);
+                      if (p == S::PP - 1)
+                        w[k] = mul_f16x2(w[k], S::LAST == 4 ? 0x4C004C00u : 0x54005400u);
+                    }
+                  }
+                  sts_u2(to + p * a.part_bytes, upper_bytes(w[0], w[1]), upper_bytes(w[2], w[3]));
+                }
+              }
+            }
+          if (raise) break;
+          // infinite: past the range of half precision
+          const bool high = (hot & 0x7C00u) == 0x7C00u || (hot & 0x7C000000u) == 0x7C000000u;
+          if (!bar_any(bar, 128, high || failed)) break;
+          raise = true;
+        }
+        if (leave) break;
+#pragma unroll
+        for (int j = 0; j < S::NC / 2; ++j)
+          if (j / 4 < nb) l[j] = add2(l[j], sum[j]);
+        if (group == 0) {
+          // Zero weights do not silence values that are not finite, and a tile's rest may
+          // hold anything: what no row sees is zeroed, and of what only some rows see the
+          // non-finite values are taken out here and added to those rows at the end.
+#pragma unroll
+          for (int g = 0; g < S::HALVES; ++g) {
+            if (pick(whole, g) || !pick(live, g)) continue;
+            const int half = S::SPLIT ? unit : g, tok = tok0 + half * kTileTok + gt;
+            const uint32_t my_v = row_v + half * (kTileTok * S::D);
+            const bool all = tok < it.lim0 && tok >= lo_last;
+            // in a step of 32 tokens that is multiplied at all
+            const bool used = (tok | 31) >= it.begin && (tok & ~31) < it.end;
+            if (!used) {
+            } else if (!pick(some, g)) {
+#pragma unroll
+              for (int k = 0; k < S::D / 16; ++k) sts_u4(my_v + k * 16, 0, 0, 0, 0);
+            } else if (!all) {
+              bool odd = false;
+#pragma unroll 4
+              for (int k = 0; k < S::D / 16; ++k) {
+                const uint4 v = lds_u4(my_v + k * 16);
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                bool hit = false;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  // bit 7 of each byte that is NaN (lower seven bits all set)
+                  const uint32_t nan = ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                  w[q] &= ~(nan | (nan - (nan >> 7)));
+                  hit |= nan != 0;
+                }
+                if (hit) sts_u4(my_v + k * 16, w[0], w[1], w[2], w[3]);
+                odd |= hit;
+              }
+              if (odd) ctl.odd[list][atomicAdd(&ctl.odd_n[list], 1)] = tok;
+            }
+          }
+        }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.p_full[pb]);
+       }
+       if (leave) break;
       }
       if (leave) {
         *abort_flag = 1;
@@ -942,44 +1099,34 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
         if (b < nb) {
-          float sum;
-          if constexpr (kPairs) {
-            float v[8];
+          float v[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) unpair(l[4 * b + k], v[2 * k], v[2 * k + 1]);
-            sum = over_four<false>(fold_columns<false>(v, lane));
-          } else {
-            sum = over_four<false>(lf[b]);
-          }
+          for (int k = 0; k < 4; ++k) unpair(l[4 * b + k], v[2 * k], v[2 * k + 1]);
+          const float sum = over_four<false>(fold_columns<false>(v, lane));
           if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = sum;
         }
       if (bar_any(bar, 128, failed || *abort_flag != 0)) {
         *abort_flag = 1;
         break;
       }
-      // every warp for itself: the factor of column j in lane j % 32
-      constexpr int kPer = (S::NC + 31) / 32;
-      float fac[kPer];
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int j = c0 + 32 * q + lane;
-        fac[q] = 1.f;
-        if (32 * q + lane < my_rows) {
-          const float sum = (ctl.red[0][j] + ctl.red[1][j]) + (ctl.red[2][j] + ctl.red[3][j]);
-          const bool seen = lims[j] > 0;
-          if (alone) fac[q] = seen ? 1.f / sum : 0.f;  // no token: O is zero
-          if (quarter == 0) {
-            const float m = -nref[j];
-            if (!alone)
-              reinterpret_cast<float2*>(a.part_ml)[part_row + j] = make_float2(m, sum);
-            else if (a.lse)
-              a.lse[it.row0 * a.Hq + it.head0 + ctl.at[j] / S::D] =
-                  seen ? plus_log2(m, sum) * 0.69314718055994531f : -INFINITY;
-          }
+      // every warp for itself: the factor of column j in lane j
+      float fac = 1.f;
+      if (lane < my_rows) {
+        const int j = c0 + lane;
+        const float total = (ctl.red[0][j] + ctl.red[1][j]) + (ctl.red[2][j] + ctl.red[3][j]);
+        const bool seen = lims[j] > 0;
+        if (alone) fac = seen ? 1.f / total : 0.f;  // no token: O is zero
+        if (quarter == 0) {
+          const float m = -nref[j];
+          if (!alone)
+            reinterpret_cast<float2*>(a.part_ml)[part_row + j] = make_float2(m, total);
+          else if (a.lse)
+            a.lse[it.row0 * a.Hq + it.head0 + ctl.at[j] / S::D] =
+                seen ? plus_log2(m, total) * 0.69314718055994531f : -INFINITY;
         }
       }
       if (it.tiles > 0) {
-        const uint32_t last = tiles - 1u;
+        const uint32_t last = units - 1u;
         failed |= !mbar_wait(&ctl.odd_full, lists & 1u);
         failed |= !mbar_wait(&ctl.pv_done[last % S::PBUFS], (last / S::PBUFS) & 1u);
         tc_fence_after();
@@ -993,25 +1140,24 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
           static_cast<uint16_t*>(a.out) + (it.row0 * a.Hq + it.head0) * S::D + d;
       const float unit = __uint_as_float(static_cast<uint32_t>(rv + 127) << 23);
       float* const part = a.part_o + (part_row + c0) * S::D + d;
-#pragma unroll 1
-      for (int b = 0; b < nb; ++b) {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        if (b >= nb) break;
         float o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = 0.f;
         if (it.tiles > 0) {
-          float parts[S::PP][8];
+          float parts[S::ACCS][8];
+          uint32_t from[S::ACCS];
 #pragma unroll
-          for (int p = 0; p < S::PP; ++p)
-            tmem_ld8(tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b, parts[p]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int p = 0; p < S::PP; ++p) tmem_arrived(parts[p]);
+          for (int p = 0; p < S::ACCS; ++p) from[p] = tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b;
+          tmem_read<S::ACCS>(from, parts);
           constexpr float kLast = 1.f / (1 << S::LAST);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            o[k] = parts[S::PP - 1][k] * kLast;
+            o[k] = parts[S::ACCS - 1][k] * kLast;
 #pragma unroll
-            for (int p = S::PP - 2; p >= 0; --p) o[k] += parts[p][k];
+            for (int p = S::ACCS - 2; p >= 0; --p) o[k] += parts[p][k];
             o[k] *= unit;
           }
         }
@@ -1030,10 +1176,9 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         const int4* at4 = reinterpret_cast<const int4*>(&ctl.at[c0 + 8 * b]);
         const int4 a0 = at4[0], a1 = at4[1];
         const int to[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-        const float mine = kPer > 1 && b >= 4 ? fac[kPer - 1] : fac[0];
         float f[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = __shfl_sync(0xFFFFFFFFu, mine, (8 * b + k) & 31);
+        for (int k = 0; k < 8; ++k) f[k] = __shfl_sync(0xFFFFFFFFu, fac, 8 * b + k);
         const int live = writer ? my_rows - 8 * b : 0;  // columns of the block to write
         if (alone) {
 #pragma unroll
