@@ -160,7 +160,7 @@ int dspark_kv_gather_q8(const void* k_cache, const void* v_cache, int64_t page_s
  *                 multiples of 16, >= 0.
  *   k_scale, v_scale  the scales, the same strides (elements, >= 0).
  *   q, out        dtype DSPARK_BF16 or DSPARK_F16. A pass over a request's keys serves
- *                 up to 80 query rows of a key head.
+ *                 up to 72 query rows of a key head.
  */
 int dspark_paged_attention_q8(
     const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_cache,

@@ -64,8 +64,14 @@ int q8_launch(LaunchQ8& c, int sms) {
     a.ring_off = ring_at(stages - stages / 2);
     return stages;
   };
-  const int stages = ring_stages(1);
-  if (ring_stages(2) < stages) ring_stages(1);
+  // A second tile of queries where it costs no tile, or where three are left: the wide blocks
+  // are bound by the arithmetic, and an item's queries take as long as a tile or two.
+  int stages = ring_stages(2);
+  const int most = ring_stages(1);
+  if (stages == most || stages >= (S::SPLIT ? 3 : most))
+    stages = ring_stages(2);
+  else
+    stages = most;
   a.k_stages = stages / 2;
   a.v_stages = stages - a.k_stages;  // values wait for the softmax, keys do not
   a.lead = 3;
@@ -87,9 +93,8 @@ int q8_launch(LaunchQ8& c, int sms) {
   return DSPARK_OK;
 }
 
-// Rows that a pass can serve: two buffers of scores and the parts of the outputs fill the
-// 512 columns of tensor memory.
-constexpr int kMaxRows = 80;
+// Rows that a pass can serve: three groups of 24 columns.
+constexpr int kMaxRows = 72;
 
 // The smallest row block that holds the rows; keys are copied once for all of them.
 template <int D, bool F16>
@@ -97,8 +102,7 @@ int q8_shape(LaunchQ8& c, int sms) {
   if (c.a.n_cols <= 16) return q8_launch<AttnQ8Shape<D, F16, 16, 1, false, 2>>(c, sms);
   if (c.a.n_cols <= 32) return q8_launch<AttnQ8Shape<D, F16, 32, 2, false, 2>>(c, sms);
   if (c.a.n_cols <= 48) return q8_launch<AttnQ8Shape<D, F16, 48, 3, false, F16 ? 1 : 2>>(c, sms);
-  if (c.a.n_cols <= 64) return q8_launch<AttnQ8Shape<D, F16, 64, 2, true, 2>>(c, sms);
-  return q8_launch<AttnQ8Shape<D, F16, kMaxRows, 3, true, 2>>(c, sms);
+  return q8_launch<AttnQ8Shape<D, F16, 80, 3, true, 2>>(c, sms);
 }
 
 }  // namespace

@@ -27,6 +27,8 @@
 // The tensor cores read K once per part of Q and V once per 256 columns.
 #pragma once
 
+#include <type_traits>
+
 #include "dspark_attention.cuh"
 #include "dspark_q8.cuh"
 
@@ -98,7 +100,8 @@ __device__ __forceinline__ void tmem_read(const uint32_t (&at)[N], float (&v)[N]
     asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]), "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7])
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]),
+        "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7])
       : "r"(at[0])
       : "memory");
   if constexpr (N == 2)
@@ -106,7 +109,10 @@ __device__ __forceinline__ void tmem_read(const uint32_t (&at)[N], float (&v)[N]
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]), "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]), "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]), "=&f"(v[1][7])
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]),
+        "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]),
+        "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]),
+        "=&f"(v[1][7])
       : "r"(at[0]), "r"(at[1])
       : "memory");
   if constexpr (N == 3)
@@ -115,7 +121,11 @@ __device__ __forceinline__ void tmem_read(const uint32_t (&at)[N], float (&v)[N]
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%25];\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%26];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]), "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]), "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]), "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]), "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7])
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]),
+        "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]),
+        "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]),
+        "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]),
+        "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7])
       : "r"(at[0]), "r"(at[1]), "r"(at[2])
       : "memory");
   if constexpr (N == 4)
@@ -125,9 +135,64 @@ __device__ __forceinline__ void tmem_read(const uint32_t (&at)[N], float (&v)[N]
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]), "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]), "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]), "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]), "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7]), "=&f"(v[3][0]), "=&f"(v[3][1]), "=&f"(v[3][2]), "=&f"(v[3][3]), "=&f"(v[3][4]), "=&f"(v[3][5]), "=&f"(v[3][6]), "=&f"(v[3][7])
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]),
+        "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]),
+        "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]),
+        "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]),
+        "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7]), "=&f"(v[3][0]),
+        "=&f"(v[3][1]), "=&f"(v[3][2]), "=&f"(v[3][3]), "=&f"(v[3][4]), "=&f"(v[3][5]),
+        "=&f"(v[3][6]), "=&f"(v[3][7])
       : "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3])
       : "memory");
+  if constexpr (N == 6)
+    asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%48];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%49];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%50];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%51];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%32, %33, %34, %35, %36, %37, %38, %39}, [%52];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%40, %41, %42, %43, %44, %45, %46, %47}, [%53];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]),
+        "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]),
+        "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]),
+        "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]),
+        "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7]), "=&f"(v[3][0]),
+        "=&f"(v[3][1]), "=&f"(v[3][2]), "=&f"(v[3][3]), "=&f"(v[3][4]), "=&f"(v[3][5]),
+        "=&f"(v[3][6]), "=&f"(v[3][7]), "=&f"(v[4][0]), "=&f"(v[4][1]), "=&f"(v[4][2]),
+        "=&f"(v[4][3]), "=&f"(v[4][4]), "=&f"(v[4][5]), "=&f"(v[4][6]), "=&f"(v[4][7]),
+        "=&f"(v[5][0]), "=&f"(v[5][1]), "=&f"(v[5][2]), "=&f"(v[5][3]), "=&f"(v[5][4]),
+        "=&f"(v[5][5]), "=&f"(v[5][6]), "=&f"(v[5][7])
+      : "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3]), "r"(at[4]), "r"(at[5])
+      : "memory");
+  if constexpr (N == 8)
+    asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%65];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%66];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%67];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%32, %33, %34, %35, %36, %37, %38, %39}, [%68];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%40, %41, %42, %43, %44, %45, %46, %47}, [%69];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%48, %49, %50, %51, %52, %53, %54, %55}, [%70];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%56, %57, %58, %59, %60, %61, %62, %63}, [%71];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]),
+        "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]),
+        "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]),
+        "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]),
+        "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7]), "=&f"(v[3][0]),
+        "=&f"(v[3][1]), "=&f"(v[3][2]), "=&f"(v[3][3]), "=&f"(v[3][4]), "=&f"(v[3][5]),
+        "=&f"(v[3][6]), "=&f"(v[3][7]), "=&f"(v[4][0]), "=&f"(v[4][1]), "=&f"(v[4][2]),
+        "=&f"(v[4][3]), "=&f"(v[4][4]), "=&f"(v[4][5]), "=&f"(v[4][6]), "=&f"(v[4][7]),
+        "=&f"(v[5][0]), "=&f"(v[5][1]), "=&f"(v[5][2]), "=&f"(v[5][3]), "=&f"(v[5][4]),
+        "=&f"(v[5][5]), "=&f"(v[5][6]), "=&f"(v[5][7]), "=&f"(v[6][0]), "=&f"(v[6][1]),
+        "=&f"(v[6][2]), "=&f"(v[6][3]), "=&f"(v[6][4]), "=&f"(v[6][5]), "=&f"(v[6][6]),
+        "=&f"(v[6][7]), "=&f"(v[7][0]), "=&f"(v[7][1]), "=&f"(v[7][2]), "=&f"(v[7][3]),
+        "=&f"(v[7][4]), "=&f"(v[7][5]), "=&f"(v[7][6]), "=&f"(v[7][7])
+      : "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3]), "r"(at[4]), "r"(at[5]), "r"(at[6]),
+        "r"(at[7])
+      : "memory");
+  static_assert(N <= 4 || N == 6 || N == 8, "no such read");
 }
 // A part of four half precision numbers (two words): their upper bytes.
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) {
@@ -136,6 +201,21 @@ __device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) {
 // What the upper bytes of a pair leave: exact, the rest's bits are the lower ones.
 __device__ __forceinline__ uint32_t without_upper(uint32_t a) {
   return sub_f16x2(a, a & 0xFF00FF00u);
+}
+
+// f(N) for N = n blocks as a constant, 1 .. MOST; n = 0: nothing.
+template <int MOST, typename F>
+__device__ __forceinline__ void by_blocks(int n, F&& f) {
+  if (n == 1) f(std::integral_constant<int, 1>());
+  if constexpr (MOST >= 2)
+    if (n == 2) f(std::integral_constant<int, 2>());
+  if constexpr (MOST >= 3)
+    if (n == 3) f(std::integral_constant<int, 3>());
+  static_assert(MOST <= 3, "more blocks");
+}
+// A store among others that a fence and an arrival follow: free to move among the arithmetic.
+__device__ __forceinline__ void sts_part(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y));
 }
 
 constexpr int kQ8MaxStages = 16;
@@ -163,15 +243,16 @@ struct AttnQ8Shape {
   static constexpr int LAST = F16 ? 6 : 4;                         // scale (log2) of P's last part
   static constexpr int ACCS = SPLIT ? 2 : PP;                      // accumulators of the outputs
   static constexpr int THREADS = 128 + 128 * GROUPS;
-  static constexpr int NC = (NB / 8 + GROUPS - 1) / GROUPS * 8;  // columns of a softmax group
-  static constexpr int WIDTH = NC * GROUPS;  // columns of all groups, NB and more
+  static constexpr int NC = SPLIT ? 24 : 16;                       // columns of a softmax group
+  static constexpr int WIDTH = NB;  // of the control block's arrays; rows are at most NC * GROUPS
   static constexpr uint32_t kStage = kQ8Tile * D;
   static constexpr int kCols = (4 + ACCS) * NB;
   static constexpr uint32_t kColS = 0, kColO = 4 * NB;
   static constexpr uint32_t kTmem = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;  // of rows of D bytes
   static_assert(kCols <= 512, "tensor memory");
-  static_assert(NC <= 32, "sums of a thread's columns in registers");
+  static_assert(NC * GROUPS <= NB, "columns");
+  static_assert(NC <= 32, "a warp has a column's factor in each lane");
 };
 
 template <class S>
@@ -184,16 +265,17 @@ struct AttnQ8Ctl {
   int32_t status, abort, start_r, start_off;
   uint32_t scan[S::THREADS / 32];
   AttnItem item[kItems];
-  // per column (row of q); a group's own. Two of what an item begins with: its
-  // slower warps may still write their results when the next one begins.
-  alignas(16) float nref[2][S::WIDTH];   // minus the rows' references
-  alignas(16) int32_t lim[2][S::WIDTH];  // a row sees the tokens below (and within the window)
-  alignas(16) int32_t at[S::WIDTH];      // element of a row in out, from the item's first
-  alignas(16) float fac[S::WIDTH];       // factor of a row's sums when its reference rises
-  alignas(16) float cq[kItems][S::WIDTH];  // per item: scale * log2(e) over the row's power of two
-  int32_t vexp[S::GROUPS][4];             // per warp of a group: exponent of the largest value scale
-  int32_t new_tok[S::WIDTH];             // new token of a column
-  float red[4][S::WIDTH];                // per warp: maxima, sums
+  // per column (row of q), for each item under way: a group that is done with one begins the
+  // next while others are still at it
+  alignas(16) float nref[kItems][S::WIDTH];   // minus the rows' references
+  alignas(16) int32_t lim[kItems][S::WIDTH];  // a row sees the tokens below (and within the window)
+  alignas(16) float cq[kItems][S::WIDTH];     // scale * log2(e) over the row's power of two
+  alignas(16) int32_t at[S::WIDTH];           // element of a row in out, from the item's first
+  int32_t new_tok[S::WIDTH];                  // new token of a column
+  // a group's own
+  alignas(16) float fac[S::GROUPS][S::NC];    // factor of a row's sums when its reference rises
+  float red[S::GROUPS][4][S::NC];             // per warp: maxima, sums
+  int32_t vexp[S::GROUPS][4];                 // per warp: exponent of the largest value scale
   int32_t odd_n[2], odd[2][2 * S::NB];  // tokens whose values are not finite and not for all rows
 };
 
@@ -690,8 +772,9 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                 w[k] = __ldg(reinterpret_cast<const uint4*>(q0 + t * a.q_row + (j - t * a.Gs) * a.q_head));
             }
           };
-          uint4 next[kDeep];
-          load(0, next);
+          uint4 next[2][kDeep];
+          load(0, next[0]);
+          load(kBatch, next[1]);
           if (wraps >= 1) ok = warp_wait(&ctl.q_empty[b], (wraps - 1u) & 1u);
           if (!ok) break;
           const uint32_t to = s_q + b * S::QP * q_part;
@@ -699,13 +782,15 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             uint32_t v[kDeep][4], top[kDeep];
 #pragma unroll
             for (int k = 0; k < kDeep; ++k) {
-              v[k][0] = next[k].x, v[k][1] = next[k].y, v[k][2] = next[k].z, v[k][3] = next[k].w;
+              const uint4 w = next[0][k];
+              v[k][0] = w.x, v[k][1] = w.y, v[k][2] = w.z, v[k][3] = w.w;
+              next[0][k] = next[1][k];
               uint32_t m = 0;  // the largest magnitudes, as 16-bit patterns
 #pragma unroll
               for (int e = 0; e < 4; ++e) m = __vmaxu2(m, v[k][e] & 0x7FFF7FFFu);
               top[k] = max(m & 0xFFFFu, m >> 16);
             }
-            if (j0 + kBatch < rows) load(j0 + kBatch, next);
+            if (j0 + 2 * kBatch < rows) load(j0 + 2 * kBatch, next[1]);
 #pragma unroll
             for (int o = LPR / 2; o >= 1; o >>= 1)
 #pragma unroll
@@ -779,11 +864,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     // softmax, results
     // =====================================================================
     const int group = (warp - 4) >> 2, quarter = warp & 3, bar = 1 + group;
-    const int gt = (quarter << 5) | lane;  // this thread's token of a tile, and lane of S and O
+    const int gt = (quarter << 5) | lane;  // this thread's token of 128, and lane of S and O
     constexpr int kBlocks = S::NC / 8;     // of 8 columns
-    const int cols = a.Gs * a.t_chunk;
-    const int blocks = (cols + 8 * S::GROUPS - 1) / (8 * S::GROUPS);  // of the group, in use
-    const int c0 = group * blocks * 8;     // the group's first column
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;  // (32 * quarter) << 16
     const uint32_t window = static_cast<uint32_t>(a.window);
     volatile int32_t* abort_flag = &ctl.abort;
@@ -792,68 +874,77 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     uint32_t v_s = a.k_stages, v_phase = 0;  // ring position of the next tile of values
     int rv = 0;                              // weights stand for 2^-rv of their values
     bool recorded = false;
-    for (int j = c0 + gt; j < min(c0 + 8 * blocks, S::NB); j += 128) {
+    float(&red)[4][S::NC] = ctl.red[group];
+    float(&fac)[S::NC] = ctl.fac[group];
+    for (int j = tid - 128; j < S::NB; j += 128 * S::GROUPS) {
       const int t = j / a.Gs;
       ctl.new_tok[j] = t;
       ctl.at[j] = (t * a.Hq + j - t * a.Gs) * S::D;
     }
-    bar_sync(bar, 128);
+    bar_sync(1 + S::GROUPS, 128 * S::GROUPS);
     for (;;) {
       const uint32_t slot = items % kItems, list = lists & 1u;
       bool failed = !mbar_wait(&ctl.item_full[slot], (items / kItems) & 1u);
       const AttnItem& it = ctl.item[slot];
-      if (!failed && it.tiles > 0) failed = !mbar_wait(&ctl.factors[slot], (items / kItems) & 1u);
-      const float* const cq = ctl.cq[slot];
-      float* const nref = ctl.nref[items & 1u];
-      int32_t* const lims = ctl.lim[items & 1u];
       // (the item that ends the line has nothing but its mark)
       const int rows = failed || it.tiles < 0 ? 0 : it.t_rows * a.Gs;
+      // the item's columns, in blocks of 8 dealt out evenly to the groups
+      const int blocks = ((rows + 7) / 8 + S::GROUPS - 1) / S::GROUPS;
+      const int c0 = group * blocks * 8;  // the group's first column
       const int my_rows = max(0, min(8 * blocks, rows - c0));
       const int nb = (my_rows + 7) >> 3;
-      for (int j = c0 + gt; j < c0 + 8 * nb; j += 128) {
+      float* const nref = ctl.nref[slot] + c0;
+      int32_t* const lims = ctl.lim[slot] + c0;
+      const float* const cq = ctl.cq[slot] + c0;
+      if (gt < 8 * nb) {
         // a column past the rows takes no part: all its scores are below its reference
-        nref[j] = j < rows ? kNoRef : -INFINITY;
-        lims[j] = j < rows ? it.lim0 + ctl.new_tok[j] : INT_MIN / 2;
+        nref[gt] = gt < my_rows ? kNoRef : -INFINITY;
+        lims[gt] = gt < my_rows ? it.lim0 + ctl.new_tok[c0 + gt] : INT_MIN / 2;
       }
       if (group == 0 && gt == 0) ctl.odd_n[list] = 0;
+      if (!failed && it.tiles > 0) failed = !mbar_wait(&ctl.factors[slot], (items / kItems) & 1u);
       if (bar_any(bar, 128, failed || *abort_flag != 0)) {
         *abort_flag = 1;
         break;
       }
       if (it.tiles < 0) break;
       ++items;
-      const int lim_last = it.lim0 + it.t_rows - 1;
+      const int tiles = it.tiles, begin = it.begin, end = it.end, lim0 = it.lim0;
+      const int lim_last = lim0 + it.t_rows - 1;
       const int lo_last = a.window == INT_MAX ? 0 : max(0, lim_last - a.window);
       uint64_t l[S::NC / 2];  // sums of the columns' weights over the thread's tokens, in pairs
 #pragma unroll
       for (int j = 0; j < S::NC / 2; ++j) l[j] = 0;
 
       bool leave = false;
-      for (int i = 0; i < it.tiles; ++i, ++done) {
+      int tok0 = it.tile0 * kQ8Tile;
+      for (int i = 0; i < tiles; ++i, ++done, tok0 += kQ8Tile) {
         const uint32_t sbuf = done & 1u;
-        const int tok0 = (it.tile0 + i) * kQ8Tile;
         // of each 128 tokens: whether all are visible to every row, whether some are to some;
         // this thread's token, its scales (what no row sees has none)
         bool whole[2], live[2], some[2];
         float ks[2], vs[2];
         failed |= !mbar_wait(&ctl.full[v_s], v_phase);
         const uint32_t row_v = s_ring + v_s * S::kStage + gt * S::D;
+        {
+          const uint32_t at_s = s_scale + (v_s - a.k_stages) * (8u * a.n_scales);
+          bool good = true;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int from = tok0 + h * kTileTok, tok = from + gt;
-          whole[h] = from + kTileTok <= it.lim0 && from >= lo_last;
-          live[h] = from < it.end && from + kTileTok > it.begin;
-          some[h] = tok >= it.begin && tok < it.end;
-          ks[h] = vs[h] = 0.f;
-          if (some[h]) {
-            const uint32_t at_s = s_scale + (v_s - a.k_stages) * (8u * a.n_scales) +
-                                  4u * ((h * kTileTok + gt) >> min(a.b_shift, 8));
-            ks[h] = lds_f32(at_s);
-            vs[h] = lds_f32(at_s + 4u * a.n_scales);
-            if (!is_scale(ks[h]) || !is_scale(vs[h])) {
-              set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
-              ks[h] = vs[h] = 1.f;
-            }
+          for (int h = 0; h < 2; ++h) {
+            const int from = tok0 + h * kTileTok, tok = from + gt;
+            whole[h] = from + kTileTok <= lim0 && from >= lo_last;
+            live[h] = from < end && from + kTileTok > begin;
+            some[h] = tok >= begin && tok < end;
+            const uint32_t at_h = at_s + 4u * ((h * kTileTok + gt) >> min(a.b_shift, 8));
+            ks[h] = lds_f32(at_h);
+            vs[h] = lds_f32(at_h + 4u * a.n_scales);
+            good = good && (!some[h] || (is_scale(ks[h]) && is_scale(vs[h])));
+            ks[h] = some[h] ? ks[h] : 0.f;
+            vs[h] = some[h] ? vs[h] : 0.f;
+          }
+          if (!good) {
+            set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
+            ks[0] = ks[1] = vs[0] = vs[1] = 1.f;
           }
         }
         if (++v_s == v_end) v_s = a.k_stages, v_phase ^= 1u;
@@ -861,151 +952,118 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         tc_fence_after();
         const uint32_t s_tile = tmem + lanes + S::kColS + sbuf * (2 * S::NB) + c0;
 #pragma unroll 1
-       for (int unit = 0; unit < S::UNITS; ++unit, ++units) {
-        const uint32_t pb = units % S::PBUFS, use = units / S::PBUFS;
-        const bool begins = i == 0 && unit == 0;
-        const uint32_t s_addr = s_tile + unit * S::NB;  // (the unit's first 128)
-        auto pick = [&](auto& x, int g) { return S::SPLIT ? (unit ? x[1] : x[0]) : x[g]; };
-        int vexp = -126;  // vs < 2^vexp
+        for (int unit = 0; unit < S::UNITS; ++unit, ++units) {
+          const uint32_t pb = units % S::PBUFS, use = units / S::PBUFS;
+          const bool begins = i == 0 && unit == 0;
+          const uint32_t s_addr = s_tile + unit * S::NB;  // (the unit's first 128)
+          // this unit's: of its g-th 128 tokens
+          auto pick = [&](auto& x, int g) { return S::SPLIT ? (unit ? x[1] : x[0]) : x[g]; };
+          bool all_whole = true;
 #pragma unroll
-        for (int g = 0; g < S::HALVES; ++g)
-          vexp = max(vexp, static_cast<int>(__float_as_uint(pick(vs, g)) >> 23) - 126);
-        // -inf where the row does not see the token
-        auto hide = [&](int b, int g, float (&y)[8]) {
-          const int4* lim4 = reinterpret_cast<const int4*>(&lims[c0 + 8 * b]);
-          const int tok = tok0 + (S::SPLIT ? unit : g) * kTileTok + gt;
+          for (int g = 0; g < S::HALVES; ++g) all_whole = all_whole && pick(whole, g);
+          // -inf where the row does not see the token
+          auto hide = [&](int b, int g, float* y) {
+            const int4* lim4 = reinterpret_cast<const int4*>(&lims[8 * b]);
+            const int tok = tok0 + (S::SPLIT ? unit : g) * kTileTok + gt;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int4 m = lim4[k];
-            if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[4 * k] = -INFINITY;
-            if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[4 * k + 1] = -INFINITY;
-            if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[4 * k + 2] = -INFINITY;
-            if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[4 * k + 3] = -INFINITY;
-          }
-        };
-        // The weights are made with the references so far, the check that they stay in range
-        // comes with them: a unit whose weights leave it raises the references and makes them again.
-        uint64_t sum[S::NC / 2];  // of the unit's weights
-        bool raise = begins;      // the first unit's maxima
-        for (;;) {
-          if (raise) {
+            for (int k = 0; k < 2; ++k) {
+              const int4 m = lim4[k];
+              if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[4 * k] = -INFINITY;
+              if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[4 * k + 1] = -INFINITY;
+              if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[4 * k + 2] = -INFINITY;
+              if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[4 * k + 3] = -INFINITY;
+            }
+          };
+          // The scores of NBK blocks, all read at once. NBK is a constant so that the blocks'
+          // arithmetic, long chains each, runs side by side.
+          auto scores = [&](auto nbk, auto& x) {
+            constexpr int N = decltype(nbk)::value * S::HALVES;
+            uint32_t from[N];
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-              if (b < nb) {
-                const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[c0 + 8 * b]);
-                const ulonglong2 f0 = cq4[0], f1 = cq4[1];
-                const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
-                float v[8];
+            for (int q = 0; q < N; ++q)
+              from[q] = s_addr + (q % S::HALVES) * S::NB + 8 * (q / S::HALVES);
+            tmem_read<N>(from, x);
+          };
+          // The columns' largest scores, and the largest exponent of a value's scale; then the
+          // references and what is made with them so far.
+          auto raise_refs = [&](auto nbk) {
+            constexpr int NBK = decltype(nbk)::value;
+            float x[NBK * S::HALVES][8];
+            scores(nbk, x);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = -INFINITY;
+            for (int b = 0; b < NBK; ++b) {
+              const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[8 * b]);
+              const ulonglong2 f0 = cq4[0], f1 = cq4[1];
+              const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
+              float v[8];
 #pragma unroll
-                for (int g = 0; g < S::HALVES; ++g) {
-                  if (!pick(live, g)) continue;
-                  float z[1][8];
-                  const uint32_t from[1] = {s_addr + g * S::NB + 8 * b};
-                  tmem_read<1>(from, z);
-                  float(&y)[8] = z[0];
-                  const uint64_t ks2 = pair(pick(ks, g), pick(ks, g));
+              for (int k = 0; k < 8; ++k) v[k] = -INFINITY;
 #pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    unpair(mul2(mul2(pair(y[2 * k], y[2 * k + 1]), f[k]), ks2), y[2 * k], y[2 * k + 1]);
-                  if (!pick(whole, g)) hide(b, g, y);
+              for (int g = 0; g < S::HALVES; ++g) {
+                float* const y = x[b * S::HALVES + g];
+                const uint64_t ks2 = pair(pick(ks, g), pick(ks, g));
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) v[k] = fmaxf(v[k], y[k]);  // NaN takes no part
-                }
-                const float m = over_four<true>(fold_columns<true>(v, lane));
-                if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = m;
+                for (int k = 0; k < 4; ++k)
+                  unpair(mul2(mul2(pair(y[2 * k], y[2 * k + 1]), f[k]), ks2), y[2 * k], y[2 * k + 1]);
+                if (!all_whole) hide(b, g, y);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = fmaxf(v[k], y[k]);  // NaN takes no part
               }
-            const int warp_vexp = __reduce_max_sync(0xFFFFFFFFu, vexp);
-            if (lane == 0) ctl.vexp[group][quarter] = warp_vexp;
-            if (bar_any(bar, 128, failed || *abort_flag != 0)) {
-              leave = true;
-              break;
+              const float m = over_four<true>(fold_columns<true>(v, lane));
+              if ((lane & 3) == 0) red[quarter][8 * b + (lane >> 2)] = m;
             }
-            const int* const ve = ctl.vexp[group];
-            const int top_vexp = max(max(ve[0], ve[1]), max(ve[2], ve[3]));
-            const int old_rv = rv;
-            if (begins || top_vexp > rv) rv = min(max(top_vexp + kScaleRoom, -100), 120);
-            const float down_v = begins ? 1.f : exp2f(static_cast<float>(old_rv - rv));
-            for (int j = c0 + gt; j < c0 + my_rows; j += 128) {
-              float top = -INFINITY, low = INFINITY;  // of the quarters that hold a token
+          };
+          auto rescale = [&](auto nbk, float down_v) {
+            constexpr int NBK = decltype(nbk)::value;
 #pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const float v = ctl.red[w][j];
-                top = fmaxf(top, v);
-                if (v > -INFINITY) low = fminf(low, v);
+            for (int b = 0; b < NBK; ++b) {
+              const float* f = &fac[8 * b];
+#pragma unroll
+              for (int p = 0; p < S::ACCS; ++p) {
+                float z[1][8];
+                const uint32_t from[1] = {tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b};
+                tmem_read<1>(from, z);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) z[0][k] *= f[k] * down_v;
+                tmem_st8(from[0], z[0]);
               }
-              // weights are half precision numbers, whatever the outputs' type
-              const float down = top - low > kPeak ? kPeakBase<true> : kBase<true>;
-              const float ref = fabsf(top) < kNoShift ? top - down : top, old = -nref[j];
-              ctl.fac[j] = ref > old ? ex2_approx(old - ref) : 1.f;
-              if (ref > old) nref[j] = -ref;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
             }
-            bar_sync(bar, 128);
-            if (!begins) {
-              const uint32_t before = units - 1u;
-              failed |= !mbar_wait(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
-              tc_fence_after();
+            tmem_wait_st();
+          };
+          // The weights with the references so far, and the largest of them.
+          uint64_t sum[S::NC / 2];  // of the unit's weights
+          auto weights = [&](auto nbk) -> uint32_t {
+            constexpr int NBK = decltype(nbk)::value;
+            float x[NBK * S::HALVES][8];
+            scores(nbk, x);
+            uint64_t ks2[S::HALVES], vr2[S::HALVES];
 #pragma unroll
-              for (int b = 0; b < kBlocks; ++b)
-                if (b < nb) {
-                  const float* f = &ctl.fac[c0 + 8 * b];
-#pragma unroll
-                  for (int p = 0; p < S::ACCS; ++p) {
-                    const uint32_t at_o = tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b;
-                    float z[1][8];
-                    const uint32_t from[1] = {at_o};
-                    tmem_read<1>(from, z);
-                    float(&o)[8] = z[0];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] *= f[k] * down_v;
-                    tmem_st8(at_o, o);
-                  }
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
-                }
-              tmem_wait_st();
+            for (int g = 0; g < S::HALVES; ++g) {
+              const float vr = pick(vs, g) * __uint_as_float(static_cast<uint32_t>(127 - rv) << 23) *
+                               (S::PP == 3 ? kCut : 1.f);
+              vr2[g] = pair(vr, vr), ks2[g] = pair(pick(ks, g), pick(ks, g));
             }
-          }
-          uint64_t ks2[S::HALVES], vr2[S::HALVES];
+            const uint32_t p_row = s_p + pb * S::HALVES * a.p_bytes + gt * 16u;
+            uint32_t hot = 0;
 #pragma unroll
-          for (int g = 0; g < S::HALVES; ++g) {
-            const float vr = pick(vs, g) * __uint_as_float(static_cast<uint32_t>(127 - rv) << 23) *
-                             (S::PP == 3 ? kCut : 1.f);
-            vr2[g] = pair(vr, vr), ks2[g] = pair(pick(ks, g), pick(ks, g));
-          }
-          // this buffer of weights is free once its last unit has been multiplied
-          if (use >= 1 && !(raise && !begins)) failed |= !mbar_wait(&ctl.pv_done[pb], (use - 1u) & 1u);
-          uint32_t hot = 0;  // the largest weights
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b)
-            if (b < nb) {
-              float x[S::HALVES][8];
-              uint32_t from[S::HALVES];
-#pragma unroll
-              for (int g = 0; g < S::HALVES; ++g) from[g] = s_addr + g * S::NB + 8 * b;
-              tmem_read<S::HALVES>(from, x);
-              const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[c0 + 8 * b]);
-              const ulonglong2* nr4 = reinterpret_cast<const ulonglong2*>(&nref[c0 + 8 * b]);
+            for (int b = 0; b < NBK; ++b) {
+              const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[8 * b]);
+              const ulonglong2* nr4 = reinterpret_cast<const ulonglong2*>(&nref[8 * b]);
               const ulonglong2 f0 = cq4[0], f1 = cq4[1], m0 = nr4[0], m1 = nr4[1];
               const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y}, m[4] = {m0.x, m0.y, m1.x, m1.y};
               const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
 #pragma unroll
               for (int g = 0; g < S::HALVES; ++g) {
-                float* const z = x[g];
-                if (!pick(live, g)) {
-                  if (g == 0)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sum[4 * b + k] = 0;
-                  continue;
-                }
+                float* const z = x[b * S::HALVES + g];
                 float y[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)  // t - m, t = s cq ks
                   unpair(fma2(mul2(pair(z[2 * k], z[2 * k + 1]), f[k]), ks2[g], m[k]), y[2 * k],
                          y[2 * k + 1]);
-                if (!pick(whole, g)) hide(b, g, y);
+                if (!all_whole) hide(b, g, y);
                 // The weights enter the second product cut to their parts' bits (no more
                 // than the output's own rounding); their sum l is of the unrounded ones.
                 uint32_t w[4];
@@ -1018,8 +1076,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                   w[k] = pack2<true>(p0, p1);
                 }
                 hot = max_f16x2(max_f16x2(hot, w[0]), max_f16x2(max_f16x2(w[1], w[2]), w[3]));
-                const uint32_t to = s_p + (pb * S::HALVES + g) * a.p_bytes + (chunk >> 1) * 2048u +
-                                    gt * 16u + (chunk & 1u) * 8u;
+                const uint32_t to = p_row + g * a.p_bytes + (chunk >> 1) * 2048u + (chunk & 1u) * 8u;
 #pragma unroll
                 for (int p = 0; p < S::PP; ++p) {
                   if (p > 0) {
@@ -1030,63 +1087,117 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                         w[k] = mul_f16x2(w[k], S::LAST == 4 ? 0x4C004C00u : 0x54005400u);
                     }
                   }
-                  sts_u2(to + p * a.part_bytes, upper_bytes(w[0], w[1]), upper_bytes(w[2], w[3]));
+                  sts_part(to + p * a.part_bytes, upper_bytes(w[0], w[1]), upper_bytes(w[2], w[3]));
                 }
               }
             }
-          if (raise) break;
-          // infinite: past the range of half precision
-          const bool high = (hot & 0x7C00u) == 0x7C00u || (hot & 0x7C000000u) == 0x7C000000u;
-          if (!bar_any(bar, 128, high || failed)) break;
-          raise = true;
-        }
-        if (leave) break;
+            return hot;
+          };
+          bool any_live = false;
 #pragma unroll
-        for (int j = 0; j < S::NC / 2; ++j)
-          if (j / 4 < nb) l[j] = add2(l[j], sum[j]);
-        if (group == 0) {
-          // Zero weights do not silence values that are not finite, and a tile's rest may
-          // hold anything: what no row sees is zeroed, and of what only some rows see the
-          // non-finite values are taken out here and added to those rows at the end.
+          for (int g = 0; g < S::HALVES; ++g) any_live = any_live || pick(live, g);
+          const int nbl = any_live ? nb : 0;  // blocks at work
 #pragma unroll
-          for (int g = 0; g < S::HALVES; ++g) {
-            if (pick(whole, g) || !pick(live, g)) continue;
-            const int half = S::SPLIT ? unit : g, tok = tok0 + half * kTileTok + gt;
-            const uint32_t my_v = row_v + half * (kTileTok * S::D);
-            const bool all = tok < it.lim0 && tok >= lo_last;
-            // in a step of 32 tokens that is multiplied at all
-            const bool used = (tok | 31) >= it.begin && (tok & ~31) < it.end;
-            if (!used) {
-            } else if (!pick(some, g)) {
+          for (int j = 0; j < S::NC / 2; ++j) sum[j] = 0;
+          // The check that the weights stay in range comes after them: a unit whose weights
+          // leave it raises the references and makes them again.
+          bool raise = begins;  // the first unit's maxima
+          for (;;) {
+            if (raise) {
+              by_blocks<kBlocks>(nbl, raise_refs);
+              int vexp = -126;  // vs < 2^vexp
 #pragma unroll
-              for (int k = 0; k < S::D / 16; ++k) sts_u4(my_v + k * 16, 0, 0, 0, 0);
-            } else if (!all) {
-              bool odd = false;
-#pragma unroll 4
-              for (int k = 0; k < S::D / 16; ++k) {
-                const uint4 v = lds_u4(my_v + k * 16);
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                bool hit = false;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  // bit 7 of each byte that is NaN (lower seven bits all set)
-                  const uint32_t nan = ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                  w[q] &= ~(nan | (nan - (nan >> 7)));
-                  hit |= nan != 0;
-                }
-                if (hit) sts_u4(my_v + k * 16, w[0], w[1], w[2], w[3]);
-                odd |= hit;
+              for (int g = 0; g < S::HALVES; ++g)
+                vexp = max(vexp, static_cast<int>(__float_as_uint(pick(vs, g)) >> 23) - 126);
+              vexp = __reduce_max_sync(0xFFFFFFFFu, vexp);
+              if (lane == 0) ctl.vexp[group][quarter] = vexp;
+              if (bar_any(bar, 128, failed || *abort_flag != 0)) {
+                leave = true;
+                break;
               }
-              if (odd) ctl.odd[list][atomicAdd(&ctl.odd_n[list], 1)] = tok;
+              const int* const ve = ctl.vexp[group];
+              const int top_vexp = max(max(ve[0], ve[1]), max(ve[2], ve[3]));
+              const int old_rv = rv;
+              if (begins || top_vexp > rv) rv = min(max(top_vexp + kScaleRoom, -100), 120);
+              if (gt < my_rows && nbl > 0) {
+                float top = -INFINITY, low = INFINITY;  // of the quarters that hold a token
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  const float v = red[w][gt];
+                  top = fmaxf(top, v);
+                  if (v > -INFINITY) low = fminf(low, v);
+                }
+                // weights are half precision numbers, whatever the outputs' type
+                const float down = top - low > kPeak ? kPeakBase<true> : kBase<true>;
+                const float ref = fabsf(top) < kNoShift ? top - down : top, old = -nref[gt];
+                fac[gt] = ref > old ? ex2_approx(old - ref) : 1.f;
+                if (ref > old) nref[gt] = -ref;
+              }
+              bar_sync(bar, 128);
+              if (!begins) {
+                const uint32_t before = units - 1u;
+                failed |= !mbar_wait(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
+                tc_fence_after();
+                const float down_v = exp2f(static_cast<float>(old_rv - rv));
+                by_blocks<kBlocks>(nbl, [&](auto nbk) { rescale(nbk, down_v); });
+              }
+            }
+            // this buffer of weights is free once its last unit has been multiplied
+            if (use >= 1 && !(raise && !begins)) failed |= !mbar_wait(&ctl.pv_done[pb], (use - 1u) & 1u);
+            uint32_t hot = 0;
+            by_blocks<kBlocks>(nbl, [&](auto nbk) { hot = weights(nbk); });
+            if (raise) break;
+            // infinite: past the range of half precision
+            const bool high = (hot & 0x7C00u) == 0x7C00u || (hot & 0x7C000000u) == 0x7C000000u;
+            if (!bar_any(bar, 128, high || failed)) break;
+            raise = true;
+          }
+          if (leave) break;
+#pragma unroll
+          for (int j = 0; j < S::NC / 2; ++j) l[j] = add2(l[j], sum[j]);
+          if (!all_whole && group == 0) {
+            // Zero weights do not silence values that are not finite, and a tile's rest may
+            // hold anything: what no row sees is zeroed, and of what only some rows see the
+            // non-finite values are taken out here and added to those rows at the end.
+#pragma unroll
+            for (int g = 0; g < S::HALVES; ++g) {
+              if (pick(whole, g) || !pick(live, g)) continue;
+              const int half = S::SPLIT ? unit : g, tok = tok0 + half * kTileTok + gt;
+              const uint32_t my_v = row_v + half * (kTileTok * S::D);
+              const bool all = tok < lim0 && tok >= lo_last;
+              // in a step of 32 tokens that is multiplied at all
+              const bool used = (tok | 31) >= begin && (tok & ~31) < end;
+              if (!used) {
+              } else if (!pick(some, g)) {
+#pragma unroll
+                for (int k = 0; k < S::D / 16; ++k) sts_u4(my_v + k * 16, 0, 0, 0, 0);
+              } else if (!all) {
+                bool odd = false;
+#pragma unroll 4
+                for (int k = 0; k < S::D / 16; ++k) {
+                  const uint4 v = lds_u4(my_v + k * 16);
+                  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                  bool hit = false;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    // bit 7 of each byte that is NaN (lower seven bits all set)
+                    const uint32_t nan = ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                    w[q] &= ~(nan | (nan - (nan >> 7)));
+                    hit |= nan != 0;
+                  }
+                  if (hit) sts_u4(my_v + k * 16, w[0], w[1], w[2], w[3]);
+                  odd |= hit;
+                }
+                if (odd) ctl.odd[list][atomicAdd(&ctl.odd_n[list], 1)] = tok;
+              }
             }
           }
+          fence_proxy_async();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.p_full[pb]);
         }
-        fence_proxy_async();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_full[pb]);
-       }
-       if (leave) break;
+        if (leave) break;
       }
       if (leave) {
         *abort_flag = 1;
@@ -1095,37 +1206,38 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 
       // ---- the item's rows ----------------------------------------------
       const bool alone = it.starts && it.ends;
-      const int64_t part_row = static_cast<int64_t>(2 * id + (it.starts ? 1 : 0)) * a.n_cols;
+      const int64_t part_row = static_cast<int64_t>(2 * id + (it.starts ? 1 : 0)) * a.n_cols + c0;
+      by_blocks<kBlocks>(nb, [&](auto nbk) {
+        constexpr int NBK = decltype(nbk)::value;
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-        if (b < nb) {
+        for (int b = 0; b < NBK; ++b) {
           float v[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) unpair(l[4 * b + k], v[2 * k], v[2 * k + 1]);
-          const float sum = over_four<false>(fold_columns<false>(v, lane));
-          if ((lane & 3) == 0) ctl.red[quarter][c0 + 8 * b + (lane >> 2)] = sum;
+          const float total = over_four<false>(fold_columns<false>(v, lane));
+          if ((lane & 3) == 0) red[quarter][8 * b + (lane >> 2)] = total;
         }
+      });
       if (bar_any(bar, 128, failed || *abort_flag != 0)) {
         *abort_flag = 1;
         break;
       }
       // every warp for itself: the factor of column j in lane j
-      float fac = 1.f;
+      float inv = 1.f;
       if (lane < my_rows) {
-        const int j = c0 + lane;
-        const float total = (ctl.red[0][j] + ctl.red[1][j]) + (ctl.red[2][j] + ctl.red[3][j]);
-        const bool seen = lims[j] > 0;
-        if (alone) fac = seen ? 1.f / total : 0.f;  // no token: O is zero
+        const float total = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        const bool seen = lims[lane] > 0;
+        if (alone) inv = seen ? 1.f / total : 0.f;  // no token: O is zero
         if (quarter == 0) {
-          const float m = -nref[j];
+          const float m = -nref[lane];
           if (!alone)
-            reinterpret_cast<float2*>(a.part_ml)[part_row + j] = make_float2(m, total);
+            reinterpret_cast<float2*>(a.part_ml)[part_row + lane] = make_float2(m, total);
           else if (a.lse)
-            a.lse[it.row0 * a.Hq + it.head0 + ctl.at[j] / S::D] =
+            a.lse[it.row0 * a.Hq + it.head0 + ctl.at[c0 + lane] / S::D] =
                 seen ? plus_log2(m, total) * 0.69314718055994531f : -INFINITY;
         }
       }
-      if (it.tiles > 0) {
+      if (tiles > 0) {
         const uint32_t last = units - 1u;
         failed |= !mbar_wait(&ctl.odd_full, lists & 1u);
         failed |= !mbar_wait(&ctl.pv_done[last % S::PBUFS], (last / S::PBUFS) & 1u);
@@ -1133,63 +1245,69 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         ++lists;
       }
       if (failed) *abort_flag = 1;  // seen by all at the next item
-      const int odd_n = it.tiles > 0 ? ctl.odd_n[list] : 0;
+      const int odd_n = tiles > 0 ? ctl.odd_n[list] : 0;
       const bool writer = S::D == 128 || lane < 16;  // M = 64 fills 16 lanes of each warp's 32
       const int d = S::D == 128 ? gt : quarter * 16 + lane;
       uint16_t* const out =
           static_cast<uint16_t*>(a.out) + (it.row0 * a.Hq + it.head0) * S::D + d;
-      const float unit = __uint_as_float(static_cast<uint32_t>(rv + 127) << 23);
-      float* const part = a.part_o + (part_row + c0) * S::D + d;
+      const float back = __uint_as_float(static_cast<uint32_t>(rv + 127) << 23);
+      float* const part = a.part_o + part_row * S::D + d;
+      by_blocks<kBlocks>(nb, [&](auto nbk) {
+        constexpr int NBK = decltype(nbk)::value;
+        float acc[NBK * S::ACCS][8];
+        if (tiles > 0) {
+          uint32_t from[NBK * S::ACCS];
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        if (b >= nb) break;
-        float o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = 0.f;
-        if (it.tiles > 0) {
-          float parts[S::ACCS][8];
-          uint32_t from[S::ACCS];
-#pragma unroll
-          for (int p = 0; p < S::ACCS; ++p) from[p] = tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b;
-          tmem_read<S::ACCS>(from, parts);
-          constexpr float kLast = 1.f / (1 << S::LAST);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            o[k] = parts[S::ACCS - 1][k] * kLast;
-#pragma unroll
-            for (int p = S::ACCS - 2; p >= 0; --p) o[k] += parts[p][k];
-            o[k] *= unit;
-          }
-        }
-        for (int q = 0; q < odd_n; ++q) {
-          const int u = ctl.odd[list][q];
-          const int32_t page = a.table[it.r * a.stride + (u >> a.shift)];
-          if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages) || !writer) continue;
-          const uint32_t code = static_cast<const uint8_t*>(a.v_cache)[
-              page * a.page_stride + (u & ((1 << a.shift) - 1)) * a.token_stride +
-              it.kv_head * a.head_stride + d];
-          if ((code & 0x7Fu) != 0x7Fu) continue;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (static_cast<uint32_t>(lims[c0 + 8 * b + k] - 1 - u) < window) o[k] = NAN;
-        }
-        const int4* at4 = reinterpret_cast<const int4*>(&ctl.at[c0 + 8 * b]);
-        const int4 a0 = at4[0], a1 = at4[1];
-        const int to[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-        float f[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = __shfl_sync(0xFFFFFFFFu, fac, 8 * b + k);
-        const int live = writer ? my_rows - 8 * b : 0;  // columns of the block to write
-        if (alone) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < live) out[to[k]] = static_cast<uint16_t>(pack2<S::F16>(o[k] * f[k], 0.f));
+          for (int q = 0; q < NBK * S::ACCS; ++q)
+            from[q] = tmem + lanes + S::kColO + (q % S::ACCS) * a.n_cols + c0 + 8 * (q / S::ACCS);
+          tmem_read<NBK * S::ACCS>(from, acc);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < live) part[(8 * b + k) * S::D] = o[k];
+          for (int q = 0; q < NBK * S::ACCS; ++q)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[q][k] = 0.f;
         }
-      }
+        constexpr float kLast = 1.f / (1 << S::LAST);
+#pragma unroll
+        for (int b = 0; b < NBK; ++b) {
+          float o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            o[k] = acc[b * S::ACCS + S::ACCS - 1][k] * kLast;
+#pragma unroll
+            for (int p = S::ACCS - 2; p >= 0; --p) o[k] += acc[b * S::ACCS + p][k];
+            o[k] *= back;
+          }
+          for (int q = 0; q < odd_n; ++q) {
+            const int u = ctl.odd[list][q];
+            const int32_t page = a.table[it.r * a.stride + (u >> a.shift)];
+            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages) || !writer) continue;
+            const uint32_t code = static_cast<const uint8_t*>(a.v_cache)[
+                page * a.page_stride + (u & ((1 << a.shift) - 1)) * a.token_stride +
+                it.kv_head * a.head_stride + d];
+            if ((code & 0x7Fu) != 0x7Fu) continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (static_cast<uint32_t>(lims[8 * b + k] - 1 - u) < window) o[k] = NAN;
+          }
+          const int4* at4 = reinterpret_cast<const int4*>(&ctl.at[c0 + 8 * b]);
+          const int4 a0 = at4[0], a1 = at4[1];
+          const int to[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = __shfl_sync(0xFFFFFFFFu, inv, 8 * b + k);
+          const int mine = writer ? my_rows - 8 * b : 0;  // columns of the block to write
+          if (alone) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < mine) out[to[k]] = static_cast<uint16_t>(pack2<S::F16>(o[k] * f[k], 0.f));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < mine) part[(8 * b + k) * S::D] = o[k];
+          }
+        }
+      });
       if (it.ends && !it.starts) {
         recorded = true;
         if (tid == 128) {
