@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     for (uint32_t i = 0; i < kItems; ++i) {
       mbar_init(&ctl.item_full[i], 1);
       mbar_init(&ctl.factors[i], 1);
-      mbar_init(&ctl.item_empty[i], 4 * S::GROUPS + 2);  // softmax warps, products, queries
+      mbar_init(&ctl.item_empty[i], 4 * S::GROUPS + 3);  // softmax warps, products, copies
     }
     ctl.status = DSPARK_OK;
     ctl.abort = 0;
@@ -389,121 +389,57 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 
   if (warp < 2) {
     // =====================================================================
-    // copies: warp 0 keys and the items' records, warp 1 values. A
-    // tile's copies cost a warp some fifty instructions, which share the SM's
-    // issue slots with the softmax: with both kinds in one warp and page ids
-    // fetched tile by tile the copies fell behind the memory.
+    // copies: warp 0 keys, warp 1 values and all scales. A lone warp takes some
+    // seven cycles for an instruction: what tiles inside the visible tokens do not
+    // need is apart.
     // =====================================================================
     if (u_begin < u_end) {
       const bool keys = warp == 0;
       const uint64_t policy = policy_evict_first();
       const int rows_box = min(1 << a.shift, kQ8Tile);
       const int n_box = kQ8Tile / rows_box;
-      const int box = lane % n_box;
       const bool copier = lane < n_box;
+      const int head_box = (lane % n_box) * rows_box, in_page = (1 << a.shift) - 1;
       const uint32_t box_bytes = rows_box * S::D;
       const uint32_t first_stage = keys ? 0u : static_cast<uint32_t>(a.k_stages);
       const uint32_t end_stage =
           keys ? static_cast<uint32_t>(a.k_stages) : static_cast<uint32_t>(a.k_stages + a.v_stages);
       const CUtensorMap* const map = keys ? &map_k : &map_v;
-      const uint32_t dst0 = s_ring + box * box_bytes;
-      int r = ctl.start_r, off = ctl.start_off;
-      uint32_t u = u_begin;
-      // requests r_base .. r_base+31, one per lane
-      int r_base = -1000;
-      AttnReq mine{};
+      const uint32_t dst0 = s_ring + head_box * S::D;
       uint32_t items = 0, s = first_stage, wraps = 0;
       bool ok = true;
-      while (ok) {
-        // ---- the next item of the line
-        AttnReq q;
-        int h = 0, lead_in = 0, take = 0;
-        bool found = false;
-        while (u < u_end && r < a.B) {  // (r: lengths that changed under the call)
-          if (r >= r_base + 32 || r < r_base) {
-            r_base = r;
-            mine.units = 0;
-            mine.begin = 0;
-            if (r + lane < a.B) {
-              attn_request<kQ8Tile>(a, r + lane, t0, mine);
-              if (mine.units > 0)  // the table rows of requests to come
-                prefetch_l2(a.table + (r + lane) * a.stride + (mine.begin >> a.shift));
-            }
-          }
-          const int src = r - r_base;
-          q.units = __shfl_sync(0xFFFFFFFFu, mine.units, src);
-          if (off >= q.units * a.Hkv) {
-            off -= q.units * a.Hkv;
-            ++r;
-            continue;
-          }
-          h = off / q.units;
-          lead_in = off - h * q.units;
-          take = static_cast<int>(min(static_cast<uint32_t>(q.units - lead_in), u_end - u));
-          u += take;
-          off += take;
-          if (lead_in + take > a.lead) {
-            q.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, src);
-            q.t_rows = __shfl_sync(0xFFFFFFFFu, mine.t_rows, src);
-            q.lim0 = __shfl_sync(0xFFFFFFFFu, mine.lim0, src);
-            q.begin = __shfl_sync(0xFFFFFFFFu, mine.begin, src);
-            q.end = __shfl_sync(0xFFFFFFFFu, mine.end, src);
-            found = true;
-            break;
-          }  // else nothing but the item's lead: the next CTA begins it
-        }
-        if (!found) break;
-        const int in_head = max(lead_in - a.lead, 0);
-        const int tile0 = q.begin / kQ8Tile + in_head;
-        const int tiles = q.end > 0 ? lead_in + take - a.lead - in_head : 0;
-        const int32_t* const row = a.table + r * a.stride;
-        const int last_page = max(q.end - 1, 0) >> a.shift;
-        int page0 = (tile0 * kQ8Tile) >> a.shift;  // of the 32 ids that the lanes hold
+      for (;;) {
+        const uint32_t slot = items % kItems;
+        ok = warp_wait(&ctl.item_full[slot], (items / kItems) & 1u);
+        if (!ok) break;
+        const AttnItem& it = ctl.item[slot];
+        const int tiles = it.tiles, h = it.kv_head, begin = it.begin, end = it.end;
+        int tile_tok = it.tile0 * kQ8Tile;
+        const int32_t* const row = a.table + it.r * a.stride;
+        if (__any_sync(0xFFFFFFFFu, tiles < 0)) break;
+        if (lane == 0) mbar_arrive(&ctl.item_empty[slot]);
+        ++items;
+        const int last_page = max(end - 1, 0) >> a.shift;
+        int page0 = tile_tok >> a.shift;  // of the 32 ids that the lanes hold
         int ids = 0, next_ids = 0;
-        if (tiles > 0) ids = row[min(page0 + lane, last_page)];
-        if (keys) {
-          const uint32_t slot = items % kItems, use = items / kItems;
-          if (use >= 1) ok = warp_wait(&ctl.item_empty[slot], (use - 1u) & 1u);
-          if (!ok) break;
-          if (lane == 0) {
-            AttnItem& item = ctl.item[slot];
-            item.row0 = q.row0;
-            item.r = r;
-            item.kv_head = h;
-            item.head0 = h * a.G + part * a.Gs;
-            item.tiles = tiles;
-            item.tile0 = tile0;
-            item.t_rows = q.t_rows;
-            item.lim0 = q.lim0;
-            item.begin = q.begin;
-            item.end = q.end;
-            item.starts = in_head == 0;
-            item.ends = lead_in + take == q.units;
-            item.first = line.owner(u - take - lead_in + a.lead);
-            mbar_arrive(&ctl.item_full[slot]);
-          }
-          ++items;
+        if (tiles > 0) {
+          ids = row[min(page0 + lane, last_page)];
+          next_ids = row[min(page0 + 32 + lane, last_page)];
         }
-        // ---- its tiles
-        if (tiles > 0) next_ids = row[min(page0 + 32 + lane, last_page)];
-        const int in_page = (1 << a.shift) - 1, head_box = box * rows_box;
-        int tile_tok = tile0 * kQ8Tile, rel = ((tile_tok + head_box) >> a.shift) - page0;
-        uint32_t dst = dst0 + s * S::kStage;
         const float* const ks0 = a.k_scale + h * a.scale_head;
         const float* const vs0 = a.v_scale + h * a.scale_head;
-        for (int i = 0; i < tiles; ++i) {
+        for (int i = 0; i < tiles; ++i, tile_tok += kQ8Tile) {
           if (((tile_tok >> a.shift) - page0) >= 32) {  // a window of ids holds whole tiles
             page0 += 32;
-            rel -= 32;
             ids = next_ids;
             next_ids = row[min(page0 + 32 + lane, last_page)];
           }
-          int page = __shfl_sync(0xFFFFFFFFu, ids, rel);
           const int tok = tile_tok + head_box;  // this lane's box of the tile
+          int page = __shfl_sync(0xFFFFFFFFu, ids, (tok >> a.shift) - page0);
           bool load = copier;
           uint32_t bytes = S::kStage;
-          if (tile_tok < q.begin || tile_tok + kQ8Tile > q.end) {
-            load = copier && tok < q.end && tok + rows_box > q.begin;
+          if (tile_tok < begin || tile_tok + kQ8Tile > end) {
+            load = copier && tok < end && tok + rows_box > begin;
             bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * box_bytes;
           }
           if (wraps > 0 && !warp_test(&ctl.empty[s], (wraps - 1u) & 1u)) {
@@ -516,7 +452,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
               set_status(&ctl.status, DSPARK_ERR_BAD_DATA);
               page = 0;
             }
-            tma_load_4d(dst, map, 0, tok & in_page, h, page, &ctl.full[s], policy);
+            tma_load_4d(dst0 + s * S::kStage, map, 0, tok & in_page, h, page, &ctl.full[s], policy);
           }
           if (!keys) {
             // the scales of the tile's keys and values travel with its values, whose stage
@@ -527,7 +463,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
               const int j = j0 + lane, t = tile_tok + (j << a.b_shift);
               const int id = __shfl_sync(0xFFFFFFFFu, ids, min((t >> a.shift) - page0, 31));
               // a block that starts before the first token that is seen may hold it
-              if (j < a.n_scales && t < q.end && t + (1 << a.b_shift) > q.begin &&
+              if (j < a.n_scales && t < end && t + (1 << a.b_shift) > begin &&
                   static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages)) {
                 const int64_t from = id * a.scale_page + ((t & in_page) >> a.b_shift) * a.scale_block;
                 cp_async4(to + 4u * j, ks0 + from);
@@ -536,20 +472,9 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             }
             cp_async_arrive(&ctl.full[s]);
           }
-          tile_tok += kQ8Tile;
-          rel = ((tile_tok + head_box) >> a.shift) - page0;
-          dst += S::kStage;
-          if (++s == end_stage) s = first_stage, dst = dst0 + first_stage * S::kStage, ++wraps;
+          if (++s == end_stage) s = first_stage, ++wraps;
         }
-      }
-      // the end of the line
-      if (ok && keys) {
-        const uint32_t slot = items % kItems, use = items / kItems;
-        if (use >= 1) ok = warp_wait(&ctl.item_empty[slot], (use - 1u) & 1u);
-        if (ok && lane == 0) {
-          ctl.item[slot].tiles = -1;
-          mbar_arrive(&ctl.item_full[slot]);
-        }
+        if (!ok) break;
       }
       if (!ok) {
         set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
@@ -735,33 +660,93 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     __syncwarp();
   } else if (warp == 3) {
     // =====================================================================
-    // queries: a group of lanes has a row in registers, 8 elements a lane, scales
-    // it and writes its parts. Two tiles of them where there is room, so that an
-    // item's are there when the one before it ends. Rows past an item's keep what
-    // they hold (their columns take no part), from the start zeros. One warp does this
-    // beside 16 and more tiles of 80 rows only if nothing in it waits: four rows
-    // of each group at once, the next ones' loads before the arithmetic of these,
-    // two elements an instruction (a loop without these took 74,000 cycles for 80
-    // rows, 3 times as long as their 16 tiles).
+    // The items' records, ahead of everything, and their queries: a group of lanes
+    // has a row in registers, 8 elements a lane, scales it and writes its parts. Two
+    // tiles of queries where there is room, so that an item's are there when the one
+    // before it ends. Rows past an item's keep what they hold (their columns take no
+    // part), from the start zeros. Two rows of each group at once, the next ones' loads
+    // before the arithmetic of these, two elements an instruction. (Not more at once:
+    // the first item's pass is one through instructions that no cache holds yet.)
     // =====================================================================
     if (u_begin < u_end) {
-      constexpr int LPR = S::D / 8, kRows = 32 / LPR, kDeep = 4, kBatch = kRows * kDeep;
+      constexpr int LPR = S::D / 8, kRows = 32 / LPR, kDeep = 2, kBatch = kRows * kDeep;
       const int sub = lane / LPR, l = lane % LPR;
       const uint32_t gs_inv = (65536u + a.Gs - 1u) / a.Gs;  // j / Gs = j * gs_inv >> 16 for j < 160
       for (uint32_t i = lane * 16u; i < a.q_bufs * S::QP * q_part; i += 512u) sts_u4(s_q + i, 0, 0, 0, 0);
+      int r = ctl.start_r, off = ctl.start_off;
+      uint32_t u = u_begin;
+      // requests r_base .. r_base+31, one per lane
+      int r_base = -1000;
+      AttnReq mine{};
       uint32_t items = 0, b = 0, wraps = 0;
       bool ok = true;
       for (;;) {
-        const uint32_t slot = items % kItems;
-        ok = warp_wait(&ctl.item_full[slot], (items / kItems) & 1u);
+        // ---- the next item of the line
+        AttnReq q{};
+        int h = 0, lead_in = 0, take = 0;
+        bool found = false;
+        while (u < u_end && r < a.B) {  // (r: lengths that changed under the call)
+          if (r >= r_base + 32 || r < r_base) {
+            r_base = r;
+            mine.units = 0;
+            mine.begin = 0;
+            if (r + lane < a.B) {
+              attn_request<kQ8Tile>(a, r + lane, t0, mine);
+              if (mine.units > 0)  // the table rows of requests to come
+                prefetch_l2(a.table + (r + lane) * a.stride + (mine.begin >> a.shift));
+            }
+          }
+          const int src = r - r_base;
+          q.units = __shfl_sync(0xFFFFFFFFu, mine.units, src);
+          if (off >= q.units * a.Hkv) {
+            off -= q.units * a.Hkv;
+            ++r;
+            continue;
+          }
+          h = off / q.units;
+          lead_in = off - h * q.units;
+          take = static_cast<int>(min(static_cast<uint32_t>(q.units - lead_in), u_end - u));
+          u += take;
+          off += take;
+          if (lead_in + take > a.lead) {
+            q.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, src);
+            q.t_rows = __shfl_sync(0xFFFFFFFFu, mine.t_rows, src);
+            q.lim0 = __shfl_sync(0xFFFFFFFFu, mine.lim0, src);
+            q.begin = __shfl_sync(0xFFFFFFFFu, mine.begin, src);
+            q.end = __shfl_sync(0xFFFFFFFFu, mine.end, src);
+            found = true;
+            break;
+          }  // else nothing but the item's lead: the next CTA begins it
+        }
+        const uint32_t slot = items % kItems, use = items / kItems;
+        if (use >= 1) ok = warp_wait(&ctl.item_empty[slot], (use - 1u) & 1u);
         if (!ok) break;
-        const AttnItem& it = ctl.item[slot];
-        const int tiles = __shfl_sync(0xFFFFFFFFu, it.tiles, 0);
-        if (tiles < 0) break;
-        const int rows = min(it.t_rows * a.Gs, a.n_cols);
-        const uint16_t* const q0 = a.q + it.row0 * a.q_row + it.head0 * a.q_head + 8 * l;
+        const int in_head = max(lead_in - a.lead, 0);
+        const int head0 = h * a.G + part * a.Gs;
+        const int tiles = !found ? -1 : q.end > 0 ? lead_in + take - a.lead - in_head : 0;
+        if (lane == 0) {
+          AttnItem& item = ctl.item[slot];
+          item.row0 = q.row0;
+          item.r = r;
+          item.kv_head = h;
+          item.head0 = head0;
+          item.tiles = tiles;
+          item.tile0 = q.begin / kQ8Tile + in_head;
+          item.t_rows = q.t_rows;
+          item.lim0 = q.lim0;
+          item.begin = q.begin;
+          item.end = q.end;
+          item.starts = in_head == 0;
+          item.ends = lead_in + take == q.units;
+          if (found) item.first = line.owner(u - take - lead_in + a.lead);
+          mbar_arrive(&ctl.item_full[slot]);
+        }
         ++items;
+        if (!found) break;  // the end of the line
         if (tiles > 0) {
+          // ---- its queries
+          const int rows = min(q.t_rows * a.Gs, a.n_cols);
+          const uint16_t* const q0 = a.q + q.row0 * a.q_row + head0 * a.q_head + 8 * l;
           auto load = [&](int j0, uint4 (&w)[kDeep]) {
 #pragma unroll
             for (int k = 0; k < kDeep; ++k) {
@@ -778,6 +763,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           if (wraps >= 1) ok = warp_wait(&ctl.q_empty[b], (wraps - 1u) & 1u);
           if (!ok) break;
           const uint32_t to = s_q + b * S::QP * q_part;
+#pragma unroll 1
           for (int j0 = 0; j0 < rows; j0 += kBatch) {
             uint32_t v[kDeep][4], top[kDeep];
 #pragma unroll
@@ -795,52 +781,42 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             for (int o = LPR / 2; o >= 1; o >>= 1)
 #pragma unroll
               for (int k = 0; k < kDeep; ++k) top[k] = max(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], o));
-            uint32_t part[S::QP][kDeep][2];
-            int e[kDeep];
-            bool odd = false;
 #pragma unroll
             for (int k = 0; k < kDeep; ++k) {
-              odd |= top[k] >= (S::F16 ? 0x7C00u : 0x7F80u);
               // exponent of the largest element; rows below 2^-100 keep their size
               const uint32_t bits = __float_as_uint(word_to_f32<S::F16>(top[k]).x);
-              e[k] = max(static_cast<int>(bits >> 23) - 127, -100);
-              const float f = __uint_as_float(static_cast<uint32_t>(7 - e[k] + 127) << 23);
-              uint32_t h[4];
+              const int e = max(static_cast<int>(bits >> 23) - 127, -100);
+              const float f = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+                  uint32_t h16[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float2 x = word_to_f32<S::F16>(v[k][i]);
-                h[i] = pack2<true>(x.x * f, x.y * f);
+                h16[i] = pack2<true>(x.x * f, x.y * f);
               }
-              if (odd) {  // what is not finite: NaN
+              if (top[k] >= (S::F16 ? 0x7C00u : 0x7F80u)) {  // what is not finite: NaN
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const float2 x = word_to_f32<S::F16>(v[k][i]);
-                  h[i] = pack2<true>(fabsf(x.x) < INFINITY ? x.x * f : NAN,
-                                     fabsf(x.y) < INFINITY ? x.y * f : NAN);
+                  h16[i] = pack2<true>(fabsf(x.x) < INFINITY ? x.x * f : NAN,
+                                       fabsf(x.y) < INFINITY ? x.y * f : NAN);
                 }
               }
+              const uint32_t j = j0 + k * kRows + sub;
+              const uint32_t swap = S::D == 128 ? j & 7u : (j >> 1) & 3u;
+              const uint32_t addr = to + j * S::D + (((static_cast<uint32_t>(l) >> 1) ^ swap) << 4) + (l & 1) * 8;
+              const bool real = j < static_cast<uint32_t>(a.n_cols);
 #pragma unroll
               for (int p = 0; p < S::QP; ++p) {
                 uint32_t c[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  c[i] = f16x2_to_e4m3x2(h[i]);
-                  if (p + 1 < S::QP) h[i] = sub_f16x2(h[i], e4m3x2_to_f16x2(c[i]));
+                  c[i] = f16x2_to_e4m3x2(h16[i]);
+                  if (p + 1 < S::QP) h16[i] = sub_f16x2(h16[i], e4m3x2_to_f16x2(c[i]));
                 }
-                part[p][k][0] = c[0] | (c[1] << 16);
-                part[p][k][1] = c[2] | (c[3] << 16);
+                if (real) sts_part(addr + p * q_part, c[0] | (c[1] << 16), c[2] | (c[3] << 16));
               }
-            }
-#pragma unroll
-            for (int k = 0; k < kDeep; ++k) {
-              const uint32_t j = j0 + k * kRows + sub;
-              if (j >= static_cast<uint32_t>(a.n_cols)) continue;
-              const uint32_t swap = S::D == 128 ? j & 7u : (j >> 1) & 3u;
-              const uint32_t addr = to + j * S::D + (((static_cast<uint32_t>(l) >> 1) ^ swap) << 4) + (l & 1) * 8;
-#pragma unroll
-              for (int p = 0; p < S::QP; ++p) sts_u2(addr + p * q_part, part[p][k][0], part[p][k][1]);
-              if (l == 0)
-                ctl.cq[slot][j] = a.c * __uint_as_float(static_cast<uint32_t>(e[k] - 7 + 127) << 23);
+              if (l == 0 && real)
+                ctl.cq[slot][j] = a.c * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
             }
           }
           fence_proxy_async();
@@ -849,7 +825,6 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         if (lane == 0) {
           if (tiles > 0) mbar_arrive(&ctl.q_full[b]);
           mbar_arrive(&ctl.factors[slot]);
-          mbar_arrive(&ctl.item_empty[slot]);
         }
         if (tiles > 0 && ++b == static_cast<uint32_t>(a.q_bufs)) b = 0, ++wraps;
       }
