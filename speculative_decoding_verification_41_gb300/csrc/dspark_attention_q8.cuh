@@ -144,55 +144,7 @@ __device__ __forceinline__ void tmem_read(const uint32_t (&at)[N], float (&v)[N]
         "=&f"(v[3][6]), "=&f"(v[3][7])
       : "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3])
       : "memory");
-  if constexpr (N == 6)
-    asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%48];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%49];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%50];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%51];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%32, %33, %34, %35, %36, %37, %38, %39}, [%52];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%40, %41, %42, %43, %44, %45, %46, %47}, [%53];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]),
-        "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]),
-        "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]),
-        "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]),
-        "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7]), "=&f"(v[3][0]),
-        "=&f"(v[3][1]), "=&f"(v[3][2]), "=&f"(v[3][3]), "=&f"(v[3][4]), "=&f"(v[3][5]),
-        "=&f"(v[3][6]), "=&f"(v[3][7]), "=&f"(v[4][0]), "=&f"(v[4][1]), "=&f"(v[4][2]),
-        "=&f"(v[4][3]), "=&f"(v[4][4]), "=&f"(v[4][5]), "=&f"(v[4][6]), "=&f"(v[4][7]),
-        "=&f"(v[5][0]), "=&f"(v[5][1]), "=&f"(v[5][2]), "=&f"(v[5][3]), "=&f"(v[5][4]),
-        "=&f"(v[5][5]), "=&f"(v[5][6]), "=&f"(v[5][7])
-      : "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3]), "r"(at[4]), "r"(at[5])
-      : "memory");
-  if constexpr (N == 8)
-    asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%64];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%65];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%66];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%67];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%32, %33, %34, %35, %36, %37, %38, %39}, [%68];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%40, %41, %42, %43, %44, %45, %46, %47}, [%69];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%48, %49, %50, %51, %52, %53, %54, %55}, [%70];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%56, %57, %58, %59, %60, %61, %62, %63}, [%71];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]),
-        "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]),
-        "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]),
-        "=&f"(v[1][7]), "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]),
-        "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7]), "=&f"(v[3][0]),
-        "=&f"(v[3][1]), "=&f"(v[3][2]), "=&f"(v[3][3]), "=&f"(v[3][4]), "=&f"(v[3][5]),
-        "=&f"(v[3][6]), "=&f"(v[3][7]), "=&f"(v[4][0]), "=&f"(v[4][1]), "=&f"(v[4][2]),
-        "=&f"(v[4][3]), "=&f"(v[4][4]), "=&f"(v[4][5]), "=&f"(v[4][6]), "=&f"(v[4][7]),
-        "=&f"(v[5][0]), "=&f"(v[5][1]), "=&f"(v[5][2]), "=&f"(v[5][3]), "=&f"(v[5][4]),
-        "=&f"(v[5][5]), "=&f"(v[5][6]), "=&f"(v[5][7]), "=&f"(v[6][0]), "=&f"(v[6][1]),
-        "=&f"(v[6][2]), "=&f"(v[6][3]), "=&f"(v[6][4]), "=&f"(v[6][5]), "=&f"(v[6][6]),
-        "=&f"(v[6][7]), "=&f"(v[7][0]), "=&f"(v[7][1]), "=&f"(v[7][2]), "=&f"(v[7][3]),
-        "=&f"(v[7][4]), "=&f"(v[7][5]), "=&f"(v[7][6]), "=&f"(v[7][7])
-      : "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3]), "r"(at[4]), "r"(at[5]), "r"(at[6]),
-        "r"(at[7])
-      : "memory");
-  static_assert(N <= 4 || N == 6 || N == 8, "no such read");
+  static_assert(N <= 4, "no such read");
 }
 // A part of four half precision numbers (two words): their upper bytes.
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) {
@@ -216,6 +168,41 @@ __device__ __forceinline__ void by_blocks(int n, F&& f) {
 // A store among others that a fence and an arrival follow: free to move among the arithmetic.
 __device__ __forceinline__ void sts_part(uint32_t addr, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y));
+}
+
+// Bounded waits whose loop is a function of its own: most phases are complete, or nearly, when
+// they are asked for, and thirty copies of the loop are a third of the kernel's instructions.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+  WaitClock clock;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (clock.expired()) return false;
+  }
+}
+template <bool INLINE>  // where a call's registers would be spilled ones
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
+  if constexpr (INLINE) return mbar_wait(bar, parity);
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done ? true : wait_long(smem_addr(bar), parity);
+}
+template <bool INLINE>
+__device__ __forceinline__ bool warp_wait_on(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, wait_on<INLINE>(bar, parity)) != 0;
 }
 
 constexpr int kQ8MaxStages = 16;
@@ -410,7 +397,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       bool ok = true;
       for (;;) {
         const uint32_t slot = items % kItems;
-        ok = warp_wait(&ctl.item_full[slot], (items / kItems) & 1u);
+        ok = warp_wait_on<S::SPLIT>(&ctl.item_full[slot], (items / kItems) & 1u);
         if (!ok) break;
         const AttnItem& it = ctl.item[slot];
         const int tiles = it.tiles, h = it.kv_head, begin = it.begin, end = it.end;
@@ -443,7 +430,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * box_bytes;
           }
           if (wraps > 0 && !warp_test(&ctl.empty[s], (wraps - 1u) & 1u)) {
-            ok = warp_wait(&ctl.empty[s], (wraps - 1u) & 1u);
+            ok = warp_wait_on<S::SPLIT>(&ctl.empty[s], (wraps - 1u) & 1u);
             if (!ok) break;
           }
           if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
@@ -465,7 +452,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
               // a block that starts before the first token that is seen may hold it
               if (j < a.n_scales && t < end && t + (1 << a.b_shift) > begin &&
                   static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages)) {
-                const int64_t from = id * a.scale_page + ((t & in_page) >> a.b_shift) * a.scale_block;
+                const int64_t from = id * a.scale_page +
+                                     static_cast<int64_t>(static_cast<uint32_t>(t & in_page) >> a.b_shift) * a.scale_block;
                 cp_async4(to + 4u * j, ks0 + from);
                 cp_async4(to + 4u * (a.n_scales + j), vs0 + from);
               }
@@ -482,7 +470,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       }
       // leave no copy in flight into this CTA's shared memory
       for (uint32_t i = first_stage; i < end_stage; ++i)
-        if (i < s || wraps > 0) mbar_wait(&ctl.full[i], (i < s ? wraps : wraps - 1u) & 1u);
+        if (i < s || wraps > 0) wait_on<S::SPLIT>(&ctl.full[i], (i < s ? wraps : wraps - 1u) & 1u);
     }
   } else if (warp == 2) {
     // =====================================================================
@@ -548,18 +536,20 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             --s_tiles;
             if (leader) {
               const uint64_t q0 = at(desc_kq, s_q + rq.s * S::QP * q_part);
-              auto half = [&](uint32_t h) {
+              // halves that hold a token some row sees
+              const uint32_t h0 = s_begin < s_tok + kTileTok ? 0u : 1u;
+              const uint32_t h1 = s_stop > s_tok + kTileTok ? 2u : 1u;
+#pragma unroll 1
+              for (uint32_t h = h0; h < h1; ++h) {
                 const uint64_t k0 = at(desc_kq, s_ring + rk.s * S::kStage + h * (kTileTok * S::D));
-                const uint32_t col = S::kColS + ((s_done & 1u) * 2u + h) * S::NB;
-#pragma unroll
-                for (int p = 0; p < S::QP; ++p)
+                const uint32_t col = tmem + S::kColS + ((s_done & 1u) * 2u + h) * S::NB;
+#pragma unroll 1
+                for (uint32_t p = 0; p < S::QP; ++p)
 #pragma unroll
                   for (int k = 0; k < S::D / 32; ++k)
-                    tc_mma_f8(tmem + col, k0 + static_cast<uint32_t>(2 * k),
+                    tc_mma_f8(col, k0 + static_cast<uint32_t>(2 * k),
                               q0 + (p * (q_part >> 4) + 2 * k), idesc_s, p > 0 || k > 0);
-              };
-              if (s_begin < s_tok + kTileTok) half(0);
-              if (s_stop > s_tok + kTileTok) half(1);
+              }
               tc_commit(&ctl.empty[rk.s]);
               tc_commit(&ctl.s_full[s_done & 1u]);
               if (s_tiles == 0) tc_commit(&ctl.q_empty[rq.s]);
@@ -589,10 +579,10 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             const bool last = o_sub + 1u == S::UNITS;  // unit of the tile
             // the groups' lists of the item are written
             if (leader && last && o_tiles == 1) mbar_arrive(&ctl.odd_full);
-            ok = warp_wait(&ctl.full[rv.s], rv.phase);
+            ok = warp_wait_on<S::SPLIT>(&ctl.full[rv.s], rv.phase);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (uint32_t g = 0; g < S::HALVES; ++g) {
               const uint32_t h = S::SPLIT ? o_sub : g;
               const int tok = tok0 + static_cast<int>(h) * kTileTok;
@@ -603,26 +593,20 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                 const uint64_t v0 = at(desc_v, s_ring + rv.s * S::kStage + h * (kTileTok * S::D));
                 const uint64_t p0 = at(desc_p, s_p + (buf * S::HALVES + g) * a.p_bytes);
                 constexpr uint32_t kStep = 32 * S::D >> 4;  // of V
-                auto product_o = [&](uint32_t col, uint64_t p, bool fresh) {
-                  if (k0 == 0 && k1 == kTileTok / 32) {
-#pragma unroll
-                    for (int k = 0; k < kTileTok / 32; ++k)
-                      tc_mma_f8(tmem + S::kColO + col, v0 + static_cast<uint32_t>(k * kStep),
-                                p + static_cast<uint32_t>(k * 32), idesc_o, k > 0 || !fresh);
-                  } else {
+                // split: the parts one after another, the last into columns of its own
+                constexpr uint32_t kPasses = S::SPLIT ? S::PP : 1;
 #pragma unroll 1
-                    for (int k = k0; k < k1; ++k)
-                      tc_mma_f8(tmem + S::kColO + col, v0 + static_cast<uint32_t>(k * kStep),
-                                p + static_cast<uint32_t>(k * 32), idesc_o, k > k0 || !fresh);
+                for (uint32_t p = 0; p < kPasses; ++p) {
+                  const bool apart = S::SPLIT && p + 1 == kPasses;
+                  const uint32_t col = tmem + S::kColO + (apart ? n : 0u);
+                  const uint64_t pp = p0 + p * (a.part_bytes >> 4);
+                  uint32_t more = !first || (p > 0 && !apart);
+#pragma unroll 2
+                  for (int k = k0; k < k1; ++k) {
+                    tc_mma_f8(col, v0 + static_cast<uint32_t>(k) * kStep,
+                              pp + static_cast<uint32_t>(k) * 32u, idesc_o, more);
+                    more = 1;
                   }
-                };
-                if constexpr (S::SPLIT) {
-#pragma unroll 1
-                  for (int p = 0; p + 1 < S::PP; ++p)
-                    product_o(0, p0 + p * (a.part_bytes >> 4), first && p == 0);
-                  product_o(n, p0 + (S::PP - 1) * (a.part_bytes >> 4), first);
-                } else {
-                  product_o(0, p0, first);
                 }
               }
               first = false;
@@ -654,7 +638,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
         *reinterpret_cast<volatile int32_t*>(&ctl.abort) = 1;
         if (leader) tc_commit(&ctl.drained);  // no product may outlive the CTA
-        warp_wait(&ctl.drained, 0);
+        warp_wait_on<S::SPLIT>(&ctl.drained, 0);
       }
     }
     __syncwarp();
@@ -664,12 +648,11 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     // has a row in registers, 8 elements a lane, scales it and writes its parts. Two
     // tiles of queries where there is room, so that an item's are there when the one
     // before it ends. Rows past an item's keep what they hold (their columns take no
-    // part), from the start zeros. Two rows of each group at once, the next ones' loads
-    // before the arithmetic of these, two elements an instruction. (Not more at once:
-    // the first item's pass is one through instructions that no cache holds yet.)
+    // part), from the start zeros. The loads are four rows ahead of the arithmetic, which takes
+    // two elements an instruction.
     // =====================================================================
     if (u_begin < u_end) {
-      constexpr int LPR = S::D / 8, kRows = 32 / LPR, kDeep = 2, kBatch = kRows * kDeep;
+      constexpr int LPR = S::D / 8, kRows = 32 / LPR, kDeep = 1, kBatch = kRows * kDeep;
       const int sub = lane / LPR, l = lane % LPR;
       const uint32_t gs_inv = (65536u + a.Gs - 1u) / a.Gs;  // j / Gs = j * gs_inv >> 16 for j < 160
       for (uint32_t i = lane * 16u; i < a.q_bufs * S::QP * q_part; i += 512u) sts_u4(s_q + i, 0, 0, 0, 0);
@@ -719,7 +702,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           }  // else nothing but the item's lead: the next CTA begins it
         }
         const uint32_t slot = items % kItems, use = items / kItems;
-        if (use >= 1) ok = warp_wait(&ctl.item_empty[slot], (use - 1u) & 1u);
+        if (use >= 1) ok = warp_wait_on<S::SPLIT>(&ctl.item_empty[slot], (use - 1u) & 1u);
         if (!ok) break;
         const int in_head = max(lead_in - a.lead, 0);
         const int head0 = h * a.G + part * a.Gs;
@@ -757,10 +740,10 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                 w[k] = __ldg(reinterpret_cast<const uint4*>(q0 + t * a.q_row + (j - t * a.Gs) * a.q_head));
             }
           };
-          uint4 next[2][kDeep];
-          load(0, next[0]);
-          load(kBatch, next[1]);
-          if (wraps >= 1) ok = warp_wait(&ctl.q_empty[b], (wraps - 1u) & 1u);
+          uint4 next[4][kDeep];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) load(k * kBatch, next[k]);
+          if (wraps >= 1) ok = warp_wait_on<S::SPLIT>(&ctl.q_empty[b], (wraps - 1u) & 1u);
           if (!ok) break;
           const uint32_t to = s_q + b * S::QP * q_part;
 #pragma unroll 1
@@ -770,13 +753,14 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             for (int k = 0; k < kDeep; ++k) {
               const uint4 w = next[0][k];
               v[k][0] = w.x, v[k][1] = w.y, v[k][2] = w.z, v[k][3] = w.w;
-              next[0][k] = next[1][k];
+#pragma unroll
+              for (int e = 0; e < 3; ++e) next[e][k] = next[e + 1][k];
               uint32_t m = 0;  // the largest magnitudes, as 16-bit patterns
 #pragma unroll
               for (int e = 0; e < 4; ++e) m = __vmaxu2(m, v[k][e] & 0x7FFF7FFFu);
               top[k] = max(m & 0xFFFFu, m >> 16);
             }
-            if (j0 + 2 * kBatch < rows) load(j0 + 2 * kBatch, next[1]);
+            load(j0 + 4 * kBatch, next[3]);
 #pragma unroll
             for (int o = LPR / 2; o >= 1; o >>= 1)
 #pragma unroll
@@ -859,7 +843,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     bar_sync(1 + S::GROUPS, 128 * S::GROUPS);
     for (;;) {
       const uint32_t slot = items % kItems, list = lists & 1u;
-      bool failed = !mbar_wait(&ctl.item_full[slot], (items / kItems) & 1u);
+      bool failed = !wait_on<S::SPLIT>(&ctl.item_full[slot], (items / kItems) & 1u);
       const AttnItem& it = ctl.item[slot];
       // (the item that ends the line has nothing but its mark)
       const int rows = failed || it.tiles < 0 ? 0 : it.t_rows * a.Gs;
@@ -877,7 +861,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         lims[gt] = gt < my_rows ? it.lim0 + ctl.new_tok[c0 + gt] : INT_MIN / 2;
       }
       if (group == 0 && gt == 0) ctl.odd_n[list] = 0;
-      if (!failed && it.tiles > 0) failed = !mbar_wait(&ctl.factors[slot], (items / kItems) & 1u);
+      if (!failed && it.tiles > 0) failed = !wait_on<S::SPLIT>(&ctl.factors[slot], (items / kItems) & 1u);
       if (bar_any(bar, 128, failed || *abort_flag != 0)) {
         *abort_flag = 1;
         break;
@@ -899,7 +883,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         // this thread's token, its scales (what no row sees has none)
         bool whole[2], live[2], some[2];
         float ks[2], vs[2];
-        failed |= !mbar_wait(&ctl.full[v_s], v_phase);
+        failed |= !wait_on<S::SPLIT>(&ctl.full[v_s], v_phase);
         const uint32_t row_v = s_ring + v_s * S::kStage + gt * S::D;
         {
           const uint32_t at_s = s_scale + (v_s - a.k_stages) * (8u * a.n_scales);
@@ -923,7 +907,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           }
         }
         if (++v_s == v_end) v_s = a.k_stages, v_phase ^= 1u;
-        failed |= !mbar_wait(&ctl.s_full[sbuf], (done >> 1) & 1u);
+        failed |= !wait_on<S::SPLIT>(&ctl.s_full[sbuf], (done >> 1) & 1u);
         tc_fence_after();
         const uint32_t s_tile = tmem + lanes + S::kColS + sbuf * (2 * S::NB) + c0;
 #pragma unroll 1
@@ -949,51 +933,41 @@ __global__ void __launch_bounds__(S::THREADS, 1)
               if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[4 * k + 3] = -INFINITY;
             }
           };
-          // The scores of NBK blocks, all read at once. NBK is a constant so that the blocks'
-          // arithmetic, long chains each, runs side by side.
-          auto scores = [&](auto nbk, auto& x) {
-            constexpr int N = decltype(nbk)::value * S::HALVES;
-            uint32_t from[N];
-#pragma unroll
-            for (int q = 0; q < N; ++q)
-              from[q] = s_addr + (q % S::HALVES) * S::NB + 8 * (q / S::HALVES);
-            tmem_read<N>(from, x);
-          };
           // The columns' largest scores, and the largest exponent of a value's scale; then the
           // references and what is made with them so far.
-          auto raise_refs = [&](auto nbk) {
-            constexpr int NBK = decltype(nbk)::value;
-            float x[NBK * S::HALVES][8];
-            scores(nbk, x);
-#pragma unroll
-            for (int b = 0; b < NBK; ++b) {
+          auto raise_refs = [&](int n) {
+#pragma unroll 1
+            for (int b = 0; b < n; ++b) {
               const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[8 * b]);
               const ulonglong2 f0 = cq4[0], f1 = cq4[1];
               const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
-              float v[8];
+              float x[S::HALVES][8], v[8];
+              uint32_t from[S::HALVES];
+#pragma unroll
+              for (int g = 0; g < S::HALVES; ++g) from[g] = s_addr + g * S::NB + 8 * b;
+              tmem_read<S::HALVES>(from, x);
 #pragma unroll
               for (int k = 0; k < 8; ++k) v[k] = -INFINITY;
 #pragma unroll
               for (int g = 0; g < S::HALVES; ++g) {
-                float* const y = x[b * S::HALVES + g];
                 const uint64_t ks2 = pair(pick(ks, g), pick(ks, g));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  unpair(mul2(mul2(pair(y[2 * k], y[2 * k + 1]), f[k]), ks2), y[2 * k], y[2 * k + 1]);
-                if (!all_whole) hide(b, g, y);
+                  unpair(mul2(mul2(pair(x[g][2 * k], x[g][2 * k + 1]), f[k]), ks2), x[g][2 * k],
+                         x[g][2 * k + 1]);
+                if (!all_whole) hide(b, g, x[g]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = fmaxf(v[k], y[k]);  // NaN takes no part
+                for (int k = 0; k < 8; ++k) v[k] = fmaxf(v[k], x[g][k]);  // NaN takes no part
               }
               const float m = over_four<true>(fold_columns<true>(v, lane));
               if ((lane & 3) == 0) red[quarter][8 * b + (lane >> 2)] = m;
             }
           };
-          auto rescale = [&](auto nbk, float down_v) {
-            constexpr int NBK = decltype(nbk)::value;
-#pragma unroll
-            for (int b = 0; b < NBK; ++b) {
+          auto rescale = [&](int n, float down_v) {
+#pragma unroll 1
+            for (int b = 0; b < n; ++b) {
               const float* f = &fac[8 * b];
-#pragma unroll
+#pragma unroll 1
               for (int p = 0; p < S::ACCS; ++p) {
                 float z[1][8];
                 const uint32_t from[1] = {tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b};
@@ -1002,41 +976,44 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                 for (int k = 0; k < 8; ++k) z[0][k] *= f[k] * down_v;
                 tmem_st8(from[0], z[0]);
               }
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                l[4 * b + k] = mul2(l[4 * b + k], pair(f[2 * k], f[2 * k + 1]));
             }
             tmem_wait_st();
+#pragma unroll
+            for (int j = 0; j < S::NC / 2; ++j)
+              if (j / 4 < n) l[j] = mul2(l[j], pair(fac[2 * j], fac[2 * j + 1]));
           };
           // The weights with the references so far, and the largest of them.
           uint64_t sum[S::NC / 2];  // of the unit's weights
           auto weights = [&](auto nbk) -> uint32_t {
+            // NBK blocks at once: their arithmetic, long chains each, runs side by side. (And
+            // no more than these: what the warps of a CTA run has to stay in the instruction
+            // cache. The two halves unrolled, or 4 rows of queries at once above, cost 10 to 20%.)
             constexpr int NBK = decltype(nbk)::value;
-            float x[NBK * S::HALVES][8];
-            scores(nbk, x);
-            uint64_t ks2[S::HALVES], vr2[S::HALVES];
-#pragma unroll
-            for (int g = 0; g < S::HALVES; ++g) {
-              const float vr = pick(vs, g) * __uint_as_float(static_cast<uint32_t>(127 - rv) << 23) *
-                               (S::PP == 3 ? kCut : 1.f);
-              vr2[g] = pair(vr, vr), ks2[g] = pair(pick(ks, g), pick(ks, g));
-            }
-            const uint32_t p_row = s_p + pb * S::HALVES * a.p_bytes + gt * 16u;
             uint32_t hot = 0;
+#pragma unroll 1
+            for (int g = 0; g < S::HALVES; ++g) {
+              const int half = S::SPLIT ? unit : g;
+              float x[NBK][8];
+              uint32_t from[NBK];
 #pragma unroll
-            for (int b = 0; b < NBK; ++b) {
-              const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[8 * b]);
-              const ulonglong2* nr4 = reinterpret_cast<const ulonglong2*>(&nref[8 * b]);
-              const ulonglong2 f0 = cq4[0], f1 = cq4[1], m0 = nr4[0], m1 = nr4[1];
-              const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y}, m[4] = {m0.x, m0.y, m1.x, m1.y};
-              const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
+              for (int b = 0; b < NBK; ++b) from[b] = s_addr + g * S::NB + 8 * b;
+              tmem_read<NBK>(from, x);
+              const float ksh = half ? ks[1] : ks[0];
+              const float vr = (half ? vs[1] : vs[0]) * __uint_as_float(static_cast<uint32_t>(127 - rv) << 23) *
+                               (S::PP == 3 ? kCut : 1.f);
+              const uint64_t vr2 = pair(vr, vr), ks2 = pair(ksh, ksh);
+              const uint32_t p_row = s_p + (pb * S::HALVES + g) * a.p_bytes + gt * 16u;
 #pragma unroll
-              for (int g = 0; g < S::HALVES; ++g) {
-                float* const z = x[b * S::HALVES + g];
+              for (int b = 0; b < NBK; ++b) {
+                const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[8 * b]);
+                const ulonglong2* nr4 = reinterpret_cast<const ulonglong2*>(&nref[8 * b]);
+                const ulonglong2 f0 = cq4[0], f1 = cq4[1], m0 = nr4[0], m1 = nr4[1];
+                const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y}, m[4] = {m0.x, m0.y, m1.x, m1.y};
+                const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
                 float y[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)  // t - m, t = s cq ks
-                  unpair(fma2(mul2(pair(z[2 * k], z[2 * k + 1]), f[k]), ks2[g], m[k]), y[2 * k],
+                  unpair(fma2(mul2(pair(x[b][2 * k], x[b][2 * k + 1]), f[k]), ks2, m[k]), y[2 * k],
                          y[2 * k + 1]);
                 if (!all_whole) hide(b, g, y);
                 // The weights enter the second product cut to their parts' bits (no more
@@ -1045,13 +1022,13 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const uint64_t e = pair(ex2_approx(y[2 * k]), ex2_approx(y[2 * k + 1]));
-                  sum[4 * b + k] = g == 0 ? e : add2(sum[4 * b + k], e);
+                  sum[4 * b + k] = add2(sum[4 * b + k], e);
                   float p0, p1;
-                  unpair(mul2(e, vr2[g]), p0, p1);
+                  unpair(mul2(e, vr2), p0, p1);
                   w[k] = pack2<true>(p0, p1);
                 }
                 hot = max_f16x2(max_f16x2(hot, w[0]), max_f16x2(max_f16x2(w[1], w[2]), w[3]));
-                const uint32_t to = p_row + g * a.p_bytes + (chunk >> 1) * 2048u + (chunk & 1u) * 8u;
+                const uint32_t to = p_row + (chunk >> 1) * 2048u + (chunk & 1u) * 8u;
 #pragma unroll
                 for (int p = 0; p < S::PP; ++p) {
                   if (p > 0) {
@@ -1072,14 +1049,12 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 #pragma unroll
           for (int g = 0; g < S::HALVES; ++g) any_live = any_live || pick(live, g);
           const int nbl = any_live ? nb : 0;  // blocks at work
-#pragma unroll
-          for (int j = 0; j < S::NC / 2; ++j) sum[j] = 0;
           // The check that the weights stay in range comes after them: a unit whose weights
           // leave it raises the references and makes them again.
           bool raise = begins;  // the first unit's maxima
           for (;;) {
             if (raise) {
-              by_blocks<kBlocks>(nbl, raise_refs);
+              raise_refs(nbl);
               int vexp = -126;  // vs < 2^vexp
 #pragma unroll
               for (int g = 0; g < S::HALVES; ++g)
@@ -1111,15 +1086,17 @@ __global__ void __launch_bounds__(S::THREADS, 1)
               bar_sync(bar, 128);
               if (!begins) {
                 const uint32_t before = units - 1u;
-                failed |= !mbar_wait(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
+                failed |= !wait_on<S::SPLIT>(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
                 tc_fence_after();
                 const float down_v = exp2f(static_cast<float>(old_rv - rv));
-                by_blocks<kBlocks>(nbl, [&](auto nbk) { rescale(nbk, down_v); });
+                rescale(nbl, down_v);
               }
             }
             // this buffer of weights is free once its last unit has been multiplied
-            if (use >= 1 && !(raise && !begins)) failed |= !mbar_wait(&ctl.pv_done[pb], (use - 1u) & 1u);
+            if (use >= 1 && !(raise && !begins)) failed |= !wait_on<S::SPLIT>(&ctl.pv_done[pb], (use - 1u) & 1u);
             uint32_t hot = 0;
+#pragma unroll
+            for (int j = 0; j < S::NC / 2; ++j) sum[j] = 0;
             by_blocks<kBlocks>(nbl, [&](auto nbk) { hot = weights(nbk); });
             if (raise) break;
             // infinite: past the range of half precision
@@ -1134,21 +1111,21 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             // Zero weights do not silence values that are not finite, and a tile's rest may
             // hold anything: what no row sees is zeroed, and of what only some rows see the
             // non-finite values are taken out here and added to those rows at the end.
-#pragma unroll
+#pragma unroll 1
             for (int g = 0; g < S::HALVES; ++g) {
-              if (pick(whole, g) || !pick(live, g)) continue;
+              if (S::SPLIT || g == 0 ? pick(whole, 0) || !pick(live, 0) : whole[1] || !live[1]) continue;
               const int half = S::SPLIT ? unit : g, tok = tok0 + half * kTileTok + gt;
               const uint32_t my_v = row_v + half * (kTileTok * S::D);
               const bool all = tok < lim0 && tok >= lo_last;
               // in a step of 32 tokens that is multiplied at all
               const bool used = (tok | 31) >= begin && (tok & ~31) < end;
               if (!used) {
-              } else if (!pick(some, g)) {
-#pragma unroll
+              } else if (!(half ? some[1] : some[0])) {
+#pragma unroll 1
                 for (int k = 0; k < S::D / 16; ++k) sts_u4(my_v + k * 16, 0, 0, 0, 0);
               } else if (!all) {
                 bool odd = false;
-#pragma unroll 4
+#pragma unroll 1
                 for (int k = 0; k < S::D / 16; ++k) {
                   const uint4 v = lds_u4(my_v + k * 16);
                   uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -1214,8 +1191,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       }
       if (tiles > 0) {
         const uint32_t last = units - 1u;
-        failed |= !mbar_wait(&ctl.odd_full, lists & 1u);
-        failed |= !mbar_wait(&ctl.pv_done[last % S::PBUFS], (last / S::PBUFS) & 1u);
+        failed |= !wait_on<S::SPLIT>(&ctl.odd_full, lists & 1u);
+        failed |= !wait_on<S::SPLIT>(&ctl.pv_done[last % S::PBUFS], (last / S::PBUFS) & 1u);
         tc_fence_after();
         ++lists;
       }
@@ -1227,62 +1204,59 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           static_cast<uint16_t*>(a.out) + (it.row0 * a.Hq + it.head0) * S::D + d;
       const float back = __uint_as_float(static_cast<uint32_t>(rv + 127) << 23);
       float* const part = a.part_o + part_row * S::D + d;
-      by_blocks<kBlocks>(nb, [&](auto nbk) {
-        constexpr int NBK = decltype(nbk)::value;
-        float acc[NBK * S::ACCS][8];
+      uint32_t nan_columns = 0;  // that see a value of row d that is NaN
+#pragma unroll 1
+      for (int q = 0; q < odd_n; ++q) {
+        const int u = ctl.odd[list][q];
+        const int32_t page = a.table[it.r * a.stride + (u >> a.shift)];
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages) || !writer) continue;
+        const uint32_t code = static_cast<const uint8_t*>(a.v_cache)[
+            page * a.page_stride + (u & ((1 << a.shift) - 1)) * a.token_stride +
+            it.kv_head * a.head_stride + d];
+        if ((code & 0x7Fu) != 0x7Fu) continue;
+#pragma unroll 1
+        for (int k = 0; k < my_rows; ++k)
+          if (static_cast<uint32_t>(lims[k] - 1 - u) < window) nan_columns |= 1u << k;
+      }
+#pragma unroll 1
+      for (int b = 0; b < nb; ++b) {
+        float acc[S::ACCS][8], o[8];
         if (tiles > 0) {
-          uint32_t from[NBK * S::ACCS];
+          uint32_t from[S::ACCS];
 #pragma unroll
-          for (int q = 0; q < NBK * S::ACCS; ++q)
-            from[q] = tmem + lanes + S::kColO + (q % S::ACCS) * a.n_cols + c0 + 8 * (q / S::ACCS);
-          tmem_read<NBK * S::ACCS>(from, acc);
+          for (int p = 0; p < S::ACCS; ++p) from[p] = tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b;
+          tmem_read<S::ACCS>(from, acc);
         } else {
 #pragma unroll
-          for (int q = 0; q < NBK * S::ACCS; ++q)
+          for (int p = 0; p < S::ACCS; ++p)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[q][k] = 0.f;
+            for (int k = 0; k < 8; ++k) acc[p][k] = 0.f;
         }
         constexpr float kLast = 1.f / (1 << S::LAST);
+        const int4* at4 = reinterpret_cast<const int4*>(&ctl.at[c0 + 8 * b]);
+        const int4 a0 = at4[0], a1 = at4[1];
+        const int to[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+        const int mine = writer ? my_rows - 8 * b : 0;  // columns of the block to write
 #pragma unroll
-        for (int b = 0; b < NBK; ++b) {
-          float o[8];
+        for (int k = 0; k < 8; ++k) {
+          o[k] = acc[S::ACCS - 1][k] * kLast;
+#pragma unroll
+          for (int p = S::ACCS - 2; p >= 0; --p) o[k] += acc[p][k];
+          o[k] *= back;
+          if ((nan_columns >> (8 * b + k)) & 1u) o[k] = NAN;
+        }
+        if (alone) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            o[k] = acc[b * S::ACCS + S::ACCS - 1][k] * kLast;
-#pragma unroll
-            for (int p = S::ACCS - 2; p >= 0; --p) o[k] += acc[b * S::ACCS + p][k];
-            o[k] *= back;
+            const float f = __shfl_sync(0xFFFFFFFFu, inv, 8 * b + k);
+            if (k < mine) out[to[k]] = static_cast<uint16_t>(pack2<S::F16>(o[k] * f, 0.f));
           }
-          for (int q = 0; q < odd_n; ++q) {
-            const int u = ctl.odd[list][q];
-            const int32_t page = a.table[it.r * a.stride + (u >> a.shift)];
-            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages) || !writer) continue;
-            const uint32_t code = static_cast<const uint8_t*>(a.v_cache)[
-                page * a.page_stride + (u & ((1 << a.shift) - 1)) * a.token_stride +
-                it.kv_head * a.head_stride + d];
-            if ((code & 0x7Fu) != 0x7Fu) continue;
+        } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (static_cast<uint32_t>(lims[8 * b + k] - 1 - u) < window) o[k] = NAN;
-          }
-          const int4* at4 = reinterpret_cast<const int4*>(&ctl.at[c0 + 8 * b]);
-          const int4 a0 = at4[0], a1 = at4[1];
-          const int to[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-          float f[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = __shfl_sync(0xFFFFFFFFu, inv, 8 * b + k);
-          const int mine = writer ? my_rows - 8 * b : 0;  // columns of the block to write
-          if (alone) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k < mine) out[to[k]] = static_cast<uint16_t>(pack2<S::F16>(o[k] * f[k], 0.f));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k < mine) part[(8 * b + k) * S::D] = o[k];
-          }
+          for (int k = 0; k < 8; ++k)
+            if (k < mine) part[(8 * b + k) * S::D] = o[k];
         }
-      });
+      }
       if (it.ends && !it.starts) {
         recorded = true;
         if (tid == 128) {
