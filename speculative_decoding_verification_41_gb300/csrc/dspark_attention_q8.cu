@@ -55,7 +55,7 @@ int q8_launch(LaunchQ8& c, int sms) {
   auto ring_stages = [&](int q_bufs) {
     a.q_bufs = q_bufs;
     a.p_off = kQ8CtlBytes<S> + q_bufs * q_bytes;
-    a.scale_off = a.p_off + S::PBUFS * S::HALVES * a.p_bytes;
+    a.scale_off = a.p_off + S::PBUFS * 2 * a.p_bytes;
     auto ring_at = [&](int v_stages) {
       return (a.scale_off + v_stages * 8u * a.n_scales + 1023u) & ~1023u;
     };
@@ -68,7 +68,7 @@ int q8_launch(LaunchQ8& c, int sms) {
   // are bound by the arithmetic, and an item's queries take as long as a tile or two.
   int stages = ring_stages(2);
   const int most = ring_stages(1);
-  if (stages == most || stages >= (S::SPLIT ? 3 : most))
+  if (stages == most || stages >= (S::PASSES ? 3 : most))
     stages = ring_stages(2);
   else
     stages = most;
@@ -102,7 +102,7 @@ int q8_shape(LaunchQ8& c, int sms) {
   if (c.a.n_cols <= 16) return q8_launch<AttnQ8Shape<D, F16, 16, 1, false, 2>>(c, sms);
   if (c.a.n_cols <= 32) return q8_launch<AttnQ8Shape<D, F16, 32, 2, false, 2>>(c, sms);
   if (c.a.n_cols <= 48) return q8_launch<AttnQ8Shape<D, F16, 48, 3, false, F16 ? 1 : 2>>(c, sms);
-  return q8_launch<AttnQ8Shape<D, F16, 80, 3, true, 2>>(c, sms);
+  return q8_launch<AttnQ8Shape<D, F16, 80, 3, true, 1>>(c, sms);
 }
 
 }  // namespace

@@ -218,19 +218,18 @@ constexpr int kScaleRoom = 1;
 // power of two, like a row's largest one can be, free of rounding.
 constexpr float kCut = 1.f + 0.7213f / 512.f;
 
-// SPLIT: a tile's weights are made and multiplied in two units, one per 128 tokens, and the
-// parts of P but the last add up in one accumulator: for the rows whose weights and outputs
-// would not fit otherwise. PBUFS: buffers of a unit's weights. There are two of a tile's scores.
-template <int D_, bool F16_, int NB_, int GROUPS_, bool SPLIT_, int PBUFS_>
+// PASSES: the parts of P one after another, all but the last into one accumulator, for the
+// rows whose outputs would not fit otherwise; else side by side. PBUFS: buffers of a tile's
+// weights. There are two of a tile's scores.
+template <int D_, bool F16_, int NB_, int GROUPS_, bool PASSES_, int PBUFS_>
 struct AttnQ8Shape {
   static constexpr int D = D_, NB = NB_, GROUPS = GROUPS_, PBUFS = PBUFS_;
-  static constexpr bool F16 = F16_, SPLIT = SPLIT_;
-  static constexpr int UNITS = SPLIT ? 2 : 1, HALVES = 2 / UNITS;  // of a tile; 128s of a unit
-  static constexpr int QP = F16 ? 3 : 2, PP = F16 ? 4 : 3;         // parts of Q and of P
-  static constexpr int LAST = F16 ? 6 : 4;                         // scale (log2) of P's last part
-  static constexpr int ACCS = SPLIT ? 2 : PP;                      // accumulators of the outputs
+  static constexpr bool F16 = F16_, PASSES = PASSES_;
+  static constexpr int QP = F16 ? 3 : 2, PP = F16 ? 4 : 3;  // parts of Q and of P
+  static constexpr int LAST = F16 ? 6 : 4;                  // scale (log2) of P's last part
+  static constexpr int ACCS = PASSES ? 2 : PP;              // accumulators of the outputs
   static constexpr int THREADS = 128 + 128 * GROUPS;
-  static constexpr int NC = SPLIT ? 24 : 16;                       // columns of a softmax group
+  static constexpr int NC = PASSES ? 24 : 16;               // columns of a softmax group
   static constexpr int WIDTH = NB;  // of the control block's arrays; rows are at most NC * GROUPS
   static constexpr uint32_t kStage = kQ8Tile * D;
   static constexpr int kCols = (4 + ACCS) * NB;
@@ -245,7 +244,7 @@ struct AttnQ8Shape {
 template <class S>
 struct AttnQ8Ctl {
   uint64_t full[kQ8MaxStages], empty[kQ8MaxStages];  // of key tiles, then of value tiles
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2][2];  // pv_done: of each 128 tokens
   uint64_t item_full[kItems], item_empty[kItems], factors[kItems];
   uint64_t odd_full, drained;
   uint32_t tmem;
@@ -293,7 +292,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       mbar_init(&ctl.q_empty[i], 1);
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_full[i], 4 * S::GROUPS);
-      mbar_init(&ctl.pv_done[i], 1);
+      mbar_init(&ctl.pv_done[i][0], 1);
+      mbar_init(&ctl.pv_done[i][1], 1);
     }
     for (uint32_t i = 0; i < kItems; ++i) {
       mbar_init(&ctl.item_full[i], 1);
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       bool ok = true;
       for (;;) {
         const uint32_t slot = items % kItems;
-        ok = warp_wait_on<S::SPLIT>(&ctl.item_full[slot], (items / kItems) & 1u);
+        ok = warp_wait_on<S::PASSES>(&ctl.item_full[slot], (items / kItems) & 1u);
         if (!ok) break;
         const AttnItem& it = ctl.item[slot];
         const int tiles = it.tiles, h = it.kv_head, begin = it.begin, end = it.end;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * box_bytes;
           }
           if (wraps > 0 && !warp_test(&ctl.empty[s], (wraps - 1u) & 1u)) {
-            ok = warp_wait_on<S::SPLIT>(&ctl.empty[s], (wraps - 1u) & 1u);
+            ok = warp_wait_on<S::PASSES>(&ctl.empty[s], (wraps - 1u) & 1u);
             if (!ok) break;
           }
           if (lane == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       }
       // leave no copy in flight into this CTA's shared memory
       for (uint32_t i = first_stage; i < end_stage; ++i)
-        if (i < s || wraps > 0) wait_on<S::SPLIT>(&ctl.full[i], (i < s ? wraps : wraps - 1u) & 1u);
+        if (i < s || wraps > 0) wait_on<S::PASSES>(&ctl.full[i], (i < s ? wraps : wraps - 1u) & 1u);
     }
   } else if (warp == 2) {
     // =====================================================================
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       const uint32_t n = static_cast<uint32_t>(a.n_cols);
       const uint32_t idesc_s = attn_idesc_f8(0, kTileTok, n, false, false);
       // the parts of P side by side or, split, one after another
-      const uint32_t idesc_o = attn_idesc_f8(1, S::D, S::SPLIT ? n : S::PP * n, true, true);
+      const uint32_t idesc_o = attn_idesc_f8(1, S::D, S::PASSES ? n : S::PP * n, true, true);
       // K and Q: rows of D bytes, 8-row groups together
       const uint64_t desc_kq = attn_desc(16, 8 * S::D, S::kSwizzle);
       // V: a token's D bytes together, 8-token groups after one another
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
       int s_tiles = 0;                        // tiles of the item to come
       int s_tok = 0, s_begin = 0, s_stop = 0; // the next tile's first token, those that are seen
       bool s_end = false, s_queries = false;  // no more items; the item's queries are there
-      uint32_t o_items = 0, o_done = 0, o_units = 0, o_sub = 0;  // outputs: tiles, units done
+      uint32_t o_items = 0, o_done = 0;       // outputs
       int o_tiles = 0, tok0 = 0, begin = 0, end = 0;
       bool first = true, ok = true;
       WaitClock clock;
@@ -574,56 +574,47 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             done = true;
           }
         } else if (o_done < s_done) {
-          const uint32_t buf = o_units % S::PBUFS;
-          if (warp_test(&ctl.p_full[buf], (o_units / S::PBUFS) & 1u)) {
-            const bool last = o_sub + 1u == S::UNITS;  // unit of the tile
+          const uint32_t buf = o_done % S::PBUFS;
+          if (warp_test(&ctl.p_full[buf], (o_done / S::PBUFS) & 1u)) {
             // the groups' lists of the item are written
-            if (leader && last && o_tiles == 1) mbar_arrive(&ctl.odd_full);
-            ok = warp_wait_on<S::SPLIT>(&ctl.full[rv.s], rv.phase);
+            if (leader && o_tiles == 1) mbar_arrive(&ctl.odd_full);
+            ok = warp_wait_on<S::PASSES>(&ctl.full[rv.s], rv.phase);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (uint32_t g = 0; g < S::HALVES; ++g) {
-              const uint32_t h = S::SPLIT ? o_sub : g;
-              const int tok = tok0 + static_cast<int>(h) * kTileTok;
-              // the steps of 32 tokens that some row sees
-              const int k0 = max(begin - tok, 0) >> 5, k1 = (min(end - tok, kTileTok) + 31) >> 5;
-              if (k0 >= k1) continue;
-              if (leader) {
-                const uint64_t v0 = at(desc_v, s_ring + rv.s * S::kStage + h * (kTileTok * S::D));
-                const uint64_t p0 = at(desc_p, s_p + (buf * S::HALVES + g) * a.p_bytes);
-                constexpr uint32_t kStep = 32 * S::D >> 4;  // of V
-                // split: the parts one after another, the last into columns of its own
-                constexpr uint32_t kPasses = S::SPLIT ? S::PP : 1;
-#pragma unroll 1
-                for (uint32_t p = 0; p < kPasses; ++p) {
-                  const bool apart = S::SPLIT && p + 1 == kPasses;
-                  const uint32_t col = tmem + S::kColO + (apart ? n : 0u);
-                  const uint64_t pp = p0 + p * (a.part_bytes >> 4);
-                  uint32_t more = !first || (p > 0 && !apart);
-#pragma unroll 2
-                  for (int k = k0; k < k1; ++k) {
-                    tc_mma_f8(col, v0 + static_cast<uint32_t>(k) * kStep,
-                              pp + static_cast<uint32_t>(k) * 32u, idesc_o, more);
-                    more = 1;
-                  }
-                }
-              }
-              first = false;
-            }
             if (leader) {
-              if (last) tc_commit(&ctl.empty[rv.s]);
-              tc_commit(&ctl.pv_done[buf]);
+#pragma unroll 1
+              for (uint32_t h = 0; h < 2u; ++h) {
+                const int tok = tok0 + static_cast<int>(h) * kTileTok;
+                // the steps of 32 tokens that some row sees
+                const int k0 = max(begin - tok, 0) >> 5, k1 = (min(end - tok, kTileTok) + 31) >> 5;
+                if (k0 < k1) {
+                  const uint64_t v0 = at(desc_v, s_ring + rv.s * S::kStage + h * (kTileTok * S::D));
+                  const uint64_t p0 = at(desc_p, s_p + (buf * 2u + h) * a.p_bytes);
+                  constexpr uint32_t kStep = 32 * S::D >> 4;  // of V
+                  constexpr uint32_t kPasses = S::PASSES ? S::PP : 1;
+#pragma unroll 1
+                  for (uint32_t p = 0; p < kPasses; ++p) {
+                    const bool apart = S::PASSES && p + 1 == kPasses;  // in columns of its own
+                    const uint32_t col = tmem + S::kColO + (apart ? n : 0u);
+                    const uint64_t pp = p0 + p * (a.part_bytes >> 4);
+                    uint32_t more = !first || (p > 0 && !apart);
+#pragma unroll 2
+                    for (int k = k0; k < k1; ++k) {
+                      tc_mma_f8(col, v0 + static_cast<uint32_t>(k) * kStep,
+                                pp + static_cast<uint32_t>(k) * 32u, idesc_o, more);
+                      more = 1;
+                    }
+                  }
+                  first = false;
+                }
+                tc_commit(&ctl.pv_done[buf][h]);
+              }
+              tc_commit(&ctl.empty[rv.s]);
             }
-            ++o_units;
-            ++o_sub;
-            if (last) {
-              rv.on();
-              o_sub = 0;
-              ++o_done;
-              --o_tiles;
-              tok0 += kQ8Tile;
-            }
+            rv.on();
+            ++o_done;
+            --o_tiles;
+            tok0 += kQ8Tile;
             done = true;
           }
         }
@@ -638,7 +629,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         set_status(&ctl.status, DSPARK_ERR_TIMEOUT);
         *reinterpret_cast<volatile int32_t*>(&ctl.abort) = 1;
         if (leader) tc_commit(&ctl.drained);  // no product may outlive the CTA
-        warp_wait_on<S::SPLIT>(&ctl.drained, 0);
+        warp_wait_on<S::PASSES>(&ctl.drained, 0);
       }
     }
     __syncwarp();
@@ -652,7 +643,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     // two elements an instruction.
     // =====================================================================
     if (u_begin < u_end) {
-      constexpr int LPR = S::D / 8, kRows = 32 / LPR, kDeep = 1, kBatch = kRows * kDeep;
+      constexpr int LPR = S::D / 8, kRows = 32 / LPR, kDeep = 2, kBatch = kRows * kDeep;
       const int sub = lane / LPR, l = lane % LPR;
       const uint32_t gs_inv = (65536u + a.Gs - 1u) / a.Gs;  // j / Gs = j * gs_inv >> 16 for j < 160
       for (uint32_t i = lane * 16u; i < a.q_bufs * S::QP * q_part; i += 512u) sts_u4(s_q + i, 0, 0, 0, 0);
@@ -702,7 +693,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           }  // else nothing but the item's lead: the next CTA begins it
         }
         const uint32_t slot = items % kItems, use = items / kItems;
-        if (use >= 1) ok = warp_wait_on<S::SPLIT>(&ctl.item_empty[slot], (use - 1u) & 1u);
+        if (use >= 1) ok = warp_wait_on<S::PASSES>(&ctl.item_empty[slot], (use - 1u) & 1u);
         if (!ok) break;
         const int in_head = max(lead_in - a.lead, 0);
         const int head0 = h * a.G + part * a.Gs;
@@ -743,7 +734,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           uint4 next[4][kDeep];
 #pragma unroll
           for (int k = 0; k < 4; ++k) load(k * kBatch, next[k]);
-          if (wraps >= 1) ok = warp_wait_on<S::SPLIT>(&ctl.q_empty[b], (wraps - 1u) & 1u);
+          if (wraps >= 1) ok = warp_wait_on<S::PASSES>(&ctl.q_empty[b], (wraps - 1u) & 1u);
           if (!ok) break;
           const uint32_t to = s_q + b * S::QP * q_part;
 #pragma unroll 1
@@ -828,7 +819,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;  // (32 * quarter) << 16
     const uint32_t window = static_cast<uint32_t>(a.window);
     volatile int32_t* abort_flag = &ctl.abort;
-    uint32_t done = 0, units = 0, items = 0, lists = 0;  // tiles, units
+    uint32_t done = 0, items = 0, lists = 0;  // tiles
     const uint32_t v_end = a.k_stages + a.v_stages;
     uint32_t v_s = a.k_stages, v_phase = 0;  // ring position of the next tile of values
     int rv = 0;                              // weights stand for 2^-rv of their values
@@ -843,7 +834,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     bar_sync(1 + S::GROUPS, 128 * S::GROUPS);
     for (;;) {
       const uint32_t slot = items % kItems, list = lists & 1u;
-      bool failed = !wait_on<S::SPLIT>(&ctl.item_full[slot], (items / kItems) & 1u);
+      bool failed = !wait_on<S::PASSES>(&ctl.item_full[slot], (items / kItems) & 1u);
       const AttnItem& it = ctl.item[slot];
       // (the item that ends the line has nothing but its mark)
       const int rows = failed || it.tiles < 0 ? 0 : it.t_rows * a.Gs;
@@ -861,7 +852,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         lims[gt] = gt < my_rows ? it.lim0 + ctl.new_tok[c0 + gt] : INT_MIN / 2;
       }
       if (group == 0 && gt == 0) ctl.odd_n[list] = 0;
-      if (!failed && it.tiles > 0) failed = !wait_on<S::SPLIT>(&ctl.factors[slot], (items / kItems) & 1u);
+      if (!failed && it.tiles > 0) failed = !wait_on<S::PASSES>(&ctl.factors[slot], (items / kItems) & 1u);
       if (bar_any(bar, 128, failed || *abort_flag != 0)) {
         *abort_flag = 1;
         break;
@@ -883,7 +874,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         // this thread's token, its scales (what no row sees has none)
         bool whole[2], live[2], some[2];
         float ks[2], vs[2];
-        failed |= !wait_on<S::SPLIT>(&ctl.full[v_s], v_phase);
+        failed |= !wait_on<S::PASSES>(&ctl.full[v_s], v_phase);
         const uint32_t row_v = s_ring + v_s * S::kStage + gt * S::D;
         {
           const uint32_t at_s = s_scale + (v_s - a.k_stages) * (8u * a.n_scales);
@@ -907,249 +898,237 @@ __global__ void __launch_bounds__(S::THREADS, 1)
           }
         }
         if (++v_s == v_end) v_s = a.k_stages, v_phase ^= 1u;
-        failed |= !wait_on<S::SPLIT>(&ctl.s_full[sbuf], (done >> 1) & 1u);
+        failed |= !wait_on<S::PASSES>(&ctl.s_full[sbuf], (done >> 1) & 1u);
         tc_fence_after();
         const uint32_t s_tile = tmem + lanes + S::kColS + sbuf * (2 * S::NB) + c0;
+        const uint32_t pb = done % S::PBUFS, use = done / S::PBUFS;
+        const bool all_whole = whole[0] && whole[1];
+        // (a tile's second half may hold no token that is seen, or its first)
+        const int g0 = live[0] ? 0 : 1, g1 = live[1] ? 2 : 1;
+        // -inf where the row does not see the token
+        auto hide = [&](int b, int g, float* y) {
+          const int4* lim4 = reinterpret_cast<const int4*>(&lims[8 * b]);
+          const int tok = tok0 + g * kTileTok + gt;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int4 m = lim4[k];
+            if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[4 * k] = -INFINITY;
+            if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[4 * k + 1] = -INFINITY;
+            if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[4 * k + 2] = -INFINITY;
+            if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[4 * k + 3] = -INFINITY;
+          }
+        };
+        // The columns' largest scores, and the largest exponent of a value's scale; then the
+        // references and what is made with them so far.
+        auto raise_refs = [&](int n) {
 #pragma unroll 1
-        for (int unit = 0; unit < S::UNITS; ++unit, ++units) {
-          const uint32_t pb = units % S::PBUFS, use = units / S::PBUFS;
-          const bool begins = i == 0 && unit == 0;
-          const uint32_t s_addr = s_tile + unit * S::NB;  // (the unit's first 128)
-          // this unit's: of its g-th 128 tokens
-          auto pick = [&](auto& x, int g) { return S::SPLIT ? (unit ? x[1] : x[0]) : x[g]; };
-          bool all_whole = true;
+          for (int b = 0; b < n; ++b) {
+            const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[8 * b]);
+            const ulonglong2 f0 = cq4[0], f1 = cq4[1];
+            const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
+            float v[8];
 #pragma unroll
-          for (int g = 0; g < S::HALVES; ++g) all_whole = all_whole && pick(whole, g);
-          // -inf where the row does not see the token
-          auto hide = [&](int b, int g, float* y) {
-            const int4* lim4 = reinterpret_cast<const int4*>(&lims[8 * b]);
-            const int tok = tok0 + (S::SPLIT ? unit : g) * kTileTok + gt;
+            for (int k = 0; k < 8; ++k) v[k] = -INFINITY;
+#pragma unroll 1
+            for (int g = g0; g < g1; ++g) {
+              float x[1][8];
+              const uint32_t from[1] = {s_tile + g * S::NB + 8 * b};
+              tmem_read<1>(from, x);
+              const float ksg = g ? ks[1] : ks[0];
+              const uint64_t ks2 = pair(ksg, ksg);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int4 m = lim4[k];
-              if (static_cast<uint32_t>(m.x - 1 - tok) >= window) y[4 * k] = -INFINITY;
-              if (static_cast<uint32_t>(m.y - 1 - tok) >= window) y[4 * k + 1] = -INFINITY;
-              if (static_cast<uint32_t>(m.z - 1 - tok) >= window) y[4 * k + 2] = -INFINITY;
-              if (static_cast<uint32_t>(m.w - 1 - tok) >= window) y[4 * k + 3] = -INFINITY;
+              for (int k = 0; k < 4; ++k)
+                unpair(mul2(mul2(pair(x[0][2 * k], x[0][2 * k + 1]), f[k]), ks2), x[0][2 * k],
+                       x[0][2 * k + 1]);
+              if (!all_whole) hide(b, g, x[0]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = fmaxf(v[k], x[0][k]);  // NaN takes no part
             }
-          };
-          // The columns' largest scores, and the largest exponent of a value's scale; then the
-          // references and what is made with them so far.
-          auto raise_refs = [&](int n) {
+            const float m = over_four<true>(fold_columns<true>(v, lane));
+            if ((lane & 3) == 0) red[quarter][8 * b + (lane >> 2)] = m;
+          }
+        };
+        auto rescale = [&](int n, float down_v) {
 #pragma unroll 1
-            for (int b = 0; b < n; ++b) {
+          for (int b = 0; b < n; ++b) {
+            const float* f = &fac[8 * b];
+#pragma unroll 1
+            for (int p = 0; p < S::ACCS; ++p) {
+              float z[1][8];
+              const uint32_t from[1] = {tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b};
+              tmem_read<1>(from, z);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) z[0][k] *= f[k] * down_v;
+              tmem_st8(from[0], z[0]);
+            }
+          }
+          tmem_wait_st();
+#pragma unroll
+          for (int j = 0; j < S::NC / 2; ++j)
+            if (j / 4 < n) l[j] = mul2(l[j], pair(fac[2 * j], fac[2 * j + 1]));
+        };
+        // The weights with the references so far, and the largest of them.
+        uint64_t sum[S::NC / 2];  // of the tile's weights
+        auto weights = [&](auto nbk, bool wait) -> uint32_t {
+          // NBK blocks at once: their arithmetic, long chains each, runs side by side. (And
+          // no more than these: what the warps of a CTA run has to stay in the instruction
+          // cache. The two halves unrolled, or 4 rows of queries at once above, cost 10 to 20%.)
+          constexpr int NBK = decltype(nbk)::value;
+          uint32_t hot = 0;
+#pragma unroll 1
+          for (int g = g0; g < g1; ++g) {
+            float x[NBK][8];
+            uint32_t from[NBK];
+#pragma unroll
+            for (int b = 0; b < NBK; ++b) from[b] = s_tile + g * S::NB + 8 * b;
+            tmem_read<NBK>(from, x);
+            const float ksh = g ? ks[1] : ks[0];
+            const float vr = (g ? vs[1] : vs[0]) * __uint_as_float(static_cast<uint32_t>(127 - rv) << 23) *
+                             (S::PP == 3 ? kCut : 1.f);
+            const uint64_t vr2 = pair(vr, vr), ks2 = pair(ksh, ksh);
+            const uint32_t p_row = s_p + (pb * 2u + g) * a.p_bytes + gt * 16u;
+            // this half of the buffer is free once its last weights have been multiplied
+            if (wait) failed |= !wait_on<S::PASSES>(&ctl.pv_done[pb][g], (use - 1u) & 1u);
+#pragma unroll
+            for (int b = 0; b < NBK; ++b) {
               const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[8 * b]);
-              const ulonglong2 f0 = cq4[0], f1 = cq4[1];
-              const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y};
-              float x[S::HALVES][8], v[8];
-              uint32_t from[S::HALVES];
+              const ulonglong2* nr4 = reinterpret_cast<const ulonglong2*>(&nref[8 * b]);
+              const ulonglong2 f0 = cq4[0], f1 = cq4[1], m0 = nr4[0], m1 = nr4[1];
+              const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y}, m[4] = {m0.x, m0.y, m1.x, m1.y};
+              const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
+              float y[8];
 #pragma unroll
-              for (int g = 0; g < S::HALVES; ++g) from[g] = s_addr + g * S::NB + 8 * b;
-              tmem_read<S::HALVES>(from, x);
+              for (int k = 0; k < 4; ++k)  // t - m, t = s cq ks
+                unpair(fma2(mul2(pair(x[b][2 * k], x[b][2 * k + 1]), f[k]), ks2, m[k]), y[2 * k],
+                       y[2 * k + 1]);
+              if (!all_whole) hide(b, g, y);
+              // The weights enter the second product cut to their parts' bits (no more
+              // than the output's own rounding); their sum l is of the unrounded ones.
+              uint32_t w[4];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = -INFINITY;
-#pragma unroll
-              for (int g = 0; g < S::HALVES; ++g) {
-                const uint64_t ks2 = pair(pick(ks, g), pick(ks, g));
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  unpair(mul2(mul2(pair(x[g][2 * k], x[g][2 * k + 1]), f[k]), ks2), x[g][2 * k],
-                         x[g][2 * k + 1]);
-                if (!all_whole) hide(b, g, x[g]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = fmaxf(v[k], x[g][k]);  // NaN takes no part
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t e = pair(ex2_approx(y[2 * k]), ex2_approx(y[2 * k + 1]));
+                sum[4 * b + k] = add2(sum[4 * b + k], e);
+                float p0, p1;
+                unpair(mul2(e, vr2), p0, p1);
+                w[k] = pack2<true>(p0, p1);
               }
-              const float m = over_four<true>(fold_columns<true>(v, lane));
-              if ((lane & 3) == 0) red[quarter][8 * b + (lane >> 2)] = m;
-            }
-          };
-          auto rescale = [&](int n, float down_v) {
-#pragma unroll 1
-            for (int b = 0; b < n; ++b) {
-              const float* f = &fac[8 * b];
-#pragma unroll 1
-              for (int p = 0; p < S::ACCS; ++p) {
-                float z[1][8];
-                const uint32_t from[1] = {tmem + lanes + S::kColO + p * a.n_cols + c0 + 8 * b};
-                tmem_read<1>(from, z);
+              hot = max_f16x2(max_f16x2(hot, w[0]), max_f16x2(max_f16x2(w[1], w[2]), w[3]));
+              const uint32_t to = p_row + (chunk >> 1) * 2048u + (chunk & 1u) * 8u;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) z[0][k] *= f[k] * down_v;
-                tmem_st8(from[0], z[0]);
-              }
-            }
-            tmem_wait_st();
+              for (int p = 0; p < S::PP; ++p) {
+                if (p > 0) {
 #pragma unroll
-            for (int j = 0; j < S::NC / 2; ++j)
-              if (j / 4 < n) l[j] = mul2(l[j], pair(fac[2 * j], fac[2 * j + 1]));
-          };
-          // The weights with the references so far, and the largest of them.
-          uint64_t sum[S::NC / 2];  // of the unit's weights
-          auto weights = [&](auto nbk) -> uint32_t {
-            // NBK blocks at once: their arithmetic, long chains each, runs side by side. (And
-            // no more than these: what the warps of a CTA run has to stay in the instruction
-            // cache. The two halves unrolled, or 4 rows of queries at once above, cost 10 to 20%.)
-            constexpr int NBK = decltype(nbk)::value;
-            uint32_t hot = 0;
-#pragma unroll 1
-            for (int g = 0; g < S::HALVES; ++g) {
-              const int half = S::SPLIT ? unit : g;
-              float x[NBK][8];
-              uint32_t from[NBK];
-#pragma unroll
-              for (int b = 0; b < NBK; ++b) from[b] = s_addr + g * S::NB + 8 * b;
-              tmem_read<NBK>(from, x);
-              const float ksh = half ? ks[1] : ks[0];
-              const float vr = (half ? vs[1] : vs[0]) * __uint_as_float(static_cast<uint32_t>(127 - rv) << 23) *
-                               (S::PP == 3 ? kCut : 1.f);
-              const uint64_t vr2 = pair(vr, vr), ks2 = pair(ksh, ksh);
-              const uint32_t p_row = s_p + (pb * S::HALVES + g) * a.p_bytes + gt * 16u;
-#pragma unroll
-              for (int b = 0; b < NBK; ++b) {
-                const ulonglong2* cq4 = reinterpret_cast<const ulonglong2*>(&cq[8 * b]);
-                const ulonglong2* nr4 = reinterpret_cast<const ulonglong2*>(&nref[8 * b]);
-                const ulonglong2 f0 = cq4[0], f1 = cq4[1], m0 = nr4[0], m1 = nr4[1];
-                const uint64_t f[4] = {f0.x, f0.y, f1.x, f1.y}, m[4] = {m0.x, m0.y, m1.x, m1.y};
-                const uint32_t chunk = static_cast<uint32_t>((c0 >> 3) + b);
-                float y[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)  // t - m, t = s cq ks
-                  unpair(fma2(mul2(pair(x[b][2 * k], x[b][2 * k + 1]), f[k]), ks2, m[k]), y[2 * k],
-                         y[2 * k + 1]);
-                if (!all_whole) hide(b, g, y);
-                // The weights enter the second product cut to their parts' bits (no more
-                // than the output's own rounding); their sum l is of the unrounded ones.
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint64_t e = pair(ex2_approx(y[2 * k]), ex2_approx(y[2 * k + 1]));
-                  sum[4 * b + k] = add2(sum[4 * b + k], e);
-                  float p0, p1;
-                  unpair(mul2(e, vr2), p0, p1);
-                  w[k] = pack2<true>(p0, p1);
-                }
-                hot = max_f16x2(max_f16x2(hot, w[0]), max_f16x2(max_f16x2(w[1], w[2]), w[3]));
-                const uint32_t to = p_row + (chunk >> 1) * 2048u + (chunk & 1u) * 8u;
-#pragma unroll
-                for (int p = 0; p < S::PP; ++p) {
-                  if (p > 0) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                      w[k] = without_upper(w[k]);
-                      if (p == S::PP - 1)
-                        w[k] = mul_f16x2(w[k], S::LAST == 4 ? 0x4C004C00u : 0x54005400u);
-                    }
+                  for (int k = 0; k < 4; ++k) {
+                    w[k] = without_upper(w[k]);
+                    if (p == S::PP - 1)
+                      w[k] = mul_f16x2(w[k], S::LAST == 4 ? 0x4C004C00u : 0x54005400u);
                   }
-                  sts_part(to + p * a.part_bytes, upper_bytes(w[0], w[1]), upper_bytes(w[2], w[3]));
                 }
-              }
-            }
-            return hot;
-          };
-          bool any_live = false;
-#pragma unroll
-          for (int g = 0; g < S::HALVES; ++g) any_live = any_live || pick(live, g);
-          const int nbl = any_live ? nb : 0;  // blocks at work
-          // The check that the weights stay in range comes after them: a unit whose weights
-          // leave it raises the references and makes them again.
-          bool raise = begins;  // the first unit's maxima
-          for (;;) {
-            if (raise) {
-              raise_refs(nbl);
-              int vexp = -126;  // vs < 2^vexp
-#pragma unroll
-              for (int g = 0; g < S::HALVES; ++g)
-                vexp = max(vexp, static_cast<int>(__float_as_uint(pick(vs, g)) >> 23) - 126);
-              vexp = __reduce_max_sync(0xFFFFFFFFu, vexp);
-              if (lane == 0) ctl.vexp[group][quarter] = vexp;
-              if (bar_any(bar, 128, failed || *abort_flag != 0)) {
-                leave = true;
-                break;
-              }
-              const int* const ve = ctl.vexp[group];
-              const int top_vexp = max(max(ve[0], ve[1]), max(ve[2], ve[3]));
-              const int old_rv = rv;
-              if (begins || top_vexp > rv) rv = min(max(top_vexp + kScaleRoom, -100), 120);
-              if (gt < my_rows && nbl > 0) {
-                float top = -INFINITY, low = INFINITY;  // of the quarters that hold a token
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  const float v = red[w][gt];
-                  top = fmaxf(top, v);
-                  if (v > -INFINITY) low = fminf(low, v);
-                }
-                // weights are half precision numbers, whatever the outputs' type
-                const float down = top - low > kPeak ? kPeakBase<true> : kBase<true>;
-                const float ref = fabsf(top) < kNoShift ? top - down : top, old = -nref[gt];
-                fac[gt] = ref > old ? ex2_approx(old - ref) : 1.f;
-                if (ref > old) nref[gt] = -ref;
-              }
-              bar_sync(bar, 128);
-              if (!begins) {
-                const uint32_t before = units - 1u;
-                failed |= !wait_on<S::SPLIT>(&ctl.pv_done[before % S::PBUFS], (before / S::PBUFS) & 1u);
-                tc_fence_after();
-                const float down_v = exp2f(static_cast<float>(old_rv - rv));
-                rescale(nbl, down_v);
-              }
-            }
-            // this buffer of weights is free once its last unit has been multiplied
-            if (use >= 1 && !(raise && !begins)) failed |= !wait_on<S::SPLIT>(&ctl.pv_done[pb], (use - 1u) & 1u);
-            uint32_t hot = 0;
-#pragma unroll
-            for (int j = 0; j < S::NC / 2; ++j) sum[j] = 0;
-            by_blocks<kBlocks>(nbl, [&](auto nbk) { hot = weights(nbk); });
-            if (raise) break;
-            // infinite: past the range of half precision
-            const bool high = (hot & 0x7C00u) == 0x7C00u || (hot & 0x7C000000u) == 0x7C000000u;
-            if (!bar_any(bar, 128, high || failed)) break;
-            raise = true;
-          }
-          if (leave) break;
-#pragma unroll
-          for (int j = 0; j < S::NC / 2; ++j) l[j] = add2(l[j], sum[j]);
-          if (!all_whole && group == 0) {
-            // Zero weights do not silence values that are not finite, and a tile's rest may
-            // hold anything: what no row sees is zeroed, and of what only some rows see the
-            // non-finite values are taken out here and added to those rows at the end.
-#pragma unroll 1
-            for (int g = 0; g < S::HALVES; ++g) {
-              if (S::SPLIT || g == 0 ? pick(whole, 0) || !pick(live, 0) : whole[1] || !live[1]) continue;
-              const int half = S::SPLIT ? unit : g, tok = tok0 + half * kTileTok + gt;
-              const uint32_t my_v = row_v + half * (kTileTok * S::D);
-              const bool all = tok < lim0 && tok >= lo_last;
-              // in a step of 32 tokens that is multiplied at all
-              const bool used = (tok | 31) >= begin && (tok & ~31) < end;
-              if (!used) {
-              } else if (!(half ? some[1] : some[0])) {
-#pragma unroll 1
-                for (int k = 0; k < S::D / 16; ++k) sts_u4(my_v + k * 16, 0, 0, 0, 0);
-              } else if (!all) {
-                bool odd = false;
-#pragma unroll 1
-                for (int k = 0; k < S::D / 16; ++k) {
-                  const uint4 v = lds_u4(my_v + k * 16);
-                  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                  bool hit = false;
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    // bit 7 of each byte that is NaN (lower seven bits all set)
-                    const uint32_t nan = ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                    w[q] &= ~(nan | (nan - (nan >> 7)));
-                    hit |= nan != 0;
-                  }
-                  if (hit) sts_u4(my_v + k * 16, w[0], w[1], w[2], w[3]);
-                  odd |= hit;
-                }
-                if (odd) ctl.odd[list][atomicAdd(&ctl.odd_n[list], 1)] = tok;
+                sts_part(to + p * a.part_bytes, upper_bytes(w[0], w[1]), upper_bytes(w[2], w[3]));
               }
             }
           }
-          fence_proxy_async();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.p_full[pb]);
+          return hot;
+        };
+        // The check that the weights stay in range comes after them: a tile whose weights
+        // leave it raises the references and makes them again.
+        bool raise = i == 0;  // the first tile's maxima
+        for (;;) {
+          if (raise) {
+            raise_refs(nb);
+            int vexp = max(static_cast<int>(__float_as_uint(vs[0]) >> 23),
+                           static_cast<int>(__float_as_uint(vs[1]) >> 23)) - 126;  // vs < 2^vexp
+            vexp = __reduce_max_sync(0xFFFFFFFFu, vexp);
+            if (lane == 0) ctl.vexp[group][quarter] = vexp;
+            if (bar_any(bar, 128, failed || *abort_flag != 0)) {
+              leave = true;
+              break;
+            }
+            const int* const ve = ctl.vexp[group];
+            const int top_vexp = max(max(ve[0], ve[1]), max(ve[2], ve[3]));
+            const int old_rv = rv;
+            if (i == 0 || top_vexp > rv) rv = min(max(top_vexp + kScaleRoom, -100), 120);
+            if (gt < my_rows) {
+              float top = -INFINITY, low = INFINITY;  // of the quarters that hold a token
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const float v = red[w][gt];
+                top = fmaxf(top, v);
+                if (v > -INFINITY) low = fminf(low, v);
+              }
+              // weights are half precision numbers, whatever the outputs' type
+              const float down = top - low > kPeak ? kPeakBase<true> : kBase<true>;
+              const float ref = fabsf(top) < kNoShift ? top - down : top, old = -nref[gt];
+              fac[gt] = ref > old ? ex2_approx(old - ref) : 1.f;
+              if (ref > old) nref[gt] = -ref;
+            }
+            bar_sync(bar, 128);
+            if (i > 0) {
+              const uint32_t before = done - 1u;
+              failed |= !wait_on<S::PASSES>(&ctl.pv_done[before % S::PBUFS][1], (before / S::PBUFS) & 1u);
+              tc_fence_after();
+              rescale(nb, exp2f(static_cast<float>(old_rv - rv)));
+            }
+          }
+          uint32_t hot = 0;
+#pragma unroll
+          for (int j = 0; j < S::NC / 2; ++j) sum[j] = 0;
+          // A group without rows waits too: no warp arrives for a buffer's next weights before all
+          // have for the last ones.
+          const bool wait = use >= 1 && (!raise || i == 0);
+          if (nb == 0 && wait) failed |= !wait_on<S::PASSES>(&ctl.pv_done[pb][1], (use - 1u) & 1u);
+          by_blocks<kBlocks>(nb, [&](auto nbk) { hot = weights(nbk, wait); });
+          if (raise) break;
+          // infinite: past the range of half precision
+          const bool high = (hot & 0x7C00u) == 0x7C00u || (hot & 0x7C000000u) == 0x7C000000u;
+          if (!bar_any(bar, 128, high || failed)) break;
+          raise = true;
         }
         if (leave) break;
+#pragma unroll
+        for (int j = 0; j < S::NC / 2; ++j) l[j] = add2(l[j], sum[j]);
+        if (!all_whole && group == 0) {
+          // Zero weights do not silence values that are not finite, and a tile's rest may
+          // hold anything: what no row sees is zeroed, and of what only some rows see the
+          // non-finite values are taken out here and added to those rows at the end.
+#pragma unroll 1
+          for (int g = g0; g < g1; ++g) {
+            if (g ? whole[1] : whole[0]) continue;
+            const int tok = tok0 + g * kTileTok + gt;
+            const uint32_t my_v = row_v + g * (kTileTok * S::D);
+            const bool all = tok < lim0 && tok >= lo_last;
+            // in a step of 32 tokens that is multiplied at all
+            const bool used = (tok | 31) >= begin && (tok & ~31) < end;
+            if (!used) {
+            } else if (!(g ? some[1] : some[0])) {
+#pragma unroll 1
+              for (int k = 0; k < S::D / 16; ++k) sts_u4(my_v + k * 16, 0, 0, 0, 0);
+            } else if (!all) {
+              bool odd = false;
+#pragma unroll 1
+              for (int k = 0; k < S::D / 16; ++k) {
+                const uint4 v = lds_u4(my_v + k * 16);
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                bool hit = false;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  // bit 7 of each byte that is NaN (lower seven bits all set)
+                  const uint32_t nan = ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                  w[q] &= ~(nan | (nan - (nan >> 7)));
+                  hit |= nan != 0;
+                }
+                if (hit) sts_u4(my_v + k * 16, w[0], w[1], w[2], w[3]);
+                odd |= hit;
+              }
+              if (odd) ctl.odd[list][atomicAdd(&ctl.odd_n[list], 1)] = tok;
+            }
+          }
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p_full[pb]);
       }
       if (leave) {
         *abort_flag = 1;
@@ -1190,9 +1169,9 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         }
       }
       if (tiles > 0) {
-        const uint32_t last = units - 1u;
-        failed |= !wait_on<S::SPLIT>(&ctl.odd_full, lists & 1u);
-        failed |= !wait_on<S::SPLIT>(&ctl.pv_done[last % S::PBUFS], (last / S::PBUFS) & 1u);
+        const uint32_t last = done - 1u;
+        failed |= !wait_on<S::PASSES>(&ctl.odd_full, lists & 1u);
+        failed |= !wait_on<S::PASSES>(&ctl.pv_done[last % S::PBUFS][1], (last / S::PBUFS) & 1u);
         tc_fence_after();
         ++lists;
       }
