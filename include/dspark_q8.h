@@ -91,8 +91,9 @@ int dspark_rotary(const void* x, int64_t row_stride, int64_t head_stride,
  * NaN become NaN and do not count in a.
  *
  * Rows of one block must be neighbours in slot_map (as dspark_pages_reserve gives
- * them), in any order; a block that is written by rows with others in between has
- * unspecified codes and scales. Slots that occur twice leave either row.
+ * them), in any order, skipped rows not counted; a block that is written by rows with
+ * other blocks' in between has unspecified codes and scales. Slots that occur twice leave
+ * either row.
  *
  * Arguments
  *   k, v          dtype (DSPARK_BF16, DSPARK_F16): head h of row i at element

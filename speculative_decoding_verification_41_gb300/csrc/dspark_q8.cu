@@ -4,13 +4,15 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <mutex>
+#include <type_traits>
 
 #include "dspark_q8.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kMaxPairs = 64;  // of a head
+constexpr int kQ8Threads = 256;
 
 struct Turns {
   const uint64_t* turns;
@@ -18,6 +20,15 @@ struct Turns {
   float gain;
   int32_t rot;    // elements of a head that turn
   bool inter;     // pairs are neighbours
+};
+
+// i / d for i < 2^16 and 8 <= d <= 2^12, by a multiplication
+struct Quotient {
+  uint32_t inv;
+  __device__ __forceinline__ explicit Quotient(int d) : inv(0xFFFFFFFFu / static_cast<uint32_t>(d) + 1u) {}
+  __device__ __forceinline__ int of(int i) const {
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(i), inv));
+  }
 };
 
 // Cosine and sine of pair j at a position, times the gain. The angle in turns is
@@ -29,109 +40,131 @@ __device__ __forceinline__ float2 turn_of(const Turns& t, int32_t position, int 
   sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 0x1p-31f, &s, &c);
   return make_float2(c * t.gain, s * t.gain);
 }
+// ... of all pairs of `rows` rows, by the whole CTA
+__device__ __forceinline__ void make_turns(const Turns& t, int row0, int rows, int sign, float* s_cos,
+                                           float* s_sin) {
+  const int pairs = t.rot / 2;
+  const Quotient by_pairs(pairs);
+  for (int i = threadIdx.x; i < rows * pairs; i += kQ8Threads) {
+    const int r = by_pairs.of(i);
+    const float2 cs = turn_of(t, t.positions[row0 + r], i - r * pairs);
+    s_cos[i] = cs.x;
+    s_sin[i] = sign * cs.y;
+  }
+}
+
+template <bool F16>
+__device__ __forceinline__ void piece_to_f32(const uint4& w, float (&y)[8]) {
+  const uint32_t own[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float2 p = word_to_f32<F16>(own[q]);
+    y[2 * q] = p.x, y[2 * q + 1] = p.y;
+  }
+}
+// The 8 elements of piece `lane` of a head that lies in shared memory at `head`, turned. c, s:
+// the row's cosines and sines. With halves a piece's partners are a piece as well (rot_dim is a
+// multiple of 16).
+template <bool F16>
+__device__ __forceinline__ void turned_piece(const Turns& t, const uint4* head, int lane, const float* c,
+                                             const float* s, float (&y)[8]) {
+  piece_to_f32<F16>(head[lane], y);
+  if (8 * lane >= t.rot) return;
+  if (t.inter) {
+    const float4 cc = *reinterpret_cast<const float4*>(c + 4 * lane);
+    const float4 ss = *reinterpret_cast<const float4*>(s + 4 * lane);
+    const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float p = y[2 * q], o = y[2 * q + 1];
+      y[2 * q] = fmaf(p, c4[q], -o * s4[q]);
+      y[2 * q + 1] = fmaf(o, c4[q], p * s4[q]);
+    }
+  } else {
+    const int half = t.rot >> 4;  // pieces of a half
+    const bool upper = lane >= half;
+    const int j = upper ? lane - half : lane;
+    const float sign = upper ? 1.f : -1.f;
+    float o[8];
+    piece_to_f32<F16>(head[upper ? lane - half : lane + half], o);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float4 cc = reinterpret_cast<const float4*>(c + 8 * j)[q];
+      const float4 ss = reinterpret_cast<const float4*>(s + 8 * j)[q];
+      const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[4 * q + e] = fmaf(y[4 * q + e], c4[e], sign * o[4 * q + e] * s4[e]);
+    }
+  }
+}
 
 // ---------------------------------------------------------------------------
 // dspark_rotary
 // ---------------------------------------------------------------------------
-// A thread turns `unit` u of a head: the 8 elements 8u .. 8u+7 and, with halves, their
-// 8 partners; units past the turned part are copied. Its unit is the same for all the
-// heads and rows it takes, so cosines and sines, made once per row and pair, are read
-// from shared memory.
-constexpr int kRotThreads = 256;
-constexpr int kRotRows = 16;  // rows of a CTA, at most
-constexpr int kRotDeep = 2;   // units in flight per thread
+// A CTA copies some rows' heads to shared memory (asynchronously: what is in flight
+// needs no registers), makes the rows' cosines and sines meanwhile, once for all heads,
+// and turns and stores 16-byte pieces. The loops are rolled: a small call runs them once,
+// and most of its time is the first fetch of each instruction.
+constexpr int kRotPieces = 2048;  // of a CTA, at most (32 KB), but a row at least
 
 struct RotaryArgs {
   const uint16_t* x;
   uint16_t* out;
   int64_t row, head, orow, ohead;
   Turns t;
-  int32_t n, heads, units, pair_units, rows, sign;
+  int32_t n, heads, slice, d_shift, rows, sign;  // heads and rows of a CTA
 };
 
 template <bool F16>
-__global__ void __launch_bounds__(kRotThreads) k_rotary(const RotaryArgs a) {
-  __shared__ float s_cos[kRotRows * kMaxPairs], s_sin[kRotRows * kMaxPairs];
-  __shared__ int32_t s_pos[kRotRows];
+__global__ void __launch_bounds__(kQ8Threads) k_rotary(const RotaryArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, pairs = a.t.rot / 2;
   const int r0 = blockIdx.x * a.rows, rows = min(a.rows, a.n - r0);
-  const int u = tid % a.units, lane = tid / a.units, lanes = kRotThreads / a.units;
-  const bool turns = u < a.pair_units, halves = !a.t.inter;
-  const int d0 = halves && !turns ? a.t.rot + 8 * (u - a.pair_units) : 8 * u;
-  const int items = lane < lanes ? rows * a.heads : 0;
-  bool ready = false;
-  for (int i0 = lane;; i0 += kRotDeep * lanes) {
-    uint4 x[kRotDeep], y[kRotDeep];
-    int row[kRotDeep];
-#pragma unroll
-    for (int k = 0; k < kRotDeep; ++k) {
-      const int i = i0 + k * lanes;
-      row[k] = -1;
-      if (i >= items) continue;
-      row[k] = i / a.heads;
-      const uint16_t* from = a.x + (r0 + row[k]) * a.row + (i - row[k] * a.heads) * a.head + d0;
-      x[k] = *reinterpret_cast<const uint4*>(from);
-      if (halves && turns) y[k] = *reinterpret_cast<const uint4*>(from + pairs);
-    }
-    if (!ready) {
-      for (int i = tid; i < rows * pairs; i += kRotThreads) {
-        const int r = i / pairs, j = i - r * pairs;
-        const float2 cs = turn_of(a.t, a.t.positions[r0 + r], j);
-        s_cos[r * kMaxPairs + j] = cs.x;
-        s_sin[r * kMaxPairs + j] = a.sign * cs.y;
-      }
-      if (tid < rows) s_pos[tid] = a.t.positions[r0 + tid];
-      __syncthreads();
-      ready = true;
-    }
-    if (i0 >= items) break;
-#pragma unroll
-    for (int k = 0; k < kRotDeep; ++k) {
-      if (row[k] < 0 || s_pos[row[k]] < 0) continue;
-      const int i = i0 + k * lanes;
-      uint16_t* to = a.out + (r0 + row[k]) * a.orow + (i - row[k] * a.heads) * a.ohead + d0;
-      uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-      if (turns && halves) {
-        uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
-        const float* c = s_cos + row[k] * kMaxPairs + d0;
-        const float* s = s_sin + row[k] * kMaxPairs + d0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 p = word_to_f32<F16>(v[q]), r = word_to_f32<F16>(w[q]);
-          const float2 cc = *reinterpret_cast<const float2*>(c + 2 * q);
-          const float2 ss = *reinterpret_cast<const float2*>(s + 2 * q);
-          v[q] = f32_to_word<F16>(p.x * cc.x - r.x * ss.x, p.y * cc.y - r.y * ss.y);
-          w[q] = f32_to_word<F16>(r.x * cc.x + p.x * ss.x, r.y * cc.y + p.y * ss.y);
-        }
-        *reinterpret_cast<uint4*>(to + pairs) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else if (turns) {
-        const float4 c = *reinterpret_cast<const float4*>(s_cos + row[k] * kMaxPairs + 4 * u);
-        const float4 s = *reinterpret_cast<const float4*>(s_sin + row[k] * kMaxPairs + 4 * u);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 p = word_to_f32<F16>(v[q]);
-          v[q] = f32_to_word<F16>(p.x * cc[q] - p.y * ss[q], p.y * cc[q] + p.x * ss[q]);
-        }
-      }
-      *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
-    }
+  const int h0 = blockIdx.y * a.slice, heads = min(a.slice, a.heads - h0);
+  const int per_row = heads << a.d_shift, total = rows * per_row, dmask = (1 << a.d_shift) - 1;
+  const Quotient by_row(per_row);
+  uint4* const data = reinterpret_cast<uint4*>(smem);
+  float* const s_cos = reinterpret_cast<float*>(data + a.rows * (a.slice << a.d_shift));
+  float* const s_sin = s_cos + a.rows * pairs;
+  const uint16_t* const x = a.x + r0 * a.row + h0 * a.head;
+  uint16_t* const out = a.out + r0 * a.orow + h0 * a.ohead;
+#pragma unroll 4
+  for (int i = tid; i < total; i += kQ8Threads) {
+    const int r = by_row.of(i), w = i - r * per_row;
+    cp_async16(data + i, x + r * a.row + (w >> a.d_shift) * a.head + 8 * (w & dmask));
+  }
+  cp_async_commit();
+  make_turns(a.t, r0, rows, a.sign, s_cos, s_sin);
+  cp_async_wait<0>();
+  __syncthreads();
+#pragma unroll 2
+  for (int i = tid; i < total; i += kQ8Threads) {
+    const int r = by_row.of(i), w = i - r * per_row, lane = w & dmask;
+    if (a.t.positions[r0 + r] < 0) continue;
+    float y[8];
+    turned_piece<F16>(a.t, data + i - lane, lane, s_cos + r * pairs, s_sin + r * pairs, y);
+    *reinterpret_cast<uint4*>(out + r * a.orow + (w >> a.d_shift) * a.ohead + 8 * lane) =
+        make_uint4(f32_to_word<F16>(y[0], y[1]), f32_to_word<F16>(y[2], y[3]),
+                   f32_to_word<F16>(y[4], y[5]), f32_to_word<F16>(y[6], y[7]));
   }
 }
 
 // ---------------------------------------------------------------------------
 // dspark_kv_append_q8
 // ---------------------------------------------------------------------------
-// A run is the neighbouring rows of slot_map that one block takes. A CTA takes the
-// runs that begin among its kChunk rows, in batches of whole runs of kBatch rows at
-// most (a longer run by itself, in pieces, twice: its size first). A group of D / 8
-// lanes has a batch's rows of one head of K or V in registers, 8 elements a lane, finds
-// the size of every run, then the scales, and writes the codes.
-// CTA 0 only judges the slots, so that one CTA writes the status.
-constexpr int kQ8Threads = 256;
-constexpr int kChunk = 16, kBatch = 16;
+// A run is the neighbouring rows of slot_map that one block takes (skipped rows do not
+// count). A CTA takes some heads
+// of K or of V and the runs that begin among `chunk` rows; its window of `cap` rows holds
+// them whole (cap >= chunk + block - 1, or the last run's rest comes in windows of its own).
+// The window's rows lie in shared memory, so they are fetched once: (1) sizes of runs, a
+// maximum per run and head; (2) a scale each, and the blocks whose scale rises rounded
+// again; (3) the codes. CTA (0, 0, 0) only judges the slots, so that one CTA writes the
+// status.
+constexpr int kAppendPieces8 = 4096;  // of a window, at most (64 KB)
+constexpr int kMaxWindow = 256;       // rows
 
 struct AppendQ8Args {
   const uint16_t *k, *v;
@@ -142,281 +175,375 @@ struct AppendQ8Args {
   int64_t row, head;                  // of k and v, elements
   int64_t page, token, chead;         // of the codes, bytes
   int64_t spage, sblock, shead;       // of the scales, elements
-  Turns t;
-  int32_t n, heads, n_slots, p_shift, b_shift;
+  Turns t;                            // turns NULL: none
+  int32_t n, heads, n_slots, p_shift, b_shift, d_shift, slice, chunk, cap, slices;
 };
 
-// the smallest e >= -126 with a <= 448 * 2^e, as the bits of 2^e; a: bits of a finite
-// magnitude
+// the smallest e >= -126 with a <= 448 * 2^e, as 2^e; a: bits of a finite magnitude
 __device__ __forceinline__ float scale_for(uint32_t a) {
   const int e = static_cast<int>(a >> 23) - 127 - 8 + ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
 }
-// Quantised with 1 / s where that is exact.
-__device__ __forceinline__ bool power_of_two(float s) {
-  return (__float_as_uint(s) & 0x7FFFFFu) == 0;
+
+__device__ __forceinline__ void judge_slots(const int32_t* slots, int n, int n_slots, int32_t* status) {
+  bool bad = false;
+  if ((reinterpret_cast<uintptr_t>(slots) & 15u) == 0) {
+    const int4* s4 = reinterpret_cast<const int4*>(slots);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n / 4; i += kQ8Threads) {
+      const int4 s = s4[i];
+      bad |= max(max(s.x, s.y), max(s.z, s.w)) >= n_slots;
+    }
+    for (int i = (n & ~3) + threadIdx.x; i < n; i += kQ8Threads) bad |= slots[i] >= n_slots;
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kQ8Threads) bad |= slots[i] >= n_slots;
+  }
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *status = any ? DSPARK_ERR_BAD_DATA : DSPARK_OK;
 }
 
-template <int D, bool F16, int ROT>  // ROT: 0 none, 1 halves, 2 neighbours
+template <int D, bool F16>
 __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args a) {
-  constexpr int LPR = D / 8;                   // lanes of a group
-  constexpr int kGroups = kQ8Threads / LPR;
-  constexpr int kTrig = ROT ? kBatch * kMaxPairs : 1;
-  __shared__ alignas(16) float s_cos[kTrig], s_sin[kTrig];
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int32_t s_slot[kMaxWindow];   // of the window's rows; -1: nothing to write
+  __shared__ int16_t s_run[kMaxWindow];    // their runs
+  __shared__ int32_t s_first[kMaxWindow];  // a slot of each run
+  __shared__ uint8_t s_fresh[kMaxWindow];  // it has its block's first token
+  __shared__ int32_t s_count[kQ8Threads / 32], s_last[kQ8Threads / 32];
+  __shared__ int32_t s_found, s_odd, s_lo, s_hi;  // rows of the window from s_lo to before s_hi
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, wl = tid & 31, lane = tid % LPR, group = tid / LPR;
+  const int tid = threadIdx.x, wl = tid & 31, warp = tid >> 5;
   if (blockIdx.x == 0) {
-    bool bad = false;
-#pragma unroll 8
-    for (int i = tid; i < a.n; i += kQ8Threads) bad |= a.slots[i] >= a.n_slots;
-    const int any = __syncthreads_or(bad);
-    if (tid == 0) *a.status = any ? DSPARK_ERR_BAD_DATA : DSPARK_OK;
+    if (blockIdx.y == 0) judge_slots(a.slots, a.n, a.n_slots, a.status);
     return;
   }
+  const bool value = blockIdx.y >= static_cast<uint32_t>(a.slices);
+  const bool turns = a.t.turns != nullptr && !value;
+  const int h0 = (blockIdx.y - (value ? a.slices : 0)) * a.slice, heads = min(a.slice, a.heads - h0);
   const int bmask = (1 << a.b_shift) - 1, pmask = (1 << a.p_shift) - 1;
-  auto slot_of = [&](int i) {  // -1: nothing to write
+  constexpr int LPR = D / 8, dmask = LPR - 1;  // pieces of a head
+  const int pairs = a.t.rot / 2, per_row = heads * LPR;
+  const Quotient by_row(per_row);
+  uint4* const data = reinterpret_cast<uint4*>(smem);
+  uint32_t* const s_size = reinterpret_cast<uint32_t*>(data + a.cap * (a.slice << a.d_shift));
+  float* const s_scale = reinterpret_cast<float*>(s_size + a.cap * a.slice);
+  float* const s_cos = s_scale + a.cap * a.slice;
+  float* const s_sin = s_cos + a.cap * pairs;
+  const uint16_t* in = (value ? a.v : a.k) + h0 * a.head;
+  uint8_t* codes = (value ? a.vc : a.kc) + h0 * a.chead;  // (of this thread's piece, later)
+  float* const scales = (value ? a.vs : a.ks) + h0 * a.shead;
+  const int r0 = (blockIdx.x - 1) * a.chunk;
+  auto slot_of = [&](int i) {
     if (i < 0 || i >= a.n) return -1;
     int32_t s = a.slots[i];
-    if (s >= a.n_slots) s = -1;
-    if (ROT && a.t.positions[i] < 0) s = -1;
+    if (s >= a.n_slots || (a.t.turns && a.t.positions[i] < 0)) s = -1;
     return s;
   };
-  const int r0 = (blockIdx.x - 1) * kChunk;
-  // rows r0 - 1 + wl in the lanes: which begin a run, which count
-  const int my_slot = slot_of(r0 - 1 + wl);
-  const int my_block = my_slot < 0 ? -1 : my_slot >> a.b_shift;
-  const int before = __shfl_up_sync(0xFFFFFFFFu, my_block, 1);
-  const uint32_t begins = __ballot_sync(0xFFFFFFFFu, wl > 0 && my_block >= 0 && my_block != before) >> 1;
-  const uint32_t counts = __ballot_sync(0xFFFFFFFFu, my_block >= 0) >> 1;  // bit j: row r0 + j
-  auto run_end = [&](int j) -> int {  // of the run that begins at row r0 + j, relative
-    const uint32_t past = ~((2u << j) - 1u);
-    const uint32_t stop = (begins | ~counts) & past & 0x7FFFFFFFu;
-    if (stop) return __ffs(stop) - 1;
-    const int block = __shfl_sync(0xFFFFFFFFu, my_block, j + 1);
-    for (int i = r0 + 31;; i += 32) {
-      const int s = slot_of(i + wl);
-      const uint32_t other = __ballot_sync(0xFFFFFFFFu, s < 0 || (s >> a.b_shift) != block);
-      if (other) return i - r0 + __ffs(other) - 1;
-    }
+  auto code_at = [&](int slot) {
+    return codes + (slot >> a.p_shift) * a.page + static_cast<int64_t>(slot & pmask) * a.token;
   };
-  uint32_t todo = begins & ((1u << kChunk) - 1u);
-  const int rounds = (2 * a.heads + kGroups - 1) / kGroups;
 
-  while (todo) {
-    const int j0 = __ffs(todo) - 1;
-    int end = run_end(j0);
-    todo &= todo - 1;
-    while (todo) {  // runs that fit in the batch
-      const int e = run_end(__ffs(todo) - 1);
-      if (e - j0 > kBatch) break;
-      end = e;
-      todo &= todo - 1;
+  // The first row from `from` on that is not skipped, n if there is none; by the whole CTA.
+  auto next_row = [&](int from) {
+    if (from < a.n && slot_of(from) >= 0) return from;  // mostly (the same for all threads)
+    for (; from < a.n; from += 4 * kQ8Threads) {
+      __syncthreads();
+      if (tid == 0) s_found = a.n;
+      __syncthreads();
+      int at = a.n;
+#pragma unroll
+      for (int k = 3; k >= 0; --k)
+        if (slot_of(from + k * kQ8Threads + tid) >= 0) at = from + k * kQ8Threads + tid;
+      if (at < a.n) atomicMin(&s_found, at);
+      __syncthreads();
+      if (s_found < a.n) return static_cast<int>(s_found);
     }
-    const int s0 = r0 + j0, rows = end - j0;
-    const bool one = rows <= kBatch;
-    // rows s0 + wl in the lanes
-    auto trig = [&](int from, int n) {  // of rows from .. from + n - 1
-      if constexpr (ROT != 0) {
-        const int pairs = a.t.rot / 2;
-        __syncthreads();
-        for (int i = tid; i < n * pairs; i += kQ8Threads) {
-          const int r = i / pairs, j = i - r * pairs;
-          const float2 cs = turn_of(a.t, a.t.positions[from + r], j);
-          s_cos[r * kMaxPairs + j] = cs.x;
-          s_sin[r * kMaxPairs + j] = cs.y;
-        }
-        __syncthreads();
-      }
+    return a.n;
+  };
+
+  // ---- the first window: which row begins a run, the runs' numbers
+  int runs = 0;
+  {
+    // threads 0 .. cap - 1, a row each (cap <= the CTA's threads)
+    const int j = tid, s = j < a.cap ? slot_of(r0 + j) : -1;
+    const int ahead = slot_of(r0 - 32 + wl);  // the rows in front, mostly enough of them
+    const uint32_t valid = __ballot_sync(0xFFFFFFFFu, s >= 0);
+    const int top = __shfl_sync(0xFFFFFFFFu, s, valid ? 31 - __clz(valid) : 0);
+    if (wl == 0) s_last[warp] = top;
+    if (!__syncthreads_or(s >= 0)) return;  // nothing to write
+    // the row before that is not skipped
+    const uint32_t lower = valid & ((1u << wl) - 1u);
+    int before = __shfl_sync(0xFFFFFFFFu, s, lower ? 31 - __clz(lower) : 0);
+    if (!lower) {
+      before = -1;
+      for (int w = warp - 1; w >= 0 && before < 0; --w) before = s_last[w];
+    }
+    int front = -1;
+    for (int from = r0 - 32; front < 0 && from > -32; from -= 32) {
+      const int f = from == r0 - 32 ? ahead : slot_of(from + wl);
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, f >= 0);
+      if (m) front = __shfl_sync(0xFFFFFFFFu, f, 31 - __clz(m));
+    }
+    if (before < 0) before = front;
+    const bool begins = s >= 0 && (before < 0 || (before >> a.b_shift) != (s >> a.b_shift));
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, begins);
+    const uint32_t late = __ballot_sync(0xFFFFFFFFu, begins && j >= a.chunk);
+    if (wl == 0) s_count[warp] = __popc(m & ~late) | (late ? 256 : 0);
+    __syncthreads();
+    int run = __popc(m & ~late & ((2u << wl) - 1u)) - 1;
+    bool stopped = (late & ((2u << wl) - 1u)) != 0;  // a run of the next CTA has begun
+    bool ends = false;
+#pragma unroll
+    for (int w = 0; w < kQ8Threads / 32; ++w) {
+      if (w < warp) run += s_count[w] & 255, stopped |= s_count[w] >= 256;
+      runs += s_count[w] & 255;
+      ends |= s_count[w] >= 256;
+    }
+    if (runs == 0) return;
+    const bool mine = s >= 0 && run >= 0 && !stopped;
+    if (j < a.cap) {
+      s_slot[j] = mine ? s : -1;
+      s_run[j] = static_cast<int16_t>(run);
+    }
+    if (mine && begins) s_first[run] = s, s_fresh[run] = 0;
+    if (tid == 0) s_odd = 0, s_lo = a.cap, s_hi = 0;
+    __syncthreads();
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, mine);
+    if (wl == 0 && all) {
+      atomicMin(&s_lo, 32 * warp + __ffs(all) - 1);
+      atomicMax(&s_hi, 32 * warp + 32 - __clz(all));
+    }
+    for (int i = tid; i < a.cap * a.slice; i += kQ8Threads) s_size[i] = 0;
+    __syncthreads();
+    if (mine && (s & bmask) == 0) s_fresh[run] = 1;
+    if (ends) runs |= 1 << 30;  // no run goes on past the window
+  }
+  // the row past the window where the last run goes on, n if it does not
+  const int block = s_first[(runs & 0xFFFF) - 1] >> a.b_shift;
+  auto goes_on = [&](int from) {
+    const int at = next_row(from);
+    return at < a.n && (slot_of(at) >> a.b_shift) == block ? at : a.n;
+  };
+  const int rest = runs >> 30 ? a.n : goes_on(r0 + a.cap);
+  runs &= 0xFFFF;
+
+  // A thread has one piece of a head, the same in every row it takes.
+  const int rp = by_row.of(tid), w0 = tid - rp * per_row, lane = w0 & dmask, head = w0 / LPR;
+  const int step = kQ8Threads / per_row;  // rows side by side
+  const uint32_t group = ((1u << LPR) - 1u) << (wl & ~dmask);
+  const int first_row = rp < step ? rp : kMaxWindow;
+  in += head * a.head + 8 * lane;
+  codes += head * a.chead + 8 * lane;
+  auto fetch = [&](int from) {  // the window's rows that are this CTA's
+#pragma unroll 4
+    for (int r = first_row + s_lo; r < s_hi; r += step)
+      if (s_slot[r] >= 0) cp_async16(data + r * per_row + w0, in + (from + r) * a.row);
+    cp_async_commit();
+    if (turns) make_turns(a.t, from, min(a.cap, a.n - from), 1, s_cos, s_sin);
+    cp_async_wait<0>();
+    __syncthreads();
+  };
+  auto piece = [&](auto turned, int r, float (&y)[8]) {
+    const uint4* const h = data + r * per_row + (w0 - lane);
+    if constexpr (decltype(turned)::value)
+      turned_piece<F16>(a.t, h, lane, s_cos + r * pairs, s_sin + r * pairs, y);
+    else
+      piece_to_f32<F16>(h[lane], y);
+  };
+  // Both passes take several rows at once: a window's time is that of a thread's chain of
+  // loads and arithmetic, of which three CTAs on an SM hide little.
+  auto sizes_of = [&](auto turned) {
+    constexpr bool kTurned = decltype(turned)::value;
+    constexpr int kRows = kTurned ? 2 : 4;
+    uint32_t m = 0;  // bits of the largest finite magnitude in this run so far
+    int cur = -1;
+    auto flush = [&]() {
+      if (cur < 0) return;
+#pragma unroll
+      for (int o = LPR / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(group, m, o));
+      if (lane == 0) atomicMax(&s_size[cur * heads + head], m);
     };
-    if (one) trig(s0, rows);
-    for (int round = 0; round < rounds; ++round) {
-      const int task = round * kGroups + group;
-      const bool active = task < 2 * a.heads;
-      const bool value = task >= a.heads;
-      const int head = active ? (value ? task - a.heads : task) : 0;
-      const uint16_t* const in = (value ? a.v : a.k) + head * a.head + 8 * lane;
-      uint8_t* const codes = (value ? a.vc : a.kc) + head * a.chead + 8 * lane;
-      float* const scales = (value ? a.vs : a.ks) + head * a.shead;
-      // 8 elements of a row in binary32, turned if they are of a key; r: row of the trig
-      auto elements = [&](const uint4& w, int r, float (&y)[8]) {
-        const uint32_t own[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+    for (int r = first_row + s_lo; r < s_hi; r += kRows * step) {
+      int run[kRows];
+      uint32_t top[kRows];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 p = word_to_f32<F16>(own[q]);
-          y[2 * q] = p.x, y[2 * q + 1] = p.y;
+      for (int k = 0; k < kRows; ++k) {
+        const int at = min(r + k * step, a.cap - 1);
+        run[k] = r + k * step < s_hi && s_slot[at] >= 0 ? s_run[at] : -1;
+        top[k] = 0;
+        if constexpr (kTurned) {
+          float y[8];
+          piece(turned, at, y);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) top[k] = max(top[k], __float_as_uint(y[q]) & 0x7FFFFFFFu);
+        } else {
+          const uint4 v = data[at * per_row + w0];
+          const uint32_t t2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+          top[k] = __float_as_uint(word_to_f32<F16>(max(t2 & 0xFFFFu, t2 >> 16)).x);
         }
-        if constexpr (ROT == 1) {
-          const int half = a.t.rot / 16;  // lanes of a half
-          const int other = lane < half ? lane + half : lane < 2 * half ? lane - half : lane;
-          uint32_t got[4];
+      }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) got[q] = __shfl_sync(0xFFFFFFFFu, own[q], other, LPR);
-          if (!value && lane < 2 * half) {
-            const int j = 8 * (lane < half ? lane : lane - half);
-            const float sign = lane < half ? -1.f : 1.f;
-            const float* c = s_cos + r * kMaxPairs + j;
-            const float* s = s_sin + r * kMaxPairs + j;
+      for (int k = 0; k < kRows; ++k) {
+        if (run[k] < 0) continue;
+        if (top[k] >= 0x7F800000u) {  // what is not finite does not count
+          s_odd = 1;
+          float y[8];
+          piece(turned, r + k * step, y);
+          top[k] = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float2 p = word_to_f32<F16>(got[q]);
-              y[2 * q] = fmaf(y[2 * q], c[2 * q], sign * p.x * s[2 * q]);
-              y[2 * q + 1] = fmaf(y[2 * q + 1], c[2 * q + 1], sign * p.y * s[2 * q + 1]);
-            }
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t bits = __float_as_uint(y[q]) & 0x7FFFFFFFu;
+            top[k] = max(top[k], bits < 0x7F800000u ? bits : 0u);
           }
         }
-        if constexpr (ROT == 2) {
-          if (!value && 8 * lane < a.t.rot) {
-            const float* c = s_cos + r * kMaxPairs + 4 * lane;
-            const float* s = s_sin + r * kMaxPairs + 4 * lane;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float p = y[2 * q], o = y[2 * q + 1];
-              y[2 * q] = fmaf(p, c[q], -o * s[q]);
-              y[2 * q + 1] = fmaf(o, c[q], p * s[q]);
-            }
-          }
+        if (run[k] != cur) {
+          flush();
+          cur = run[k];
+          m = 0;
         }
-      };
-      auto size_of = [&](const float (&y)[8]) {  // bits of the largest finite magnitude
-        uint32_t m = 0;
+        m = max(m, top[k]);
+      }
+    }
+    flush();
+  };
+  auto write_of = [&](auto turned) {
+    constexpr int kRows = decltype(turned)::value ? 2 : 4;
+    const bool odd = s_odd != 0;
+#pragma unroll 1
+    for (int r = first_row + s_lo; r < s_hi; r += kRows * step) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t b = __float_as_uint(y[q]) & 0x7FFFFFFFu;
-          m = max(m, b < 0x7F800000u ? b : 0u);
+      for (int k = 0; k < kRows; ++k) {
+        const int at = min(r + k * step, a.cap - 1), slot = s_slot[at];
+        if (r + k * step >= s_hi || slot < 0) continue;
+        const float s = s_scale[s_run[at] * heads + head];
+        float y[8];
+        piece(turned, at, y);
+        if (odd) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) y[q] = fabsf(y[q]) < INFINITY ? y[q] : NAN;
         }
-        return m;
-      };
-      auto over_group = [&](uint32_t m) {
-#pragma unroll
-        for (int o = LPR / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        return m;
-      };
-      auto put = [&](int slot, const float (&y)[8], float s) {
-        uint32_t lo, hi;
-        float z[8];
-        if (power_of_two(s)) {
+        if ((__float_as_uint(s) & 0x7FFFFFu) == 0) {  // a power of two: 1 / s is exact
           const float inv = 1.f / s;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) z[q] = y[q] * inv;
+          for (int q = 0; q < 8; ++q) y[q] *= inv;
         } else {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) z[q] = __fdiv_rn(y[q], s);
+          for (int q = 0; q < 8; ++q) y[q] = __fdiv_rn(y[q], s);
         }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (fabsf(y[q]) == INFINITY) z[q] = NAN;
-        lo = e4m3x4(z[0], z[1], z[2], z[3]);
-        hi = e4m3x4(z[4], z[5], z[6], z[7]);
-        *reinterpret_cast<uint2*>(codes + (slot >> a.p_shift) * a.page +
-                                  (slot & pmask) * a.token) = make_uint2(lo, hi);
-      };
-      // The scale of the run whose rows have this size, with its block's other tokens
-      // rounded again where it rises.
-      auto settle = [&](int slot, bool fresh, uint32_t size) {
-        float* const at = scales + (slot >> a.p_shift) * a.spage +
-                          ((slot & pmask) >> a.b_shift) * a.sblock;
-        float s = scale_for(size);
-        const float old = fresh ? 0.f : *at;
-        if (is_scale(old)) {
-          if (__uint_as_float(size) <= 448.f * old) {
-            s = old;
-          } else {
-            const float f = old / s;  // 2^e > old
-            uint8_t* const first = codes + (slot >> a.p_shift) * a.page +
-                                   ((slot & pmask) & ~bmask) * a.token;
-            for (int t = 0; t <= bmask; ++t) {
-              uint2* const p = reinterpret_cast<uint2*>(first + t * a.token);
-              const uint2 c = *p;
-              const float2 c0 = e4m3x2_to_f32(c.x), c1 = e4m3x2_to_f32(c.x >> 16);
-              const float2 c2 = e4m3x2_to_f32(c.y), c3 = e4m3x2_to_f32(c.y >> 16);
-              *p = make_uint2(e4m3x4(c0.x * f, c0.y * f, c1.x * f, c1.y * f),
-                              e4m3x4(c2.x * f, c2.y * f, c3.x * f, c3.y * f));
-            }
-          }
-        }
-        __syncwarp(LPR == 32 ? 0xFFFFFFFFu : ((1u << LPR) - 1u) << (wl & ~(LPR - 1)));
-        if (lane == 0) *at = s;  // every lane has read it
-        return s;
-      };
-      if (one) {
-        const int slot_l = wl < rows ? slot_of(s0 + wl) : -1;
-        const uint32_t live = __ballot_sync(0xFFFFFFFFu, slot_l >= 0);
-        const uint32_t starts = (begins >> j0) & ((1u << rows) - 1u);
-        // which of the lanes' rows are in a run that has its block's first token
-        const uint32_t zero = __ballot_sync(0xFFFFFFFFu, slot_l >= 0 && (slot_l & bmask) == 0);
-        const uint32_t upto = (2u << wl) - 1u;  // (lane 31: all)
-        const int from = 31 - __clz(starts & upto);
-        const uint32_t later = starts & ~upto;
-        const uint32_t mine = (later ? (1u << (__ffs(later) - 1)) - 1u : 0xFFFFFFFFu) &
-                              ~((1u << from) - 1u);
-        const uint32_t fresh = __ballot_sync(0xFFFFFFFFu, (zero & mine) != 0);
-        uint4 x[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          x[j] = make_uint4(0, 0, 0, 0);
-          if (active && (live >> j) & 1u)
-            x[j] = *reinterpret_cast<const uint4*>(in + (s0 + j) * a.row);
-        }
-        uint32_t size[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          size[j] = 0;
-          if (j < rows) {
-            float y[8];
-            elements(x[j], j, y);
-            size[j] = over_group(size_of(y));
-          }
-        }
-        // of a run: in its first row
-#pragma unroll
-        for (int j = kBatch - 2; j >= 0; --j)
-          if (!((starts >> (j + 1)) & 1u)) size[j] = max(size[j], size[j + 1]);
-        float s = 1.f;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          if (j >= rows) break;
-          const int slot = __shfl_sync(0xFFFFFFFFu, slot_l, j);
-          if (active && (starts >> j) & 1u) s = settle(slot, (fresh >> j) & 1u, size[j]);
-          __syncwarp();
-          float y[8];
-          elements(x[j], j, y);
-          if (active && slot >= 0) put(slot, y, s);
-        }
-      } else {
-        // a run of more rows than the registers hold
-        uint32_t size = 0;
-        bool fresh = false;
-        for (int b = 0; b < rows; b += kBatch) {
-          const int m = min(kBatch, rows - b);
-          trig(s0 + b, m);
-#pragma unroll 4
-          for (int j = 0; j < m; ++j) {
-            const int slot = slot_of(s0 + b + j);
-            fresh |= slot >= 0 && (slot & bmask) == 0;
-            const uint4 x = *reinterpret_cast<const uint4*>(in + (s0 + b + j) * a.row);
-            float y[8];
-            elements(x, j, y);
-            size = max(size, size_of(y));
-          }
-        }
-        size = over_group(size);
-        float s = 1.f;
-        if (active) s = settle(slot_of(s0), fresh, size);
-        __syncwarp();
-        for (int b = 0; b < rows; b += kBatch) {
-          const int m = min(kBatch, rows - b);
-          trig(s0 + b, m);
-#pragma unroll 4
-          for (int j = 0; j < m; ++j) {
-            const uint4 x = *reinterpret_cast<const uint4*>(in + (s0 + b + j) * a.row);
-            float y[8];
-            elements(x, j, y);
-            if (active) put(slot_of(s0 + b + j), y, s);
-          }
-        }
+        *reinterpret_cast<uint2*>(code_at(slot)) =
+            make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
       }
     }
+  };
+  auto sizes = [&]() {
+    if (turns)
+      sizes_of(std::true_type());
+    else
+      sizes_of(std::false_type());
+  };
+  auto write = [&]() {
+    if (turns)
+      write_of(std::true_type());
+    else
+      write_of(std::false_type());
+  };
+  // the rest of the last run: the window that begins with row `from`, which it has
+  auto next_window = [&](int from) {
+    __syncthreads();
+    const int s = tid < a.cap ? slot_of(from + tid) : -1;
+    const uint32_t other = __ballot_sync(0xFFFFFFFFu, s >= 0 && (s >> a.b_shift) != block);
+    if (wl == 0) s_count[warp] = other ? __ffs(other) - 1 : 32;
+    __syncthreads();
+    bool mine = s >= 0 && wl < s_count[warp];
+    for (int w = 0; w < warp; ++w) mine = mine && s_count[w] == 32;
+    bool ends = false;
+    for (int w = 0; w < kQ8Threads / 32; ++w) ends |= s_count[w] != 32;
+    if (tid < a.cap) {
+      s_slot[tid] = mine ? s : -1;
+      s_run[tid] = static_cast<int16_t>(runs - 1);
+    }
+    if (mine && (s & bmask) == 0) s_fresh[runs - 1] = 1;
+    if (tid == 0) s_lo = 0, s_hi = a.cap;
+    __syncthreads();
+    return ends ? a.n : goes_on(from + a.cap);
+  };
+
+  // ---- (1) sizes
+  fetch(r0);
+  sizes();
+#pragma unroll 1
+  for (int from = rest; from < a.n;) {
+    const int next = next_window(from);
+    fetch(from);
+    sizes();
+    from = next;
+  }
+  __syncthreads();
+  // ---- (2) scales
+  bool rises = false;
+  for (int i = tid; i < runs * heads; i += kQ8Threads) {
+    const int run = i / heads, h = i - run * heads, slot = s_first[run];
+    float* const at = scales + (slot >> a.p_shift) * a.spage +
+                      static_cast<int64_t>((slot & pmask) >> a.b_shift) * a.sblock + h * a.shead;
+    float s = scale_for(s_size[i]);
+    const float old = s_fresh[run] ? 0.f : *at;
+    float f = 0.f;  // what the other tokens' codes are multiplied with
+    if (is_scale(old)) {
+      if (__uint_as_float(s_size[i]) <= 448.f * old)
+        s = old;
+      else
+        f = old / s, rises = true;  // 2^e > old
+    }
+    *at = s;
+    s_scale[i] = s;
+    s_size[i] = __float_as_uint(f);
+  }
+  if (__syncthreads_or(rises)) {
+#pragma unroll 1
+    for (int run = 0; run < runs; ++run) {
+      const float f = rp < step ? __uint_as_float(s_size[run * heads + head]) : 0.f;
+      if (f == 0.f) continue;
+      const int block0 = s_first[run] & ~bmask;
+#pragma unroll 4
+      for (int t = rp; t <= bmask; t += step) {
+        uint2* const p = reinterpret_cast<uint2*>(code_at(block0 + t));
+        const uint2 c = *p;
+        const float2 c0 = e4m3x2_to_f32(c.x), c1 = e4m3x2_to_f32(c.x >> 16);
+        const float2 c2 = e4m3x2_to_f32(c.y), c3 = e4m3x2_to_f32(c.y >> 16);
+        *p = make_uint2(e4m3x4(c0.x * f, c0.y * f, c1.x * f, c1.y * f),
+                        e4m3x4(c2.x * f, c2.y * f, c3.x * f, c3.y * f));
+      }
+    }
+    __syncthreads();
+  }
+  // ---- (3) codes
+  if (rest < a.n) {
+    // the last window is there now, the first one again
+    const int s = tid < a.cap ? slot_of(r0 + tid) : -1;
+    __syncthreads();
+    if (tid < a.cap) {
+      // rows of this CTA's runs, by their blocks: neighbours, in the runs' order
+      int run = -1;
+      for (int q = 0; q < runs && run < 0; ++q)
+        if (s >= 0 && (s_first[q] >> a.b_shift) == (s >> a.b_shift)) run = q;
+      s_slot[tid] = run >= 0 ? s : -1;
+      s_run[tid] = static_cast<int16_t>(run);
+    }
+    if (tid == 0) s_lo = 0, s_hi = a.cap;
+    __syncthreads();
+    fetch(r0);
+  }
+  write();
+#pragma unroll 1
+  for (int from = rest; from < a.n;) {
+    const int next = next_window(from);
+    fetch(from);
+    write();
+    from = next;
   }
 }
 
@@ -441,11 +568,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_gather_q8(const GatherQ8Args 
   pdl_trigger();
   const int tid = threadIdx.x;
   if (blockIdx.x == 0) {
-    bool bad = false;
-#pragma unroll 8
-    for (int i = tid; i < a.n; i += kQ8Threads) bad |= a.slots[i] >= a.n_slots;
-    const int any = __syncthreads_or(bad);
-    if (tid == 0) *a.status = any ? DSPARK_ERR_BAD_DATA : DSPARK_OK;
+    judge_slots(a.slots, a.n, a.n_slots, a.status);
     return;
   }
   const int pmask = (1 << a.p_shift) - 1, dmask = (1 << a.d_shift) - 1;
@@ -521,11 +644,35 @@ bool cache_ok(int32_t n, int32_t Hkv, int32_t D, int32_t dtype, int64_t page_str
          ((page_stride | token_stride | head_stride) & 15) == 0;
 }
 
+// dynamic shared memory past 48 KB
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, bool (&ready)[128], std::mutex& mutex) {
+  int dev = 0;
+  cudaError_t rc = cudaGetDevice(&dev);
+  if (rc != cudaSuccess) return rc;
+  if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (!ready[dev]) {
+    rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes));
+    ready[dev] = rc == cudaSuccess;
+  }
+  return rc;
+}
+std::mutex g_q8_mutex;
+constexpr size_t kSmemMost = 160 * 1024;
+
+template <bool F16>
+cudaError_t rotary_launch(const RotaryArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
+  static bool ready[128];
+  const cudaError_t rc = allow_smem(k_rotary<F16>, kSmemMost, ready, g_q8_mutex);
+  return rc != cudaSuccess ? rc : launch_pdl(k_rotary<F16>, grid, kQ8Threads, smem, st, a);
+}
 template <int D, bool F16>
-cudaError_t append_launch(const AppendQ8Args& a, int rot, int grid, cudaStream_t st) {
-  if (rot == 0) return launch_pdl(k_kv_append_q8<D, F16, 0>, grid, kQ8Threads, 0, st, a);
-  if (rot == 1) return launch_pdl(k_kv_append_q8<D, F16, 1>, grid, kQ8Threads, 0, st, a);
-  return launch_pdl(k_kv_append_q8<D, F16, 2>, grid, kQ8Threads, 0, st, a);
+cudaError_t append_launch(const AppendQ8Args& a, dim3 grid, size_t smem, cudaStream_t st) {
+  static bool ready[128];
+  const cudaError_t rc = allow_smem(k_kv_append_q8<D, F16>, kSmemMost, ready, g_q8_mutex);
+  return rc != cudaSuccess ? rc : launch_pdl(k_kv_append_q8<D, F16>, grid, kQ8Threads, smem, st, a);
 }
 
 }  // namespace
@@ -553,15 +700,20 @@ extern "C" int dspark_rotary(const void* x, int64_t row_stride, int64_t head_str
   a.t = Turns{rotation->turns, positions, rotation->gain, rotation->rot_dim,
               rotation->pairs == DSPARK_ROTARY_INTERLEAVED};
   a.n = n, a.heads = heads;
-  a.pair_units = rotation->rot_dim / (a.t.inter ? 8 : 16);
-  a.units = a.pair_units + (D - rotation->rot_dim) / 8;
+  a.d_shift = D == 64 ? 3 : 4;
   a.sign = inverse ? -1 : 1;
-  a.rows = std::clamp(kRotDeep * (kRotThreads / a.units) / heads, 1, kRotRows);
-  const int grid = static_cast<int>(DSPARK_CEILDIV(n, a.rows));
+  // heads of a CTA: all, or what fits
+  a.slice = std::min(heads, kRotPieces >> a.d_shift);
+  a.rows = std::max(1, std::min<int>(kRotPieces / (a.slice << a.d_shift), 32));
+  // a few rows on many SMs: fewer rows a CTA
+  while (a.rows > 1 && DSPARK_CEILDIV(n, a.rows) < 148) a.rows /= 2;
+  const dim3 grid(static_cast<unsigned>(DSPARK_CEILDIV(n, a.rows)),
+                  static_cast<unsigned>(DSPARK_CEILDIV(heads, a.slice)));
+  const size_t smem = static_cast<size_t>(a.rows) * (a.slice << a.d_shift) * 16 +
+                      static_cast<size_t>(a.rows) * rotation->rot_dim * 4;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t rc = dtype == DSPARK_F16
-                             ? launch_pdl(k_rotary<true>, grid, kRotThreads, 0, st, a)
-                             : launch_pdl(k_rotary<false>, grid, kRotThreads, 0, st, a);
+  const cudaError_t rc = dtype == DSPARK_F16 ? rotary_launch<true>(a, grid, smem, st)
+                                             : rotary_launch<false>(a, grid, smem, st);
   return rc == cudaSuccess && cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
@@ -589,19 +741,33 @@ extern "C" int dspark_kv_append_q8(
   a.chead = head_stride, a.spage = scale_page_stride, a.sblock = scale_block_stride;
   a.shead = scale_head_stride, a.n = n, a.heads = Hkv, a.n_slots = num_pages * page_size;
   a.p_shift = shift_of(page_size, 3, 10), a.b_shift = shift_of(block, 0, 10);
-  int rot = 0;
-  if (rotation) {
+  if (rotation)
     a.t = Turns{rotation->turns, positions, rotation->gain, rotation->rot_dim,
                 rotation->pairs == DSPARK_ROTARY_INTERLEAVED};
-    rot = a.t.inter ? 2 : 1;
-  }
-  const int grid = 1 + static_cast<int>(DSPARK_CEILDIV(n, kChunk));
+  a.d_shift = D == 64 ? 3 : 4;
+  // The window: twice a block's rows, so that every second row's run begins in it, as far as
+  // shared memory goes (rows, sizes and scales, cosines and sines); heads are left to other CTAs
+  // for more rows.
+  int cap = std::min(std::max(2 * block, 16), kMaxWindow);
+  const int pairs = rotation ? rotation->rot_dim / 2 : 0;
+  while (cap > 16 && cap * pairs * 8 > 64 * 1024) cap /= 2;
+  a.slice = std::clamp((kAppendPieces8 >> a.d_shift) / cap, 1, Hkv);
+  // few heads: more rows
+  while (cap * 2 <= kMaxWindow && cap * 2 * (a.slice << a.d_shift) <= kAppendPieces8 &&
+         cap * 2 * pairs * 8 <= 64 * 1024 && DSPARK_CEILDIV(n, cap) > 296)
+    cap *= 2;
+  a.cap = cap;
+  a.chunk = std::max(cap / 2, cap - block + 1);
+  a.slices = static_cast<int32_t>(DSPARK_CEILDIV(Hkv, a.slice));
+  const dim3 grid(1u + static_cast<unsigned>(DSPARK_CEILDIV(n, a.chunk)), 2u * a.slices);
+  const size_t smem = static_cast<size_t>(cap) * (a.slice << a.d_shift) * 16 +
+                      static_cast<size_t>(cap) * a.slice * 8 + static_cast<size_t>(cap) * pairs * 8;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f16 = dtype == DSPARK_F16;
-  const cudaError_t rc = D == 64 ? (f16 ? append_launch<64, true>(a, rot, grid, st)
-                                        : append_launch<64, false>(a, rot, grid, st))
-                                 : (f16 ? append_launch<128, true>(a, rot, grid, st)
-                                        : append_launch<128, false>(a, rot, grid, st));
+  const cudaError_t rc = D == 64 ? (f16 ? append_launch<64, true>(a, grid, smem, st)
+                                        : append_launch<64, false>(a, grid, smem, st))
+                                 : (f16 ? append_launch<128, true>(a, grid, smem, st)
+                                        : append_launch<128, false>(a, grid, smem, st));
   return rc == cudaSuccess && cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
