@@ -92,8 +92,8 @@ int dspark_rotary(const void* x, int64_t row_stride, int64_t head_stride,
  *
  * Rows of one block must be neighbours in slot_map (as dspark_pages_reserve gives
  * them), in any order, skipped rows not counted; a block that is written by rows with
- * other blocks' in between has unspecified codes and scales. Slots that occur twice leave
- * either row.
+ * other blocks' in between has unspecified codes and scales. Of rows with the same
+ * slot the last is left; the scale counts them all, or the last alone in blocks of one.
  *
  * Arguments
  *   k, v          dtype (DSPARK_BF16, DSPARK_F16): head h of row i at element

@@ -22,7 +22,7 @@ struct Turns {
   bool inter;     // pairs are neighbours
 };
 
-// i / d for i < 2^16 and 8 <= d <= 2^12, by a multiplication
+// i / d for i < 2^16 and 2 <= d <= 2^12, by a multiplication
 struct Quotient {
   uint32_t inv;
   __device__ __forceinline__ explicit Quotient(int d) : inv(0xFFFFFFFFu / static_cast<uint32_t>(d) + 1u) {}
@@ -62,31 +62,25 @@ __device__ __forceinline__ void piece_to_f32(const uint4& w, float (&y)[8]) {
     y[2 * q] = p.x, y[2 * q + 1] = p.y;
   }
 }
-// The 8 elements of piece `lane` of a head that lies in shared memory at `head`, turned. c, s:
-// the row's cosines and sines. With halves a piece's partners are a piece as well (rot_dim is a
-// multiple of 16).
-template <bool F16>
-__device__ __forceinline__ void turned_piece(const Turns& t, const uint4* head, int lane, const float* c,
-                                             const float* s, float (&y)[8]) {
-  piece_to_f32<F16>(head[lane], y);
-  if (8 * lane >= t.rot) return;
+// The 8 elements y of piece `lane` of a head, turned. o: the partners; c, s: the row's cosines
+// and sines. With halves a piece's partners are a piece as well (rot_dim is a multiple of 16).
+__device__ __forceinline__ void turn_piece(const Turns& t, int lane, const float (&o)[8], const float* c,
+                                           const float* s, float (&y)[8]) {
   if (t.inter) {
     const float4 cc = *reinterpret_cast<const float4*>(c + 4 * lane);
     const float4 ss = *reinterpret_cast<const float4*>(s + 4 * lane);
     const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float p = y[2 * q], o = y[2 * q + 1];
-      y[2 * q] = fmaf(p, c4[q], -o * s4[q]);
-      y[2 * q + 1] = fmaf(o, c4[q], p * s4[q]);
+      const float p = y[2 * q], r = y[2 * q + 1];
+      y[2 * q] = fmaf(p, c4[q], -r * s4[q]);
+      y[2 * q + 1] = fmaf(r, c4[q], p * s4[q]);
     }
   } else {
     const int half = t.rot >> 4;  // pieces of a half
     const bool upper = lane >= half;
     const int j = upper ? lane - half : lane;
     const float sign = upper ? 1.f : -1.f;
-    float o[8];
-    piece_to_f32<F16>(head[upper ? lane - half : lane + half], o);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const float4 cc = reinterpret_cast<const float4*>(c + 8 * j)[q];
@@ -98,7 +92,21 @@ __device__ __forceinline__ void turned_piece(const Turns& t, const uint4* head, 
     }
   }
 }
-
+// the piece that has the partners of piece `lane`
+__device__ __forceinline__ int partner_of(const Turns& t, int lane) {
+  const int half = t.rot >> 4;
+  return t.inter || lane >= 2 * half ? lane : lane < half ? lane + half : lane - half;
+}
+// ... of a head that lies in shared memory
+template <bool F16>
+__device__ __forceinline__ void turned_piece(const Turns& t, const uint4* head, int lane, const float* c,
+                                             const float* s, float (&y)[8]) {
+  piece_to_f32<F16>(head[lane], y);
+  if (8 * lane >= t.rot) return;
+  float o[8];
+  piece_to_f32<F16>(head[partner_of(t, lane)], o);
+  turn_piece(t, lane, o, c, s, y);
+}
 // ---------------------------------------------------------------------------
 // dspark_rotary
 // ---------------------------------------------------------------------------
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_rotary(const RotaryArgs a) {
 // The window's rows lie in shared memory, so they are fetched once: (1) sizes of runs, a
 // maximum per run and head; (2) a scale each, and the blocks whose scale rises rounded
 // again; (3) the codes. CTA (0, 0, 0) only judges the slots, so that one CTA writes the
-// status.
+// status. Blocks of one token have a kernel of their own, without runs.
 constexpr int kAppendPieces8 = 4096;  // of a window, at most (64 KB)
 constexpr int kMaxWindow = 256;       // rows
 
@@ -177,6 +185,7 @@ struct AppendQ8Args {
   int64_t spage, sblock, shead;       // of the scales, elements
   Turns t;                            // turns NULL: none
   int32_t n, heads, n_slots, p_shift, b_shift, d_shift, slice, chunk, cap, slices;
+  int32_t rows;  // of a CTA, blocks of one token
 };
 
 // the smallest e >= -126 with a <= 448 * 2^e, as 2^e; a: bits of a finite magnitude
@@ -203,15 +212,46 @@ __device__ __forceinline__ void judge_slots(const int32_t* slots, int n, int n_s
   if (threadIdx.x == 0) *status = any ? DSPARK_ERR_BAD_DATA : DSPARK_OK;
 }
 
+__device__ __forceinline__ int slot_of(const AppendQ8Args& a, int i) {
+  if (i < 0 || i >= a.n) return -1;
+  const int32_t s = a.slots[i];
+  return s >= a.n_slots || (a.t.turns && a.t.positions[i] < 0) ? -1 : s;
+}
+
+// The first row from `from` on that is not skipped, n if there is none; by the whole CTA.
+__device__ __noinline__ int next_row(const AppendQ8Args& a, int from, int* s_found) {
+  for (; from < a.n; from += 4 * kQ8Threads) {
+    __syncthreads();
+    if (threadIdx.x == 0) *s_found = a.n;
+    __syncthreads();
+    int at = a.n;
+#pragma unroll
+    for (int k = 3; k >= 0; --k) {
+      const int i = from + k * kQ8Threads + static_cast<int>(threadIdx.x);
+      if (slot_of(a, i) >= 0) at = i;
+    }
+    if (at < a.n) atomicMin(s_found, at);
+    __syncthreads();
+    if (*s_found < a.n) return *s_found;
+  }
+  return a.n;
+}
+
+// a power of two s, 2^-126 <= s < 2^127: its inverse
+__device__ __forceinline__ bool has_inverse(float s) {
+  return (__float_as_uint(s) & 0x7FFFFFu) == 0 && __float_as_uint(s) < 0x7F000000u;
+}
+__device__ __forceinline__ float inverse_of(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args a) {
+__global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_constant__ AppendQ8Args a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int32_t s_slot[kMaxWindow];   // of the window's rows; -1: nothing to write
   __shared__ int16_t s_run[kMaxWindow];    // their runs
   __shared__ int32_t s_first[kMaxWindow];  // a slot of each run
   __shared__ uint8_t s_fresh[kMaxWindow];  // it has its block's first token
   __shared__ int32_t s_count[kQ8Threads / 32], s_last[kQ8Threads / 32];
-  __shared__ int32_t s_found, s_odd, s_lo, s_hi;  // rows of the window from s_lo to before s_hi
+  __shared__ int32_t s_found, s_odd, s_mixed, s_lo, s_hi;  // rows of the window from s_lo to before s_hi
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, wl = tid & 31, warp = tid >> 5;
@@ -235,43 +275,20 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args 
   uint8_t* codes = (value ? a.vc : a.kc) + h0 * a.chead;  // (of this thread's piece, later)
   float* const scales = (value ? a.vs : a.ks) + h0 * a.shead;
   const int r0 = (blockIdx.x - 1) * a.chunk;
-  auto slot_of = [&](int i) {
-    if (i < 0 || i >= a.n) return -1;
-    int32_t s = a.slots[i];
-    if (s >= a.n_slots || (a.t.turns && a.t.positions[i] < 0)) s = -1;
-    return s;
-  };
   auto code_at = [&](int slot) {
     return codes + (slot >> a.p_shift) * a.page + static_cast<int64_t>(slot & pmask) * a.token;
-  };
-
-  // The first row from `from` on that is not skipped, n if there is none; by the whole CTA.
-  auto next_row = [&](int from) {
-    if (from < a.n && slot_of(from) >= 0) return from;  // mostly (the same for all threads)
-    for (; from < a.n; from += 4 * kQ8Threads) {
-      __syncthreads();
-      if (tid == 0) s_found = a.n;
-      __syncthreads();
-      int at = a.n;
-#pragma unroll
-      for (int k = 3; k >= 0; --k)
-        if (slot_of(from + k * kQ8Threads + tid) >= 0) at = from + k * kQ8Threads + tid;
-      if (at < a.n) atomicMin(&s_found, at);
-      __syncthreads();
-      if (s_found < a.n) return static_cast<int>(s_found);
-    }
-    return a.n;
   };
 
   // ---- the first window: which row begins a run, the runs' numbers
   int runs = 0;
   {
     // threads 0 .. cap - 1, a row each (cap <= the CTA's threads)
-    const int j = tid, s = j < a.cap ? slot_of(r0 + j) : -1;
-    const int ahead = slot_of(r0 - 32 + wl);  // the rows in front, mostly enough of them
+    const int j = tid, s = j < a.cap ? slot_of(a, r0 + j) : -1;
+    const int ahead = slot_of(a, r0 - 32 + wl);  // the rows in front, mostly enough of them
     const uint32_t valid = __ballot_sync(0xFFFFFFFFu, s >= 0);
     const int top = __shfl_sync(0xFFFFFFFFu, s, valid ? 31 - __clz(valid) : 0);
     if (wl == 0) s_last[warp] = top;
+    if (tid == 0) s_mixed = 0;
     if (!__syncthreads_or(s >= 0)) return;  // nothing to write
     // the row before that is not skipped
     const uint32_t lower = valid & ((1u << wl) - 1u);
@@ -282,12 +299,13 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args 
     }
     int front = -1;
     for (int from = r0 - 32; front < 0 && from > -32; from -= 32) {
-      const int f = from == r0 - 32 ? ahead : slot_of(from + wl);
+      const int f = from == r0 - 32 ? ahead : slot_of(a, from + wl);
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, f >= 0);
       if (m) front = __shfl_sync(0xFFFFFFFFu, f, 31 - __clz(m));
     }
     if (before < 0) before = front;
     const bool begins = s >= 0 && (before < 0 || (before >> a.b_shift) != (s >> a.b_shift));
+    if (s >= 0 && !begins && s <= before) s_mixed = 1;  // a slot may occur twice
     const uint32_t m = __ballot_sync(0xFFFFFFFFu, begins);
     const uint32_t late = __ballot_sync(0xFFFFFFFFu, begins && j >= a.chunk);
     if (wl == 0) s_count[warp] = __popc(m & ~late) | (late ? 256 : 0);
@@ -323,8 +341,8 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args 
   // the row past the window where the last run goes on, n if it does not
   const int block = s_first[(runs & 0xFFFF) - 1] >> a.b_shift;
   auto goes_on = [&](int from) {
-    const int at = next_row(from);
-    return at < a.n && (slot_of(at) >> a.b_shift) == block ? at : a.n;
+    const int at = from < a.n && slot_of(a, from) >= 0 ? from : next_row(a, from, &s_found);
+    return at < a.n && (slot_of(a, at) >> a.b_shift) == block ? at : a.n;
   };
   const int rest = runs >> 30 ? a.n : goes_on(r0 + a.cap);
   runs &= 0xFFFF;
@@ -413,12 +431,14 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args 
   auto write_of = [&](auto turned) {
     constexpr int kRows = decltype(turned)::value ? 2 : 4;
     const bool odd = s_odd != 0;
+    // Of rows with one slot the last is left: then each thread stores its piece of all rows.
+    const int ws = s_mixed ? 1 : step, w_first = !s_mixed ? first_row : rp == 0 ? 0 : kMaxWindow;
 #pragma unroll 1
-    for (int r = first_row + s_lo; r < s_hi; r += kRows * step) {
+    for (int r = w_first + s_lo; r < s_hi; r += kRows * ws) {
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
-        const int at = min(r + k * step, a.cap - 1), slot = s_slot[at];
-        if (r + k * step >= s_hi || slot < 0) continue;
+        const int at = min(r + k * ws, a.cap - 1), slot = s_slot[at];
+        if (r + k * ws >= s_hi || slot < 0) continue;
         const float s = s_scale[s_run[at] * heads + head];
         float y[8];
         piece(turned, at, y);
@@ -426,8 +446,8 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args 
 #pragma unroll
           for (int q = 0; q < 8; ++q) y[q] = fabsf(y[q]) < INFINITY ? y[q] : NAN;
         }
-        if ((__float_as_uint(s) & 0x7FFFFFu) == 0) {  // a power of two: 1 / s is exact
-          const float inv = 1.f / s;
+        if (has_inverse(s)) {
+          const float inv = inverse_of(s);
 #pragma unroll
           for (int q = 0; q < 8; ++q) y[q] *= inv;
         } else {
@@ -454,7 +474,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args 
   // the rest of the last run: the window that begins with row `from`, which it has
   auto next_window = [&](int from) {
     __syncthreads();
-    const int s = tid < a.cap ? slot_of(from + tid) : -1;
+    const int s = tid < a.cap ? slot_of(a, from + tid) : -1;
     const uint32_t other = __ballot_sync(0xFFFFFFFFu, s >= 0 && (s >> a.b_shift) != block);
     if (wl == 0) s_count[warp] = other ? __ffs(other) - 1 : 32;
     __syncthreads();
@@ -467,6 +487,8 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args 
       s_run[tid] = static_cast<int16_t>(runs - 1);
     }
     if (mine && (s & bmask) == 0) s_fresh[runs - 1] = 1;
+    if (mine && s <= slot_of(a, from + tid - 1)) s_mixed = 1;
+    if (mine && slot_of(a, from + tid - 1) < 0) s_mixed = 1;
     if (tid == 0) s_lo = 0, s_hi = a.cap;
     __syncthreads();
     return ends ? a.n : goes_on(from + a.cap);
@@ -523,7 +545,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args 
   // ---- (3) codes
   if (rest < a.n) {
     // the last window is there now, the first one again
-    const int s = tid < a.cap ? slot_of(r0 + tid) : -1;
+    const int s = tid < a.cap ? slot_of(a, r0 + tid) : -1;
     __syncthreads();
     if (tid < a.cap) {
       // rows of this CTA's runs, by their blocks: neighbours, in the runs' order
@@ -544,6 +566,134 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const AppendQ8Args 
     fetch(from);
     write();
     from = next;
+  }
+}
+
+// 16 elements of a head, a lane's: two pieces, and their partners if they turn
+template <bool TURNS>
+struct Strip {
+  uint4 x[2], o[TURNS ? 2 : 1];
+};
+template <bool TURNS>
+__device__ __forceinline__ void load_strip(const Turns& r, const uint16_t* head, int lane, Strip<TURNS>& t) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) t.x[u] = reinterpret_cast<const uint4*>(head)[2 * lane + u];
+  if constexpr (TURNS) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)  // (mostly in L1 by then)
+      t.o[u] = r.inter ? t.x[u] : reinterpret_cast<const uint4*>(head)[partner_of(r, 2 * lane + u)];
+  }
+}
+// piece u of a strip as binary32, turned
+template <bool F16, bool TURNS>
+__device__ __forceinline__ void strip_values(const Turns& r, const Strip<TURNS>& t, int u, int lane, const float* c,
+                                             const float* s, float (&y)[8]) {
+  piece_to_f32<F16>(t.x[u], y);
+  if constexpr (TURNS) {
+    if (8 * (2 * lane + u) >= r.rot) return;
+    float o[8];
+    piece_to_f32<F16>(t.o[u], o);
+    turn_piece(r, 2 * lane + u, o, c, s, y);
+  }
+}
+__device__ __forceinline__ float largest(const float (&y)[8]) {  // leaves NaN out
+  return fmaxf(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))),
+               fmaxf(fmaxf(fabsf(y[4]), fabsf(y[5])), fmaxf(fabsf(y[6]), fabsf(y[7]))));
+}
+// the codes of a piece, times inv
+__device__ __forceinline__ uint2 codes_of(float (&y)[8], float inv) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) y[q] *= inv;
+  return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+}
+// Blocks of one token: each row a scale of its own, nothing is rounded again. A CTA takes `rows`
+// rows, a lane a piece of 8 elements at a time, of K and of V.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kQ8Threads, 3) k_kv_append_q8_tokens(const __grid_constant__ AppendQ8Args a) {
+  constexpr int LPR = D / 16;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int32_t s_slot[kQ8Threads];
+  __shared__ int32_t s_found;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0) {
+    judge_slots(a.slots, a.n, a.n_slots, a.status);
+    return;
+  }
+  const int r0 = (blockIdx.x - 1) * a.rows, rows = min(a.rows, a.n - r0);
+  const int pairs = a.t.rot / 2, pmask = (1 << a.p_shift) - 1;
+  float* const s_cos = reinterpret_cast<float*>(smem);
+  float* const s_sin = s_cos + a.rows * pairs;
+  const int mine = tid < rows ? slot_of(a, r0 + tid) : -1;
+  s_slot[tid] = mine;
+  if (a.t.turns) make_turns(a.t, r0, rows, 1, s_cos, s_sin);
+  // of neighbours with one slot the last counts
+  const int last = __syncthreads_or(mine >= 0 && slot_of(a, r0 + tid + 1) != mine + 1);
+  if (last) {
+    int next = -1;
+    for (int q = tid + 1; q < rows && next < 0; ++q) next = s_slot[q];
+    const bool ends = mine >= 0 && next < 0;
+    if (__syncthreads_or(ends)) {
+      int at = r0 + rows;
+      if (slot_of(a, at) < 0) at = next_row(a, at, &s_found);
+      if (ends) next = slot_of(a, at);
+      if (mine >= 0 && next == mine) s_slot[tid] = -1;
+      __syncthreads();
+    }
+  }
+  const int per_row = a.heads * LPR, total = rows * per_row;
+  const int lane = tid % LPR;
+  const Quotient by_row(min(per_row, 4096));
+  // one row's one head: its maximum, its scale, its codes
+  auto store = [&](auto turned, const uint16_t* in, uint8_t* codes, float* scales, int row, int head, int slot) {
+    constexpr bool TURNS = decltype(turned)::value;
+    const int64_t page = max(slot, 0) >> a.p_shift, t = max(slot, 0) & pmask;
+    float y[2][8] = {};
+    if (slot >= 0) {
+      Strip<TURNS> x;
+      load_strip(a.t, in + (r0 + row) * a.row + head * a.head, lane, x);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        strip_values<F16>(a.t, x, u, lane, s_cos + row * pairs, s_sin + row * pairs, y[u]);
+    }
+    float m = fmaxf(largest(y[0]), largest(y[1]));
+    const bool odd = m == INFINITY;
+    if (odd) {
+      m = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (fabsf(y[u][q]) < INFINITY) m = fmaxf(m, fabsf(y[u][q]));
+    }
+    m = fmaxf(m, 0.f);  // (NaN alone)
+#pragma unroll
+    for (int o = LPR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float s = scale_for(__float_as_uint(m));
+    if (slot < 0) return;
+    if (odd) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) y[u][q] = fabsf(y[u][q]) < INFINITY ? y[u][q] : NAN;
+    }
+    const float inv = inverse_of(s);  // (below 2^127, as no finite element is larger)
+    const uint2 c0 = codes_of(y[0], inv), c1 = codes_of(y[1], inv);
+    *reinterpret_cast<uint4*>(codes + page * a.page + t * a.token + head * a.chead + 16 * lane) =
+        make_uint4(c0.x, c0.y, c1.x, c1.y);
+    if (lane == 0) scales[page * a.spage + t * a.sblock + head * a.shead] = s;
+  };
+#pragma unroll 1
+  for (int base = 0; base < total; base += kQ8Threads) {
+    const int i = min(base + tid, total - 1), row = rows == 1 ? 0 : by_row.of(i);
+    const int head = (i - row * per_row) / LPR;
+    const int slot = base + tid < total ? s_slot[row] : -1;
+    store(std::false_type(), a.v, a.vc, a.vs, row, head, slot);
+    if (a.t.turns)
+      store(std::true_type(), a.k, a.kc, a.ks, row, head, slot);
+    else
+      store(std::false_type(), a.k, a.kc, a.ks, row, head, slot);
   }
 }
 
@@ -675,6 +825,14 @@ cudaError_t append_launch(const AppendQ8Args& a, dim3 grid, size_t smem, cudaStr
   return rc != cudaSuccess ? rc : launch_pdl(k_kv_append_q8<D, F16>, grid, kQ8Threads, smem, st, a);
 }
 
+template <int D, bool F16>
+cudaError_t tokens_launch(const AppendQ8Args& a, unsigned grid, size_t smem, cudaStream_t st) {
+  static bool ready[128];
+  const cudaError_t rc = allow_smem(k_kv_append_q8_tokens<D, F16>, kSmemMost, ready, g_q8_mutex);
+  return rc != cudaSuccess ? rc
+                           : launch_pdl(k_kv_append_q8_tokens<D, F16>, grid, kQ8Threads, smem, st, a);
+}
+
 }  // namespace
 }  // namespace dspark
 
@@ -745,11 +903,23 @@ extern "C" int dspark_kv_append_q8(
     a.t = Turns{rotation->turns, positions, rotation->gain, rotation->rot_dim,
                 rotation->pairs == DSPARK_ROTARY_INTERLEAVED};
   a.d_shift = D == 64 ? 3 : 4;
+  const int pairs = rotation ? rotation->rot_dim / 2 : 0;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool f16 = dtype == DSPARK_F16;
+  if (block == 1) {
+    a.rows = std::clamp(1024 / (Hkv * (D / 16)), 1, kQ8Threads);
+    const unsigned grid = 1u + static_cast<unsigned>(DSPARK_CEILDIV(n, a.rows));
+    const size_t smem = static_cast<size_t>(a.rows) * pairs * 8;
+    const cudaError_t rc = D == 64 ? (f16 ? tokens_launch<64, true>(a, grid, smem, st)
+                                          : tokens_launch<64, false>(a, grid, smem, st))
+                                   : (f16 ? tokens_launch<128, true>(a, grid, smem, st)
+                                          : tokens_launch<128, false>(a, grid, smem, st));
+    return rc == cudaSuccess && cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  }
   // The window: twice a block's rows, so that every second row's run begins in it, as far as
   // shared memory goes (rows, sizes and scales, cosines and sines); heads are left to other CTAs
   // for more rows.
   int cap = std::min(std::max(2 * block, 16), kMaxWindow);
-  const int pairs = rotation ? rotation->rot_dim / 2 : 0;
   while (cap > 16 && cap * pairs * 8 > 64 * 1024) cap /= 2;
   a.slice = std::clamp((kAppendPieces8 >> a.d_shift) / cap, 1, Hkv);
   // few heads: more rows
@@ -762,8 +932,6 @@ extern "C" int dspark_kv_append_q8(
   const dim3 grid(1u + static_cast<unsigned>(DSPARK_CEILDIV(n, a.chunk)), 2u * a.slices);
   const size_t smem = static_cast<size_t>(cap) * (a.slice << a.d_shift) * 16 +
                       static_cast<size_t>(cap) * a.slice * 8 + static_cast<size_t>(cap) * pairs * 8;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool f16 = dtype == DSPARK_F16;
   const cudaError_t rc = D == 64 ? (f16 ? append_launch<64, true>(a, grid, smem, st)
                                         : append_launch<64, false>(a, grid, smem, st))
                                  : (f16 ? append_launch<128, true>(a, grid, smem, st)

@@ -314,3 +314,24 @@ def test_no_rows(dev):
     assert torch.equal(kc.view(torch.uint8), before)
     assert paged_q8.dspark_kv_gather_q8(kc, vc, ks, vs, none, check=True)["k"].shape == (0, 1, 64)
     assert paged_q8.dspark_rotary(k, none, t)["out"].shape == (0, 1, 64)
+
+
+@pytest.mark.parametrize("page,block", [(32, 1), (32, 16), (512, 512)])
+def test_append_of_rows_with_one_slot_leaves_the_last(dev, page, block):
+    """All rows of a block are as large, so the scale is the same whichever rows count."""
+    g = torch.Generator().manual_seed(11)
+    n = 2 * block + 600 if block > 256 else 300
+    k, v = ((torch.randint(1, 8, (n, 3, 64), generator=g) / 4).to(torch.float16) for _ in range(2))
+    k[..., 0] = v[..., 0] = 7.0
+    slots = (torch.arange(n) // 3 * 2).to(torch.int32)
+    slots[torch.randperm(n, generator=g)[:n // 5]] = -1
+    slots[200:240] = -1
+    pages = int(slots.max()) // page + 1
+    cache = make_cache(pages, page, 3, 64, block, 5, dev)
+    last = {int(x): i for i, x in enumerate(slots.tolist()) if x >= 0}
+    out = paged_q8.dspark_kv_append_q8(k.to(dev), v.to(dev), slots.to(dev), *cache)
+    assert int(out["device_status"]) == 0
+    rows = torch.tensor(list(last.values()))
+    got = paged_q8.dspark_kv_gather_q8(*cache, torch.tensor(list(last), dtype=torch.int32, device=dev),
+                                       dtype=torch.float16)
+    assert torch.equal(got["k"].cpu(), k[rows]) and torch.equal(got["v"].cpu(), v[rows])
