@@ -7,28 +7,47 @@ takes back the pages that only rejected tokens used.
 
 No call waits for the host and every shape is fixed by the batch, so a step can
 be captured in a CUDA graph and replayed. `ToyTarget` stands for the target: one
-attention layer with random weights.
+attention layer with random weights. The cache may hold 16-bit elements or 8-bit
+codes with a scale per block of tokens (dspark_kv_append_q8,
+dspark_paged_attention_q8), and turn queries and keys by their positions
+(dspark_rotary).
 
-    python -m speculative_decoding_verification_41_gb300.paged_step
+    python -m speculative_decoding_verification_41_gb300.paged_step [--8bit]
 """
 from __future__ import annotations
 
+import sys
+from typing import Optional
+
 import torch
 
-from . import binding, paged
+from . import binding, paged, paged_q8
 
 
 class PagedCache:
     """Keys and values of B requests in pages, and the books about them. The lengths
-    and the free pages are updated in place."""
+    and the free pages are updated in place.
+
+    block > 0: 8-bit codes with a scale per `block` tokens and head (a power of two that divides
+    page_size; 16-bit tensors come in and out all the same). rotary: queries and keys are turned
+    by their positions, which `append` and `attend` know."""
 
     def __init__(self, B: int, num_pages: int, page_size: int, max_pages: int, Hkv: int, D: int,
-                 max_new: int, dtype=torch.bfloat16, device="cuda"):
+                 max_new: int, dtype=torch.bfloat16, device="cuda", *, block: int = 0,
+                 rotary: Optional[paged_q8.RotaryTable] = None):
         dev = torch.device(device)
         i32 = dict(dtype=torch.int32, device=dev)
+        if block < 0 or (block and (block & (block - 1) or page_size % block)):
+            raise ValueError(f"block must be a power of two that divides page_size {page_size} (or "
+                             f"0: 16-bit elements), got {block}")
         self.B, self.page_size, self.max_new = B, page_size, max_new
-        self.k = torch.zeros(num_pages, page_size, Hkv, D, dtype=dtype, device=dev)
+        self.rotary, self.scales = rotary, None
+        self.k = torch.zeros(num_pages, page_size, Hkv, D, device=dev,
+                             dtype=paged_q8.E4M3 if block else dtype)
         self.v = torch.zeros_like(self.k)
+        if block:
+            self.scales = tuple(torch.zeros(num_pages, page_size // block, Hkv,
+                                            dtype=torch.float32, device=dev) for _ in range(2))
         self.block_table = torch.zeros(B, max_pages, **i32)
         self.free_pages = torch.arange(num_pages, **i32)
         self.free_count = torch.full((1,), num_pages, **i32)
@@ -38,7 +57,7 @@ class PagedCache:
         self._kept = paged.ReleaseBuffers(B, dev)
         self._kept.context_len, self._kept.free_count = self.context_len, self.free_count
         self._append_status = torch.zeros(1, **i32)
-        self._attention = None
+        self._attention = self._turned = None
 
     def reserve(self, new_len: torch.Tensor, extra: int = 1) -> dict:
         """Pages for new_len[r] + extra tokens; the rows of the step (dspark_pages_reserve)."""
@@ -48,19 +67,47 @@ class PagedCache:
             buffers=self.rows)
 
     def append(self, k: torch.Tensor, v: torch.Tensor) -> None:
-        paged.dspark_kv_append(k, v, self.rows.slot_map, self.k, self.v,
+        rows = self.rows
+        if self.scales is not None:
+            paged_q8.dspark_kv_append_q8(
+                k, v, rows.slot_map, self.k, self.v, *self.scales, rotary=self.rotary,
+                positions=None if self.rotary is None else rows.positions,
+                device_status=self._append_status)
+            return
+        if self.rotary is not None:
+            k = paged_q8.dspark_rotary(k, rows.positions, self.rotary)["out"]
+        paged.dspark_kv_append(k, v, rows.slot_map, self.k, self.v,
                                device_status=self._append_status)
 
     def attend(self, q: torch.Tensor) -> torch.Tensor:
         """Attention of the step's rows. The result is a buffer that the next call for rows of this
         shape overwrites (another layer's): copy what has to outlive it."""
         n, Hq, D = q.shape
+        rows, scale = self.rows, D ** -0.5
         if self._attention is None or self._attention.out.shape != q.shape:
             self._attention = paged.AttentionBuffers(n, Hq, self.k.shape[2], D, self.max_new,
                                                      q.dtype, q.device)
+            # rows of no token stay zero
+            self._turned = None if self.rotary is None else torch.zeros_like(
+                q, memory_format=torch.contiguous_format)
+        if self.rotary is not None:
+            q = paged_q8.dspark_rotary(q, rows.positions, self.rotary, out=self._turned)["out"]
+        if self.scales is not None:
+            return paged_q8.dspark_paged_attention_q8(
+                q, self.k, self.v, *self.scales, self.block_table, rows.context_len, rows.row_off,
+                scale=scale, max_new=self.max_new, buffers=self._attention)["out"]
         return paged.dspark_paged_attention(
-            q, self.k, self.v, self.block_table, self.rows.context_len, self.rows.row_off,
-            scale=D ** -0.5, max_new=self.max_new, buffers=self._attention)["out"]
+            q, self.k, self.v, self.block_table, rows.context_len, rows.row_off, scale=scale,
+            max_new=self.max_new, buffers=self._attention)["out"]
+
+    def stored(self, slots: torch.Tensor, dtype=torch.bfloat16):
+        """Keys (turned, if the cache turns them) and values of these slots, [n, heads, D]; those of
+        an 8-bit cache as `dtype` (dspark_kv_gather_q8)."""
+        if self.scales is not None:
+            got = paged_q8.dspark_kv_gather_q8(self.k, self.v, *self.scales, slots, dtype=dtype)
+            return got["k"], got["v"]
+        page, at = slots.long() // self.page_size, slots.long() % self.page_size
+        return self.k[page, at], self.v[page, at]
 
     def release(self, kept_len: torch.Tensor, extra: int = 1) -> None:
         """Keep kept_len[r] + extra of the reserved tokens (-1: the request is finished)."""
@@ -138,14 +185,16 @@ def speculative_step(cache: PagedCache, target: ToyTarget, anchors: torch.Tensor
             "reserve_status": rows["device_status"].clone()}
 
 
-def demo(B: int = 32, gamma: int = 4, V: int = 4096, steps: int = 8, device="cuda") -> dict:
-    """A few steps with the Markov drafter, the scheduler and the toy target."""
+def demo(B: int = 32, gamma: int = 4, V: int = 4096, steps: int = 8, device="cuda", *,
+         block: int = 0, rotary: Optional[paged_q8.RotaryTable] = None) -> dict:
+    """A few steps with the Markov drafter, the scheduler and the toy target; block and rotary as
+    for PagedCache."""
     from . import workloads
     dev = torch.device(device)
     g = torch.Generator(device=dev).manual_seed(1)
     target = ToyTarget(V, 16, 4, 64, device=dev)
     cache = PagedCache(B, num_pages=B * 8, page_size=16, max_pages=16, Hkv=4, D=64,
-                       max_new=gamma + 1, device=dev)
+                       max_new=gamma + 1, device=dev, block=block, rotary=rotary)
     d = workloads.make_markov_draft(B, gamma, V, 64, temperature=1.0, seed=2, device=dev)
     profile = torch.from_numpy(
         workloads.step_time_profile(B * (gamma + 1) + 1, base_ms=1.0, slope_ms=0.002)).to(dev)
@@ -167,4 +216,7 @@ def demo(B: int = 32, gamma: int = 4, V: int = 4096, steps: int = 8, device="cud
 
 
 if __name__ == "__main__":
-    print(demo())
+    if "--8bit" in sys.argv[1:]:
+        print(demo(block=16, rotary=paged_q8.RotaryTable(64)))
+    else:
+        print(demo())
