@@ -237,6 +237,10 @@ __device__ __noinline__ int next_row(const AppendQ8Args& a, int from, int* s_fou
   return a.n;
 }
 
+__device__ __forceinline__ float largest(const float (&y)[8]) {  // leaves NaN out
+  return fmaxf(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))),
+               fmaxf(fmaxf(fabsf(y[4]), fabsf(y[5])), fmaxf(fabsf(y[6]), fabsf(y[7]))));
+}
 // a power of two s, 2^-126 <= s < 2^127: its inverse
 __device__ __forceinline__ bool has_inverse(float s) {
   return (__float_as_uint(s) & 0x7FFFFFu) == 0 && __float_as_uint(s) < 0x7F000000u;
@@ -248,6 +252,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int32_t s_slot[kMaxWindow];   // of the window's rows; -1: nothing to write
   __shared__ int16_t s_run[kMaxWindow];    // their runs
+  __shared__ int64_t s_code[kMaxWindow];   // where their codes are
   __shared__ int32_t s_first[kMaxWindow];  // a slot of each run
   __shared__ uint8_t s_fresh[kMaxWindow];  // it has its block's first token
   __shared__ int32_t s_count[kQ8Threads / 32], s_last[kQ8Threads / 32];
@@ -275,8 +280,8 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
   uint8_t* codes = (value ? a.vc : a.kc) + h0 * a.chead;  // (of this thread's piece, later)
   float* const scales = (value ? a.vs : a.ks) + h0 * a.shead;
   const int r0 = (blockIdx.x - 1) * a.chunk;
-  auto code_at = [&](int slot) {
-    return codes + (slot >> a.p_shift) * a.page + static_cast<int64_t>(slot & pmask) * a.token;
+  auto code_offset = [&](int slot) {
+    return (slot >> a.p_shift) * a.page + static_cast<int64_t>(slot & pmask) * a.token;
   };
 
   // ---- the first window: which row begins a run, the runs' numbers
@@ -324,6 +329,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
     if (j < a.cap) {
       s_slot[j] = mine ? s : -1;
       s_run[j] = static_cast<int16_t>(run);
+      s_code[j] = code_offset(max(s, 0));
     }
     if (mine && begins) s_first[run] = s, s_fresh[run] = 0;
     if (tid == 0) s_odd = 0, s_lo = a.cap, s_hi = 0;
@@ -395,8 +401,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
         if constexpr (kTurned) {
           float y[8];
           piece(turned, at, y);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) top[k] = max(top[k], __float_as_uint(y[q]) & 0x7FFFFFFFu);
+          top[k] = __float_as_uint(fmaxf(largest(y), 0.f));  // (leaves NaN out)
         } else {
           const uint4 v = data[at * per_row + w0];
           const uint32_t t2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
@@ -440,6 +445,15 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
         const int at = min(r + k * ws, a.cap - 1), slot = s_slot[at];
         if (r + k * ws >= s_hi || slot < 0) continue;
         const float s = s_scale[s_run[at] * heads + head];
+        if (F16 && !decltype(turned)::value && !odd && has_inverse(s) && s >= 0x1p-15f && s <= 0x1p14f) {
+          // exact in half precision, but for what is so small that its code is 0
+          const uint32_t inv = f32_to_word<true>(inverse_of(s), inverse_of(s));
+          const uint4 v = data[at * per_row + w0];
+          *reinterpret_cast<uint2*>(codes + s_code[at]) = make_uint2(
+              f16x2_to_e4m3x2(mul_f16x2(v.x, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.y, inv)) << 16),
+              f16x2_to_e4m3x2(mul_f16x2(v.z, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.w, inv)) << 16));
+          continue;
+        }
         float y[8];
         piece(turned, at, y);
         if (odd) {
@@ -454,7 +468,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
 #pragma unroll
           for (int q = 0; q < 8; ++q) y[q] = __fdiv_rn(y[q], s);
         }
-        *reinterpret_cast<uint2*>(code_at(slot)) =
+        *reinterpret_cast<uint2*>(codes + s_code[at]) =
             make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
       }
     }
@@ -484,6 +498,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
     for (int w = 0; w < kQ8Threads / 32; ++w) ends |= s_count[w] != 32;
     if (tid < a.cap) {
       s_slot[tid] = mine ? s : -1;
+      s_code[tid] = code_offset(max(s, 0));
       s_run[tid] = static_cast<int16_t>(runs - 1);
     }
     if (mine && (s & bmask) == 0) s_fresh[runs - 1] = 1;
@@ -532,7 +547,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
       const int block0 = s_first[run] & ~bmask;
 #pragma unroll 4
       for (int t = rp; t <= bmask; t += step) {
-        uint2* const p = reinterpret_cast<uint2*>(code_at(block0 + t));
+        uint2* const p = reinterpret_cast<uint2*>(codes + code_offset(block0 + t));
         const uint2 c = *p;
         const float2 c0 = e4m3x2_to_f32(c.x), c1 = e4m3x2_to_f32(c.x >> 16);
         const float2 c2 = e4m3x2_to_f32(c.y), c3 = e4m3x2_to_f32(c.y >> 16);
@@ -553,6 +568,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
       for (int q = 0; q < runs && run < 0; ++q)
         if (s >= 0 && (s_first[q] >> a.b_shift) == (s >> a.b_shift)) run = q;
       s_slot[tid] = run >= 0 ? s : -1;
+      s_code[tid] = code_offset(max(s, 0));
       s_run[tid] = static_cast<int16_t>(run);
     }
     if (tid == 0) s_lo = 0, s_hi = a.cap;
@@ -595,10 +611,6 @@ __device__ __forceinline__ void strip_values(const Turns& r, const Strip<TURNS>&
     piece_to_f32<F16>(t.o[u], o);
     turn_piece(r, 2 * lane + u, o, c, s, y);
   }
-}
-__device__ __forceinline__ float largest(const float (&y)[8]) {  // leaves NaN out
-  return fmaxf(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))),
-               fmaxf(fmaxf(fabsf(y[4]), fabsf(y[5])), fmaxf(fabsf(y[6]), fabsf(y[7]))));
 }
 // the codes of a piece, times inv
 __device__ __forceinline__ uint2 codes_of(float (&y)[8], float inv) {
