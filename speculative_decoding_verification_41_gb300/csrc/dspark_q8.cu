@@ -164,13 +164,17 @@ __global__ void __launch_bounds__(kQ8Threads) k_rotary(const RotaryArgs a) {
 // dspark_kv_append_q8
 // ---------------------------------------------------------------------------
 // A run is the neighbouring rows of slot_map that one block takes (skipped rows do not
-// count). A CTA takes some heads
-// of K or of V and the runs that begin among `chunk` rows; its window of `cap` rows holds
-// them whole (cap >= chunk + block - 1, or the last run's rest comes in windows of its own).
-// The window's rows lie in shared memory, so they are fetched once: (1) sizes of runs, a
-// maximum per run and head; (2) a scale each, and the blocks whose scale rises rounded
-// again; (3) the codes. CTA (0, 0, 0) only judges the slots, so that one CTA writes the
-// status. Blocks of one token have a kernel of their own, without runs.
+// count). A CTA has the runs that begin among `chunk` rows; its window of `cap` rows holds them
+// whole (cap >= chunk + block - 1, or the last run's rest comes in windows of its own). It takes
+// some heads of K or of V at a time, whose rows lie in shared memory, so they are fetched once:
+// (1) sizes of runs, a maximum per run and head; (2) a scale each, and the blocks whose scale
+// rises rounded again; (3) the codes. CTA (0, 0) only judges the slots, so that one CTA writes
+// the status. Blocks of one token have a kernel of their own, without runs.
+//
+// Bound by instructions, not by bytes: 100,000 rows of 8 heads (615 MB) 195 us, 46% of the copy
+// rate; 2,300 rows in 256 runs 15.5 us, a chain of launch, slots, rows, maxima and codes.
+// Measured and left: a warp per run and head with its rows in registers (337 us) or read twice
+// (207), tiles by bulk copies with a barrier for each (230).
 constexpr int kAppendPieces8 = 4096;  // of a window, at most (64 KB)
 constexpr int kMaxWindow = 256;       // rows
 
@@ -264,22 +268,15 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
     if (blockIdx.y == 0) judge_slots(a.slots, a.n, a.n_slots, a.status);
     return;
   }
-  const bool value = blockIdx.y >= static_cast<uint32_t>(a.slices);
-  const bool turns = a.t.turns != nullptr && !value;
-  const int h0 = (blockIdx.y - (value ? a.slices : 0)) * a.slice, heads = min(a.slice, a.heads - h0);
   const int bmask = (1 << a.b_shift) - 1, pmask = (1 << a.p_shift) - 1;
   constexpr int LPR = D / 8, dmask = LPR - 1;  // pieces of a head
-  const int pairs = a.t.rot / 2, per_row = heads * LPR;
-  const Quotient by_row(per_row);
+  const int pairs = a.t.rot / 2;
   uint4* const data = reinterpret_cast<uint4*>(smem);
   uint32_t* const s_size = reinterpret_cast<uint32_t*>(data + a.cap * (a.slice << a.d_shift));
   float* const s_scale = reinterpret_cast<float*>(s_size + a.cap * a.slice);
   float* const s_cos = s_scale + a.cap * a.slice;
   float* const s_sin = s_cos + a.cap * pairs;
-  const uint16_t* in = (value ? a.v : a.k) + h0 * a.head;
-  uint8_t* codes = (value ? a.vc : a.kc) + h0 * a.chead;  // (of this thread's piece, later)
-  float* const scales = (value ? a.vs : a.ks) + h0 * a.shead;
-  const int r0 = (blockIdx.x - 1) * a.chunk;
+  const int r0 = (blockIdx.x - 1) * a.chunk, y0 = blockIdx.y;
   auto code_offset = [&](int slot) {
     return (slot >> a.p_shift) * a.page + static_cast<int64_t>(slot & pmask) * a.token;
   };
@@ -339,7 +336,6 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
       atomicMin(&s_lo, 32 * warp + __ffs(all) - 1);
       atomicMax(&s_hi, 32 * warp + 32 - __clz(all));
     }
-    for (int i = tid; i < a.cap * a.slice; i += kQ8Threads) s_size[i] = 0;
     __syncthreads();
     if (mine && (s & bmask) == 0) s_fresh[run] = 1;
     if (ends) runs |= 1 << 30;  // no run goes on past the window
@@ -353,235 +349,256 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
   const int rest = runs >> 30 ? a.n : goes_on(r0 + a.cap);
   runs &= 0xFFFF;
 
-  // A thread has one piece of a head, the same in every row it takes.
-  const int rp = by_row.of(tid), w0 = tid - rp * per_row, lane = w0 & dmask, head = w0 / LPR;
-  const int step = kQ8Threads / per_row;  // rows side by side
-  const uint32_t group = ((1u << LPR) - 1u) << (wl & ~dmask);
-  const int first_row = rp < step ? rp : kMaxWindow;
-  in += head * a.head + 8 * lane;
-  codes += head * a.chead + 8 * lane;
-  auto fetch = [&](int from) {  // the window's rows that are this CTA's
-#pragma unroll 4
-    for (int r = first_row + s_lo; r < s_hi; r += step)
-      if (s_slot[r] >= 0) cp_async16(data + r * per_row + w0, in + (from + r) * a.row);
-    cp_async_commit();
-    if (turns) make_turns(a.t, from, min(a.cap, a.n - from), 1, s_cos, s_sin);
-    cp_async_wait<0>();
-    __syncthreads();
-  };
-  auto piece = [&](auto turned, int r, float (&y)[8]) {
-    const uint4* const h = data + r * per_row + (w0 - lane);
-    if constexpr (decltype(turned)::value)
-      turned_piece<F16>(a.t, h, lane, s_cos + r * pairs, s_sin + r * pairs, y);
-    else
-      piece_to_f32<F16>(h[lane], y);
-  };
-  // Both passes take several rows at once: a window's time is that of a thread's chain of
-  // loads and arithmetic, of which three CTAs on an SM hide little.
-  auto sizes_of = [&](auto turned) {
-    constexpr bool kTurned = decltype(turned)::value;
-    constexpr int kRows = kTurned ? 2 : 4;
-    uint32_t m = 0;  // bits of the largest finite magnitude in this run so far
-    int cur = -1;
-    auto flush = [&]() {
-      if (cur < 0) return;
-#pragma unroll
-      for (int o = LPR / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(group, m, o));
-      if (lane == 0) atomicMax(&s_size[cur * heads + head], m);
-    };
+  // ---- some heads of K or of V after the other, those of K first
 #pragma unroll 1
-    for (int r = first_row + s_lo; r < s_hi; r += kRows * step) {
-      int run[kRows];
-      uint32_t top[kRows];
+  for (int y = y0; y < 2 * a.slices; y += gridDim.y) {
+    const bool value = y >= a.slices;
+    const bool turns = a.t.turns != nullptr && !value;
+    const int h0 = (y - (value ? a.slices : 0)) * a.slice, heads = min(a.slice, a.heads - h0);
+    const int per_row = heads * LPR;
+    const Quotient by_row(per_row);
+    // A thread has one piece of a head, the same in every row it takes.
+    const int rp = by_row.of(tid), w0 = tid - rp * per_row, lane = w0 & dmask, head = w0 / LPR;
+    const int step = kQ8Threads / per_row;  // rows side by side
+    const uint32_t group = ((1u << LPR) - 1u) << (wl & ~dmask);
+    const int first_row = rp < step ? rp : kMaxWindow;
+    const uint16_t* const in = (value ? a.v : a.k) + (h0 + head) * a.head + 8 * lane;
+    uint8_t* const codes = (value ? a.vc : a.kc) + (h0 + head) * a.chead + 8 * lane;
+    float* const scales = (value ? a.vs : a.ks) + h0 * a.shead;
+    auto fetch = [&](int from) {  // the window's rows that are this CTA's
+#pragma unroll 4
+      for (int r = first_row + s_lo; r < s_hi; r += step)
+        if (s_slot[r] >= 0) cp_async16(data + r * per_row + w0, in + (from + r) * a.row);
+      cp_async_commit();
+      if (turns && (y == y0 || rest < a.n)) make_turns(a.t, from, min(a.cap, a.n - from), 1, s_cos, s_sin);
+      cp_async_wait<0>();
+      __syncthreads();
+    };
+    auto piece = [&](auto turned, int r, float (&y)[8]) {
+      const uint4* const h = data + r * per_row + (w0 - lane);
+      if constexpr (decltype(turned)::value)
+        turned_piece<F16>(a.t, h, lane, s_cos + r * pairs, s_sin + r * pairs, y);
+      else
+        piece_to_f32<F16>(h[lane], y);
+    };
+    // Both passes take several rows at once: a window's time is that of a thread's chain of
+    // loads and arithmetic, of which three CTAs on an SM hide little.
+    auto sizes_of = [&](auto turned) {
+      constexpr bool kTurned = decltype(turned)::value;
+      constexpr int kRows = kTurned ? 2 : 4;
+      uint32_t m = 0;  // bits of the largest finite magnitude in this run so far
+      int cur = -1;
+      auto flush = [&]() {
+        if (cur < 0) return;
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const int at = min(r + k * step, a.cap - 1);
-        run[k] = r + k * step < s_hi && s_slot[at] >= 0 ? s_run[at] : -1;
-        top[k] = 0;
-        if constexpr (kTurned) {
-          float y[8];
-          piece(turned, at, y);
-          top[k] = __float_as_uint(fmaxf(largest(y), 0.f));  // (leaves NaN out)
-        } else {
-          const uint4 v = data[at * per_row + w0];
-          const uint32_t t2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-          top[k] = __float_as_uint(word_to_f32<F16>(max(t2 & 0xFFFFu, t2 >> 16)).x);
-        }
-      }
+        for (int o = LPR / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(group, m, o));
+        if (lane == 0) atomicMax(&s_size[cur * heads + head], m);
+      };
+#pragma unroll 1
+      for (int r = first_row + s_lo; r < s_hi; r += kRows * step) {
+        int run[kRows];
+        uint32_t top[kRows];
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        if (run[k] < 0) continue;
-        if (top[k] >= 0x7F800000u) {  // what is not finite does not count
-          s_odd = 1;
-          float y[8];
-          piece(turned, r + k * step, y);
+        for (int k = 0; k < kRows; ++k) {
+          const int at = min(r + k * step, a.cap - 1);
+          run[k] = r + k * step < s_hi && s_slot[at] >= 0 ? s_run[at] : -1;
           top[k] = 0;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t bits = __float_as_uint(y[q]) & 0x7FFFFFFFu;
-            top[k] = max(top[k], bits < 0x7F800000u ? bits : 0u);
+          if constexpr (kTurned) {
+            float y[8];
+            piece(turned, at, y);
+            top[k] = __float_as_uint(fmaxf(largest(y), 0.f));  // (leaves NaN out)
+          } else {
+            const uint4 v = data[at * per_row + w0];
+            const uint32_t t2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+            top[k] = __float_as_uint(word_to_f32<F16>(max(t2 & 0xFFFFu, t2 >> 16)).x);
           }
         }
-        if (run[k] != cur) {
-          flush();
-          cur = run[k];
-          m = 0;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          if (run[k] < 0) continue;
+          if (top[k] >= 0x7F800000u) {  // what is not finite does not count
+            s_odd = 1;
+            float y[8];
+            piece(turned, r + k * step, y);
+            top[k] = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const uint32_t bits = __float_as_uint(y[q]) & 0x7FFFFFFFu;
+              top[k] = max(top[k], bits < 0x7F800000u ? bits : 0u);
+            }
+          }
+          if (run[k] != cur) {
+            flush();
+            cur = run[k];
+            m = 0;
+          }
+          m = max(m, top[k]);
         }
-        m = max(m, top[k]);
       }
-    }
-    flush();
-  };
-  auto write_of = [&](auto turned) {
-    constexpr int kRows = decltype(turned)::value ? 2 : 4;
-    const bool odd = s_odd != 0;
-    // Of rows with one slot the last is left: then each thread stores its piece of all rows.
-    const int ws = s_mixed ? 1 : step, w_first = !s_mixed ? first_row : rp == 0 ? 0 : kMaxWindow;
+      flush();
+    };
+    auto write_of = [&](auto turned) {
+      constexpr int kRows = decltype(turned)::value ? 2 : 4;
+      const bool odd = s_odd != 0;
+      // Of rows with one slot the last is left: then each thread stores its piece of all rows.
+      const int ws = s_mixed ? 1 : step, w_first = !s_mixed ? first_row : rp == 0 ? 0 : kMaxWindow;
 #pragma unroll 1
-    for (int r = w_first + s_lo; r < s_hi; r += kRows * ws) {
+      for (int r = w_first + s_lo; r < s_hi; r += kRows * ws) {
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const int at = min(r + k * ws, a.cap - 1), slot = s_slot[at];
-        if (r + k * ws >= s_hi || slot < 0) continue;
-        const float s = s_scale[s_run[at] * heads + head];
-        if (F16 && !decltype(turned)::value && !odd && has_inverse(s) && s >= 0x1p-15f && s <= 0x1p14f) {
-          // exact in half precision, but for what is so small that its code is 0
-          const uint32_t inv = f32_to_word<true>(inverse_of(s), inverse_of(s));
-          const uint4 v = data[at * per_row + w0];
-          *reinterpret_cast<uint2*>(codes + s_code[at]) = make_uint2(
-              f16x2_to_e4m3x2(mul_f16x2(v.x, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.y, inv)) << 16),
-              f16x2_to_e4m3x2(mul_f16x2(v.z, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.w, inv)) << 16));
-          continue;
+        for (int k = 0; k < kRows; ++k) {
+          const int at = min(r + k * ws, a.cap - 1), slot = s_slot[at];
+          if (r + k * ws >= s_hi || slot < 0) continue;
+          const float s = s_scale[s_run[at] * heads + head];
+          if (F16 && !decltype(turned)::value && !odd && has_inverse(s) && s >= 0x1p-15f && s <= 0x1p14f) {
+            // exact in half precision, but for what is so small that its code is 0
+            const uint32_t inv = f32_to_word<true>(inverse_of(s), inverse_of(s));
+            const uint4 v = data[at * per_row + w0];
+            *reinterpret_cast<uint2*>(codes + s_code[at]) = make_uint2(
+                f16x2_to_e4m3x2(mul_f16x2(v.x, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.y, inv)) << 16),
+                f16x2_to_e4m3x2(mul_f16x2(v.z, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.w, inv)) << 16));
+            continue;
+          }
+          float y[8];
+          piece(turned, at, y);
+          if (odd) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] = fabsf(y[q]) < INFINITY ? y[q] : NAN;
+          }
+          if (has_inverse(s)) {
+            const float inv = inverse_of(s);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] *= inv;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] = __fdiv_rn(y[q], s);
+          }
+          *reinterpret_cast<uint2*>(codes + s_code[at]) =
+              make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
         }
-        float y[8];
-        piece(turned, at, y);
-        if (odd) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) y[q] = fabsf(y[q]) < INFINITY ? y[q] : NAN;
-        }
-        if (has_inverse(s)) {
-          const float inv = inverse_of(s);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) y[q] *= inv;
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) y[q] = __fdiv_rn(y[q], s);
-        }
-        *reinterpret_cast<uint2*>(codes + s_code[at]) =
-            make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
       }
-    }
-  };
-  auto sizes = [&]() {
-    if (turns)
-      sizes_of(std::true_type());
-    else
-      sizes_of(std::false_type());
-  };
-  auto write = [&]() {
-    if (turns)
-      write_of(std::true_type());
-    else
-      write_of(std::false_type());
-  };
-  // the rest of the last run: the window that begins with row `from`, which it has
-  auto next_window = [&](int from) {
-    __syncthreads();
-    const int s = tid < a.cap ? slot_of(a, from + tid) : -1;
-    const uint32_t other = __ballot_sync(0xFFFFFFFFu, s >= 0 && (s >> a.b_shift) != block);
-    if (wl == 0) s_count[warp] = other ? __ffs(other) - 1 : 32;
-    __syncthreads();
-    bool mine = s >= 0 && wl < s_count[warp];
-    for (int w = 0; w < warp; ++w) mine = mine && s_count[w] == 32;
-    bool ends = false;
-    for (int w = 0; w < kQ8Threads / 32; ++w) ends |= s_count[w] != 32;
-    if (tid < a.cap) {
-      s_slot[tid] = mine ? s : -1;
-      s_code[tid] = code_offset(max(s, 0));
-      s_run[tid] = static_cast<int16_t>(runs - 1);
-    }
-    if (mine && (s & bmask) == 0) s_fresh[runs - 1] = 1;
-    if (mine && s <= slot_of(a, from + tid - 1)) s_mixed = 1;
-    if (mine && slot_of(a, from + tid - 1) < 0) s_mixed = 1;
-    if (tid == 0) s_lo = 0, s_hi = a.cap;
-    __syncthreads();
-    return ends ? a.n : goes_on(from + a.cap);
-  };
-
-  // ---- (1) sizes
-  fetch(r0);
-  sizes();
-#pragma unroll 1
-  for (int from = rest; from < a.n;) {
-    const int next = next_window(from);
-    fetch(from);
-    sizes();
-    from = next;
-  }
-  __syncthreads();
-  // ---- (2) scales
-  bool rises = false;
-  for (int i = tid; i < runs * heads; i += kQ8Threads) {
-    const int run = i / heads, h = i - run * heads, slot = s_first[run];
-    float* const at = scales + (slot >> a.p_shift) * a.spage +
-                      static_cast<int64_t>((slot & pmask) >> a.b_shift) * a.sblock + h * a.shead;
-    float s = scale_for(s_size[i]);
-    const float old = s_fresh[run] ? 0.f : *at;
-    float f = 0.f;  // what the other tokens' codes are multiplied with
-    if (is_scale(old)) {
-      if (__uint_as_float(s_size[i]) <= 448.f * old)
-        s = old;
+    };
+    auto sizes = [&]() {
+      if (turns)
+        sizes_of(std::true_type());
       else
-        f = old / s, rises = true;  // 2^e > old
-    }
-    *at = s;
-    s_scale[i] = s;
-    s_size[i] = __float_as_uint(f);
-  }
-  if (__syncthreads_or(rises)) {
-#pragma unroll 1
-    for (int run = 0; run < runs; ++run) {
-      const float f = rp < step ? __uint_as_float(s_size[run * heads + head]) : 0.f;
-      if (f == 0.f) continue;
-      const int block0 = s_first[run] & ~bmask;
-#pragma unroll 4
-      for (int t = rp; t <= bmask; t += step) {
-        uint2* const p = reinterpret_cast<uint2*>(codes + code_offset(block0 + t));
-        const uint2 c = *p;
-        const float2 c0 = e4m3x2_to_f32(c.x), c1 = e4m3x2_to_f32(c.x >> 16);
-        const float2 c2 = e4m3x2_to_f32(c.y), c3 = e4m3x2_to_f32(c.y >> 16);
-        *p = make_uint2(e4m3x4(c0.x * f, c0.y * f, c1.x * f, c1.y * f),
-                        e4m3x4(c2.x * f, c2.y * f, c3.x * f, c3.y * f));
+        sizes_of(std::false_type());
+    };
+    auto write = [&]() {
+      if (turns)
+        write_of(std::true_type());
+      else
+        write_of(std::false_type());
+    };
+    // the rest of the last run: the window that begins with row `from`, which it has
+    auto next_window = [&](int from) {
+      __syncthreads();
+      const int s = tid < a.cap ? slot_of(a, from + tid) : -1;
+      const uint32_t other = __ballot_sync(0xFFFFFFFFu, s >= 0 && (s >> a.b_shift) != block);
+      if (wl == 0) s_count[warp] = other ? __ffs(other) - 1 : 32;
+      __syncthreads();
+      bool mine = s >= 0 && wl < s_count[warp];
+      for (int w = 0; w < warp; ++w) mine = mine && s_count[w] == 32;
+      bool ends = false;
+      for (int w = 0; w < kQ8Threads / 32; ++w) ends |= s_count[w] != 32;
+      if (tid < a.cap) {
+        s_slot[tid] = mine ? s : -1;
+        s_code[tid] = code_offset(max(s, 0));
+        s_run[tid] = static_cast<int16_t>(runs - 1);
       }
+      if (mine && (s & bmask) == 0) s_fresh[runs - 1] = 1;
+      if (mine && s <= slot_of(a, from + tid - 1)) s_mixed = 1;
+      if (mine && slot_of(a, from + tid - 1) < 0) s_mixed = 1;
+      if (tid == 0) s_lo = 0, s_hi = a.cap;
+      __syncthreads();
+      return ends ? a.n : goes_on(from + a.cap);
+    };
+
+    // The first window again, where a later one is.
+    auto first_window = [&]() {
+      __syncthreads();
+      const int s = tid < a.cap ? slot_of(a, r0 + tid) : -1;
+      __syncthreads();
+      if (tid < a.cap) {
+        // rows of this CTA's runs, by their blocks: neighbours, in the runs' order
+        int run = -1;
+        for (int q = 0; q < runs && run < 0; ++q)
+          if (s >= 0 && (s_first[q] >> a.b_shift) == (s >> a.b_shift)) run = q;
+        s_slot[tid] = run >= 0 ? s : -1;
+        s_code[tid] = code_offset(max(s, 0));
+        s_run[tid] = static_cast<int16_t>(run);
+      }
+      if (tid == 0) s_lo = 0, s_hi = a.cap;
+      __syncthreads();
+    };
+    // ---- (1) sizes
+    if (y != y0) {
+      if (rest < a.n)
+        first_window();
+      else
+        __syncthreads();
     }
-    __syncthreads();
-  }
-  // ---- (3) codes
-  if (rest < a.n) {
-    // the last window is there now, the first one again
-    const int s = tid < a.cap ? slot_of(a, r0 + tid) : -1;
-    __syncthreads();
-    if (tid < a.cap) {
-      // rows of this CTA's runs, by their blocks: neighbours, in the runs' order
-      int run = -1;
-      for (int q = 0; q < runs && run < 0; ++q)
-        if (s >= 0 && (s_first[q] >> a.b_shift) == (s >> a.b_shift)) run = q;
-      s_slot[tid] = run >= 0 ? s : -1;
-      s_code[tid] = code_offset(max(s, 0));
-      s_run[tid] = static_cast<int16_t>(run);
-    }
-    if (tid == 0) s_lo = 0, s_hi = a.cap;
-    __syncthreads();
+    for (int i = tid; i < runs * heads; i += kQ8Threads) s_size[i] = 0;
     fetch(r0);
-  }
-  write();
+    sizes();
 #pragma unroll 1
-  for (int from = rest; from < a.n;) {
-    const int next = next_window(from);
-    fetch(from);
+    for (int from = rest; from < a.n;) {
+      const int next = next_window(from);
+      fetch(from);
+      sizes();
+      from = next;
+    }
+    __syncthreads();
+    // ---- (2) scales
+    bool rises = false;
+    for (int i = tid; i < runs * heads; i += kQ8Threads) {
+      const int run = i / heads, h = i - run * heads, slot = s_first[run];
+      float* const at = scales + (slot >> a.p_shift) * a.spage +
+                        static_cast<int64_t>((slot & pmask) >> a.b_shift) * a.sblock + h * a.shead;
+      float s = scale_for(s_size[i]);
+      const float old = s_fresh[run] ? 0.f : *at;
+      float f = 0.f;  // what the other tokens' codes are multiplied with
+      if (is_scale(old)) {
+        if (__uint_as_float(s_size[i]) <= 448.f * old)
+          s = old;
+        else
+          f = old / s, rises = true;  // 2^e > old
+      }
+      *at = s;
+      s_scale[i] = s;
+      s_size[i] = __float_as_uint(f);
+    }
+    if (__syncthreads_or(rises)) {
+#pragma unroll 1
+      for (int run = 0; run < runs; ++run) {
+        const float f = rp < step ? __uint_as_float(s_size[run * heads + head]) : 0.f;
+        if (f == 0.f) continue;
+        const int block0 = s_first[run] & ~bmask;
+#pragma unroll 4
+        for (int t = rp; t <= bmask; t += step) {
+          uint2* const p = reinterpret_cast<uint2*>(codes + code_offset(block0 + t));
+          const uint2 c = *p;
+          const float2 c0 = e4m3x2_to_f32(c.x), c1 = e4m3x2_to_f32(c.x >> 16);
+          const float2 c2 = e4m3x2_to_f32(c.y), c3 = e4m3x2_to_f32(c.y >> 16);
+          *p = make_uint2(e4m3x4(c0.x * f, c0.y * f, c1.x * f, c1.y * f),
+                          e4m3x4(c2.x * f, c2.y * f, c3.x * f, c3.y * f));
+        }
+      }
+      __syncthreads();
+    }
+    // ---- (3) codes
+    if (rest < a.n) {
+      first_window();
+      fetch(r0);
+    }
     write();
-    from = next;
+#pragma unroll 1
+    for (int from = rest; from < a.n;) {
+      const int next = next_window(from);
+      fetch(from);
+      write();
+      from = next;
+    }
   }
 }
 
@@ -940,8 +957,14 @@ extern "C" int dspark_kv_append_q8(
     cap *= 2;
   a.cap = cap;
   a.chunk = std::max(cap / 2, cap - block + 1);
+  const int64_t windows = static_cast<int64_t>(DSPARK_CEILDIV(n, a.chunk));
+  // Where that is not three CTAs per SM, fewer heads for each (2,300 rows of 8 heads: 17.7 -> 15.5
+  // us); where it is many more, a CTA has several slices, so that it looks for the runs once
+  // (100,000 rows: 219 us with a slice each, 195 with half of them, 212 with all).
+  while (a.slice > 1 && windows * 2 * DSPARK_CEILDIV(Hkv, a.slice) < 450) a.slice = (a.slice + 1) / 2;
   a.slices = static_cast<int32_t>(DSPARK_CEILDIV(Hkv, a.slice));
-  const dim3 grid(1u + static_cast<unsigned>(DSPARK_CEILDIV(n, a.chunk)), 2u * a.slices);
+  const int64_t ys = std::clamp<int64_t>(3600 / std::max<int64_t>(windows, 1), 1, std::min(2 * a.slices, 65535));
+  const dim3 grid(1u + static_cast<unsigned>(windows), static_cast<unsigned>(ys));
   const size_t smem = static_cast<size_t>(cap) * (a.slice << a.d_shift) * 16 +
                       static_cast<size_t>(cap) * a.slice * 8 + static_cast<size_t>(cap) * pairs * 8;
   const cudaError_t rc = D == 64 ? (f16 ? append_launch<64, true>(a, grid, smem, st)
