@@ -17,7 +17,8 @@ bool q8_map(CUtensorMap* map, const void* base, int D, const cuuint64_t* dims,
   return g_attn_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
                        strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                       // no fetch past a row (24 heads of 64, no window: 300 -> 220 to 284 us)
+                       D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -38,17 +39,17 @@ int q8_launch(LaunchQ8& c, int sms) {
     std::lock_guard<std::mutex> lock(g_attn_mutex);
     if (!ready[dev]) {
       if (cudaFuncSetAttribute(k_attention_q8<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kSmemCta<1>) != cudaSuccess)
+                               kSmemCta<S::CTAS>) != cudaSuccess)
         return DSPARK_ERR_CUDA;
       ready[dev] = true;
     }
   }
   AttnQ8Args& a = c.a;
-  a.ctas = std::max(1, std::min(sms, DSPARK_PAGED_MAX_CTAS) / a.n_chunks);
+  a.ctas = std::max(1, std::min(S::CTAS * sms, DSPARK_PAGED_MAX_CTAS) / a.n_chunks);
   const int grid = a.ctas * a.n_chunks;
   // Shared memory: what the queries, the weights and the scales leave is the rings'. A
   // second tile of queries where it costs them no tile.
-  constexpr uint32_t kSmem = kSmemCta<1>;
+  constexpr uint32_t kSmem = kSmemCta<S::CTAS>;
   const uint32_t q_bytes = static_cast<uint32_t>(S::QP * S::D * a.n_cols);
   a.part_bytes = static_cast<uint32_t>(a.n_cols / 16 * 2048);
   a.p_bytes = S::PP * a.part_bytes;
@@ -99,7 +100,10 @@ constexpr int kMaxRows = 72;
 // The smallest row block that holds the rows; keys are copied once for all of them.
 template <int D, bool F16>
 int q8_shape(LaunchQ8& c, int sms) {
-  if (c.a.n_cols <= 16) return q8_launch<AttnQ8Shape<D, F16, 16, 1, false, 2>>(c, sms);
+  // Two CTAs per SM for up to 16 rows of 64 elements (one buffer of weights each): 45 requests in
+  // a window of 1,023 84 -> 71 us. Of 128 elements two CTAs have two tiles
+  // each in flight, which is not enough: 64 single tokens 95 -> 104.
+  if (c.a.n_cols <= 16) return q8_launch<AttnQ8Shape<D, F16, 16, 1, false, D == 64 ? 1 : 2, D == 64 ? 2 : 1>>(c, sms);
   if (c.a.n_cols <= 32) return q8_launch<AttnQ8Shape<D, F16, 32, 2, false, 2>>(c, sms);
   if (c.a.n_cols <= 48) return q8_launch<AttnQ8Shape<D, F16, 48, 3, false, F16 ? 1 : 2>>(c, sms);
   return q8_launch<AttnQ8Shape<D, F16, 80, 3, true, 1>>(c, sms);

@@ -3,7 +3,7 @@
 //
 // Mathematics. As dspark_attention.cuh, whose split of the work, items, references and
 // join it shares, with keys ks_u K_u and values vs_u V_u: codes K, V in e4m3 and a scale
-// each per token u (of its block and head). In tiles of 128 tokens
+// each per token u (of its block and head). In tiles of 256 tokens, two instructions' of 128,
 //   S^T = K Q^T            (128 tokens x R rows, tcgen05 kind::f8f6f4, f32)
 //   P^T = vs 2^(t - m),     t = S^T ks c_r,  l += 2^(t - m)
 //   O^T += V^T P^T          (D x R)
@@ -23,8 +23,15 @@
 // first tile, with room above, and raised when a larger one comes), so that weights keep
 // the upper end of half precision's range.
 //
-// Bound. 2 D bytes per token and key head: 11 cycles of an SM's part of HBM for D = 128.
-// The tensor cores read K once per part of Q and V once per 256 columns.
+// Bound. 2 D bytes per token and key head: 11 cycles of an SM's part of HBM for D = 128. The
+// tensor cores read K once per part of Q and V once per 256 columns, and are idle four fifths
+// of the time or more. What counts is instructions: a warp alone takes seven cycles for one,
+// thirty for one that is not in its instruction cache, so loops are rolled where they are not
+// the softmax's, and a tile is 256 tokens, because its way through barriers and copies takes
+// each warp some 1,000 cycles whatever its work. Measured: 64 single tokens over up to 8,191
+// (539 MB) 95 us, 84% of the copy rate; 3 requests of 48 rows over up to 131,071 (711 MB) 155
+// us, 67%; 256 draft blocks of 32 rows over up to 4,096 (1.1 GB) 255 us, 64%, of 68 rows 411 us,
+// 40% (there the splitting of P: some 25 instructions per weight and three products of it).
 #pragma once
 
 #include <type_traits>
@@ -216,22 +223,23 @@ constexpr float kCut = 1.f + 0.7213f / 512.f;
 // PASSES: the parts of P one after another, all but the last into one accumulator, for the
 // rows whose outputs would not fit otherwise; else side by side. PBUFS: buffers of a tile's
 // weights. There are two of a tile's scores.
-template <int D_, bool F16_, int NB_, int GROUPS_, bool PASSES_, int PBUFS_>
+template <int D_, bool F16_, int NB_, int GROUPS_, bool PASSES_, int PBUFS_, int CTAS_ = 1>
 struct AttnQ8Shape {
   static constexpr int D = D_, NB = NB_, GROUPS = GROUPS_, PBUFS = PBUFS_;
+  static constexpr int CTAS = CTAS_;  // per SM
   static constexpr bool F16 = F16_, PASSES = PASSES_;
   static constexpr int QP = F16 ? 3 : 2, PP = F16 ? 4 : 3;  // parts of Q and of P
   static constexpr int LAST = F16 ? 6 : 4;                  // scale (log2) of P's last part
   static constexpr int ACCS = PASSES ? 2 : PP;              // accumulators of the outputs
   static constexpr int THREADS = 128 + 128 * GROUPS;
-  static constexpr int NC = PASSES ? 24 : 16;               // columns of a softmax group
+  static constexpr int NC = PASSES ? 24 : NB / GROUPS;               // columns of a softmax group
   static constexpr int WIDTH = NB;  // of the control block's arrays; rows are at most NC * GROUPS
   static constexpr uint32_t kStage = kQ8Tile * D;
   static constexpr int kCols = (4 + ACCS) * NB;
   static constexpr uint32_t kColS = 0, kColO = 4 * NB;
   static constexpr uint32_t kTmem = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;  // of rows of D bytes
-  static_assert(kCols <= 512, "tensor memory");
+  static_assert(CTAS * kTmem <= 512 && kCols <= kTmem, "tensor memory");
   static_assert(NC * GROUPS <= NB, "columns");
   static_assert(NC <= 32, "a warp has a column's factor in each lane");
 };
@@ -264,7 +272,7 @@ template <class S>
 constexpr uint32_t kQ8CtlBytes = (static_cast<uint32_t>(sizeof(AttnQ8Ctl<S>)) + 1023u) & ~1023u;
 
 template <class S>
-__global__ void __launch_bounds__(S::THREADS, 1)
+__global__ void __launch_bounds__(S::THREADS, S::CTAS)
     k_attention_q8(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ AttnQ8Args a) {
   extern __shared__ __align__(1024) unsigned char smem[];
