@@ -1,6 +1,7 @@
 // dspark_q8.cu -- rotary positions, and the write of the 8-bit paged cache and its
 // reading back (sm_103a): dspark_rotary, dspark_kv_append_q8, dspark_kv_gather_q8
-// (include/dspark_q8.h). All three are bound by the bytes they move.
+// (include/dspark_q8.h). Rotary and reading are bound by the bytes they move, the write by its
+// instructions; small calls by a launch and the trips that depend on one another.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -113,7 +114,8 @@ __device__ __forceinline__ void turned_piece(const Turns& t, const uint4* head, 
 // A CTA copies some rows' heads to shared memory (asynchronously: what is in flight
 // needs no registers), makes the rows' cosines and sines meanwhile, once for all heads,
 // and turns and stores 16-byte pieces. The loops are rolled: a small call runs them once,
-// and most of its time is the first fetch of each instruction.
+// and most of its time is the first fetch of each instruction (64 rows of 40 x 128: 2.9 us;
+// 30,001 rows, 615 MB: 89 us, the copy rate; unrolled, without shared memory: 151).
 constexpr int kRotPieces = 2048;  // of a CTA, at most (32 KB), but a row at least
 
 struct RotaryArgs {
@@ -171,10 +173,10 @@ __global__ void __launch_bounds__(kQ8Threads) k_rotary(const RotaryArgs a) {
 // rises rounded again; (3) the codes. CTA (0, 0) only judges the slots, so that one CTA writes
 // the status. Blocks of one token have a kernel of their own, without runs.
 //
-// Bound by instructions, not by bytes: 100,000 rows of 8 heads (615 MB) 195 us, 46% of the copy
-// rate; 2,300 rows in 256 runs 15.5 us, a chain of launch, slots, rows, maxima and codes.
-// Measured and left: a warp per run and head with its rows in registers (337 us) or read twice
-// (207), tiles by bulk copies with a barrier for each (230).
+// Bound by instructions (176 per 32 lanes' pieces of 8), not by bytes: 100,000 rows of 8 heads
+// (615 MB) 200 us, 45% of the copy rate; 2,300 rows in 256 runs 15.5 us, a chain of launch,
+// slots, rows, maxima and codes. Measured and left: a warp per run and head with its rows in
+// registers (337 us) or read twice (207), tiles by bulk copies with a barrier for each (230).
 constexpr int kAppendPieces8 = 4096;  // of a window, at most (64 KB)
 constexpr int kMaxWindow = 256;       // rows
 
@@ -636,7 +638,8 @@ __device__ __forceinline__ uint2 codes_of(float (&y)[8], float inv) {
   return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
 }
 // Blocks of one token: each row a scale of its own, nothing is rounded again. A CTA takes `rows`
-// rows, a lane a piece of 8 elements at a time, of K and of V.
+// rows, a lane 16 elements at a time, of K and of V, which stay in registers from the maximum to
+// the codes (20,300 rows of 24 x 64, 191 MB: 46 us, 61% of the copy rate; with runs, 89).
 template <int D, bool F16>
 __global__ void __launch_bounds__(kQ8Threads, 3) k_kv_append_q8_tokens(const __grid_constant__ AppendQ8Args a) {
   constexpr int LPR = D / 16;
@@ -729,6 +732,8 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_kv_append_q8_tokens(const __g
 // ---------------------------------------------------------------------------
 // dspark_kv_gather_q8
 // ---------------------------------------------------------------------------
+// Four pieces of K and of V in flight per thread (100,000 tokens, 615 MB: 93 us, 98% of the copy
+// rate).
 constexpr int kGatherPieces = 4;
 
 struct GatherQ8Args {
@@ -960,7 +965,7 @@ extern "C" int dspark_kv_append_q8(
   const int64_t windows = static_cast<int64_t>(DSPARK_CEILDIV(n, a.chunk));
   // Where that is not three CTAs per SM, fewer heads for each (2,300 rows of 8 heads: 17.7 -> 15.5
   // us); where it is many more, a CTA has several slices, so that it looks for the runs once
-  // (100,000 rows: 219 us with a slice each, 195 with half of them, 212 with all).
+  // (100,000 rows: 219 us with a slice each, 200 with four, 212 with all eight).
   while (a.slice > 1 && windows * 2 * DSPARK_CEILDIV(Hkv, a.slice) < 450) a.slice = (a.slice + 1) / 2;
   a.slices = static_cast<int32_t>(DSPARK_CEILDIV(Hkv, a.slice));
   const int64_t ys = std::clamp<int64_t>(3600 / std::max<int64_t>(windows, 1), 1, std::min(2 * a.slices, 65535));
