@@ -174,7 +174,8 @@ def check_append(dev, k, v, slots, cache, block, table=None, pos=None, status=0)
             # 2^-20 of the row's largest element of a border; scales as above
             differ = got != num
             differ &= ~np.isnan(num)
-            step = np.maximum(2.0 ** np.floor(np.log2(np.maximum(np.abs(num), 2.0 ** -6))) / 8, 2.0 ** -9)
+            size = np.maximum(np.abs(np.nan_to_num(num)), 2.0 ** -6)  # (NaN: compared above)
+            step = np.maximum(2.0 ** np.floor(np.log2(size)) / 8, 2.0 ** -9)
             assert (np.abs(np.nan_to_num(got - num)) <= step).all()
             assert differ.mean() < 2.0 ** -10
 
