@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
               const uint32_t bits = __float_as_uint(word_to_f32<S::F16>(top[k]).x);
               const int e = max(static_cast<int>(bits >> 23) - 127, -100);
               const float f = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
-                  uint32_t h16[4];
+              uint32_t h16[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float2 x = word_to_f32<S::F16>(v[k][i]);

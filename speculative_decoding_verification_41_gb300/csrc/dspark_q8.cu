@@ -173,12 +173,13 @@ __global__ void __launch_bounds__(kQ8Threads) k_rotary(const RotaryArgs a) {
 // rises rounded again; (3) the codes. CTA (0, 0) only judges the slots, so that one CTA writes
 // the status. Blocks of one token have a kernel of their own, without runs.
 //
-// Bound by instructions (176 per 32 lanes' pieces of 8), not by bytes: 100,000 rows of 8 heads
-// (615 MB) 200 us, 45% of the copy rate; 2,300 rows in 256 runs 15.5 us, a chain of launch,
+// Bound by instructions (130 per 32 lanes' pieces of 8), not by bytes: 100,000 rows of 8 heads
+// (615 MB) 153 us, 59% of the copy rate; 2,300 rows in 256 runs 13.5 us, a chain of launch,
 // slots, rows, maxima and codes. Measured and left: a warp per run and head with its rows in
 // registers (337 us) or read twice (207), tiles by bulk copies with a barrier for each (230).
-constexpr int kAppendPieces8 = 4096;  // of a window, at most (64 KB)
+constexpr int kAppendPieces8 = 4096;  // of a window, at most (64 KB; 32 KB: 188 us, 128 KB: 268)
 constexpr int kMaxWindow = 256;       // rows
+constexpr int kAppendUnits = 2;       // pieces of a lane in a row (one: 200 us, four: 168)
 
 struct AppendQ8Args {
   const uint16_t *k, *v;
@@ -254,7 +255,7 @@ __device__ __forceinline__ bool has_inverse(float s) {
 __device__ __forceinline__ float inverse_of(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_constant__ AppendQ8Args a) {
+__global__ void __launch_bounds__(kQ8Threads, 3) k_kv_append_q8(const __grid_constant__ AppendQ8Args a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int32_t s_slot[kMaxWindow];   // of the window's rows; -1: nothing to write
   __shared__ int16_t s_run[kMaxWindow];    // their runs
@@ -271,7 +272,8 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
     return;
   }
   const int bmask = (1 << a.b_shift) - 1, pmask = (1 << a.p_shift) - 1;
-  constexpr int LPR = D / 8, dmask = LPR - 1;  // pieces of a head
+  // a head's lanes, U pieces each: l, l + LPR, ..
+  constexpr int U = kAppendUnits, LPR = D / (8 * U), dmask = LPR - 1;
   const int pairs = a.t.rot / 2;
   uint4* const data = reinterpret_cast<uint4*>(smem);
   uint32_t* const s_size = reinterpret_cast<uint32_t*>(data + a.cap * (a.slice << a.d_shift));
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
     const int h0 = (y - (value ? a.slices : 0)) * a.slice, heads = min(a.slice, a.heads - h0);
     const int per_row = heads * LPR;
     const Quotient by_row(per_row);
-    // A thread has one piece of a head, the same in every row it takes.
+    // A thread has U pieces of a head, the same in every row it takes.
     const int rp = by_row.of(tid), w0 = tid - rp * per_row, lane = w0 & dmask, head = w0 / LPR;
     const int step = kQ8Threads / per_row;  // rows side by side
     const uint32_t group = ((1u << LPR) - 1u) << (wl & ~dmask);
@@ -370,24 +372,29 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
     auto fetch = [&](int from) {  // the window's rows that are this CTA's
 #pragma unroll 4
       for (int r = first_row + s_lo; r < s_hi; r += step)
-        if (s_slot[r] >= 0) cp_async16(data + r * per_row + w0, in + (from + r) * a.row);
+        if (s_slot[r] >= 0) {
+          uint4* const to = data + U * (r * per_row + w0 - lane) + lane;
+          const uint16_t* const x = in + (from + r) * a.row;
+#pragma unroll
+          for (int u = 0; u < U; ++u) cp_async16(to + u * LPR, x + 8 * u * LPR);
+        }
       cp_async_commit();
       if (turns && (y == y0 || rest < a.n)) make_turns(a.t, from, min(a.cap, a.n - from), 1, s_cos, s_sin);
       cp_async_wait<0>();
       __syncthreads();
     };
-    auto piece = [&](auto turned, int r, float (&y)[8]) {
-      const uint4* const h = data + r * per_row + (w0 - lane);
+    auto piece = [&](auto turned, int r, int u, float (&y)[8]) {
+      const uint4* const h = data + U * (r * per_row + w0 - lane);
       if constexpr (decltype(turned)::value)
-        turned_piece<F16>(a.t, h, lane, s_cos + r * pairs, s_sin + r * pairs, y);
+        turned_piece<F16>(a.t, h, lane + u * LPR, s_cos + r * pairs, s_sin + r * pairs, y);
       else
-        piece_to_f32<F16>(h[lane], y);
+        piece_to_f32<F16>(h[lane + u * LPR], y);
     };
-    // Both passes take several rows at once: a window's time is that of a thread's chain of
-    // loads and arithmetic, of which three CTAs on an SM hide little.
+    // Both passes take two rows at once where registers allow it: a window's time is that of a
+    // thread's chain of loads and arithmetic, of which three CTAs on an SM hide little.
     auto sizes_of = [&](auto turned) {
       constexpr bool kTurned = decltype(turned)::value;
-      constexpr int kRows = kTurned ? 2 : 4;
+      constexpr int kRows = kTurned ? 1 : 2;
       uint32_t m = 0;  // bits of the largest finite magnitude in this run so far
       int cur = -1;
       auto flush = [&]() {
@@ -406,14 +413,23 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
           run[k] = r + k * step < s_hi && s_slot[at] >= 0 ? s_run[at] : -1;
           top[k] = 0;
           if constexpr (kTurned) {
-            float y[8];
-            piece(turned, at, y);
-            top[k] = __float_as_uint(fmaxf(largest(y), 0.f));  // (leaves NaN out)
+            float largest_y = 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              float y[8];
+              piece(turned, at, u, y);
+              largest_y = fmaxf(largest_y, largest(y));  // (leaves NaN out)
+            }
+            top[k] = __float_as_uint(largest_y);
           } else {
-            const uint4 v = data[at * per_row + w0];
-            const uint32_t t2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-            top[k] = __float_as_uint(word_to_f32<F16>(max(t2 & 0xFFFFu, t2 >> 16)).x);
+            uint32_t m2 = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const uint4 v = data[U * (at * per_row + w0 - lane) + lane + u * LPR];
+              m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+            }
+            top[k] = __float_as_uint(word_to_f32<F16>(max(m2 & 0xFFFFu, m2 >> 16)).x);
           }
         }
 #pragma unroll
@@ -421,13 +437,16 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
           if (run[k] < 0) continue;
           if (top[k] >= 0x7F800000u) {  // what is not finite does not count
             s_odd = 1;
-            float y[8];
-            piece(turned, r + k * step, y);
             top[k] = 0;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const uint32_t bits = __float_as_uint(y[q]) & 0x7FFFFFFFu;
-              top[k] = max(top[k], bits < 0x7F800000u ? bits : 0u);
+            for (int u = 0; u < U; ++u) {
+              float y[8];
+              piece(turned, r + k * step, u, y);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const uint32_t bits = __float_as_uint(y[q]) & 0x7FFFFFFFu;
+                top[k] = max(top[k], bits < 0x7F800000u ? bits : 0u);
+              }
             }
           }
           if (run[k] != cur) {
@@ -441,7 +460,7 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
       flush();
     };
     auto write_of = [&](auto turned) {
-      constexpr int kRows = decltype(turned)::value ? 2 : 4;
+      constexpr int kRows = decltype(turned)::value ? 1 : 2;
       const bool odd = s_odd != 0;
       // Of rows with one slot the last is left: then each thread stores its piece of all rows.
       const int ws = s_mixed ? 1 : step, w_first = !s_mixed ? first_row : rp == 0 ? 0 : kMaxWindow;
@@ -452,31 +471,38 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
           const int at = min(r + k * ws, a.cap - 1), slot = s_slot[at];
           if (r + k * ws >= s_hi || slot < 0) continue;
           const float s = s_scale[s_run[at] * heads + head];
+          uint8_t* const to = codes + s_code[at];
           if (F16 && !decltype(turned)::value && !odd && has_inverse(s) && s >= 0x1p-15f && s <= 0x1p14f) {
             // exact in half precision, but for what is so small that its code is 0
             const uint32_t inv = f32_to_word<true>(inverse_of(s), inverse_of(s));
-            const uint4 v = data[at * per_row + w0];
-            *reinterpret_cast<uint2*>(codes + s_code[at]) = make_uint2(
-                f16x2_to_e4m3x2(mul_f16x2(v.x, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.y, inv)) << 16),
-                f16x2_to_e4m3x2(mul_f16x2(v.z, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.w, inv)) << 16));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const uint4 v = data[U * (at * per_row + w0 - lane) + lane + u * LPR];
+              *reinterpret_cast<uint2*>(to + 8 * u * LPR) = make_uint2(
+                  f16x2_to_e4m3x2(mul_f16x2(v.x, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.y, inv)) << 16),
+                  f16x2_to_e4m3x2(mul_f16x2(v.z, inv)) | (f16x2_to_e4m3x2(mul_f16x2(v.w, inv)) << 16));
+            }
             continue;
           }
-          float y[8];
-          piece(turned, at, y);
-          if (odd) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] = fabsf(y[q]) < INFINITY ? y[q] : NAN;
+          for (int u = 0; u < U; ++u) {
+            float y[8];
+            piece(turned, at, u, y);
+            if (odd) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) y[q] = fabsf(y[q]) < INFINITY ? y[q] : NAN;
+            }
+            if (has_inverse(s)) {
+              const float inv = inverse_of(s);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) y[q] *= inv;
+            } else {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) y[q] = __fdiv_rn(y[q], s);
+            }
+            *reinterpret_cast<uint2*>(to + 8 * u * LPR) =
+                make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
           }
-          if (has_inverse(s)) {
-            const float inv = inverse_of(s);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] *= inv;
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] = __fdiv_rn(y[q], s);
-          }
-          *reinterpret_cast<uint2*>(codes + s_code[at]) =
-              make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
         }
       }
     };
@@ -578,12 +604,15 @@ __global__ void __launch_bounds__(kQ8Threads) k_kv_append_q8(const __grid_consta
         const int block0 = s_first[run] & ~bmask;
 #pragma unroll 4
         for (int t = rp; t <= bmask; t += step) {
-          uint2* const p = reinterpret_cast<uint2*>(codes + code_offset(block0 + t));
-          const uint2 c = *p;
-          const float2 c0 = e4m3x2_to_f32(c.x), c1 = e4m3x2_to_f32(c.x >> 16);
-          const float2 c2 = e4m3x2_to_f32(c.y), c3 = e4m3x2_to_f32(c.y >> 16);
-          *p = make_uint2(e4m3x4(c0.x * f, c0.y * f, c1.x * f, c1.y * f),
-                          e4m3x4(c2.x * f, c2.y * f, c3.x * f, c3.y * f));
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            uint2* const p = reinterpret_cast<uint2*>(codes + code_offset(block0 + t) + 8 * u * LPR);
+            const uint2 c = *p;
+            const float2 c0 = e4m3x2_to_f32(c.x), c1 = e4m3x2_to_f32(c.x >> 16);
+            const float2 c2 = e4m3x2_to_f32(c.y), c3 = e4m3x2_to_f32(c.y >> 16);
+            *p = make_uint2(e4m3x4(c0.x * f, c0.y * f, c1.x * f, c1.y * f),
+                            e4m3x4(c2.x * f, c2.y * f, c3.x * f, c3.y * f));
+          }
         }
       }
       __syncthreads();
@@ -963,9 +992,9 @@ extern "C" int dspark_kv_append_q8(
   a.cap = cap;
   a.chunk = std::max(cap / 2, cap - block + 1);
   const int64_t windows = static_cast<int64_t>(DSPARK_CEILDIV(n, a.chunk));
-  // Where that is not three CTAs per SM, fewer heads for each (2,300 rows of 8 heads: 17.7 -> 15.5
+  // Where that is not three CTAs per SM, fewer heads for each (2,300 rows of 8 heads: 17.4 -> 15.7
   // us); where it is many more, a CTA has several slices, so that it looks for the runs once
-  // (100,000 rows: 219 us with a slice each, 200 with four, 212 with all eight).
+  // (100,000 rows of 8 slices: 165 us with two each, 153 with four, 160 with all).
   while (a.slice > 1 && windows * 2 * DSPARK_CEILDIV(Hkv, a.slice) < 450) a.slice = (a.slice + 1) / 2;
   a.slices = static_cast<int32_t>(DSPARK_CEILDIV(Hkv, a.slice));
   const int64_t ys = std::clamp<int64_t>(3600 / std::max<int64_t>(windows, 1), 1, std::min(2 * a.slices, 65535));
