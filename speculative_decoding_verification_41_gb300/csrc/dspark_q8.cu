@@ -668,9 +668,10 @@ __device__ __forceinline__ uint2 codes_of(float (&y)[8], float inv) {
 }
 // Blocks of one token: each row a scale of its own, nothing is rounded again. A CTA takes `rows`
 // rows, a lane 16 elements at a time, of K and of V, which stay in registers from the maximum to
-// the codes (20,300 rows of 24 x 64, 191 MB: 46 us, 61% of the copy rate; with runs, 89).
+// the codes (20,300 rows of 24 x 64, 191 MB: 43 us, 66% of the copy rate; half as many rows 44,
+// three CTAs per SM 48, with runs 89).
 template <int D, bool F16>
-__global__ void __launch_bounds__(kQ8Threads, 3) k_kv_append_q8_tokens(const __grid_constant__ AppendQ8Args a) {
+__global__ void __launch_bounds__(kQ8Threads, 4) k_kv_append_q8_tokens(const __grid_constant__ AppendQ8Args a) {
   constexpr int LPR = D / 16;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int32_t s_slot[kQ8Threads];
@@ -707,13 +708,11 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_kv_append_q8_tokens(const __g
   const int lane = tid % LPR;
   const Quotient by_row(min(per_row, 4096));
   // one row's one head: its maximum, its scale, its codes
-  auto store = [&](auto turned, const uint16_t* in, uint8_t* codes, float* scales, int row, int head, int slot) {
+  auto store = [&](auto turned, const auto& x, uint8_t* codes, float* scales, int row, int head, int slot) {
     constexpr bool TURNS = decltype(turned)::value;
     const int64_t page = max(slot, 0) >> a.p_shift, t = max(slot, 0) & pmask;
     float y[2][8] = {};
     if (slot >= 0) {
-      Strip<TURNS> x;
-      load_strip(a.t, in + (r0 + row) * a.row + head * a.head, lane, x);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         strip_values<F16>(a.t, x, u, lane, s_cos + row * pairs, s_sin + row * pairs, y[u]);
@@ -750,11 +749,20 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_kv_append_q8_tokens(const __g
     const int i = min(base + tid, total - 1), row = rows == 1 ? 0 : by_row.of(i);
     const int head = (i - row * per_row) / LPR;
     const int slot = base + tid < total ? s_slot[row] : -1;
-    store(std::false_type(), a.v, a.vc, a.vs, row, head, slot);
-    if (a.t.turns)
-      store(std::true_type(), a.k, a.kc, a.ks, row, head, slot);
-    else
-      store(std::false_type(), a.k, a.kc, a.ks, row, head, slot);
+    const int64_t at = (r0 + row) * a.row + head * a.head;
+    Strip<false> v;
+    if (slot >= 0) load_strip(a.t, a.v + at, lane, v);
+    if (a.t.turns) {
+      Strip<true> k;
+      if (slot >= 0) load_strip(a.t, a.k + at, lane, k);
+      store(std::false_type(), v, a.vc, a.vs, row, head, slot);
+      store(std::true_type(), k, a.kc, a.ks, row, head, slot);
+    } else {
+      Strip<false> k;
+      if (slot >= 0) load_strip(a.t, a.k + at, lane, k);
+      store(std::false_type(), v, a.vc, a.vs, row, head, slot);
+      store(std::false_type(), k, a.kc, a.ks, row, head, slot);
+    }
   }
 }
 
@@ -970,7 +978,8 @@ extern "C" int dspark_kv_append_q8(
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f16 = dtype == DSPARK_F16;
   if (block == 1) {
-    a.rows = std::clamp(1024 / (Hkv * (D / 16)), 1, kQ8Threads);
+    a.rows = std::clamp(2048 / (Hkv * (D / 16)), 1, kQ8Threads / 2);
+    while (a.rows > 1 && DSPARK_CEILDIV(n, a.rows) < 304) a.rows /= 2;
     const unsigned grid = 1u + static_cast<unsigned>(DSPARK_CEILDIV(n, a.rows));
     const size_t smem = static_cast<size_t>(a.rows) * pairs * 8;
     const cudaError_t rc = D == 64 ? (f16 ? tokens_launch<64, true>(a, grid, smem, st)
