@@ -225,17 +225,25 @@ __device__ __forceinline__ int slot_of(const AppendQ8Args& a, int i) {
   return s >= a.n_slots || (a.t.turns && a.t.positions[i] < 0) ? -1 : s;
 }
 
-// The first row from `from` on that is not skipped, n if there is none; by the whole CTA.
+// The first row from `from` on that is not skipped, n if there is none; by the whole CTA. (Behind
+// a batch's last row there may be many that are: 16 of them per thread at a time.)
 __device__ __noinline__ int next_row(const AppendQ8Args& a, int from, int* s_found) {
-  for (; from < a.n; from += 4 * kQ8Threads) {
+  constexpr int kAhead = 16;
+  for (; from < a.n; from += kAhead * kQ8Threads) {
     __syncthreads();
     if (threadIdx.x == 0) *s_found = a.n;
     __syncthreads();
+    int32_t s[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = from + k * kQ8Threads + static_cast<int>(threadIdx.x);
+      s[k] = i < a.n ? a.slots[i] : -1;
+    }
     int at = a.n;
 #pragma unroll
-    for (int k = 3; k >= 0; --k) {
+    for (int k = kAhead - 1; k >= 0; --k) {
       const int i = from + k * kQ8Threads + static_cast<int>(threadIdx.x);
-      if (slot_of(a, i) >= 0) at = i;
+      if (s[k] >= 0 && slot_of(a, i) >= 0) at = i;
     }
     if (at < a.n) atomicMin(s_found, at);
     __syncthreads();
